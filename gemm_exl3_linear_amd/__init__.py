@@ -30,6 +30,12 @@ CODEBOOK_MUL1 = 2
 MAX_TOPK = 16
 MAX_MULTI = 8
 SCRATCH_BYTES = 32 << 20  # EXL3_SCRATCH_BYTES
+MX4_BLOCK = 32
+MX4_LINEAR_MAX_ROWS = 64
+MX4_MOE_MAX_TOKENS = 16
+MX4_MOE_MAX_EXPERTS = 1024
+ROUTE_SOFTMAX = 0
+ROUTE_SIGMOID = 1
 
 
 class Exl3Error(RuntimeError):
@@ -52,6 +58,23 @@ class _Arena(ctypes.Structure):
 
 class _Widths(ctypes.Structure):
     _fields_ = [("bits_host", ctypes.c_void_p), ("bits", ctypes.c_void_p), ("offsets", ctypes.c_void_p)]
+
+
+class _Mx4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("k", ctypes.c_int64)]
+
+
+class _Mx4Experts(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("experts", ctypes.c_int32),
+                ("slots", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32)]
+
+
+class _Mx4MoeLayer(ctypes.Structure):
+    _fields_ = [("router", ctypes.c_void_p), ("router_bias", ctypes.c_void_p), ("scoring", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("gate_up", _Mx4Experts),
+                ("down", _Mx4Experts), ("shared_gate_up", _Mx4Experts), ("shared_down", _Mx4Experts),
+                ("shared_gate", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,6 +133,23 @@ def lib() -> ctypes.CDLL:
     L.exl3_grouped_experts_mixed.restype = i32
     L.exl3_grouped_experts_mixed.argtypes = [ctypes.POINTER(_Arena), Wp, ctypes.POINTER(_Arena), Wp, vp, vp, vp,
                                              i64, i32, vp, vp, sz, vp]
+    Mp, Lp = ctypes.POINTER(_Mx4), ctypes.POINTER(_Mx4MoeLayer)
+    L.exl3_mx4_quantize.restype = i32
+    L.exl3_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.exl3_mx4_reconstruct.restype = i32
+    L.exl3_mx4_reconstruct.argtypes = [Mp, vp, i32, i64, vp]
+    L.exl3_mx4_matmul_workspace_size.restype = sz
+    L.exl3_mx4_matmul_workspace_size.argtypes = [Mp, Mp]
+    L.exl3_mx4_matmul.restype = i32
+    L.exl3_mx4_matmul.argtypes = [Mp, Mp, vp, vp, i64, i32, vp, sz, vp]
+    L.exl3_mx4_linear_workspace_size.restype = sz
+    L.exl3_mx4_linear_workspace_size.argtypes = [Mp, i64]
+    L.exl3_mx4_linear.restype = i32
+    L.exl3_mx4_linear.argtypes = [Mp, vp, vp, i64, i64, vp, i64, i32, vp, sz, vp]
+    L.exl3_mx4_moe_workspace_size.restype = sz
+    L.exl3_mx4_moe_workspace_size.argtypes = [Lp, i64, i32]
+    L.exl3_mx4_moe.restype = i32
+    L.exl3_mx4_moe.argtypes = [Lp, vp, i64, i64, i32, vp, i64, i32, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -462,4 +502,282 @@ def exl3_grouped_experts_mixed(x, topk_ids, topk_weights, gate_up: Exl3MixedAren
     _check(lib().exl3_grouped_experts_mixed(ctypes.byref(a), ctypes.byref(wa), ctypes.byref(b), ctypes.byref(wb),
                                             _ptr(x), _ptr(topk_ids), _ptr(topk_weights), t, topk, _ptr(out),
                                             _ptr(workspace), wsb, _stream(stream)), "exl3_grouped_experts_mixed")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 (microscaled 4-bit floating point)
+# ---------------------------------------------------------------------------
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _device_index(t, what: str) -> int:
+    """Index of the GPU that holds t, which has to be the current one: the
+    library launches on the current device's stream."""
+    import torch
+    _need(t.is_cuda, f"{what} is not on a GPU")
+    i = t.device.index
+    _need(i == torch.cuda.current_device(), f"{what} is on GPU {i}, not on the current device")
+    return i
+
+
+def _tensor(t, what: str, dtype, shape=None):
+    """t, checked: dtype, shape (None entries are free), contiguous."""
+    _need(t.dtype == dtype, f"{what} is {t.dtype}, not {dtype}")
+    if shape is not None:
+        _need(t.dim() == len(shape) and all(s is None or s == d for s, d in zip(shape, t.shape)),
+              f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    _need(t.is_contiguous(), f"{what} is not contiguous")
+    return t
+
+
+def _rows(t, what: str, dtypes, rows=None, cols=None):
+    """t, checked as a matrix whose rows are contiguous; its row stride."""
+    _need(t.dim() == 2 and t.dtype in dtypes, f"{what} has to be a matrix of {dtypes}")
+    _need((rows is None or t.shape[0] == rows) and (cols is None or t.shape[1] == cols),
+          f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{what} has to have contiguous rows")
+    # with fewer than two rows the stride says nothing (and may be anything)
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _blob(ws):
+    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _scratch(workspace, need: int, device, what: str):
+    """The caller's workspace, or a zero-filled one of `need` bytes."""
+    import torch
+    if workspace is None:
+        return torch.zeros(need, dtype=torch.uint8, device=device) if need else None
+    if workspace.numel():
+        _need(workspace.is_contiguous(), f"{what} is not contiguous")
+        _device_index(workspace, what)
+    return workspace
+
+
+@dataclass(frozen=True)
+class Exl3Mx4:
+    """An MXFP4 matrix on the GPU: codes uint8 [rows, k/2] (the even element in
+    a byte's low half), scales uint8 [rows, k/32] (2^(s - 127), 255 is NaN)."""
+    codes: "object"
+    scales: "object"
+
+    def __post_init__(self):
+        import torch
+        _tensor(self.codes, "codes", torch.uint8, (None, None))
+        _need(self.codes.shape[1] > 0 and self.codes.shape[1] % (MX4_BLOCK // 2) == 0,
+              f"codes have {self.codes.shape[1]} bytes a row, not a multiple of {MX4_BLOCK // 2}")
+        _tensor(self.scales, "scales", torch.uint8, (self.codes.shape[0], self.codes.shape[1] // (MX4_BLOCK // 2)))
+        _need(self.codes.device == self.scales.device, "codes and scales are on different devices")
+        object.__setattr__(self, "_record", _Mx4(_ptr(self.codes), _ptr(self.scales), self.rows, self.k))
+
+    @property
+    def rows(self) -> int:
+        return int(self.codes.shape[0])
+
+    @property
+    def k(self) -> int:
+        return int(self.codes.shape[1]) * 2
+
+    @staticmethod
+    def empty(rows: int, k: int, device="cuda"):
+        import torch
+        return Exl3Mx4(torch.empty((rows, k // 2), dtype=torch.uint8, device=device),
+                       torch.empty((rows, k // MX4_BLOCK), dtype=torch.uint8, device=device))
+
+
+@dataclass(frozen=True)
+class Exl3Mx4Arena:
+    """MXFP4 tensors of experts on the GPU: codes uint8 [E, slots, n, k/2],
+    scales uint8 [E, slots, n, k/32]."""
+    codes: "object"
+    scales: "object"
+
+    def __post_init__(self):
+        import torch
+        _tensor(self.codes, "codes", torch.uint8, (None, None, None, None))
+        e, slots, n, half = self.codes.shape
+        _tensor(self.scales, "scales", torch.uint8, (e, slots, n, half // (MX4_BLOCK // 2)))
+        _need(half > 0 and half % (MX4_BLOCK // 2) == 0, f"codes have {half} bytes a row")
+        _need(self.codes.device == self.scales.device, "codes and scales are on different devices")
+
+    def _c(self) -> _Mx4Experts:
+        e, slots, n, half = self.codes.shape
+        return _Mx4Experts(_ptr(self.codes), _ptr(self.scales), e, slots, n, 2 * half)
+
+
+@dataclass(frozen=True)
+class Exl3MoeRouter:
+    """Router of a mixture-of-experts layer: weight fp16 [E, hidden], bias fp32
+    [E] or None, scoring "softmax" (chosen and weighted by softmax(l + bias)) or
+    "sigmoid" (chosen by sigmoid(l) + bias, weighted by sigmoid(l)); weights are
+    divided by their sum if `renormalize`, then multiplied by `scale`."""
+    weight: "object"
+    bias: Optional["object"] = None
+    scoring: str = "softmax"
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+@dataclass(frozen=True)
+class Exl3Mx4Shared:
+    """Shared expert: arenas of one expert, and optionally gate fp16 [hidden]
+    (its weight is sigmoid(x . gate), else 1)."""
+    gate_up: Exl3Mx4Arena
+    down: Exl3Mx4Arena
+    gate: Optional["object"] = None
+
+
+@dataclass(frozen=True)
+class Exl3Mx4Moe:
+    """A mixture-of-experts layer with MXFP4 experts: gate_up [E, 2, inter, .],
+    down [E, 1, hidden, .], and optionally a shared expert."""
+    router: Exl3MoeRouter
+    gate_up: Exl3Mx4Arena
+    down: Exl3Mx4Arena
+    shared: Optional[Exl3Mx4Shared] = None
+
+    def __post_init__(self):
+        import torch
+        gu, dn, sh, r = self.gate_up._c(), self.down._c(), self.shared, self.router
+        dev = self.gate_up.codes.device
+        tensors = [self.down.codes, _tensor(r.weight, "router weight", torch.float16, (gu.experts, gu.k))]
+        if r.bias is not None:
+            tensors.append(_tensor(r.bias, "router bias", torch.float32, (gu.experts,)))
+        _need(r.scoring in ("softmax", "sigmoid"), f"scoring {r.scoring!r} is not softmax or sigmoid")
+        sgu, sdn, gate = _Mx4Experts(), _Mx4Experts(), None
+        if sh is not None:
+            sgu, sdn, gate = sh.gate_up._c(), sh.down._c(), sh.gate
+            tensors += [sh.gate_up.codes, sh.down.codes]
+            if gate is not None:
+                tensors.append(_tensor(gate, "shared gate", torch.float16, (gu.k,)))
+        _need(all(t.device == dev for t in tensors), "the layer's tensors are on different devices")
+        scoring = ROUTE_SOFTMAX if r.scoring == "softmax" else ROUTE_SIGMOID
+        object.__setattr__(self, "_record", _Mx4MoeLayer(_ptr(r.weight), _ptr(r.bias), scoring, int(r.renormalize),
+                                                         float(r.scale), gu, dn, sgu, sdn, _ptr(gate)))
+
+    @property
+    def hidden(self) -> int:
+        return int(self._record.gate_up.k)
+
+
+def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
+    """MXFP4 of fp16 or fp32 rows x [rows, k], k a multiple of 32."""
+    import torch
+    ldx = _rows(x, "x", (torch.float16, torch.float32))
+    _device_index(x, "x")
+    rows, k = x.shape
+    if out is None:
+        _need(k > 0 and k % MX4_BLOCK == 0, f"x has {k} columns, not a multiple of {MX4_BLOCK}")
+        out = Exl3Mx4.empty(rows, k, device=x.device)
+    r = out._record
+    _need((r.rows, r.k) == (rows, k) and out.codes.device == x.device, "out does not match x")
+    _check(lib().exl3_mx4_quantize(x.data_ptr(), EXL3_F16 if x.dtype == torch.float16 else EXL3_F32, rows, k, ldx,
+                                   r.codes, r.scales, _stream(stream)), "exl3_mx4_quantize")
+    return out
+
+
+def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
+    """The values w stands for, fp16 (the default) or fp32 [rows, k]."""
+    import torch
+    _device_index(w.codes, "w")
+    if out is None:
+        out = torch.empty((w.rows, w.k), dtype=dtype or torch.float16, device=w.codes.device)
+    _need(out.device == w.codes.device, "out is on another device than w")
+    ldo = _rows(out, "out", (torch.float16, torch.float32), w.rows, w.k)
+    _check(lib().exl3_mx4_reconstruct(ctypes.byref(w._record), out.data_ptr(), _ydt(out.dtype), ldo, _stream(stream)),
+           "exl3_mx4_reconstruct")
+    return out
+
+
+def _product_out(out, out_dtype, m: int, n: int, device, bias):
+    import torch
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype or torch.float16, device=device)
+    _need(out.device == device, "out is on another device than the operands")
+    ldy = _rows(out, "out", (torch.float16, torch.float32), m, n)
+    if bias is not None:
+        _tensor(bias, "bias", torch.float16, (n,))
+        _need(bias.device == device, "bias is on another device than the operands")
+    return out, max(ldy, n), EXL3_F16 if out.dtype == torch.float16 else EXL3_F32
+
+
+def exl3_mx4_matmul_workspace_size(a: Exl3Mx4, b: Exl3Mx4) -> int:
+    return int(lib().exl3_mx4_matmul_workspace_size(ctypes.byref(a._record), ctypes.byref(b._record)))
+
+
+def exl3_mx4_matmul(a: Exl3Mx4, b: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4.  A
+    workspace passed in has to be zero-filled before its first use."""
+    device = a.codes.device
+    _device_index(a.codes, "a")
+    _need(b.codes.device == device, "a and b are on different devices")
+    out, ldy, ydt = _product_out(out, out_dtype, a.rows, b.rows, device, bias)
+    if workspace is None:
+        workspace = _scratch(None, exl3_mx4_matmul_workspace_size(a, b), device, "workspace")
+    else:
+        _scratch(workspace, 0, device, "workspace")
+    ws, wsb = _blob(workspace)
+    _check(lib().exl3_mx4_matmul(ctypes.byref(a._record), ctypes.byref(b._record), _ptr(bias), out.data_ptr(), ldy,
+                                 ydt, ws, wsb, _stream(stream)), "exl3_mx4_matmul")
+    return out
+
+
+def exl3_mx4_linear_workspace_size(w: Exl3Mx4, m: int) -> int:
+    return int(lib().exl3_mx4_linear_workspace_size(ctypes.byref(w._record), int(m)))
+
+
+def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """y [m, n] = x w^T (+ bias fp16 [n]): fp16 rows x [m, k], m up to 64,
+    against MXFP4 weights w [n, k].  A workspace passed in has to be
+    zero-filled before its first use."""
+    import torch
+    ldx = _rows(x, "x", (torch.float16,), None, w.k)
+    _device_index(x, "x")
+    device = x.device
+    _need(w.codes.device == device, "x and w are on different devices")
+    m = x.shape[0]
+    out, ldy, ydt = _product_out(out, out_dtype, m, w.rows, device, bias)
+    if workspace is None:
+        workspace = _scratch(None, exl3_mx4_linear_workspace_size(w, m), device, "workspace")
+    else:
+        _scratch(workspace, 0, device, "workspace")
+    ws, wsb = _blob(workspace)
+    _check(lib().exl3_mx4_linear(ctypes.byref(w._record), _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt,
+                                 ws, wsb, _stream(stream)), "exl3_mx4_linear")
+    return out
+
+
+def exl3_mx4_moe_workspace_size(layer: Exl3Mx4Moe, t: int, topk: int) -> int:
+    return int(lib().exl3_mx4_moe_workspace_size(ctypes.byref(layer._record), int(t), int(topk)))
+
+
+def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk_ids=None, topk_weights=None,
+                 workspace=None, stream=None):
+    """A whole mixture-of-experts layer for up to 16 tokens x fp16 [t, hidden]:
+    router, top-k, SwiGLU experts, shared expert.  topk_ids int32 and
+    topk_weights fp32 [t, topk] receive the routing if given.  A workspace
+    passed in has to be zero-filled before its first use and is then left to
+    this function."""
+    import torch
+    ldx = _rows(x, "x", (torch.float16,), None, layer.hidden)
+    _device_index(x, "x")
+    device = x.device
+    _need(layer.gate_up.codes.device == device, "x and the layer are on different devices")
+    t = x.shape[0]
+    out, ldy, ydt = _product_out(out, out_dtype, t, layer.hidden, device, None)
+    for v, what, dt in ((topk_ids, "topk_ids", torch.int32), (topk_weights, "topk_weights", torch.float32)):
+        if v is not None:
+            _tensor(v, what, dt, (t, topk))
+            _need(v.device == device, f"{what} is on another device than x")
+    if workspace is None:
+        workspace = _scratch(None, exl3_mx4_moe_workspace_size(layer, t, topk), device, "workspace")
+    else:
+        _scratch(workspace, 0, device, "workspace")
+    ws, wsb = _blob(workspace)
+    _check(lib().exl3_mx4_moe(ctypes.byref(layer._record), x.data_ptr(), t, ldx, int(topk), out.data_ptr(), ldy, ydt,
+                              _ptr(topk_ids), _ptr(topk_weights), ws, wsb, _stream(stream)), "exl3_mx4_moe")
     return out

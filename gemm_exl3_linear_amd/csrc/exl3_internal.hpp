@@ -120,4 +120,34 @@ hipError_t launch_grouped(const ArenaDesc& gu, const ArenaDesc& dn, const uint16
                           const int32_t* ids, const float* w, int64_t t, int topk, float* y,
                           void* ws, size_t ws_bytes, bool off_xcd_all, hipStream_t s);
 
+// --- MXFP4 -------------------------------------------------------------------
+hipError_t launch_mx4_quantize(const void* x, bool f32, int64_t rows, int64_t k, int64_t ldx,
+                               uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_reconstruct(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k,
+                                  void* out, bool f32, int64_t ldo, hipStream_t s);
+size_t mx4_matmul_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
+                             const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y,
+                             int64_t ldy, bool y_f32, void* ws, hipStream_t s);
+size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k,
+                             const uint16_t* bias, const uint16_t* x, int64_t m, int64_t ldx, void* y,
+                             int64_t ldy, bool y_f32, void* ws, hipStream_t s);
+
+// A mixture-of-experts layer with MXFP4 experts; shared_inter == 0: no shared
+// expert.
+struct Mx4MoeDesc {
+  const uint16_t* router;
+  const float* router_bias;
+  int scoring, renormalize;
+  float scale;
+  int experts, hidden, inter, shared_inter;
+  const uint8_t *gu_codes, *gu_scales, *dn_codes, *dn_scales;
+  const uint8_t *sgu_codes, *sgu_scales, *sdn_codes, *sdn_scales;
+  const uint16_t* shared_gate;
+};
+size_t mx4_moe_workspace(const Mx4MoeDesc& d, int64_t t, int topk);
+hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int64_t ldx, int topk, void* y,
+                          int64_t ldy, bool y_f32, int32_t* ids, float* weights, void* ws, hipStream_t s);
+
 }  // namespace exl3

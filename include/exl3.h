@@ -353,6 +353,176 @@ exl3_status exl3_grouped_experts_mixed(const exl3_expert_weights* gate_up,
                                        int64_t t, int32_t topk, float* y, void* ws,
                                        size_t ws_bytes, exl3_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floating point (the block format of the OCP
+ * Microscaling Formats specification, version 1.0: E2M1 elements, E8M0
+ * scales, blocks of 32), the matrix cores' own 4-bit format on gfx950.
+ *
+ * A matrix of `rows` rows and k columns (k a multiple of 32) is held as
+ *   codes   uint8 [rows][k/2], row-major: element 2i of a row in the low half
+ *           of byte i, element 2i+1 in the high half.  Bit 3 of a code is the
+ *           sign, bits 0..2 name 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  uint8 [rows][k/32], row-major: one byte s per 32 consecutive
+ *           elements, the factor 2^(s - 127); 255 is NaN (the whole block)
+ * Both device pointers 16-byte aligned.  0 < k < 2^24, 0 <= rows <= 2^24.
+ * A weight of a linear layer is stored [out_features][in_features].
+ * ------------------------------------------------------------------------ */
+#define EXL3_MX4_BLOCK 32
+
+typedef struct exl3_mx4 {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t rows;
+    int64_t k;
+} exl3_mx4;
+
+/* exl3_mx4_quantize - rows of fp16 or fp32 to MXFP4.
+ *   S = 2^(floor(log2 max|x|) - 2) over each block of 32 (the specification's
+ *   rule: E2M1's largest exponent is 2), the exponent not below -127;
+ *   code = x / S rounded to the nearest E2M1 value, ties to the even code,
+ *   magnitudes above 6 to 6; the sign bit is x's, also where x / S rounds to 0
+ *   x       [rows][ldx] of `dtype` (EXL3_F16 or EXL3_F32), ldx >= k, multiple
+ *           of 8
+ *   codes, scales  as above, written whole
+ * A block of zeros gets scale byte 0.  A block that holds a NaN or an
+ * infinity becomes a NaN block: scale byte 255, codes 0.  Every decision is
+ * exact, so the output is bit-exact by definition.  rows == 0 returns
+ * EXL3_OK.  rows * k must stay below 2^35 (launch size).                   */
+exl3_status exl3_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, exl3_stream_t stream);
+
+/* exl3_mx4_reconstruct - the values an MXFP4 matrix stands for.
+ *   out     [rows][ld_out] of `dtype` (EXL3_F16 or EXL3_F32), ld_out >= k,
+ *           multiple of 8
+ * Values are exact in fp32 except past its range (scale bytes 253 and 254:
+ * magnitudes from 2^128 become infinity); fp16 rounds to nearest once.  What
+ * exl3_mx4_quantize made of fp16 rows is exact in fp16.  NaN blocks give NaN.
+ * rows * k must stay below 2^39.                                           */
+exl3_status exl3_mx4_reconstruct(const exl3_mx4* w, void* out, int32_t dtype, int64_t ld_out,
+                                 exl3_stream_t stream);
+
+/* Bytes of device workspace exl3_mx4_matmul needs (0 if none is needed, or
+ * the arguments are invalid). */
+size_t exl3_mx4_matmul_workspace_size(const exl3_mx4* a, const exl3_mx4* b);
+
+/* exl3_mx4_matmul - y = A B^T (+ bias), both operands MXFP4, on the scaled
+ * 4-bit matrix cores.  Products are exact, sums fp32, one rounding to an fp16
+ * output.
+ *   a      [m][k] (rows = m), b [n][k] (rows = n), the same k; m and n any
+ *   bias   fp16 [n] device pointer or NULL (added last, in fp32)
+ *   y      [m][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= n; rows need no
+ *          alignment beyond the element's own
+ *   ws     device workspace of at least the queried size (may be NULL when
+ *          that is 0), zero-filled before its first use; calls leave its
+ *          arrival counts at zero, so it serves later calls without clearing.
+ *          Calls that overlap in time on one workspace race.
+ * m == 0 or n == 0 returns EXL3_OK.  Calls whose launch would not fit the
+ * hardware's grid (ceil(m/16) * ceil(n/16) >= 2^26) return EXL3_E_INVALID.
+ * Results are the same bits on every run of one shape; a row's result may
+ * depend on m (the tile is chosen by size), to rounding.                   */
+exl3_status exl3_mx4_matmul(const exl3_mx4* a, const exl3_mx4* b, const uint16_t* bias, void* y,
+                            int64_t ldy, int32_t y_dtype, void* ws, size_t ws_bytes,
+                            exl3_stream_t stream);
+
+/* Largest row count of exl3_mx4_linear. */
+#define EXL3_MX4_LINEAR_MAX_ROWS 64
+
+/* Bytes of device workspace exl3_mx4_linear needs for m rows (0 if none is
+ * needed, or the arguments are invalid). */
+size_t exl3_mx4_linear_workspace_size(const exl3_mx4* w, int64_t m);
+
+/* exl3_mx4_linear - y = x W^T (+ bias) for decode and verify batches: fp16
+ * activations, unrounded, against MXFP4 weights; products exact in fp32, sums
+ * fp32.  For more than EXL3_MX4_LINEAR_MAX_ROWS rows the weights' bytes no
+ * longer bound the product: quantize the rows and call exl3_mx4_matmul.
+ *   w      [n][k] (rows = n)
+ *   x      fp16 [m][ldx], ldx >= k, multiple of 8
+ *   bias, y, ldy, y_dtype, ws   as for exl3_mx4_matmul
+ * 0 <= m <= EXL3_MX4_LINEAR_MAX_ROWS; m == 0 or n == 0 returns EXL3_OK.    */
+exl3_status exl3_mx4_linear(const exl3_mx4* w, const uint16_t* bias, const void* x, int64_t m,
+                            int64_t ldx, void* y, int64_t ldy, int32_t y_dtype, void* ws,
+                            size_t ws_bytes, exl3_stream_t stream);
+
+/* Packed MXFP4 tensors of experts:
+ *   codes   uint8 [experts][slots][n][k/2]
+ *   scales  uint8 [experts][slots][n][k/32]
+ * n and k multiples of 32, at most 65536.                                  */
+typedef struct exl3_mx4_experts {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int32_t experts;
+    int32_t slots;
+    int32_t n;
+    int32_t k;
+} exl3_mx4_experts;
+
+/* How a router's logits become choices and weights (l = x W_r^T, b the bias,
+ * 0 where there is none):
+ *   EXL3_ROUTE_SOFTMAX  chosen by l + b, weight softmax(l + b) over all experts
+ *   EXL3_ROUTE_SIGMOID  chosen by sigmoid(l) + b, weight sigmoid(l)          */
+typedef enum exl3_route {
+    EXL3_ROUTE_SOFTMAX = 0,
+    EXL3_ROUTE_SIGMOID = 1
+} exl3_route;
+
+/* One mixture-of-experts layer.
+ *   router       fp16 [experts][hidden], row-major, 16-byte aligned
+ *   router_bias  fp32 [experts], 4-byte aligned, or NULL
+ *   scoring      exl3_route
+ *   renormalize  not 0: a token's weights are divided by their sum
+ *   scale        factor of the routed weights (after the division)
+ *   gate_up      slots == 2 (slot 0 = gate, slot 1 = up), k = hidden,
+ *                n = intermediate
+ *   down         slots == 1, k = intermediate, n = hidden, as many experts
+ *   shared_gate_up, shared_down   the shared expert (experts == 1, slots as
+ *                above, its own intermediate width), or codes == NULL in both
+ *   shared_gate  fp16 [hidden], 16-byte aligned, or NULL: the shared expert's
+ *                weight is sigmoid(x . shared_gate), or 1                    */
+typedef struct exl3_mx4_moe_layer {
+    const uint16_t* router;
+    const float* router_bias;
+    int32_t scoring;
+    int32_t renormalize;
+    float scale;
+    exl3_mx4_experts gate_up;
+    exl3_mx4_experts down;
+    exl3_mx4_experts shared_gate_up;
+    exl3_mx4_experts shared_down;
+    const uint16_t* shared_gate;
+} exl3_mx4_moe_layer;
+
+/* Limits of exl3_mx4_moe. */
+#define EXL3_MX4_MOE_MAX_TOKENS 16
+#define EXL3_MX4_MOE_MAX_EXPERTS 1024
+
+/* Bytes of device workspace exl3_mx4_moe needs (0 if the arguments are
+ * invalid or t == 0). */
+size_t exl3_mx4_moe_workspace_size(const exl3_mx4_moe_layer* layer, int64_t t, int32_t topk);
+
+/* exl3_mx4_moe - a whole mixture-of-experts layer for a few tokens:
+ *   y[i] = sum over the chosen experts e of w[i][e] * down_e(a_e)
+ *          (+ w_s[i] * down_s(a_s)),   a = silu(gate(x_i)) * up(x_i)
+ * Activations are not rounded to 4 bits: x enters as fp16, a is held to 24
+ * bits, every sum and the routing in fp32.
+ *   x             fp16 [t][ldx], ldx >= hidden, multiple of 8
+ *   topk          experts per token, 1..min(EXL3_MAX_TOPK, experts); equal
+ *                 scores go to the lower expert
+ *   y             [t][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= hidden
+ *   topk_ids      int32 [t][topk] device pointer or NULL: the choices, best
+ *                 first
+ *   topk_weights  fp32 [t][topk] device pointer or NULL: their weights
+ *   ws            device workspace of at least the queried size, zero-filled
+ *                 before its first use and then left to this entry point
+ *                 (calls of any layer and size may share it, one after the
+ *                 other); calls that overlap on it race
+ * 0 <= t <= EXL3_MX4_MOE_MAX_TOKENS, experts <= EXL3_MX4_MOE_MAX_EXPERTS;
+ * t == 0 returns EXL3_OK.  A NaN score counts as the lowest, so the ids are
+ * always valid; a token with NaN or infinite logits gets NaN weights.  For
+ * more tokens: a router and exl3_grouped_experts, or quantized rows.        */
+exl3_status exl3_mx4_moe(const exl3_mx4_moe_layer* layer, const void* x, int64_t t, int64_t ldx,
+                         int32_t topk, void* y, int64_t ldy, int32_t y_dtype, int32_t* topk_ids,
+                         float* topk_weights, void* ws, size_t ws_bytes, exl3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
