@@ -508,54 +508,69 @@ def exl3_grouped_experts_mixed(x, topk_ids, topk_weights, gate_up: Exl3MixedAren
 # ---------------------------------------------------------------------------
 # MXFP4 (microscaled 4-bit floating point)
 # ---------------------------------------------------------------------------
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _device_index(t, what: str) -> int:
-    """Index of the GPU that holds t, which has to be the current one: the
-    library launches on the current device's stream."""
+def _stream_for(t, what: str, stream) -> int:
+    """The stream's handle (the current one if None) for a call on t, which has
+    to be on the current device: the library launches there.  The raw query
+    costs 0.1 us of host time where torch.cuda.current_stream() costs 2.9."""
     import torch
-    _need(t.is_cuda, f"{what} is not on a GPU")
-    i = t.device.index
-    _need(i == torch.cuda.current_device(), f"{what} is on GPU {i}, not on the current device")
-    return i
+    if not t.is_cuda:
+        _refuse(f"{what} is not on a GPU")
+    i = t.get_device()
+    if i != torch._C._cuda_getDevice():
+        _refuse(f"{what} is on GPU {i}, not on the current device")
+    return torch._C._cuda_getCurrentRawStream(i) if stream is None else int(stream.cuda_stream)
 
 
-def _tensor(t, what: str, dtype, shape=None):
+def _tensor(t, what: str, dtype, shape):
     """t, checked: dtype, shape (None entries are free), contiguous."""
-    _need(t.dtype == dtype, f"{what} is {t.dtype}, not {dtype}")
-    if shape is not None:
-        _need(t.dim() == len(shape) and all(s is None or s == d for s, d in zip(shape, t.shape)),
-              f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    _need(t.is_contiguous(), f"{what} is not contiguous")
+    if t.dtype != dtype:
+        _refuse(f"{what} is {t.dtype}, not {dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape)):
+        _refuse(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        _refuse(f"{what} is not contiguous")
     return t
 
 
-def _rows(t, what: str, dtypes, rows=None, cols=None):
-    """t, checked as a matrix whose rows are contiguous; its row stride."""
-    _need(t.dim() == 2 and t.dtype in dtypes, f"{what} has to be a matrix of {dtypes}")
-    _need((rows is None or t.shape[0] == rows) and (cols is None or t.shape[1] == cols),
-          f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{what} has to have contiguous rows")
-    # with fewer than two rows the stride says nothing (and may be anything)
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+def _f16_f32(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.float16:
+        return EXL3_F16
+    if t.dtype != torch.float32:
+        _refuse(f"{what} is {t.dtype}, not fp16 or fp32")
+    return EXL3_F32
 
 
-def _blob(ws):
-    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
+    """Row stride of t, checked as a matrix of contiguous rows.  With fewer than
+    two rows the stride says nothing and the width, rounded up to 8, stands in."""
+    if t.dim() != 2:
+        _refuse(f"{what} is not a matrix")
+    m, n = t.shape
+    if (rows is not None and m != rows) or (cols is not None and n != cols):
+        _refuse(f"{what} has shape {(m, n)}, not {(rows, cols)}")
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        _refuse(f"{what} does not have contiguous rows")
+    return ld if m > 1 else -(-n // 8) * 8
 
 
-def _scratch(workspace, need: int, device, what: str):
-    """The caller's workspace, or a zero-filled one of `need` bytes."""
+def _scratch(workspace, need, args, device):
+    """Address and bytes of the caller's workspace, or of a zero-filled one (of
+    need(*args) bytes) and the tensor that holds it."""
     import torch
     if workspace is None:
-        return torch.zeros(need, dtype=torch.uint8, device=device) if need else None
-    if workspace.numel():
-        _need(workspace.is_contiguous(), f"{what} is not contiguous")
-        _device_index(workspace, what)
-    return workspace
+        n = need(*args)
+        if not n:
+            return 0, 0, None
+        workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+    elif workspace.numel() and (workspace.device != device or not workspace.is_contiguous()):
+        _refuse("the workspace is on another device than the operands, or not contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 @dataclass(frozen=True)
@@ -568,11 +583,14 @@ class Exl3Mx4:
     def __post_init__(self):
         import torch
         _tensor(self.codes, "codes", torch.uint8, (None, None))
-        _need(self.codes.shape[1] > 0 and self.codes.shape[1] % (MX4_BLOCK // 2) == 0,
-              f"codes have {self.codes.shape[1]} bytes a row, not a multiple of {MX4_BLOCK // 2}")
+        if self.codes.shape[1] == 0 or self.codes.shape[1] % (MX4_BLOCK // 2):
+            _refuse(f"codes have {self.codes.shape[1]} bytes a row, not a multiple of {MX4_BLOCK // 2}")
         _tensor(self.scales, "scales", torch.uint8, (self.codes.shape[0], self.codes.shape[1] // (MX4_BLOCK // 2)))
-        _need(self.codes.device == self.scales.device, "codes and scales are on different devices")
-        object.__setattr__(self, "_record", _Mx4(_ptr(self.codes), _ptr(self.scales), self.rows, self.k))
+        if self.codes.device != self.scales.device:
+            _refuse("codes and scales are on different devices")
+        record = _Mx4(_ptr(self.codes), _ptr(self.scales), self.rows, self.k)
+        object.__setattr__(self, "_record", record)
+        object.__setattr__(self, "_ref", ctypes.byref(record))
 
     @property
     def rows(self) -> int:
@@ -601,8 +619,10 @@ class Exl3Mx4Arena:
         _tensor(self.codes, "codes", torch.uint8, (None, None, None, None))
         e, slots, n, half = self.codes.shape
         _tensor(self.scales, "scales", torch.uint8, (e, slots, n, half // (MX4_BLOCK // 2)))
-        _need(half > 0 and half % (MX4_BLOCK // 2) == 0, f"codes have {half} bytes a row")
-        _need(self.codes.device == self.scales.device, "codes and scales are on different devices")
+        if half == 0 or half % (MX4_BLOCK // 2):
+            _refuse(f"codes have {half} bytes a row, not a multiple of {MX4_BLOCK // 2}")
+        if self.codes.device != self.scales.device:
+            _refuse("codes and scales are on different devices")
 
     def _c(self) -> _Mx4Experts:
         e, slots, n, half = self.codes.shape
@@ -647,87 +667,90 @@ class Exl3Mx4Moe:
         tensors = [self.down.codes, _tensor(r.weight, "router weight", torch.float16, (gu.experts, gu.k))]
         if r.bias is not None:
             tensors.append(_tensor(r.bias, "router bias", torch.float32, (gu.experts,)))
-        _need(r.scoring in ("softmax", "sigmoid"), f"scoring {r.scoring!r} is not softmax or sigmoid")
+        if r.scoring not in ("softmax", "sigmoid"):
+            _refuse(f"scoring {r.scoring!r} is not softmax or sigmoid")
         sgu, sdn, gate = _Mx4Experts(), _Mx4Experts(), None
         if sh is not None:
             sgu, sdn, gate = sh.gate_up._c(), sh.down._c(), sh.gate
             tensors += [sh.gate_up.codes, sh.down.codes]
             if gate is not None:
                 tensors.append(_tensor(gate, "shared gate", torch.float16, (gu.k,)))
-        _need(all(t.device == dev for t in tensors), "the layer's tensors are on different devices")
+        if any(t.device != dev for t in tensors):
+            _refuse("the layer's tensors are on different devices")
         scoring = ROUTE_SOFTMAX if r.scoring == "softmax" else ROUTE_SIGMOID
-        object.__setattr__(self, "_record", _Mx4MoeLayer(_ptr(r.weight), _ptr(r.bias), scoring, int(r.renormalize),
-                                                         float(r.scale), gu, dn, sgu, sdn, _ptr(gate)))
-
-    @property
-    def hidden(self) -> int:
-        return int(self._record.gate_up.k)
-
+        record = _Mx4MoeLayer(_ptr(r.weight), _ptr(r.bias), scoring, int(r.renormalize), float(r.scale), gu, dn,
+                              sgu, sdn, _ptr(gate))
+        object.__setattr__(self, "_record", record)
+        object.__setattr__(self, "_ref", ctypes.byref(record))
 
 def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     """MXFP4 of fp16 or fp32 rows x [rows, k], k a multiple of 32."""
-    import torch
-    ldx = _rows(x, "x", (torch.float16, torch.float32))
-    _device_index(x, "x")
+    ldx = _row_stride(x, "x", None, None)
+    dtype = _f16_f32(x, "x")
+    on = _stream_for(x, "x", stream)
     rows, k = x.shape
     if out is None:
-        _need(k > 0 and k % MX4_BLOCK == 0, f"x has {k} columns, not a multiple of {MX4_BLOCK}")
+        if k == 0 or k % MX4_BLOCK:
+            _refuse(f"x has {k} columns, not a multiple of {MX4_BLOCK}")
         out = Exl3Mx4.empty(rows, k, device=x.device)
     r = out._record
-    _need((r.rows, r.k) == (rows, k) and out.codes.device == x.device, "out does not match x")
-    _check(lib().exl3_mx4_quantize(x.data_ptr(), EXL3_F16 if x.dtype == torch.float16 else EXL3_F32, rows, k, ldx,
-                                   r.codes, r.scales, _stream(stream)), "exl3_mx4_quantize")
+    if r.rows != rows or r.k != k or out.codes.device != x.device:
+        _refuse("out does not match x")
+    _check(lib().exl3_mx4_quantize(x.data_ptr(), dtype, rows, k, ldx, r.codes, r.scales, on),
+           "exl3_mx4_quantize")
     return out
 
 
 def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     """The values w stands for, fp16 (the default) or fp32 [rows, k]."""
     import torch
-    _device_index(w.codes, "w")
+    on = _stream_for(w.codes, "w", stream)
+    r = w._record
     if out is None:
-        out = torch.empty((w.rows, w.k), dtype=dtype or torch.float16, device=w.codes.device)
-    _need(out.device == w.codes.device, "out is on another device than w")
-    ldo = _rows(out, "out", (torch.float16, torch.float32), w.rows, w.k)
-    _check(lib().exl3_mx4_reconstruct(ctypes.byref(w._record), out.data_ptr(), _ydt(out.dtype), ldo, _stream(stream)),
+        out = torch.empty((r.rows, r.k), dtype=dtype or torch.float16, device=w.codes.device)
+    elif out.device != w.codes.device:
+        _refuse("out is on another device than w")
+    ldo = _row_stride(out, "out", r.rows, r.k)
+    _check(lib().exl3_mx4_reconstruct(w._ref, out.data_ptr(), _f16_f32(out, "out"), ldo, on),
            "exl3_mx4_reconstruct")
     return out
 
 
 def _product_out(out, out_dtype, m: int, n: int, device, bias):
+    """The output of a product (a new one if none is given), its row stride and type."""
     import torch
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype or torch.float16, device=device)
-    _need(out.device == device, "out is on another device than the operands")
-    ldy = _rows(out, "out", (torch.float16, torch.float32), m, n)
+    elif out.device != device:
+        _refuse("out is on another device than the operands")
+    ldy = _row_stride(out, "out", m, n)
     if bias is not None:
         _tensor(bias, "bias", torch.float16, (n,))
-        _need(bias.device == device, "bias is on another device than the operands")
-    return out, max(ldy, n), EXL3_F16 if out.dtype == torch.float16 else EXL3_F32
+        if bias.device != device:
+            _refuse("bias is on another device than the operands")
+    return out, ldy, _f16_f32(out, "out")
 
 
 def exl3_mx4_matmul_workspace_size(a: Exl3Mx4, b: Exl3Mx4) -> int:
-    return int(lib().exl3_mx4_matmul_workspace_size(ctypes.byref(a._record), ctypes.byref(b._record)))
+    return int(lib().exl3_mx4_matmul_workspace_size(a._ref, b._ref))
 
 
 def exl3_mx4_matmul(a: Exl3Mx4, b: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4.  A
     workspace passed in has to be zero-filled before its first use."""
     device = a.codes.device
-    _device_index(a.codes, "a")
-    _need(b.codes.device == device, "a and b are on different devices")
-    out, ldy, ydt = _product_out(out, out_dtype, a.rows, b.rows, device, bias)
-    if workspace is None:
-        workspace = _scratch(None, exl3_mx4_matmul_workspace_size(a, b), device, "workspace")
-    else:
-        _scratch(workspace, 0, device, "workspace")
-    ws, wsb = _blob(workspace)
-    _check(lib().exl3_mx4_matmul(ctypes.byref(a._record), ctypes.byref(b._record), _ptr(bias), out.data_ptr(), ldy,
-                                 ydt, ws, wsb, _stream(stream)), "exl3_mx4_matmul")
+    on = _stream_for(a.codes, "a", stream)
+    if b.codes.device != device:
+        _refuse("a and b are on different devices")
+    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, device, bias)
+    ws, nws, _keep = _scratch(workspace, exl3_mx4_matmul_workspace_size, (a, b), device)
+    _check(lib().exl3_mx4_matmul(a._ref, b._ref, _ptr(bias), out.data_ptr(), ldy, ydt, ws, nws, on),
+           "exl3_mx4_matmul")
     return out
 
 
 def exl3_mx4_linear_workspace_size(w: Exl3Mx4, m: int) -> int:
-    return int(lib().exl3_mx4_linear_workspace_size(ctypes.byref(w._record), int(m)))
+    return int(lib().exl3_mx4_linear_workspace_size(w._ref, int(m)))
 
 
 def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
@@ -735,24 +758,24 @@ def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspac
     against MXFP4 weights w [n, k].  A workspace passed in has to be
     zero-filled before its first use."""
     import torch
-    ldx = _rows(x, "x", (torch.float16,), None, w.k)
-    _device_index(x, "x")
+    r = w._record
+    ldx = _row_stride(x, "x", None, r.k)
+    if x.dtype != torch.float16:
+        _refuse(f"x is {x.dtype}, not fp16")
+    on = _stream_for(x, "x", stream)
     device = x.device
-    _need(w.codes.device == device, "x and w are on different devices")
+    if w.codes.device != device:
+        _refuse("x and w are on different devices")
     m = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, m, w.rows, device, bias)
-    if workspace is None:
-        workspace = _scratch(None, exl3_mx4_linear_workspace_size(w, m), device, "workspace")
-    else:
-        _scratch(workspace, 0, device, "workspace")
-    ws, wsb = _blob(workspace)
-    _check(lib().exl3_mx4_linear(ctypes.byref(w._record), _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt,
-                                 ws, wsb, _stream(stream)), "exl3_mx4_linear")
+    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, device, bias)
+    ws, nws, _keep = _scratch(workspace, exl3_mx4_linear_workspace_size, (w, m), device)
+    _check(lib().exl3_mx4_linear(w._ref, _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt, ws, nws,
+                                 on), "exl3_mx4_linear")
     return out
 
 
 def exl3_mx4_moe_workspace_size(layer: Exl3Mx4Moe, t: int, topk: int) -> int:
-    return int(lib().exl3_mx4_moe_workspace_size(ctypes.byref(layer._record), int(t), int(topk)))
+    return int(lib().exl3_mx4_moe_workspace_size(layer._ref, int(t), int(topk)))
 
 
 def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk_ids=None, topk_weights=None,
@@ -763,21 +786,20 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
     passed in has to be zero-filled before its first use and is then left to
     this function."""
     import torch
-    ldx = _rows(x, "x", (torch.float16,), None, layer.hidden)
-    _device_index(x, "x")
+    hidden = layer._record.gate_up.k
+    ldx = _row_stride(x, "x", None, hidden)
+    if x.dtype != torch.float16:
+        _refuse(f"x is {x.dtype}, not fp16")
+    on = _stream_for(x, "x", stream)
     device = x.device
-    _need(layer.gate_up.codes.device == device, "x and the layer are on different devices")
+    if layer.gate_up.codes.device != device:
+        _refuse("x and the layer are on different devices")
     t = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, t, layer.hidden, device, None)
+    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, device, None)
     for v, what, dt in ((topk_ids, "topk_ids", torch.int32), (topk_weights, "topk_weights", torch.float32)):
-        if v is not None:
-            _tensor(v, what, dt, (t, topk))
-            _need(v.device == device, f"{what} is on another device than x")
-    if workspace is None:
-        workspace = _scratch(None, exl3_mx4_moe_workspace_size(layer, t, topk), device, "workspace")
-    else:
-        _scratch(workspace, 0, device, "workspace")
-    ws, wsb = _blob(workspace)
-    _check(lib().exl3_mx4_moe(ctypes.byref(layer._record), x.data_ptr(), t, ldx, int(topk), out.data_ptr(), ldy, ydt,
-                              _ptr(topk_ids), _ptr(topk_weights), ws, wsb, _stream(stream)), "exl3_mx4_moe")
+        if v is not None and _tensor(v, what, dt, (t, topk)).device != device:
+            _refuse(f"{what} is on another device than x")
+    ws, nws, _keep = _scratch(workspace, exl3_mx4_moe_workspace_size, (layer, t, topk), device)
+    _check(lib().exl3_mx4_moe(layer._ref, x.data_ptr(), t, ldx, topk, out.data_ptr(), ldy, ydt, _ptr(topk_ids),
+                              _ptr(topk_weights), ws, nws, on), "exl3_mx4_moe")
     return out

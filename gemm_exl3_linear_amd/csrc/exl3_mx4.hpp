@@ -30,12 +30,12 @@ __device__ __forceinline__ float mx4_scale(uint32_t s) {
   return __uint_as_float((s << 23) | (odd <= 1u ? 0x00400000u : 0u));
 }
 
-// Eight codes to eight unscaled fp16 values (0 .. 6 are exact).
-__device__ __forceinline__ f16x8_t mx4_to_f16(uint32_t codes) {
-  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0);
-  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1);
-  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2);
-  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3);
+// Eight codes times a scale to eight fp16 values.
+__device__ __forceinline__ f16x8_t mx4_to_f16(uint32_t codes, float scale = 1.0f) {
+  const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0);
+  const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1);
+  const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2);
+  const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3);
   return f16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
@@ -47,21 +47,6 @@ __device__ __forceinline__ bf16x8_t mx4_to_bf16(uint32_t codes, float scale) {
   const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
   const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
   return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// 4 x 4 transpose of dwords between a wave's four groups of 16 lanes: on entry
-// lane group g holds dword j of its own block in d[j], on exit dword g of block
-// j.  So four 16-byte loads of one block per lane group become four matrix
-// operands of one block each (its eight dwords' worth of k over the groups).
-__device__ __forceinline__ void lane_group_transpose(uint32_t (&d)[4]) {
-  const u32x2_t a = __builtin_amdgcn_permlane16_swap(d[0], d[1], false, false);
-  const u32x2_t b = __builtin_amdgcn_permlane16_swap(d[2], d[3], false, false);
-  const u32x2_t e = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false);
-  const u32x2_t o = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
-  d[0] = e.x;
-  d[1] = o.x;
-  d[2] = e.y;
-  d[3] = o.y;
 }
 
 // One 16 x 16 product over 128 k: lane (r = l % 16, g = l / 16) holds the

@@ -1,0 +1,367 @@
+// exl3_mx4_matmul for many rows: an LDS-tiled product on the scaled 4-bit
+// matrix cores.
+//
+// A workgroup computes a TM x TN tile over all of k.  A stage is 256 k: one
+// 128-byte line of codes of every row of both operands and their scale bytes,
+// copied straight from memory to LDS while the other stage is multiplied.
+#include "exl3_internal.hpp"
+#include "exl3_mx4_rows.hpp"
+
+namespace exl3 {
+
+constexpr int kStageK = 256;
+constexpr int kStageLine = kStageK / 2;             // bytes of codes of a row
+constexpr int kStageBlocks = kStageK / kMx4Block;   // scale bytes of a row
+constexpr int kStages = 2;
+constexpr int kScaleTile = 64;                      // rows of one staged group of scales (256 bytes)
+
+// LDS place of 16-byte chunk c of a row's line: a wave's 16-byte reads take
+// one chunk of sixteen rows for every lane group, and the lanes that are served
+// together then fall on different banks.
+__device__ __forceinline__ int stage_place(int row, int c) { return c ^ (row & 7); }
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+__device__ __forceinline__ u32x4_t lds_read16(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4_t*>((const lds_u8*)(uintptr_t)at);
+}
+__device__ __forceinline__ u32x2_t lds_read8(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x2_t*>((const lds_u8*)(uintptr_t)at);
+}
+
+// 16 (4) bytes a lane from a buffer to LDS: lane l's land at `at` + 16 l (4 l).
+// Written as assembly so that the compiler, which cannot tell the stages
+// apart, does not wait for it before every LDS read; the kernel waits itself
+// before the barrier that hands a stage over.  (M0 needs one wait state before
+// its use.)
+__device__ __forceinline__ void lds_copy16(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
+               : "memory");
+}
+__device__ __forceinline__ void lds_copy4(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
+               : "memory");
+}
+
+// Raw buffer descriptor over [p, p + bytes): loads past its end give zeros.
+__device__ __forceinline__ u32x4_t buffer_words(const uint8_t* p, uint64_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  u32x4_t w = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kBufferRsrcWord3};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)w[i]);
+  return w;
+}
+
+struct Mx4GemmArgs {
+  const uint8_t* a;         // codes [m][k/2]
+  const uint8_t* b;         // codes [n][k/2]
+  const uint8_t* a_scales;  // staged, see mx4_stage_scales
+  const uint8_t* b_scales;
+  uint32_t a_step, b_step;  // bytes of one step of staged scales
+  const uint16_t* bias;
+  void* y;
+  int64_t ldy;
+  int64_t m, n;
+  int kb;
+  int steps;
+  int y_f32;
+  int wide;                 // 16-byte stores of y fit its alignment
+  uint32_t tiles_m, tiles_n;
+};
+
+// Scales as the matrix instructions take them: per step and group of 64 rows
+// two dwords for each lane (r = l % 16, g = l / 16); byte j of dword h is the
+// scale of block 4 h + g of row 16 j + r, so one LDS read serves eight
+// operands.  127 past a row's end and past the last row.
+struct StageScales {
+  const uint8_t* s;
+  uint32_t* out;
+  int64_t rows;
+  uint32_t groups;  // of 64 rows
+};
+__global__ __launch_bounds__(256) void mx4_stage_scales(StageScales a, StageScales b, int kb, int steps) {
+  const bool second = blockIdx.x >= a.groups;
+  const StageScales& q = second ? b : a;
+  const uint32_t group = blockIdx.x - (second ? a.groups : 0);
+  const int r = threadIdx.x & 15, half = blockIdx.y * 16 + (threadIdx.x >> 4);  // 128 k
+  if (half >= steps * 2) return;
+  const int left = kb - half * 4;
+  uint32_t v[4];  // blocks of row j
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t row = (int64_t)group * kScaleTile + 16 * j + r;
+    v[j] = 0x7F7F7F7Fu;
+    if (row < q.rows) {
+      const uint8_t* p = q.s + row * kb + half * 4;
+      if (left >= 4) {
+        __builtin_memcpy(&v[j], p, 4);
+      } else {
+        v[j] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[j] |= (c < left ? (uint32_t)p[c] : kMx4One) << (8 * c);
+      }
+    }
+  }
+  uint32_t* o = q.out + ((int64_t)(half >> 1) * q.groups + group) * 128 + 2 * r + (half & 1);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= ((v[j] >> (8 * g)) & 0xFFu) << (8 * j);
+    o[32 * g] = w;
+  }
+}
+
+// acc += b a^T with byte JB, JA of the scale dwords.
+template <int JB, int JA>
+__device__ __forceinline__ float4_t mfma_mx4_sel(u32x4_t b, uint32_t sb, u32x4_t a, uint32_t sa, float4_t c) {
+  const i32x8_t B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  const i32x8_t A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(B, A, c, kMfmaFp4, kMfmaFp4, JB, (int)sb, JA, (int)sa);
+}
+
+template <int I, int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(PowC<I>{});
+    unrolled<I + 1, N>(f);
+  }
+}
+
+template <int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q) {
+  constexpr int NW = WM * WN;
+  constexpr int MI = TM / WM / 16, NI = TN / WN / 16;  // 16 x 16 tiles of a wave
+  static_assert(MI % 4 == 0 && NI % 4 == 0, "a scale dword serves four operands");
+  constexpr uint32_t kA = 0, kB = kA + TM * kStageLine, kSA = kB + TN * kStageLine, kSB = kSA + TM * kStageBlocks,
+                     kBytes = kSB + TN * kStageBlocks;
+  constexpr int CA = TM / 8 / NW, CB = TN / 8 / NW;  // code copies of a wave and stage, 8 rows each
+  static_assert(CA * NW * 8 == TM && CB * NW * 8 == TN && (TM + TN) / 64 == NW, "copies are even");
+  constexpr int kOutBytes = TM / WM * 128;             // a wave's region when it writes y
+  static_assert(kOutBytes * NW <= kBytes * kStages, "output regions fit");
+  __shared__ __align__(128) uint8_t smem[kStages * kBytes];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int g = lane >> 4, r = lane & 15;
+  // tiles in XCD order: workgroups b, b + 8, ... share an XCD and its L2
+  const uint32_t total = q.tiles_m * q.tiles_n;
+  const uint32_t x = blockIdx.x & 7, per = total >> 3, rest = total & 7;
+  const uint32_t tile = x * per + (x < rest ? x : rest) + (blockIdx.x >> 3);
+  constexpr uint32_t kGroup = 8;  // row tiles walked together
+  const uint32_t group = tile / (kGroup * q.tiles_n);
+  const uint32_t gm = q.tiles_m - group * kGroup < kGroup ? q.tiles_m - group * kGroup : kGroup;
+  const uint32_t in = tile - group * kGroup * q.tiles_n;
+  const uint32_t tn = in / gm, tm = group * kGroup + (in - tn * gm);
+  const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
+  const int wm = wave % WM, wn = wave / WM;
+  const uint32_t pitch = (uint32_t)q.kb * 16;
+
+  // rows past the end read as zeros, with staged scales of 1
+  auto buffer = [&](const uint8_t* p, int64_t row0, int64_t rows, int most) {
+    const int64_t left = rows - row0 < most ? rows - row0 : most;
+    return buffer_words(p + row0 * pitch, (uint64_t)left * pitch);
+  };
+  const u32x4_t ra = buffer(q.a, m0, q.m, TM), rb = buffer(q.b, n0, q.n, TN);
+  const u32x4_t rsa = buffer_words(q.a_scales, (uint64_t)q.steps * q.a_step);
+  const u32x4_t rsb = buffer_words(q.b_scales, (uint64_t)q.steps * q.b_step);
+  const int lane_chunk = stage_place(lane >> 3, lane & 7);
+  const uint32_t lane_off = pitch * (lane >> 3) + 16 * lane_chunk;
+  const bool scales_of_b = wave >= TM / 64;
+  const u32x4_t rss = scales_of_b ? rsb : rsa;
+  const uint32_t s_step = scales_of_b ? q.b_step : q.a_step;
+  const uint32_t s_off = scales_of_b ? (uint32_t)(n0 * kStageBlocks) + (wave - TM / 64) * 512
+                                     : (uint32_t)(m0 * kStageBlocks) + wave * 512;
+  auto copy = [&](uint32_t stage, int step) {
+    // chunks past a row's end, and steps past the last, read past the buffer: zeros
+    const uint32_t at_lane = step * kStageBlocks + lane_chunk < q.kb ? lane_off : 0xFFFFFFF0u;
+    const uint32_t k_off = (uint32_t)step * kStageLine;
+#pragma unroll
+    for (int c = 0; c < CA; ++c)
+      lds_copy16(ra, stage + kA + (wave * CA + c) * 1024, at_lane, pitch * 8 * (wave * CA + c) + k_off);
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      lds_copy16(rb, stage + kB + (wave * CB + c) * 1024, at_lane, pitch * 8 * (wave * CB + c) + k_off);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      lds_copy4(rss, stage + kSA + wave * 512 + c * 256, step < q.steps ? lane * 4 : 0xFFFFFFF0u,
+                s_off + (uint32_t)step * s_step + c * 256);
+  };
+
+  float4_t acc[NI][MI];
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int k = 0; k < MI; ++k) acc[j][k] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+  // LDS addresses of this lane's operands in a stage: 16 rows on is 2048 bytes
+  uint32_t va[2], vb[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    va[h] = lds0 + kA + (wm * MI * 16 + r) * kStageLine + 16 * stage_place(r, 4 * h + g);
+    vb[h] = lds0 + kB + (wn * NI * 16 + r) * kStageLine + 16 * stage_place(r, 4 * h + g);
+  }
+  const uint32_t vsa = lds0 + kSA + wm * (MI / 4) * 512 + lane * 8, vsb = lds0 + kSB + wn * (NI / 4) * 512 + lane * 8;
+  auto compute = [&](uint32_t stage) {
+    u32x2_t sa[MI / 4], sb[NI / 4];
+#pragma unroll
+    for (int j = 0; j < NI / 4; ++j) sb[j] = lds_read8(vsb + stage + j * 512);
+#pragma unroll
+    for (int j = 0; j < MI / 4; ++j) sa[j] = lds_read8(vsa + stage + j * 512);
+    unrolled<0, 2>([&](auto hc) {
+      constexpr int h = decltype(hc)::value;
+      u32x4_t fa[MI], fb[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[j] = lds_read16(vb[h] + stage + j * 16 * kStageLine);
+#pragma unroll
+      for (int j = 0; j < MI; ++j) fa[j] = lds_read16(va[h] + stage + j * 16 * kStageLine);
+      unrolled<0, MI>([&](auto kc) {
+        constexpr int k = decltype(kc)::value;
+        unrolled<0, NI>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          acc[j][k] = mfma_mx4_sel<j % 4, k % 4>(fb[j], sb[j / 4][h], fa[k], sa[k / 4][h], acc[j][k]);
+        });
+      });
+    });
+  };
+
+  copy(lds0, 0);
+  uint32_t stage = 0;
+  for (int s = 0; s < q.steps; ++s) {
+    // this wave's copies of stage s are in, its LDS reads of the stage before
+    // are done; then everybody's
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    copy(lds0 + (kBytes - stage), s + 1);  // the stage that was read last
+    compute(stage);
+    stage = kBytes - stage;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // A lane holds row l % 16, columns 4 (l / 16) .. + 3 of a 16 x 16 tile.
+  // Whole rows of a wave's columns go through its own piece of LDS, so that
+  // stores cover whole lines (in place, eight bytes a lane, they were four times
+  // as long); chunks of 16 bytes are spread over the banks by the row.
+  const int64_t wave_m = m0 + wm * MI * 16, wave_n = n0 + wn * NI * 16;
+  if (q.bias) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t col = wave_n + 16 * j + 4 * g + c;
+        const float b = col < q.n ? h2f(q.bias[col]) : 0.f;
+#pragma unroll
+        for (int k = 0; k < MI; ++k) acc[j][k][c] += b;
+      }
+  }
+  uint8_t* out = smem + wave * kOutBytes;
+  if (q.wide && !q.y_f32) {
+    static_assert(NI == 4, "a row of a wave's columns is 128 bytes of fp16");
+#pragma unroll
+    for (int k = 0; k < MI; ++k)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const float4_t v = acc[j][k];
+        const uint2 h = make_uint2((uint32_t)f2h(v[0]) | ((uint32_t)f2h(v[1]) << 16),
+                                   (uint32_t)f2h(v[2]) | ((uint32_t)f2h(v[3]) << 16));
+        *reinterpret_cast<uint2*>(out + (16 * k + r) * 128 + (((2 * j + (g >> 1)) ^ (r & 7)) * 16) + 8 * (g & 1)) = h;
+      }
+    uint16_t* y = static_cast<uint16_t*>(q.y);
+    const int c = lane & 7;
+    const int64_t col = wave_n + 8 * c;
+#pragma unroll 4
+    for (int i = 0; i < MI * 2; ++i) {
+      const int row = 8 * i + (lane >> 3);
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(out + row * 128 + ((c ^ (row & 7)) * 16));
+      if (wave_m + row >= q.m) continue;
+      uint16_t* o = y + (wave_m + row) * q.ldy + col;
+      if (col + 8 <= q.n) {
+        *reinterpret_cast<u32x4_t*>(o) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < q.n) o[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+      }
+    }
+  } else if (q.wide) {
+    float* y = static_cast<float*>(q.y);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // 32 columns: 128 bytes a row
+#pragma unroll
+      for (int k = 0; k < MI; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4_t*>(out + (16 * k + r) * 128 + (((4 * j + g) ^ (r & 7)) * 16)) = acc[2 * half + j][k];
+      const int c = lane & 7;
+      const int64_t col = wave_n + 32 * half + 4 * c;
+#pragma unroll 4
+      for (int i = 0; i < MI * 2; ++i) {
+        const int row = 8 * i + (lane >> 3);
+        const float4_t v = *reinterpret_cast<const float4_t*>(out + row * 128 + ((c ^ (row & 7)) * 16));
+        if (wave_m + row >= q.m) continue;
+        float* o = y + (wave_m + row) * q.ldy + col;
+        if (col + 4 <= q.n) {
+          *reinterpret_cast<float4_t*>(o) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < q.n) o[e] = v[e];
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < MI; ++k) {
+      const int64_t row = wave_m + 16 * k + r;
+      if (row >= q.m) continue;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t col = wave_n + 16 * j + 4 * g + c;
+          if (col >= q.n) continue;
+          if (q.y_f32)
+            static_cast<float*>(q.y)[row * q.ldy + col] = acc[j][k][c];
+          else
+            static_cast<uint16_t*>(q.y)[row * q.ldy + col] = f2h(acc[j][k][c]);
+        }
+    }
+  }
+}
+
+static uint32_t scale_groups(int64_t rows) { return (uint32_t)((rows + 255) / 256 * (256 / kScaleTile)); }
+
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
+  return (size_t)((k + kStageK - 1) / kStageK) * ((size_t)scale_groups(m) + scale_groups(n)) * 512;
+}
+
+template <int TM, int TN, int WM, int WN>
+static void launch_gemm_tiles(Mx4GemmArgs q, hipStream_t s) {
+  q.tiles_m = (uint32_t)((q.m + TM - 1) / TM);
+  q.tiles_n = (uint32_t)((q.n + TN - 1) / TN);
+  hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN>), dim3(q.tiles_m * q.tiles_n), dim3(WM * WN * 64), 0, s, q);
+}
+
+hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
+                           const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y, int64_t ldy,
+                           bool y_f32, void* ws, hipStream_t s) {
+  const int kb = (int)(k / kMx4Block), steps = (int)((k + kStageK - 1) / kStageK);
+  const uint32_t ga = scale_groups(m), gb = scale_groups(n);
+  uint8_t* sa = static_cast<uint8_t*>(ws);
+  uint8_t* sb = sa + (size_t)steps * ga * 512;
+  hipLaunchKernelGGL(mx4_stage_scales, dim3(ga + gb, (2 * steps + 15) / 16), dim3(256), 0, s,
+                     StageScales{a_scales, reinterpret_cast<uint32_t*>(sa), m, ga},
+                     StageScales{b_scales, reinterpret_cast<uint32_t*>(sb), n, gb}, kb, steps);
+  const int wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && ldy % (y_f32 ? 4 : 8) == 0;
+  const Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, bias, y, ldy, m, n, kb, steps, y_f32, wide, 0, 0};
+#ifdef SMALL_TILE
+  launch_gemm_tiles<128, 128, 2, 2>(q, s);
+#else
+  launch_gemm_tiles<256, 256, 2, 4>(q, s);
+#endif
+  return hipGetLastError();
+}
+
+}  // namespace exl3

@@ -17,20 +17,34 @@ struct Mx4RowsArgs {
   int kb;                 // blocks of 32 in a row
   int y_f32;
   uint32_t col_tiles;     // tiles of 16 NG columns
+  int splits;             // workgroups that share a tile's k
+  float* part;            // their sums [split][m][n], where there are several
 };
 
 // Output tiles that fit the LDS of one combine round, at a kilobyte a wave.
 constexpr int kMx4CombineTiles = 64;
 
-template <bool A4, int MG, int NG, int NW>
+__device__ __forceinline__ void mx4_store(const Mx4RowsArgs& q, int64_t row, int64_t col, float v) {
+  const float y = v + (q.bias ? h2f(q.bias[col]) : 0.f);
+  if (q.y_f32)
+    static_cast<float*>(q.y)[row * q.ldy + col] = y;
+  else
+    static_cast<uint16_t*>(q.y)[row * q.ldy + col] = f2h(y);
+}
+
+// 16 MG rows (A4: 4-bit, else fp16 in operands of P pieces, P = 1 unless
+// MG = 1), 16 NG columns, NW waves.
+template <bool A4, int MG, int P, int NG, int NW>
 __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
+  static_assert(P == 1 || (MG == 1 && !A4), "pieces are for few fp16 rows");
   constexpr int T = MG * NG;
   constexpr int R = T * NW <= kMx4CombineTiles ? T : kMx4CombineTiles / NW;  // tiles a round
-  static_assert(T % R == 0, "combine rounds are whole");
+  constexpr int kRows = Mx4X<P>::kRows, kLoads = Mx4X<P>::kLoads;
   __shared__ float4_t part[NW * R * 64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
-  const uint32_t tm = blockIdx.x / q.col_tiles, tn = blockIdx.x - tm * q.col_tiles;
+  const uint32_t tile = blockIdx.x / (uint32_t)q.splits, split = blockIdx.x - tile * (uint32_t)q.splits;
+  const uint32_t tm = tile / q.col_tiles, tn = tile - tm * q.col_tiles;
   const int64_t m0 = (int64_t)tm * (16 * MG), n0 = (int64_t)tn * (16 * NG);
   const int kb = q.kb;
   const int64_t pitch = (int64_t)kb * 16;
@@ -49,7 +63,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   bool there[MG];
 #pragma unroll
   for (int mg = 0; mg < MG; ++mg) {
-    int64_t row = m0 + 16 * mg + r;
+    int64_t row = m0 + 16 * mg + r % kRows;
     there[mg] = row < q.m;
     row = there[mg] ? row : q.m - 1;
     if constexpr (A4) {
@@ -61,19 +75,24 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
     }
   }
 
-  float4_t acc[NG][MG];
+  float4_t acc[NG][MG][P];
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-    for (int mg = 0; mg < MG; ++mg) acc[ng][mg] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int mg = 0; mg < MG; ++mg)
+#pragma unroll
+      for (int p = 0; p < P; ++p) acc[ng][mg][p] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
-  for (int u = wave; u < units; u += NW) {
-    Mx4Unit w[NG];
+  const int first = (int)split * NW + wave, stride = NW * q.splits;
+  auto load_w = [&](Mx4Unit (&w)[NG], int u) {
 #pragma unroll
     for (int ng = 0; ng < NG; ++ng) mx4_load_unit(bc[ng], bs[ng], kb, u, g, w[ng]);
-    if constexpr (A4) {
-      Mx4Unit x[MG];
+  };
+  if constexpr (A4) {
+    for (int u = first; u < units; u += stride) {
+      Mx4Unit w[NG], x[MG];
+      load_w(w, u);
 #pragma unroll
       for (int mg = 0; mg < MG; ++mg) mx4_load_unit(ac[mg], as[mg], kb, u, g, x[mg]);
 #pragma unroll
@@ -82,77 +101,138 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int mg = 0; mg < MG; ++mg)
-            acc[ng][mg] = mfma_mx4(x[mg].half[h], mx4_own_scale(x[mg], h, g), w[ng].half[h],
-                                   mx4_own_scale(w[ng], h, g), acc[ng][mg]);
-    } else {
+            acc[ng][mg][0] = mfma_mx4(x[mg].half[h], mx4_own_scale(x[mg], h, g), w[ng].half[h],
+                                      mx4_own_scale(w[ng], h, g), acc[ng][mg][0]);
+    }
+  } else {
+    auto load_x = [&](f16x8_t (&x)[MG][kLoads], int h, int u) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f16x8_t x[MG][4];
+      for (int mg = 0; mg < MG; ++mg)
 #pragma unroll
-        for (int mg = 0; mg < MG; ++mg)
-          mx4_load_x(reinterpret_cast<const uint16_t*>(ac[mg]), there[mg], kb, u, h, g, x[mg]);
+        for (int i = 0; i < kLoads; ++i)
+          x[mg][i] = mx4_load_x<P>(reinterpret_cast<const uint16_t*>(ac[mg]), there[mg], kb, u, h, g, r, i);
+    };
+    for (int u = first; u < units; u += stride) {
+      Mx4Unit w[NG];
+      f16x8_t x[2][MG][kLoads];
+      load_w(w, u);
+      load_x(x[0], 0, u);
+      if constexpr (P < 8) load_x(x[1], 1, u);
 #pragma unroll
-        for (int ng = 0; ng < NG; ++ng) mx4_mma_f16<MG>(x, w[ng], h, acc[ng]);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) mx4_mma_f16<MG, P>(x[P < 8 ? h : 0], w[ng], h, g, acc[ng]);
     }
   }
 
-  // Sum over the waves in wave order, R output tiles a round; lane l of a tile
-  // holds rows 4 (l / 16) .. + 3 of column l % 16.
+  // Sum over the waves in wave order, R output tiles a round.  Lane l of a 16 x
+  // 16 tile holds operand rows 4 (l / 16) .. + 3 of column l % 16.
 #pragma unroll
-  for (int t0 = 0; t0 < T; t0 += R) {
-    if (t0) __syncthreads();
+  for (int b = 0; b < T; b += R) {
+    if (b) __syncthreads();
+    const int some = T - b < R ? T - b : R;
 #pragma unroll
-    for (int i = 0; i < R; ++i) part[(wave * R + i) * 64 + lane] = acc[(t0 + i) / MG][(t0 + i) % MG];
+    for (int i = 0; i < R; ++i)
+      if (b + i < T) part[(wave * R + i) * 64 + lane] = mx4_pick<P>(acc[(b + i) / MG][(b + i) % MG], g);
     __syncthreads();
-    for (int e = threadIdx.x; e < R * 64; e += NW * 64) {
+    for (int e = threadIdx.x; e < some * 64; e += NW * 64) {
       float4_t v = part[e];
 #pragma unroll
       for (int w = 1; w < NW; ++w) v += part[w * R * 64 + e];
-      const int t = t0 + (e >> 6), l = e & 63;
+      const int t = b + (e >> 6), l = e & 63;
       const int64_t col = n0 + 16 * (t / MG) + (l & 15);
+      int64_t row = m0 + 16 * (t % MG) + 4 * (l >> 4);
+      if constexpr (P > 1) {  // the pieces' sums, in piece order, by the lanes of the first rows
+        part[e] = v;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int p = 1; p < P; ++p) {
+          const int at = p * kRows;  // operand row of the piece's row 0
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * (l >> 4) + i < kRows) {
+              const int o = at + 4 * (l >> 4) + i;
+              v[i] += part[(e & ~63) + 16 * (o >> 2) + (l & 15)][o & 3];
+            }
+        }
+      }
       if (col >= q.n) continue;
-      const int64_t row = m0 + 16 * (t % MG) + 4 * (l >> 4);
-      const float bias = q.bias ? h2f(q.bias[col]) : 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (row + i >= q.m) break;
-        const int64_t at = (row + i) * q.ldy + col;
-        if (q.y_f32)
-          static_cast<float*>(q.y)[at] = v[i] + bias;
+        if (q.splits == 1)
+          mx4_store(q, row + i, col, v[i]);
         else
-          static_cast<uint16_t*>(q.y)[at] = f2h(v[i] + bias);
+          q.part[((int64_t)split * q.m + row + i) * q.n + col] = v[i];
       }
     }
   }
 }
 
-template <bool A4, int MG, int NG, int NW>
-static hipError_t launch_rows(Mx4RowsArgs q, hipStream_t s) {
+// y = sum of the splits in order (+ bias).
+__global__ __launch_bounds__(256) void mx4_rows_finish(Mx4RowsArgs q) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = q.m * q.n;
+  if (i >= size) return;
+  float v = q.part[i];
+  for (int s = 1; s < q.splits; ++s) v += q.part[s * size + i];
+  const int64_t row = i / q.n;
+  mx4_store(q, row, i - row * q.n, v);
+}
+
+template <bool A4, int MG, int P, int NG, int NW>
+static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s) {
   q.col_tiles = (uint32_t)((q.n + 16 * NG - 1) / (16 * NG));
-  const uint32_t row_tiles = (uint32_t)((q.m + 16 * MG - 1) / (16 * MG));
-  hipLaunchKernelGGL((mx4_rows_kernel<A4, MG, NG, NW>), dim3(q.col_tiles * row_tiles), dim3(NW * 64), 0, s, q);
+  const uint32_t tiles = q.col_tiles * (uint32_t)((q.m + 16 * MG - 1) / (16 * MG));
+  q.splits = splits;
+  q.part = static_cast<float*>(ws);
+  hipLaunchKernelGGL((mx4_rows_kernel<A4, MG, P, NG, NW>), dim3(tiles * (uint32_t)splits), dim3(NW * 64), 0, s, q);
+  if (splits > 1) hipLaunchKernelGGL(mx4_rows_finish, dim3((uint32_t)((q.m * q.n + 255) / 256)), dim3(256), 0, s, q);
   return hipGetLastError();
 }
 
-size_t mx4_matmul_workspace(int64_t, int64_t, int64_t) { return 0; }
-size_t mx4_linear_workspace(int64_t, int64_t, int64_t) { return 0; }
+// Kernel by size, as measured (us; graph replays, weights alternating among
+// three copies):
+//   fp16 rows, few: pieces (see exl3_mx4_rows.hpp)
+//     5120 -> 17408, one row: P = 4 12.8, P = 2 13.1, P = 1 16
+//   more than 16 rows and few column tiles: k in three shares
+//     37 rows 17408 -> 5120: 33.9 against 42.8 in two and 54 unsplit
+static int linear_splits(int64_t m, int64_t n, int64_t k) {
+  return m > 32 && n * 3 <= 17408 * 3 && k >= 12 * kMx4UnitK ? 3 : 1;
+}
+size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
+  const int s = linear_splits(m, n, k);
+  return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
+}
 
 hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, const uint16_t* bias,
-                             const uint16_t* x, int64_t m, int64_t ldx, void* y, int64_t ldy, bool y_f32, void*,
+                             const uint16_t* x, int64_t m, int64_t ldx, void* y, int64_t ldy, bool y_f32, void* ws,
                              hipStream_t s) {
-  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0};
-  if (m <= 16) return launch_rows<false, 1, 1, 8>(q, s);
-  if (m <= 32) return launch_rows<false, 2, 1, 8>(q, s);
-  return launch_rows<false, 4, 1, 8>(q, s);
+  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
+  const bool wide = n >= 2048;  // 32 columns a workgroup still fill the chip's half
+  if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, 1, ws, s);
+  if (m <= 8) return wide ? launch_rows<false, 1, 2, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 2, 1, 8>(q, 1, ws, s);
+  if (m <= 16) return wide ? launch_rows<false, 1, 1, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 1, 1, 8>(q, 1, ws, s);
+  if (m <= 32) return wide ? launch_rows<false, 2, 1, 2, 8>(q, 1, ws, s) : launch_rows<false, 2, 1, 1, 8>(q, 1, ws, s);
+  const int splits = linear_splits(m, n, k);
+  if (m <= 48) return launch_rows<false, 3, 1, 4, 4>(q, splits, ws, s);
+  return launch_rows<false, 4, 1, 4, 4>(q, splits, ws, s);
+}
+
+static bool use_gemm(int64_t m, int64_t n, int64_t k) {
+  return m >= 512 && n >= 512 && mx4_gemm_workspace(m, n, k) < ((size_t)1 << 32);
+}
+size_t mx4_matmul_workspace(int64_t m, int64_t n, int64_t k) {
+  return use_gemm(m, n, k) ? mx4_gemm_workspace(m, n, k) : 0;
 }
 
 hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
                              const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y, int64_t ldy,
-                             bool y_f32, void*, hipStream_t s) {
-  const Mx4RowsArgs q{a, a_scales, 0, b, b_scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0};
-  if (m <= 16) return launch_rows<true, 1, 1, 8>(q, s);
-  return launch_rows<true, 4, 4, 4>(q, s);
+                             bool y_f32, void* ws, hipStream_t s) {
+  if (use_gemm(m, n, k)) return launch_mx4_gemm(a, a_scales, m, b, b_scales, n, k, bias, y, ldy, y_f32, ws, s);
+  const Mx4RowsArgs q{a, a_scales, 0, b, b_scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
+  if (m <= 16) return launch_rows<true, 1, 1, 1, 8>(q, 1, ws, s);
+  if (((m + 63) / 64) * ((n + 63) / 64) >= 160) return launch_rows<true, 4, 1, 4, 4>(q, 1, ws, s);
+  return launch_rows<true, 4, 1, 2, 8>(q, 1, ws, s);
 }
 
 }  // namespace exl3

@@ -7,12 +7,15 @@
 // the two loads cover one whole 128-byte line.  Either 128-k half of a unit is
 //  - with 4-bit rows: the operand of one scaled 16x16x128 matrix instruction as
 //    loaded (the instruction applies both scales; no arithmetic of our own);
-//  - with fp16 rows: after a 4 x 4 transpose between the lane groups
-//    (lane_group_transpose) dword j of every lane is a piece of block j, so
-//    four 16x16x32 fp16 instructions take one block each, on the unscaled codes
-//    (exact in fp16), and one fp32 multiply-add per sum applies the block's
-//    scale.  A block's sum is formed before its scale, so any scale byte is
-//    exact: weights times scales would leave fp16's range.
+//  - with fp16 rows: 16 conversions to fp16 (code times scale, exact for scale
+//    bytes 104 .. 140) and four 16x16x32 fp16 instructions, the j-th on the j-th
+//    dword (piece) of every lane's block.  A wave that holds a block with another
+//    scale byte multiplies the unscaled codes block by block and scales the sums.
+//    Few rows: with at most 16 / P of them, one operand carries P pieces, piece p
+//    of row t in operand row p 16 / P + t, and piece p has sums of its own of which
+//    only those rows are wanted.  One load then brings P pieces; loads of one
+//    piece each, mostly masked, cost as much and bounded the time (5120 -> 17408,
+//    one row: 16 us against 12.8 with four pieces).
 // Output columns are the weight rows (matrix operand B), so a lane's sums all
 // belong to the column whose scales it loaded.
 #pragma once
@@ -58,35 +61,89 @@ __device__ __forceinline__ void mx4_load_unit(const uint8_t* codes, const uint8_
 // Scale byte of block g of half h, in the low byte.
 __device__ __forceinline__ uint32_t mx4_own_scale(const Mx4Unit& t, int h, int g) { return t.sc[h] >> (8 * g); }
 
-// fp16 activations of half h of unit u, row x: [j] holds elements 8g .. 8g + 7
-// of block j, zeros past the row's end or where the row is not there.
-__device__ __forceinline__ void mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g,
-                                           f16x8_t (&f)[4]) {
+// Operand rows of fp16 activations: P pieces of 16 / P rows.
+template <int P>
+struct Mx4X {
+  static constexpr int kRows = 16 / P;            // rows of x
+  static constexpr int kLoads = P >= 4 ? 1 : 4 / P;  // operands of one 128-k half (P = 8: of a whole unit)
+};
+
+// Operand `q` of half h of unit u: lane (r, g) holds 8 elements of block 4 h + g
+// (P = 8: of both halves), piece q P + r / kRows, of row r % kRows; zeros past
+// the row's end or where the row is not there.  x: this lane's row.
+template <int P>
+__device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g, int r, int q) {
+  const int piece = q * P + r / Mx4X<P>::kRows;  // 0 .. 3, or 0 .. 7 over two halves
+  const int b = u * kMx4UnitBlocks + 4 * (P == 8 ? piece >> 2 : h) + g;
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * (piece & 3));
+  return __builtin_bit_cast(f16x8_t, v);
+}
+
+// Scale bytes whose blocks are exact in fp16: 0.5 * 2^(104 - 127) = 2^-24, the
+// least subnormal, to 6 * 2^(140 - 127) < 65504.
+constexpr uint32_t kMx4ScaleLow = 104, kMx4ScaleHigh = 140;
+
+// acc += x times the half h of a unit of 16 weight rows; x[mg][q] as loaded by
+// mx4_load_x, acc[mg][p] the sums of piece p (mod P).
+template <int MG, int P>
+__device__ __forceinline__ void mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h, int g,
+                                            float4_t (&acc)[MG][P]) {
+  constexpr int kPer = P < 4 ? P : 4;  // pieces of an operand in one half
+  const uint32_t own = mx4_own_scale(w, h, g) & 0xFFu;
+  const u32x4_t d = w.half[h];
+  bool plain = own - kMx4ScaleLow <= kMx4ScaleHigh - kMx4ScaleLow;
+  float s = __uint_as_float(own << 23);
+  if (__builtin_expect(!__all(plain), 0)) {
+    // a block of zeros is zero at any scale (but NaN)
+    if (!plain && own != 255u && ((d.x | d.y | d.z | d.w) & 0x77777777u) == 0) {
+      plain = true;
+      s = 1.0f;
+    }
+    if (!__all(plain)) {
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const float sb = mx4_scale((w.sc[h] >> (8 * b)) & 0xFFu);
+        const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f16x8_t c = mx4_to_f16(d[j] & keep);
+#pragma unroll
+          for (int mg = 0; mg < MG; ++mg) {
+            const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], sb, a[i]);
+          }
+        }
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int b = u * kMx4UnitBlocks + 4 * h + j;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * g);
-    f[j] = __builtin_bit_cast(f16x8_t, v);
+    const f16x8_t c = mx4_to_f16(d[j], s);
+#pragma unroll
+    for (int mg = 0; mg < MG; ++mg) {
+      float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
+      a = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, a, 0, 0, 0);
+    }
   }
 }
 
-// acc[mg] += x[mg] times the half h of a unit of 16 weight rows.
-template <int MG>
-__device__ __forceinline__ void mx4_mma_f16(const f16x8_t (&x)[MG][4], const Mx4Unit& w, int h, float4_t (&acc)[MG]) {
-  uint32_t d[4] = {w.half[h].x, w.half[h].y, w.half[h].z, w.half[h].w};
-  lane_group_transpose(d);
+// One 16 x 16 tile of the sums of P pieces: operand row 4 g + i is wanted of
+// piece (4 g + i) / kRows only.
+template <int P>
+__device__ __forceinline__ float4_t mx4_pick(const float4_t (&acc)[P], int g) {
+  if constexpr (P == 1) return acc[0];
+  float4_t v;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const f16x8_t b = mx4_to_f16(d[j]);
-    const float s = mx4_scale((w.sc[h] >> (8 * j)) & 0xFFu);
+  for (int i = 0; i < 4; ++i) {
+    v[i] = acc[i / Mx4X<P>::kRows][i];
 #pragma unroll
-    for (int mg = 0; mg < MG; ++mg) {
-      const float4_t p = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j], b, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mg][i] = __builtin_fmaf(p[i], s, acc[mg][i]);
-    }
+    for (int k = 1; k < 4; ++k) v[i] = g == k ? acc[(4 * k + i) / Mx4X<P>::kRows][i] : v[i];
   }
+  return v;
 }
 
 }  // namespace exl3
