@@ -1,5 +1,5 @@
 // exl3_mx4_moe: a whole mixture-of-experts layer for 1 to 16 tokens, in three
-// launches.
+// launches (four for many listed experts).
 //
 //   1. mx4_moe_router  logits x W_r^T (the shared expert's gate as one more
 //      row): workgroup (16 experts, k share), fp16 matrix instructions.  The last
@@ -8,7 +8,8 @@
 //   2. mx4_moe_gate_up workgroup (16 columns, listed expert): gate and up over
 //      the waves' shares of k, a = silu(g) * u.
 //   3. mx4_moe_down    workgroup (16 columns): the waves share the (expert, 256
-//      k) units, sums are weighted per expert and meet in LDS.
+//      k) units, sums are weighted per expert and meet in LDS; many experts are
+//      shared among workgroups, whose sums mx4_moe_finish adds.
 //
 // A token chooses an expert at most once, so 16 tokens fill at most one 16-row
 // matrix operand per expert and each expert's weights are read once, whatever
@@ -61,6 +62,8 @@ struct MoeArgs {
   int* count;         // routed entries
   float* wtab;        // [most + 1][16]: weight of an entry's i-th token
   uint16_t* act[2];   // bf16 [3][rows][inter]
+  int down_splits;    // workgroups that share the entries of 16 columns
+  float* down;        // their sums [split][t][hidden], where there are several
 };
 
 // ---------------------------------------------------------------------------
@@ -73,23 +76,30 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((lane_id() ^ (uint32_t)m) << 2), (int)v);
-    v = v > o ? v : o;
-  }
-  return v;
+// Reductions over a wave on the vector unit alone: shifts by 1, 2, 4, 8 inside
+// the rows of 16 lanes, then row ends to the next row and to the upper half; lane
+// 63 ends with the result.  (Six LDS permutes took 6 x 100 cycles a choice.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, shfl_xor_f(v, m));
-  return v;
+template <class Op>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {  // 0 is neutral
+  v = op(v, dpp_or_zero<0x111, 0xF>(v));
+  v = op(v, dpp_or_zero<0x112, 0xF>(v));
+  v = op(v, dpp_or_zero<0x114, 0xF>(v));
+  v = op(v, dpp_or_zero<0x118, 0xF>(v));
+  v = op(v, dpp_or_zero<0x142, 0xA>(v));
+  v = op(v, dpp_or_zero<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 __device__ __forceinline__ float wave_sum_f(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += shfl_xor_f(v, m);
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 // Top-k and weights of one token by one wave, from its logits; lane s ends with
@@ -100,7 +110,7 @@ __device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane,
   float score[EPL];
   uint32_t key[EPL];
   bool open[EPL];  // not yet chosen
-  float top = -__builtin_inff();
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
@@ -113,21 +123,22 @@ __device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane,
       if (q.d.scoring == 0) {
         choice += b;
         score[i] = choice;
-        top = fmaxf(top, choice);
       } else {
         score[i] = 1.f / (1.f + expf(-choice));
         choice = q.d.router_bias ? score[i] + b : choice;
       }
       key[i] = order_key(choice);
+      top = top > key[i] ? top : key[i];
     }
   }
+  top = wave_max_u32(top);
   if (q.d.scoring == 0) {
-    top = wave_max_f(top);
+    const float high = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);  // NaN if every one is
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (open[i]) {
-        score[i] = expf(score[i] - top);
+        score[i] = expf(score[i] - high);
         sum += score[i];
       }
     sum = wave_sum_f(sum);
@@ -138,10 +149,13 @@ __device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane,
   weight = 0.f;
   float total = 0.f;
   for (int s = 0; s < q.topk; ++s) {
-    uint32_t best = 0;
+    uint32_t best = top;
+    if (s) {
+      best = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) best = open[i] && key[i] > best ? key[i] : best;
-    best = wave_max_u32(best);
+      for (int i = 0; i < EPL; ++i) best = open[i] && key[i] > best ? key[i] : best;
+      best = wave_max_u32(best);
+    }
     // the lowest expert among the equal ones: lowest i, then lowest lane
     int at = -1, from = 0;
     float mine = 0.f;
@@ -155,7 +169,7 @@ __device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane,
         if (lane == from) open[i] = false;
       }
     }
-    const float w = __shfl(mine, from);
+    const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), from));
     total += w;
     if (lane == s) {
       id = 64 * at + from;
@@ -166,28 +180,34 @@ __device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane,
   weight *= q.d.scale;
 }
 
+template <int EPL>
 struct MoeRouteLds {
-  float logits[kMoeTokens * (kMoeExperts + 1)];
-  uint32_t masks[kMoeExperts];
-  int place[kMoeExperts];
-  int chunk_entries[kMoeExperts / 64], chunk_rows[kMoeExperts / 64];
+  static constexpr int kCols = 64 * EPL + 1;  // the experts and the shared gate
+  float logits[kMoeTokens * kCols];
+  uint32_t masks[64 * EPL];
+  int place[64 * EPL];
+  int chunk_entries[EPL], chunk_rows[EPL];
 };
 
 // Routing of all tokens by one workgroup, from the partial logits.
 template <int EPL>
-__device__ void moe_route(const MoeArgs& q, MoeRouteLds& s) {
+__device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
+  constexpr int cols = MoeRouteLds<EPL>::kCols;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int E = q.d.experts, cols = E + 1;
-  for (int e = tid; e < kMoeExperts; e += kMoeRouterThreads) s.masks[e] = 0;
-  for (int t = 0; t < q.t; ++t)
-    for (int e = tid; e < cols; e += kMoeRouterThreads) {
-      if (e == E && !q.d.shared_gate) continue;
-      const float* p = q.logits + (int64_t)t * q.lstride + e;
-      float v = 0.f;
-      for (int k = 0; k < q.splits; ++k)
-        v += __hip_atomic_load(p + (int64_t)k * kMoeTokens * q.lstride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s.logits[t * cols + e] = v;
-    }
+  const int E = q.d.experts;
+  for (int e = tid; e < 64 * EPL; e += kMoeRouterThreads) s.masks[e] = 0;
+  // rows of lstride = 16 n floats, four a thread; columns past the gate's are junk
+  const int quads = q.lstride / 4;
+  for (int i = tid; i < q.t * quads; i += kMoeRouterThreads) {
+    const int t = i / quads, e = 4 * (i - t * quads);
+    float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < q.splits; ++k)
+      v += *reinterpret_cast<const float4_t*>(q.logits + ((int64_t)k * kMoeTokens + t) * q.lstride + e);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (e + c <= E) s.logits[t * cols + e + c] = v[c];
+  }
   __syncthreads();
   constexpr int kTurns = kMoeTokens / kMoeRouterWaves;
   int id[kTurns];
@@ -204,33 +224,40 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds& s) {
     }
   }
   __syncthreads();
-  // entries in expert order: 64 experts at a time, then over the chunks before
-  constexpr int kChunks = kMoeExperts / 64 / kMoeRouterWaves;
+  // entries in expert order: 64 experts a wave, then over the chunks before
+  constexpr int kChunks = (EPL + kMoeRouterWaves - 1) / kMoeRouterWaves;
   int before[kChunks], rows[kChunks];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int chunk = wave + kMoeRouterWaves * c;
+    if (chunk >= EPL) break;
     const uint32_t mask = s.masks[chunk * 64 + lane];
     const uint64_t chosen = __ballot(mask != 0);
     before[c] = __popcll(chosen & ((1ull << lane) - 1));
-    int sum = __popc(mask);
-    for (int m = 1; m < 64; m <<= 1) {
-      const int o = __shfl_up(sum, m);
-      if (lane >= m) sum += o;
+    // pairs of the lanes before: bit by bit of their counts (at most 16)
+    const int n = __popc(mask);
+    int sum = 0, all = 0;
+#pragma unroll
+    for (int bit = 0; bit < 5; ++bit) {
+      const uint64_t b = __ballot((n >> bit) & 1);
+      sum += __popcll(b & ((1ull << lane) - 1)) << bit;
+      all += __popcll(b) << bit;
     }
-    rows[c] = sum - __popc(mask);
-    if (lane == 63) {
+    rows[c] = sum;
+    if (lane == 0) {
       s.chunk_entries[chunk] = __popcll(chosen);
-      s.chunk_rows[chunk] = sum;
+      s.chunk_rows[chunk] = all;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int chunk = wave + kMoeRouterWaves * c;
-    for (int o = 0; o < chunk; ++o) {
-      before[c] += s.chunk_entries[o];
-      rows[c] += s.chunk_rows[o];
+    if (chunk >= EPL) break;
+#pragma unroll
+    for (int o = 0; o < EPL; ++o) {
+      before[c] += o < chunk ? s.chunk_entries[o] : 0;
+      rows[c] += o < chunk ? s.chunk_rows[o] : 0;
     }
     uint32_t mask = s.masks[chunk * 64 + lane];
     if (mask) {
@@ -239,8 +266,8 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds& s) {
       q.entries[before[c]] = en;
       s.place[chunk * 64 + lane] = before[c];
     }
-    if (chunk == kMoeExperts / 64 - 1 && lane == 63) {
-      q.count[0] = before[c] + (s.masks[kMoeExperts - 1] != 0);
+    if (chunk == EPL - 1 && lane == 63) {
+      q.count[0] = before[c] + (s.masks[64 * EPL - 1] != 0);
       q.entries[q.most] = MoeEntry{-1, q.t, 0, 0, 0xFEDCBA9876543210ull, 0};
     }
   }
@@ -265,7 +292,7 @@ template <int EPL>
 __global__ __launch_bounds__(kMoeRouterThreads) void mx4_moe_router(MoeArgs q) {
   __shared__ union {
     float4_t part[kMoeRouterWaves * 64];
-    MoeRouteLds route;
+    MoeRouteLds<EPL> route;
   } s;
   __shared__ uint32_t before;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -276,13 +303,20 @@ __global__ __launch_bounds__(kMoeRouterThreads) void mx4_moe_router(MoeArgs q) {
   const uint16_t* w = e < E ? q.d.router + (int64_t)e * H : q.d.shared_gate;
   const bool there = e < E || (e == E && q.d.shared_gate);
   float4_t acc = {0.f, 0.f, 0.f, 0.f};
-  const int steps = H / 32;
-#pragma unroll 4
-  for (int st = split * kMoeRouterWaves + wave; st < steps; st += kMoeRouterWaves * q.splits) {
-    u32x4_t a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
-    if (r < q.t) a = load16(q.x + r * q.ldx + 32 * st + 8 * g);
-    if (there) b = load16(w + 32 * st + 8 * g);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), acc, 0, 0, 0);
+  const int steps = H / 32, stride = kMoeRouterWaves * q.splits;
+  for (int st = split * kMoeRouterWaves + wave; st < steps; st += 4 * stride) {
+    u32x4_t a[4], b[4];  // four steps' loads at a time
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = st + i * stride;
+      a[i] = b[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (r < q.t && at < steps) a[i] = load16(q.x + r * q.ldx + 32 * at + 8 * g);
+      if (there && at < steps) b[i] = load16(w + 32 * at + 8 * g);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a[i]), __builtin_bit_cast(f16x8_t, b[i]),
+                                                   acc, 0, 0, 0);
   }
   s.part[wave * 64 + lane] = acc;
   __syncthreads();
@@ -318,73 +352,80 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&p)[3]) {
   }
 }
 
-// Sums of this wave's share of k for 16 gate and 16 up rows; operand rows are
-// the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
+// An entry by a uniform index, through scalar loads.
+__device__ __forceinline__ MoeEntry load_entry(const MoeEntry* p, int i) {
+  typedef __attribute__((address_space(4))) const uint64_t* words;
+  const words w = (words)(uintptr_t)(p + i);
+  uint64_t v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = w[k];
+  static_assert(sizeof(MoeEntry) == 32, "four words");
+  return MoeEntry{(int)(uint32_t)v[0], (int)(v[0] >> 32), (int)(uint32_t)v[1], 0, v[2], 0};
+}
+__device__ __forceinline__ int load_uniform(const int* p) {
+  return *(__attribute__((address_space(4))) const int*)(uintptr_t)p;
+}
+
+// Sums of 16 weight rows over every fourth unit of k from `first`; operand rows
+// are the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
+constexpr int kMoeGateUpShares = kMoeGateUpWaves / 2;
 template <int P>
-__device__ void moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const uint8_t* codes, const uint8_t* scales,
-                                 int64_t row, int64_t up, int wave, int g, int r, float4_t& vg, float4_t& vu) {
+__device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const uint8_t* codes,
+                                                     const uint8_t* scales, int first, int g, int r) {
   constexpr int kLoads = Mx4X<P>::kLoads;
   const int kb = q.d.hidden / kMx4Block;
   const int i = r % Mx4X<P>::kRows;
   const bool there = i < en.count;
   const uint16_t* x = q.x + (there ? en.token(i) : 0) * q.ldx;
-  float4_t ag[1][P], au[1][P];
+  float4_t acc[1][P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) ag[0][p] = au[0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < P; ++p) acc[0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
-  for (int u = wave; u < units; u += kMoeGateUpWaves) {
-    Mx4Unit wg, wu;
-    mx4_load_unit(codes + row * kb * 16, scales + row * kb, kb, u, g, wg);
-    mx4_load_unit(codes + up * kb * 16, scales + up * kb, kb, u, g, wu);
-    f16x8_t f[2][1][kLoads];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int l = 0; l < kLoads; ++l) f[h][0][l] = mx4_load_x<P>(x, there, kb, u, h, g, r, l);
+  for (int u = first; u < units; u += kMoeGateUpShares) {
+    Mx4Unit w;
+    mx4_load_unit(codes, scales, kb, u, g, w);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mx4_mma_f16<1, P>(f[h], wg, h, g, ag);
-      mx4_mma_f16<1, P>(f[h], wu, h, g, au);
+      f16x8_t f[1][kLoads];
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) f[0][l] = mx4_load_x<P>(x, there, kb, u, h, g, r, l);
+      mx4_mma_f16<1, P>(f, w, h, g, acc);
     }
   }
-  vg = mx4_pick<P>(ag[0], g);
-  vu = mx4_pick<P>(au[0], g);
+  return mx4_pick<P>(acc[0], g);
 }
 
 __global__ __launch_bounds__(kMoeGateUpWaves * 64) void mx4_moe_gate_up(MoeArgs q) {
-  __shared__ float part[kMoeGateUpWaves][2][16][16];  // [wave][gate, up][operand row][column]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  __shared__ float part[kMoeGateUpWaves][16][16];  // [wave][operand row][column]; the first half of the waves: gate
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int entry = blockIdx.y;
   const bool shared = entry == q.most;
-  const MoeEntry en = q.entries[entry];
-  if (!shared && entry >= q.count[0]) return;
+  const MoeEntry en = load_entry(q.entries, entry);
+  if (!shared && entry >= load_uniform(q.count)) return;
   const int inter = shared ? q.d.shared_inter : q.d.inter;
   const int i0 = blockIdx.x * 16;
   if (i0 >= inter) return;
   const int64_t kb = q.d.hidden / kMx4Block;
-  const uint8_t* codes = shared ? q.d.sgu_codes : q.d.gu_codes + (int64_t)en.e * 2 * inter * kb * 16;
-  const uint8_t* scales = shared ? q.d.sgu_scales : q.d.gu_scales + (int64_t)en.e * 2 * inter * kb;
+  const int64_t row = (shared ? 0 : (int64_t)en.e * 2 * inter) + (wave >= kMoeGateUpShares ? inter : 0) + i0 + r;
+  const uint8_t* codes = (shared ? q.d.sgu_codes : q.d.gu_codes) + row * kb * 16;
+  const uint8_t* scales = (shared ? q.d.sgu_scales : q.d.gu_scales) + row * kb;
+  const int first = wave % kMoeGateUpShares;
   const bool few = en.count <= 4;
-  float4_t vg, vu;
-  if (few)
-    moe_gate_up_wave<4>(q, en, codes, scales, i0 + r, i0 + r + inter, wave, g, r, vg, vu);
-  else
-    moe_gate_up_wave<1>(q, en, codes, scales, i0 + r, i0 + r + inter, wave, g, r, vg, vu);
+  const float4_t v = few ? moe_gate_up_wave<4>(q, en, codes, scales, first, g, r)
+                         : moe_gate_up_wave<1>(q, en, codes, scales, first, g, r);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    part[wave][0][4 * g + i][r] = vg[i];
-    part[wave][1][4 * g + i][r] = vu[i];
-  }
+  for (int i = 0; i < 4; ++i) part[wave][4 * g + i][r] = v[i];
   __syncthreads();
   // thread (token i, column c): the waves in order, of each the pieces in order
   const int i = threadIdx.x >> 4, c = threadIdx.x & 15;
   if (i >= en.count) return;
   float sg = 0.f, su = 0.f;
-  for (int w = 0; w < kMoeGateUpWaves; ++w)
-    for (int row = i; row < 16; row += few ? 4 : 16) {
-      sg += part[w][0][row][c];
-      su += part[w][1][row][c];
+#pragma unroll
+  for (int w = 0; w < kMoeGateUpShares; ++w)
+    for (int o = i; o < 16; o += few ? 4 : 16) {
+      sg += part[w][o][c];
+      su += part[kMoeGateUpShares + w][o][c];
     }
   uint16_t p[3];
   split_bf16(sg / (1.0f + expf(-sg)) * su, p);
@@ -399,6 +440,13 @@ __global__ __launch_bounds__(kMoeGateUpWaves * 64) void mx4_moe_gate_up(MoeArgs 
 // down
 // ---------------------------------------------------------------------------
 constexpr int kMoeDownWide = 5;  // tokens whose three pieces fit one operand
+
+__device__ __forceinline__ void moe_store(const MoeArgs& q, int t, int64_t h, float v) {
+  if (q.y_f32)
+    static_cast<float*>(q.y)[t * q.ldy + h] = v;
+  else
+    static_cast<uint16_t*>(q.y)[t * q.ldy + h] = f2h(v);
+}
 
 // A wave's task: unit u of an entry's k, for this workgroup's 16 columns.
 struct MoeDownTask {
@@ -417,7 +465,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int64_t h0 = (int64_t)blockIdx.x * 16, H = q.d.hidden;
-  const int routed = q.count[0];
+  const int routed = load_uniform(q.count);
   const int units = (q.d.inter / kMx4Block + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   const int tasks = routed * units + (q.d.shared_inter / kMx4Block + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   auto task = [&](int id) {
@@ -425,7 +473,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
     const bool shared = id >= routed * units;
     const int entry = shared ? q.most : id / units;
     t.u = shared ? id - routed * units : id - entry * units;
-    t.en = q.entries[entry];
+    t.en = load_entry(q.entries, entry);
     t.inter = shared ? q.d.shared_inter : q.d.inter;
     t.kb = t.inter / kMx4Block;
     t.plane = (int64_t)q.rows[shared] * t.inter;
@@ -441,14 +489,15 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
   // the weights of the next task are fetched before this one's product
   MoeDownTask now, next;
   Mx4Unit w, wn;
-  if (wave < tasks) {
-    now = task(wave);
+  const int first = (int)blockIdx.y * kMoeDownWaves + wave, stride = kMoeDownWaves * q.down_splits;
+  if (first < tasks) {
+    now = task(first);
     mx4_load_unit(now.codes, now.scales, now.kb, now.u, g, w);
   }
-  for (int id = wave; id < tasks; id += kMoeDownWaves) {
-    const bool more = id + kMoeDownWaves < tasks;
+  for (int id = first; id < tasks; id += stride) {
+    const bool more = id + stride < tasks;
     if (more) {
-      next = task(id + kMoeDownWaves);
+      next = task(id + stride);
       mx4_load_unit(next.codes, next.scales, next.kb, next.u, g, wn);
     }
     const int n = now.en.count;
@@ -525,11 +574,20 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
   float v = 0.f;
 #pragma unroll
   for (int o = 0; o < kMoeDownWaves; ++o) v += tiles[o][t][c];
-  const int64_t at = t * q.ldy + h0 + c;
-  if (q.y_f32)
-    static_cast<float*>(q.y)[at] = v;
+  if (q.down_splits == 1)
+    moe_store(q, t, h0 + c, v);
   else
-    static_cast<uint16_t*>(q.y)[at] = f2h(v);
+    q.down[((int64_t)blockIdx.y * q.t + t) * H + h0 + c] = v;
+}
+
+// y = sum of the down splits in order.
+__global__ __launch_bounds__(256) void mx4_moe_finish(MoeArgs q) {
+  const int t = blockIdx.y, h = blockIdx.x * 256 + threadIdx.x, H = q.d.hidden;
+  if (h >= H) return;
+  float v = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < q.down_splits; ++s) v += q.down[((int64_t)s * q.t + t) * H + h];
+  moe_store(q, t, h, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -547,8 +605,18 @@ int moe_splits(const Mx4MoeDesc& d) {
   return s < 1 ? 1 : (s > 8 ? 8 : s);
 }
 
+// Shares of the down product's entries: about four tasks a wave where there
+// may be so many, and no more than the chip takes at once (two workgroups a CU).
+int moe_down_splits(const Mx4MoeDesc& d, int64_t t, int topk) {
+  const int units = (d.inter + kMx4UnitK - 1) / kMx4UnitK, tasks = moe_most(d, t, topk) * units;
+  const int room = 512 / (d.hidden / 16);
+  int s = tasks / (4 * kMoeDownWaves);
+  if (s > room) s = room;
+  return s < 1 ? 1 : s;
+}
+
 struct MoeLayout {
-  size_t arrived, logits, entries, count, wtab, act[2], total;
+  size_t arrived, logits, entries, count, wtab, act[2], down, total;
   int lstride;
 };
 MoeLayout moe_layout(const Mx4MoeDesc& d, int64_t t, int topk) {
@@ -568,6 +636,8 @@ MoeLayout moe_layout(const Mx4MoeDesc& d, int64_t t, int topk) {
   L.wtab = take(most * kMoeTokens * 4);
   L.act[0] = take((size_t)t * topk * d.inter * 6);
   L.act[1] = take((size_t)t * d.shared_inter * 6);
+  const size_t splits = moe_down_splits(d, t, topk);
+  L.down = take(splits > 1 ? splits * t * d.hidden * 4 : 0);
   L.total = off;
   return L;
 }
@@ -584,15 +654,19 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
                   reinterpret_cast<uint32_t*>(w + L.arrived), reinterpret_cast<float*>(w + L.logits),
                   reinterpret_cast<MoeEntry*>(w + L.entries), reinterpret_cast<int*>(w + L.count),
                   reinterpret_cast<float*>(w + L.wtab),
-                  {reinterpret_cast<uint16_t*>(w + L.act[0]), reinterpret_cast<uint16_t*>(w + L.act[1])}};
+                  {reinterpret_cast<uint16_t*>(w + L.act[0]), reinterpret_cast<uint16_t*>(w + L.act[1])},
+                  moe_down_splits(d, t, topk), reinterpret_cast<float*>(w + L.down)};
   const dim3 rgrid((uint32_t)((d.experts / 16 + 1) * splits)), rblock(kMoeRouterThreads);
   if (d.experts <= 64) hipLaunchKernelGGL(mx4_moe_router<1>, rgrid, rblock, 0, s, q);
   else if (d.experts <= 128) hipLaunchKernelGGL(mx4_moe_router<2>, rgrid, rblock, 0, s, q);
   else if (d.experts <= 256) hipLaunchKernelGGL(mx4_moe_router<4>, rgrid, rblock, 0, s, q);
+  else if (d.experts <= 512) hipLaunchKernelGGL(mx4_moe_router<8>, rgrid, rblock, 0, s, q);
   else hipLaunchKernelGGL(mx4_moe_router<16>, rgrid, rblock, 0, s, q);
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
   hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s, q);
-  hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16), dim3(kMoeDownWaves * 64), 0, s, q);
+  hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
+  if (q.down_splits > 1)
+    hipLaunchKernelGGL(mx4_moe_finish, dim3((d.hidden + 255) / 256, (uint32_t)t), dim3(256), 0, s, q);
   return hipGetLastError();
 }
 
