@@ -47,32 +47,25 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   const uint32_t tm = tile / q.col_tiles, tn = tile - tm * q.col_tiles;
   const int64_t m0 = (int64_t)tm * (16 * MG), n0 = (int64_t)tn * (16 * NG);
   const int kb = q.kb;
-  const int64_t pitch = (int64_t)kb * 16;
 
-  const uint8_t* bc[NG];
-  const uint8_t* bs[NG];
+  Mx4Row rb[NG], ra[A4 ? MG : 1];
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng) {
-    int64_t row = n0 + 16 * ng + r;
-    row = row < q.n ? row : q.n - 1;  // columns past n are computed and not stored
-    bc[ng] = q.b + row * pitch;
-    bs[ng] = q.b_scales + row * kb;
+    // columns past n are computed and not stored
+    const int64_t left = q.n - 1 - n0;
+    rb[ng] = mx4_row(q.b, q.b_scales, n0, 16 * ng + r <= left ? 16 * ng + r : (uint32_t)left, kb);
   }
-  const uint8_t* ac[MG];
-  const uint8_t* as[MG];
+  const uint16_t* xr[MG];
   bool there[MG];
 #pragma unroll
   for (int mg = 0; mg < MG; ++mg) {
-    int64_t row = m0 + 16 * mg + r % kRows;
-    there[mg] = row < q.m;
-    row = there[mg] ? row : q.m - 1;
-    if constexpr (A4) {
-      ac[mg] = static_cast<const uint8_t*>(q.a) + row * pitch;
-      as[mg] = q.a_scales + row * kb;
-    } else {
-      ac[mg] = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(q.a) + row * q.lda);
-      as[mg] = nullptr;
-    }
+    const int i = 16 * mg + r % kRows;
+    const int64_t left = q.m - 1 - m0;
+    there[mg] = i <= left;
+    if constexpr (A4)
+      ra[mg] = mx4_row(static_cast<const uint8_t*>(q.a), q.a_scales, m0, there[mg] ? i : (uint32_t)left, kb);
+    else
+      xr[mg] = static_cast<const uint16_t*>(q.a) + (m0 + (there[mg] ? i : 0)) * q.lda;
   }
 
   float4_t acc[NG][MG][P];
@@ -87,14 +80,14 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   const int first = (int)split * NW + wave, stride = NW * q.splits;
   auto load_w = [&](Mx4Unit (&w)[NG], int u) {
 #pragma unroll
-    for (int ng = 0; ng < NG; ++ng) mx4_load_unit(bc[ng], bs[ng], kb, u, g, w[ng]);
+    for (int ng = 0; ng < NG; ++ng) mx4_load_unit(rb[ng], kb, u, g, w[ng]);
   };
   if constexpr (A4) {
     for (int u = first; u < units; u += stride) {
       Mx4Unit w[NG], x[MG];
       load_w(w, u);
 #pragma unroll
-      for (int mg = 0; mg < MG; ++mg) mx4_load_unit(ac[mg], as[mg], kb, u, g, x[mg]);
+      for (int mg = 0; mg < MG; ++mg) mx4_load_unit(ra[mg], kb, u, g, x[mg]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -110,7 +103,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
       for (int mg = 0; mg < MG; ++mg)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-          x[mg][i] = mx4_load_x<P>(reinterpret_cast<const uint16_t*>(ac[mg]), there[mg], kb, u, h, g, r, i);
+          x[mg][i] = mx4_load_x<P>(xr[mg], there[mg], kb, u, h, g, r, i);
     };
     for (int u = first; u < units; u += stride) {
       Mx4Unit w[NG];

@@ -25,7 +25,6 @@
 namespace exl3 {
 
 constexpr int kMoeTokens = 16;
-constexpr int kMoeExperts = 1024;
 constexpr int kMoeRouterWaves = 8, kMoeGateUpWaves = 8, kMoeDownWaves = 16;
 constexpr int kMoeRouterThreads = kMoeRouterWaves * 64;
 
@@ -370,8 +369,8 @@ __device__ __forceinline__ int load_uniform(const int* p) {
 // are the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
 constexpr int kMoeGateUpShares = kMoeGateUpWaves / 2;
 template <int P>
-__device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const uint8_t* codes,
-                                                     const uint8_t* scales, int first, int g, int r) {
+__device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const Mx4Row& row,
+                                                     int first, int g, int r) {
   constexpr int kLoads = Mx4X<P>::kLoads;
   const int kb = q.d.hidden / kMx4Block;
   const int i = r % Mx4X<P>::kRows;
@@ -383,7 +382,7 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   for (int u = first; u < units; u += kMoeGateUpShares) {
     Mx4Unit w;
-    mx4_load_unit(codes, scales, kb, u, g, w);
+    mx4_load_unit(row, kb, u, g, w);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f16x8_t f[1][kLoads];
@@ -395,7 +394,7 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
   return mx4_pick<P>(acc[0], g);
 }
 
-__global__ __launch_bounds__(kMoeGateUpWaves * 64) void mx4_moe_gate_up(MoeArgs q) {
+__global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeArgs q) {
   __shared__ float part[kMoeGateUpWaves][16][16];  // [wave][operand row][column]; the first half of the waves: gate
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
@@ -406,14 +405,13 @@ __global__ __launch_bounds__(kMoeGateUpWaves * 64) void mx4_moe_gate_up(MoeArgs 
   const int inter = shared ? q.d.shared_inter : q.d.inter;
   const int i0 = blockIdx.x * 16;
   if (i0 >= inter) return;
-  const int64_t kb = q.d.hidden / kMx4Block;
-  const int64_t row = (shared ? 0 : (int64_t)en.e * 2 * inter) + (wave >= kMoeGateUpShares ? inter : 0) + i0 + r;
-  const uint8_t* codes = (shared ? q.d.sgu_codes : q.d.gu_codes) + row * kb * 16;
-  const uint8_t* scales = (shared ? q.d.sgu_scales : q.d.gu_scales) + row * kb;
+  const int64_t top = (shared ? 0 : (int64_t)en.e * 2 * inter) + (wave >= kMoeGateUpShares ? inter : 0) + i0;
+  const Mx4Row row = mx4_row(shared ? q.d.sgu_codes : q.d.gu_codes, shared ? q.d.sgu_scales : q.d.gu_scales, top, r,
+                             q.d.hidden / kMx4Block);
   const int first = wave % kMoeGateUpShares;
   const bool few = en.count <= 4;
-  const float4_t v = few ? moe_gate_up_wave<4>(q, en, codes, scales, first, g, r)
-                         : moe_gate_up_wave<1>(q, en, codes, scales, first, g, r);
+  const float4_t v = few ? moe_gate_up_wave<4>(q, en, row, first, g, r)
+                         : moe_gate_up_wave<1>(q, en, row, first, g, r);
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][4 * g + i][r] = v[i];
   __syncthreads();
@@ -452,14 +450,13 @@ __device__ __forceinline__ void moe_store(const MoeArgs& q, int t, int64_t h, fl
 struct MoeDownTask {
   MoeEntry en;
   const uint16_t* a;     // the entry's activations, plane 0
-  const uint8_t* codes;  // this lane's weight row
-  const uint8_t* scales;
+  Mx4Row row;            // this lane's weight row
   const float* weights;
   int64_t plane;
   int inter, kb, u;
 };
 
-__global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
+__global__ __launch_bounds__(kMoeDownWaves * 64, 8) void mx4_moe_down(MoeArgs q) {
   __shared__ float tiles[kMoeDownWaves][kMoeTokens][16];  // weighted sums [token][column]
   __shared__ float dump[kMoeDownWaves][16][16];           // one unit's sums [operand row][column]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -479,9 +476,8 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
     t.plane = (int64_t)q.rows[shared] * t.inter;
     t.a = q.act[shared] + (int64_t)t.en.row0 * t.inter;
     t.weights = q.wtab + entry * kMoeTokens;
-    const int64_t row = (shared ? 0 : (int64_t)t.en.e * H) + h0 + r;
-    t.codes = (shared ? q.d.sdn_codes : q.d.dn_codes) + row * t.kb * 16;
-    t.scales = (shared ? q.d.sdn_scales : q.d.dn_scales) + row * t.kb;
+    t.row = mx4_row(shared ? q.d.sdn_codes : q.d.dn_codes, shared ? q.d.sdn_scales : q.d.dn_scales,
+                    (shared ? 0 : (int64_t)t.en.e * H) + h0, r, t.kb);
     return t;
   };
 #pragma unroll
@@ -492,13 +488,13 @@ __global__ __launch_bounds__(kMoeDownWaves * 64) void mx4_moe_down(MoeArgs q) {
   const int first = (int)blockIdx.y * kMoeDownWaves + wave, stride = kMoeDownWaves * q.down_splits;
   if (first < tasks) {
     now = task(first);
-    mx4_load_unit(now.codes, now.scales, now.kb, now.u, g, w);
+    mx4_load_unit(now.row, now.kb, now.u, g, w);
   }
   for (int id = first; id < tasks; id += stride) {
     const bool more = id + stride < tasks;
     if (more) {
       next = task(id + stride);
-      mx4_load_unit(next.codes, next.scales, next.kb, next.u, g, wn);
+      mx4_load_unit(next.row, next.kb, next.u, g, wn);
     }
     const int n = now.en.count;
     // 8 elements of this lane's block of half h, piece j, of plane p of token row i

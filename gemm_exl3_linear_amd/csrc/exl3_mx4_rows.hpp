@@ -34,26 +34,37 @@ struct Mx4Unit {
   uint32_t sc[2];    // scale bytes of blocks 8u .. 8u + 3 and 8u + 4 .. 8u + 7
 };
 
-// Row `row` of codes (k/2 bytes a row) and scales (kb = k/32 bytes a row),
-// unit u; blocks past the row's end read as zeros with scale 1.
-__device__ __forceinline__ void mx4_load_unit(const uint8_t* codes, const uint8_t* scales, int kb, int u, int g,
-                                              Mx4Unit& t) {
-  const uint8_t* c = codes + (int64_t)u * kMx4UnitBytes + 16 * g;
-  const uint8_t* s = scales + u * kMx4UnitBlocks;
+// Where one lane's weight row lies: uniform bases (of a workgroup's first row)
+// and 32-bit offsets, which a load takes as they are.
+struct Mx4Row {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  uint32_t code_off, scale_off;
+};
+__device__ __forceinline__ Mx4Row mx4_row(const uint8_t* codes, const uint8_t* scales, int64_t first, uint32_t row, int kb) {
+  return Mx4Row{codes + first * kb * 16, scales + first * kb, row * (uint32_t)kb * 16u, row * (uint32_t)kb};
+}
+
+// Unit u of a row of kb blocks; blocks past the row's end read as zeros with
+// scale 1.
+__device__ __forceinline__ void mx4_load_unit(const Mx4Row& row, int kb, int u, int g, Mx4Unit& t) {
+  const uint32_t c = row.code_off + (uint32_t)(u * kMx4UnitBytes + 16 * g);
+  const uint32_t s = row.scale_off + (uint32_t)(u * kMx4UnitBlocks);
   if ((u + 1) * kMx4UnitBlocks <= kb) {
-    t.half[0] = load16(c);
-    t.half[1] = load16(c + 64);
-    __builtin_memcpy(t.sc, s, 8);
+    t.half[0] = load16(row.codes + c);
+    t.half[1] = load16(row.codes + c + 64u);
+    __builtin_memcpy(t.sc, row.scales + s, 8);
   } else {
     const int left = kb - u * kMx4UnitBlocks;
     t.half[0] = t.half[1] = u32x4_t{0u, 0u, 0u, 0u};
-    if (g < left) t.half[0] = load16(c);
-    if (4 + g < left) t.half[1] = load16(c + 64);
+    if (g < left) t.half[0] = load16(row.codes + c);
+    if (4 + g < left) t.half[1] = load16(row.codes + c + 64u);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       t.sc[h] = 0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) t.sc[h] |= (4 * h + b < left ? (uint32_t)s[4 * h + b] : kMx4One) << (8 * b);
+      for (int b = 0; b < 4; ++b)
+        t.sc[h] |= (4 * h + b < left ? (uint32_t)row.scales[s + 4 * h + b] : kMx4One) << (8 * b);
     }
   }
 }
