@@ -25,8 +25,7 @@
 namespace exl3 {
 
 constexpr int kMoeTokens = 16;
-constexpr int kMoeRouterWaves = 8, kMoeGateUpWaves = 8, kMoeDownWaves = 16;
-constexpr int kMoeRouterThreads = kMoeRouterWaves * 64;
+constexpr int kMoeGateUpWaves = 8, kMoeDownWaves = 16;
 
 // A listed expert: its tokens, in order, and the first of their rows in the
 // activations.
@@ -68,9 +67,9 @@ struct MoeArgs {
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
-// Unsigned key in the order of floats, NaN lowest, both zeros equal.
+// Unsigned key in the order of floats, NaN lowest, both zeros equal; never 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0u;
+  if (f != f) return 1u;
   const uint32_t b = __float_as_uint(f + 0.f);
   return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
@@ -80,7 +79,7 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 // 63 ends with the result.  (Six LDS permutes took 6 x 100 cycles a choice.)
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF);
 }
 template <class Op>
 __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, Op op) {  // 0 is neutral
@@ -101,121 +100,107 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
-// Top-k and weights of one token by one wave, from its logits; lane s ends with
-// choice s and its weight.  Expert 64 i + lane is the lane's i-th.
+// e^x to about an ulp in few instructions: x log2 e with the product's own
+// rounding error, and log2 e's, put back after the power.  (The routing runs once
+// a call, so its instructions come from memory: their number is its time.)
+__device__ __forceinline__ float exp_f(float x) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500e-8f, kLn2 = 0.693147180559945309f;
+  const float t = x * kLog2e;
+  const float rest = __builtin_fmaf(x, kLog2eRest, __builtin_fmaf(x, kLog2e, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return t > 126.f || t < -125.f ? p : __builtin_fmaf(p, rest * kLn2, p);
+}
+
+// Top-k and weights of one token by one wave, from its keys (in the order of
+// its choices, 0 where there is no expert) and its scores, before the softmax;
+// lane s ends with choice s and its weight.  Expert 64 i + lane is the lane's i-th.
+// A choice takes the highest key of the wave and then the lowest expert that
+// holds it; its key becomes 0.
 template <int EPL>
-__device__ void moe_route_token(const MoeArgs& q, const float* logits, int lane, int& id, float& weight) {
-  const int E = q.d.experts;
-  float score[EPL];
+__device__ __forceinline__ void moe_route_token(const MoeArgs& q, const uint32_t* keys, const float* scores, int lane,
+                                                int& id, float& weight) {
   uint32_t key[EPL];
-  bool open[EPL];  // not yet chosen
-  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    open[i] = e < E;
-    score[i] = 0.f;
-    key[i] = 0;
-    if (open[i]) {
-      const float b = q.d.router_bias ? q.d.router_bias[e] : 0.f;
-      float choice = logits[e];
-      if (q.d.scoring == 0) {
-        choice += b;
-        score[i] = choice;
-      } else {
-        score[i] = 1.f / (1.f + expf(-choice));
-        choice = q.d.router_bias ? score[i] + b : choice;
-      }
-      key[i] = order_key(choice);
-      top = top > key[i] ? top : key[i];
+  for (int i = 0; i < EPL; ++i) key[i] = keys[lane + 64 * i];
+  id = 0;
+  uint32_t top = 0;
+  for (int s = 0; s < q.topk; ++s) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) best = best > key[i] ? best : key[i];
+    best = wave_max_u32(best);
+    top = s ? top : best;
+    int e = 0;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i) {
+      const uint64_t equal = __ballot(key[i] == best);
+      e = equal ? 64 * i + __ffsll((unsigned long long)equal) - 1 : e;
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = lane + 64 * i == e ? 0u : key[i];
+    id = lane == s ? e : id;
   }
-  top = wave_max_u32(top);
+  weight = scores[id];
   if (q.d.scoring == 0) {
-    const float high = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);  // NaN if every one is
+    const float high = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);  // the highest l + b (NaN if every one is)
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (open[i]) {
-        score[i] = expf(score[i] - high);
-        sum += score[i];
-      }
-    sum = wave_sum_f(sum);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) score[i] = score[i] / sum;
+    for (int i = 0; i < EPL; ++i) sum += lane + 64 * i < q.d.experts ? exp_f(scores[lane + 64 * i] - high) : 0.f;
+    weight = exp_f(weight - high) / wave_sum_f(sum);
   }
-  id = 0;
-  weight = 0.f;
-  float total = 0.f;
-  for (int s = 0; s < q.topk; ++s) {
-    uint32_t best = top;
-    if (s) {
-      best = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) best = open[i] && key[i] > best ? key[i] : best;
-      best = wave_max_u32(best);
-    }
-    // the lowest expert among the equal ones: lowest i, then lowest lane
-    int at = -1, from = 0;
-    float mine = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const uint64_t equal = __ballot(open[i] && key[i] == best);
-      if (at < 0 && equal) {
-        at = i;
-        from = __ffsll((unsigned long long)equal) - 1;
-        mine = score[i];
-        if (lane == from) open[i] = false;
-      }
-    }
-    const float w = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), from));
-    total += w;
-    if (lane == s) {
-      id = 64 * at + from;
-      weight = w;
-    }
-  }
-  if (q.d.renormalize) weight = weight / total;
+  if (q.d.renormalize) weight = weight / wave_sum_f(lane < q.topk ? weight : 0.f);
   weight *= q.d.scale;
 }
 
 template <int EPL>
 struct MoeRouteLds {
-  static constexpr int kCols = 64 * EPL + 1;  // the experts and the shared gate
-  float logits[kMoeTokens * kCols];
-  uint32_t masks[64 * EPL];
-  int place[64 * EPL];
+  static constexpr int kCols = 64 * EPL;
+  float scores[kMoeTokens * kCols];   // l + b (softmax), or sigmoid(l)
+  uint32_t keys[kMoeTokens * kCols];
+  float gates[kMoeTokens];            // the shared expert's logits
+  uint32_t masks[kCols];
+  int place[kCols];
   int chunk_entries[EPL], chunk_rows[EPL];
 };
 
 // Routing of all tokens by one workgroup, from the partial logits.
-template <int EPL>
-__device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
+template <int EPL, int NW>
+__device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
   constexpr int cols = MoeRouteLds<EPL>::kCols;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int E = q.d.experts;
-  for (int e = tid; e < 64 * EPL; e += kMoeRouterThreads) s.masks[e] = 0;
-  // rows of lstride = 16 n floats, four a thread; columns past the gate's are junk
-  const int quads = q.lstride / 4;
-  for (int i = tid; i < q.t * quads; i += kMoeRouterThreads) {
-    const int t = i / quads, e = 4 * (i - t * quads);
-    float4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int e = tid; e < cols; e += NW * 64) s.masks[e] = 0;
+#pragma unroll 2
+  for (int i = tid; i < q.t * cols; i += NW * 64) {
+    const int t = i / cols, e = i - t * cols;
+    uint32_t key = 0;
+    if (e < E) {
+      const float* p = q.logits + (int64_t)t * q.lstride + e;
+      float l = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < q.splits; ++k)
-      v += *reinterpret_cast<const float4_t*>(q.logits + ((int64_t)k * kMoeTokens + t) * q.lstride + e);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (e + c <= E) s.logits[t * cols + e + c] = v[c];
+      for (int k = 0; k < q.splits; ++k) l += p[(int64_t)k * kMoeTokens * q.lstride];
+      const float b = q.d.router_bias ? q.d.router_bias[e] : 0.f;
+      const float score = q.d.scoring == 0 ? l + b : 1.f / (1.f + exp_f(-l));
+      // without a bias the sigmoid's order is the logit's, where it has not saturated
+      key = order_key(q.d.scoring == 0 ? score : (q.d.router_bias ? score + b : l));
+      s.scores[i] = score;
+    }
+    s.keys[i] = key;
+  }
+  if (q.d.shared_gate && tid < q.t) {
+    float l = 0.f;
+    for (int k = 0; k < q.splits; ++k) l += q.logits[((int64_t)k * kMoeTokens + tid) * q.lstride + E];
+    s.gates[tid] = l;
   }
   __syncthreads();
-  constexpr int kTurns = kMoeTokens / kMoeRouterWaves;
+  constexpr int kTurns = kMoeTokens / NW;
   int id[kTurns];
   float weight[kTurns];
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const int t = wave + kMoeRouterWaves * i;
+    const int t = wave + NW * i;
     if (t >= q.t) break;
-    moe_route_token<EPL>(q, s.logits + t * cols, lane, id[i], weight[i]);
+    moe_route_token<EPL>(q, s.keys + t * cols, s.scores + t * cols, lane, id[i], weight[i]);
     if (lane < q.topk) {
       atomicOr(&s.masks[id[i]], 1u << t);
       if (q.ids) q.ids[t * q.topk + lane] = id[i];
@@ -224,11 +209,11 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
   }
   __syncthreads();
   // entries in expert order: 64 experts a wave, then over the chunks before
-  constexpr int kChunks = (EPL + kMoeRouterWaves - 1) / kMoeRouterWaves;
+  constexpr int kChunks = (EPL + NW - 1) / NW;
   int before[kChunks], rows[kChunks];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    const int chunk = wave + kMoeRouterWaves * c;
+    const int chunk = wave + NW * c;
     if (chunk >= EPL) break;
     const uint32_t mask = s.masks[chunk * 64 + lane];
     const uint64_t chosen = __ballot(mask != 0);
@@ -251,7 +236,7 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    const int chunk = wave + kMoeRouterWaves * c;
+    const int chunk = wave + NW * c;
     if (chunk >= EPL) break;
 #pragma unroll
     for (int o = 0; o < EPL; ++o) {
@@ -273,7 +258,7 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const int t = wave + kMoeRouterWaves * i;
+    const int t = wave + NW * i;
     if (t >= q.t) break;
     if (lane < q.topk) {
       const uint32_t earlier = s.masks[id[i]] & ((1u << t) - 1u);
@@ -281,16 +266,17 @@ __device__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
     }
     if (lane == 0) {
       float w = 1.f;
-      if (q.d.shared_gate) w = 1.f / (1.f + expf(-s.logits[t * cols + E]));
+      if (q.d.shared_gate) w = 1.f / (1.f + exp_f(-s.gates[t]));
       q.wtab[q.most * kMoeTokens + t] = w;
     }
   }
 }
 
-template <int EPL>
-__global__ __launch_bounds__(kMoeRouterThreads) void mx4_moe_router(MoeArgs q) {
+// NW waves: 16 where there are more than 8 tokens to route, else the quicker 8.
+template <int EPL, int NW>
+__global__ __launch_bounds__(NW * 64) void mx4_moe_router(MoeArgs q) {
   __shared__ union {
-    float4_t part[kMoeRouterWaves * 64];
+    float4_t part[NW * 64];
     MoeRouteLds<EPL> route;
   } s;
   __shared__ uint32_t before;
@@ -302,8 +288,8 @@ __global__ __launch_bounds__(kMoeRouterThreads) void mx4_moe_router(MoeArgs q) {
   const uint16_t* w = e < E ? q.d.router + (int64_t)e * H : q.d.shared_gate;
   const bool there = e < E || (e == E && q.d.shared_gate);
   float4_t acc = {0.f, 0.f, 0.f, 0.f};
-  const int steps = H / 32, stride = kMoeRouterWaves * q.splits;
-  for (int st = split * kMoeRouterWaves + wave; st < steps; st += 4 * stride) {
+  const int steps = H / 32, stride = NW * q.splits;
+  for (int st = split * NW + wave; st < steps; st += 4 * stride) {
     u32x4_t a[4], b[4];  // four steps' loads at a time
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -321,21 +307,22 @@ __global__ __launch_bounds__(kMoeRouterThreads) void mx4_moe_router(MoeArgs q) {
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
-    for (int o = 1; o < kMoeRouterWaves; ++o) acc += s.part[o * 64 + lane];
+    for (int o = 1; o < NW; ++o) acc += s.part[o * 64 + lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (there && 4 * g + i < q.t)
         __hip_atomic_store(q.logits + ((int64_t)split * kMoeTokens + 4 * g + i) * q.lstride + e, acc[i],
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // device scope: the workgroups run on different XCDs
+    // device scope: the workgroups run on different XCDs.  One wave acquires for
+    // all (sixteen took 2 us), the barrier passes it on.
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
     if (lane == 0) before = __hip_atomic_fetch_add(q.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   }
   __syncthreads();
   if (before != gridDim.x - 1) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   if (threadIdx.x == 0) __hip_atomic_store(q.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  moe_route<EPL>(q, s.route);
+  moe_route<EPL, NW>(q, s.route);
 }
 
 // ---------------------------------------------------------------------------
@@ -426,7 +413,7 @@ __global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeAr
       su += part[kMoeGateUpShares + w][o][c];
     }
   uint16_t p[3];
-  split_bf16(sg / (1.0f + expf(-sg)) * su, p);
+  split_bf16(sg / (1.0f + exp_f(-sg)) * su, p);
   const int64_t plane = (int64_t)q.rows[shared] * inter;
   uint16_t* o = q.act[shared] + (int64_t)(en.row0 + i) * inter + i0 + c;
   o[0] = p[0];
@@ -596,7 +583,7 @@ int moe_most(const Mx4MoeDesc& d, int64_t t, int topk) { return (int)(t * topk <
 // chip's 256 CUs at most one workgroup each.
 int moe_splits(const Mx4MoeDesc& d) {
   const int groups = d.experts / 16 + 1, steps = d.hidden / 32;
-  int s = steps / (2 * kMoeRouterWaves);
+  int s = steps / 16;
   if (s > 256 / groups) s = 256 / groups;
   return s < 1 ? 1 : (s > 8 ? 8 : s);
 }
@@ -639,6 +626,15 @@ MoeLayout moe_layout(const Mx4MoeDesc& d, int64_t t, int topk) {
 }
 }  // namespace
 
+template <int EPL>
+static void launch_router(const MoeArgs& q, hipStream_t s) {
+  const dim3 grid((uint32_t)((q.d.experts / 16 + 1) * q.splits));
+  if (q.t > 8)
+    hipLaunchKernelGGL((mx4_moe_router<EPL, 16>), grid, dim3(1024), 0, s, q);
+  else
+    hipLaunchKernelGGL((mx4_moe_router<EPL, 8>), grid, dim3(512), 0, s, q);
+}
+
 size_t mx4_moe_workspace(const Mx4MoeDesc& d, int64_t t, int topk) { return moe_layout(d, t, topk).total; }
 
 hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int64_t ldx, int topk, void* y,
@@ -652,12 +648,11 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
                   reinterpret_cast<float*>(w + L.wtab),
                   {reinterpret_cast<uint16_t*>(w + L.act[0]), reinterpret_cast<uint16_t*>(w + L.act[1])},
                   moe_down_splits(d, t, topk), reinterpret_cast<float*>(w + L.down)};
-  const dim3 rgrid((uint32_t)((d.experts / 16 + 1) * splits)), rblock(kMoeRouterThreads);
-  if (d.experts <= 64) hipLaunchKernelGGL(mx4_moe_router<1>, rgrid, rblock, 0, s, q);
-  else if (d.experts <= 128) hipLaunchKernelGGL(mx4_moe_router<2>, rgrid, rblock, 0, s, q);
-  else if (d.experts <= 256) hipLaunchKernelGGL(mx4_moe_router<4>, rgrid, rblock, 0, s, q);
-  else if (d.experts <= 512) hipLaunchKernelGGL(mx4_moe_router<8>, rgrid, rblock, 0, s, q);
-  else hipLaunchKernelGGL(mx4_moe_router<16>, rgrid, rblock, 0, s, q);
+  if (d.experts <= 64) launch_router<1>(q, s);
+  else if (d.experts <= 128) launch_router<2>(q, s);
+  else if (d.experts <= 256) launch_router<4>(q, s);
+  else if (d.experts <= 512) launch_router<8>(q, s);
+  else launch_router<16>(q, s);
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
   hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s, q);
   hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
