@@ -5,6 +5,7 @@
 // 128-byte line of codes of every row of both operands and their scale bytes,
 // copied straight from memory to LDS while the other stage is multiplied.
 #include "exl3_internal.hpp"
+#include "exl3_mx4_lds.hpp"
 #include "exl3_mx4_rows.hpp"
 
 namespace exl3 {
@@ -19,42 +20,6 @@ constexpr int kScaleTile = 64;                      // rows of one staged group 
 // one chunk of sixteen rows for every lane group, and the lanes that are served
 // together then fall on different banks.
 __device__ __forceinline__ int stage_place(int row, int c) { return c ^ (row & 7); }
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-__device__ __forceinline__ u32x4_t lds_read16(uint32_t at) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4_t*>((const lds_u8*)(uintptr_t)at);
-}
-__device__ __forceinline__ u32x2_t lds_read8(uint32_t at) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) u32x2_t*>((const lds_u8*)(uintptr_t)at);
-}
-
-// 16 (4) bytes a lane from a buffer to LDS: lane l's land at `at` + 16 l (4 l).
-// Written as assembly so that the compiler, which cannot tell the stages
-// apart, does not wait for it before every LDS read; the kernel waits itself
-// before the barrier that hands a stage over.  (M0 needs one wait state before
-// its use.)
-__device__ __forceinline__ void lds_copy16(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
-               : "memory");
-}
-__device__ __forceinline__ void lds_copy4(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :
-               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
-               : "memory");
-}
-
-// Raw buffer descriptor over [p, p + bytes): loads past its end give zeros.
-__device__ __forceinline__ u32x4_t buffer_words(const uint8_t* p, uint64_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(p);
-  u32x4_t w = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kBufferRsrcWord3};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)w[i]);
-  return w;
-}
 
 struct Mx4GemmArgs {
   const uint8_t* a;         // codes [m][k/2]
@@ -177,7 +142,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
                                      : (uint32_t)(m0 * kStageBlocks) + wave * 512;
   auto copy = [&](uint32_t stage, int step) {
     // chunks past a row's end, and steps past the last, read past the buffer: zeros
-    const uint32_t at_lane = step * kStageBlocks + lane_chunk < q.kb ? lane_off : 0xFFFFFFF0u;
+    const uint32_t at_lane = step * kStageBlocks + lane_chunk < q.kb ? lane_off : kPastEnd;
     const uint32_t k_off = (uint32_t)step * kStageLine;
 #pragma unroll
     for (int c = 0; c < CA; ++c)
@@ -187,7 +152,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
       lds_copy16(rb, stage + kB + (wave * CB + c) * 1024, at_lane, pitch * 8 * (wave * CB + c) + k_off);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      lds_copy4(rss, stage + kSA + wave * 512 + c * 256, step < q.steps ? lane * 4 : 0xFFFFFFF0u,
+      lds_copy4(rss, stage + kSA + wave * 512 + c * 256, step < q.steps ? lane * 4 : kPastEnd,
                 s_off + (uint32_t)step * s_step + c * 256);
   };
 

@@ -1,36 +1,11 @@
 // exl3_mx4_linear and exl3_mx4_matmul: the kernels whose waves split k.
 #include "exl3_internal.hpp"
-#include "exl3_mx4_rows.hpp"
+#include "exl3_mx4_linear.hpp"
 
 namespace exl3 {
 
-struct Mx4RowsArgs {
-  const void* a;          // fp16 [m][lda], or codes [m][k/2]
-  const uint8_t* a_scales;
-  int64_t lda;            // elements (fp16 rows only)
-  const uint8_t* b;       // codes [n][k/2]
-  const uint8_t* b_scales;
-  const uint16_t* bias;
-  void* y;
-  int64_t ldy;
-  int64_t m, n;
-  int kb;                 // blocks of 32 in a row
-  int y_f32;
-  uint32_t col_tiles;     // tiles of 16 NG columns
-  int splits;             // workgroups that share a tile's k
-  float* part;            // their sums [split][m][n], where there are several
-};
-
 // Output tiles that fit the LDS of one combine round, at a kilobyte a wave.
 constexpr int kMx4CombineTiles = 64;
-
-__device__ __forceinline__ void mx4_store(const Mx4RowsArgs& q, int64_t row, int64_t col, float v) {
-  const float y = v + (q.bias ? h2f(q.bias[col]) : 0.f);
-  if (q.y_f32)
-    static_cast<float*>(q.y)[row * q.ldy + col] = y;
-  else
-    static_cast<uint16_t*>(q.y)[row * q.ldy + col] = f2h(y);
-}
 
 // 16 MG rows (A4: 4-bit, else fp16 in operands of P pieces, P = 1 unless
 // MG = 1), 16 NG columns, NW waves.
@@ -172,6 +147,10 @@ __global__ __launch_bounds__(256) void mx4_rows_finish(Mx4RowsArgs q) {
   mx4_store(q, row, i - row * q.n, v);
 }
 
+void launch_mx4_rows_finish(const Mx4RowsArgs& q, hipStream_t s) {
+  hipLaunchKernelGGL(mx4_rows_finish, dim3((uint32_t)((q.m * q.n + 255) / 256)), dim3(256), 0, s, q);
+}
+
 template <bool A4, int MG, int P, int NG, int NW>
 static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s) {
   q.col_tiles = (uint32_t)((q.n + 16 * NG - 1) / (16 * NG));
@@ -179,7 +158,7 @@ static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s
   q.splits = splits;
   q.part = static_cast<float*>(ws);
   hipLaunchKernelGGL((mx4_rows_kernel<A4, MG, P, NG, NW>), dim3(tiles * (uint32_t)splits), dim3(NW * 64), 0, s, q);
-  if (splits > 1) hipLaunchKernelGGL(mx4_rows_finish, dim3((uint32_t)((q.m * q.n + 255) / 256)), dim3(256), 0, s, q);
+  if (splits > 1) launch_mx4_rows_finish(q, s);
   return hipGetLastError();
 }
 
@@ -187,13 +166,16 @@ static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s
 // three copies):
 //   fp16 rows, few: pieces (see exl3_mx4_rows.hpp)
 //     5120 -> 17408, one row: P = 4 12.8, P = 2 13.1, P = 1 16
-//   more than 16 rows and few column tiles: k in three shares
-//     37 rows 17408 -> 5120: 33.9 against 42.8 in two and 54 unsplit
-static int linear_splits(int64_t m, int64_t n, int64_t k) {
-  return m > 32 && n * 3 <= 17408 * 3 && k >= 12 * kMx4UnitK ? 3 : 1;
+//   more than 16 rows: exl3_mx4_wide.hip, k in as many shares as fill the chip
+//   once (one workgroup a CU)
+static int wide_splits(int64_t n, int64_t k) {
+  const int64_t tiles = (n + 127) / 128, units = (k + kMx4UnitK - 1) / kMx4UnitK;
+  int64_t s = 256 / tiles;
+  if (s > units / 4) s = units / 4;
+  return s < 1 ? 1 : (int)s;
 }
 size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  const int s = linear_splits(m, n, k);
+  const int s = m > 16 ? wide_splits(n, k) : 1;
   return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
 }
 
@@ -205,10 +187,9 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
   if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, 1, ws, s);
   if (m <= 8) return wide ? launch_rows<false, 1, 2, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 2, 1, 8>(q, 1, ws, s);
   if (m <= 16) return wide ? launch_rows<false, 1, 1, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 1, 1, 8>(q, 1, ws, s);
-  if (m <= 32) return wide ? launch_rows<false, 2, 1, 2, 8>(q, 1, ws, s) : launch_rows<false, 2, 1, 1, 8>(q, 1, ws, s);
-  const int splits = linear_splits(m, n, k);
-  if (m <= 48) return launch_rows<false, 3, 1, 4, 4>(q, splits, ws, s);
-  return launch_rows<false, 4, 1, 4, 4>(q, splits, ws, s);
+  // rows too far apart for 32-bit offsets: 16 at a time
+  if (ldx > kMx4WideMaxStride) return launch_rows<false, 1, 1, 1, 8>(q, 1, ws, s);
+  return launch_mx4_wide(q, wide_splits(n, k), ws, s);
 }
 
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
