@@ -95,41 +95,60 @@ __device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int
 // least subnormal, to 6 * 2^(140 - 127) < 65504.
 constexpr uint32_t kMx4ScaleLow = 104, kMx4ScaleHigh = 140;
 
-// acc += x times the half h of a unit of 16 weight rows; x[mg][q] as loaded by
-// mx4_load_x, acc[mg][p] the sums of piece p (mod P).
-template <int MG, int P>
-__device__ __forceinline__ void mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h, int g,
-                                            float4_t (&acc)[MG][P]) {
-  constexpr int kPer = P < 4 ? P : 4;  // pieces of an operand in one half
+// Whether this lane's block of half h is exact in fp16, and the factor then; a
+// block of zeros is zero at any scale (but NaN).
+__device__ __forceinline__ bool mx4_plain_scale(const Mx4Unit& w, int h, int g, float& s) {
   const uint32_t own = mx4_own_scale(w, h, g) & 0xFFu;
   const u32x4_t d = w.half[h];
   bool plain = own - kMx4ScaleLow <= kMx4ScaleHigh - kMx4ScaleLow;
-  float s = __uint_as_float(own << 23);
+  s = __uint_as_float(own << 23);
   if (__builtin_expect(!__all(plain), 0)) {
-    // a block of zeros is zero at any scale (but NaN)
     if (!plain && own != 255u && ((d.x | d.y | d.z | d.w) & 0x77777777u) == 0) {
       plain = true;
       s = 1.0f;
     }
-    if (!__all(plain)) {
+  }
+  return plain;
+}
+
+// acc += x times the half h of a unit, block by block: the unscaled codes, then
+// the sums by the block's scale.  x[mg][q] as loaded by mx4_load_x, acc[mg][p] the
+// sums of piece p (mod P).
+template <int MG, int P>
+__device__ __forceinline__ void mx4_mma_f16_blocks(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h,
+                                                   int g, float4_t (&acc)[MG][P]) {
+  constexpr int kPer = P < 4 ? P : 4;  // pieces of an operand in one half
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        const float sb = mx4_scale((w.sc[h] >> (8 * b)) & 0xFFu);
-        const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;
+  for (int b = 0; b < 4; ++b) {
+    const float sb = mx4_scale((w.sc[h] >> (8 * b)) & 0xFFu);
+    const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f16x8_t c = mx4_to_f16(d[j] & keep);
+    for (int j = 0; j < 4; ++j) {
+      const f16x8_t c = mx4_to_f16(w.half[h][j] & keep);
 #pragma unroll
-          for (int mg = 0; mg < MG; ++mg) {
-            const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-            float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
+      for (int mg = 0; mg < MG; ++mg) {
+        const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], sb, a[i]);
-          }
-        }
+        for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], sb, a[i]);
       }
-      return;
     }
+  }
+}
+
+// acc += x times the half h of a unit of 16 weight rows.  A wave that cannot take
+// the scales into fp16 takes the blocks one by one and then zeros: a second path
+// to the end would cost the first one copies of its registers.
+template <int MG, int P>
+__device__ __forceinline__ void mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h, int g,
+                                            float4_t (&acc)[MG][P]) {
+  constexpr int kPer = P < 4 ? P : 4;
+  u32x4_t d = w.half[h];
+  float s;
+  if (__builtin_expect(!__all(mx4_plain_scale(w, h, g, s)), 0)) {
+    mx4_mma_f16_blocks<MG, P>(x, w, h, g, acc);
+    d = u32x4_t{0u, 0u, 0u, 0u};
+    s = 1.0f;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

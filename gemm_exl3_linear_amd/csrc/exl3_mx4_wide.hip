@@ -4,21 +4,26 @@
 // With so many rows the waves can no longer each fetch the rows for their share
 // of k (exl3_mx4_rows.hpp): a wave's 16 columns bring 2 KB of weights for 8 KB of
 // rows, and the load path, not the weights, bounds the time (37 rows, 17408 ->
-// 5120: 34 us).  Here four waves take 32 columns each and the same k, so a
-// workgroup fetches the rows once for 128 columns; what is left of k's length is
-// shared among workgroups, and their sums are added by mx4_rows_finish.
+// 5120: 34 us).  Here four pairs of waves take 32 columns each and the same k, so
+// a workgroup fetches the rows once for 128 columns; what is left of k's length
+// is shared among workgroups, and their sums are added by mx4_rows_finish.  The
+// waves of a pair take the two halves of a unit: one wave a SIMD would leave its
+// LDS reads, conversions and matrix instructions one after the other (25 us).
 //
 // A stage is 256 k of everything, copied from memory straight to LDS, kept in a
-// ring of three or four: a step waits for its own stage only, so that the bytes
-// of the others are in flight meanwhile.  The product is that of the few rows
-// (mx4_mma_f16).
+// ring of three or four: a step waits for the next stage only, so that the bytes
+// of the others are in flight meanwhile.  The waves run in step, so what a step
+// does one after the other leaves the rest of the CU idle (copies 500 cycles, LDS
+// reads 900, product 1000, of 3000): a quarter of the product is followed by a
+// quarter of the copies and by the reads of the next stage into the registers
+// that it has freed.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_lds.hpp"
 #include "exl3_mx4_linear.hpp"
 
 namespace exl3 {
 
-constexpr int kWideWaves = 4, kWideCols = 128, kWideNI = kWideCols / kWideWaves / 16;
+constexpr int kWideWaves = 8, kWideCols = 128, kWideNI = 2;
 constexpr int kWideLine = kMx4UnitK * 2;  // bytes of a row of x in a stage
 
 template <int MG>
@@ -28,12 +33,12 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   constexpr uint32_t kX = 0, kB = kX + MG * 16 * kWideLine, kS = kB + kWideCols * kMx4UnitBytes,
                      kBytes = kS + kWideCols * 16;
   constexpr int kStages = 160 * 1024 / kBytes < 4 ? 160 * 1024 / kBytes : 4;
-  constexpr int kAhead = kStages - 1;
   constexpr int CX = MG * 8 / kWideWaves, CB = kWideCols / 8 / kWideWaves, kCopies = CX + CB + 1;  // a wave's, a stage
   __shared__ __align__(128) uint8_t smem[kStages * kBytes];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
+  const int h = wave >> 2, cols = (wave & 3) * 32;  // half of a unit, columns of the tile
   const uint32_t tile = blockIdx.x / (uint32_t)q.splits, split = blockIdx.x - tile * (uint32_t)q.splits;
   const int64_t n0 = (int64_t)tile * kWideCols;
   const int kb = q.kb;
@@ -42,31 +47,49 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   const int begin = (int)((int64_t)units * split / q.splits), end = (int)((int64_t)units * (split + 1) / q.splits);
 
   // x: two rows an instruction; chunk c of row i at place c ^ (i & 3), so that
-  // the lanes a 16-byte read serves together fall on different banks
+  // the lanes a 16-byte read serves together fall on different banks.  Rows past
+  // the last lie past the buffers' ends and read as zeros.
   const int64_t left = q.n - n0 < kWideCols ? q.n - n0 : kWideCols;
   const u32x4_t rx = buffer_words(static_cast<const uint8_t*>(q.a), (uint64_t)(q.m - 1) * xpitch + (uint64_t)kb * 64);
   const u32x4_t rb = buffer_words(q.b + n0 * pitch, (uint64_t)left * pitch);
   const u32x4_t rs = buffer_words(q.b_scales + ((n0 * kb) & ~(int64_t)3), ((uint64_t)left * kb + (n0 * kb & 3) + 3) & ~3ull);
-  // the row of the c-th instruction is 2 (CX wave + c) + lane / 32: its chunks'
-  // order alternates with the parity of CX wave + c
+  // a lane's chunk in this wave's even and odd instructions: pair CX wave + i
+  const uint32_t turn = 2 * ((CX * wave) & 1) + (lane >> 5);
+  const uint32_t x_chunk[2] = {(uint32_t)(lane & 31) ^ turn, (uint32_t)(lane & 31) ^ turn ^ 2u};
+  const uint32_t x_off[2] = {xpitch * (lane >> 5) + 16 * x_chunk[0], xpitch * (lane >> 5) + 16 * x_chunk[1]};
   const uint32_t b_chunk = (lane & 7) ^ ((lane >> 3) & 7), b_off = pitch * (lane >> 3) + 16 * b_chunk;
-  const uint32_t s_row = (uint32_t)(n0 * kb & 3) + (uint32_t)(wave * 32 + (lane & 31)) * kb;  // byte of its first scale
-  auto copy = [&](uint32_t stage, int u, bool there) {
+  const uint32_t s_off = ((uint32_t)(n0 * kb & 3) + (uint32_t)(wave * 16 + r) * kb) & ~3u;  // dword of its first scale
+  // Copies of unit u, in quarters (0 .. 3; the scales in the last); none of a
+  // unit past the end: zeros, from a buffer without bytes.
+  struct Copy {
+    u32x4_t rx, rb, rs;
+    uint32_t x[2], b;
+    int u;
+  };
+  auto plan = [&](int u) {
+    Copy c{rx, rb, rs, {0u, 0u}, 0u, u};
+    if (u >= end) c.rx.z = c.rb.z = c.rs.z = 0u;
+    const int left = kb - u * kMx4UnitBlocks;  // chunks past a row's end: zeros
 #pragma unroll
-    for (int c = 0; c < CX; ++c) {
-      const int pair = wave * CX + c, row = 2 * pair + (lane >> 5);
-      const uint32_t chunk = (lane & 31) ^ (row & 3);
-      const bool in = there && u * kMx4UnitBlocks + (int)(chunk >> 2) < kb && row < q.m;
-      lds_copy16(rx, stage + kX + pair * 1024, in ? xpitch * (lane >> 5) + 16 * chunk : kPastEnd,
-                 xpitch * 2 * pair + (uint32_t)u * kWideLine);
-    }
-    const bool in = there && u * kMx4UnitBlocks + (int)b_chunk < kb;
+    for (int p = 0; p < 2; ++p) c.x[p] = (int)(x_chunk[p] >> 2) < left ? x_off[p] : kPastEnd;
+    c.b = (int)b_chunk < left ? b_off : kPastEnd;
+    return c;
+  };
+  auto copy = [&](const Copy& c, int part, uint32_t stage) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-      lds_copy16(rb, stage + kB + (wave * CB + c) * 1024, in ? b_off : kPastEnd,
-                 pitch * 8 * (wave * CB + c) + (uint32_t)u * kMx4UnitBytes);
-    if (lane < 32)
-      lds_copy16(rs, stage + kS + wave * 32 * 16, there ? s_row & ~3u : kPastEnd, (uint32_t)u * kMx4UnitBlocks);
+    for (int i = 0; i < CX; ++i)
+      if (i % 4 == part) {
+        const int pair = wave * CX + i;
+        lds_copy16(c.rx, stage + kX + pair * 1024, c.x[i & 1],
+                   xpitch * 2 * pair + (uint32_t)c.u * kWideLine);
+      }
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+      if ((CX + i) % 4 == part)
+        lds_copy16(c.rb, stage + kB + (wave * CB + i) * 1024, c.b,
+                   pitch * 8 * (wave * CB + i) + (uint32_t)c.u * kMx4UnitBytes);
+    if (part == 3 && lane < 16)
+      lds_copy16(c.rs, stage + kS + wave * 16 * 16, s_off, (uint32_t)c.u * kMx4UnitBlocks);
   };
 
   float4_t acc[kWideNI][MG][1];
@@ -74,55 +97,94 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   for (int ni = 0; ni < kWideNI; ++ni)
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg) acc[ni][mg][0] = float4_t{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](uint32_t stage, int u) {
-    Mx4Unit w[kWideNI];
+  Mx4Unit w[kWideNI], wn[kWideNI];
+  f16x8_t x[MG][4];
+  auto read_w = [&](Mx4Unit (&t)[kWideNI], uint32_t stage, int u) {
 #pragma unroll
     for (int ni = 0; ni < kWideNI; ++ni) {
-      const int row = wave * 32 + 16 * ni + r;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[ni].half[h] = lds_read16(stage + kB + row * kMx4UnitBytes + (((4 * h + g) ^ (r & 7)) * 16));
+      const int row = cols + 16 * ni + r;
+      t[ni].half[0] = lds_read16(stage + kB + row * kMx4UnitBytes + (((4 * h + g) ^ (r & 7)) * 16));
+      // scale bytes 4 h .. 4 h + 3, of three dwords that hold all eight
       const uint32_t shift = ((uint32_t)(n0 * kb & 3) + (uint32_t)row * kb) & 3u;
-      const u32x4_t d = lds_read16(stage + kS + row * 16);
-      w[ni].sc[0] = __builtin_amdgcn_alignbyte(d.y, d.x, shift);
-      w[ni].sc[1] = __builtin_amdgcn_alignbyte(d.z, d.y, shift);
+      const u32x2_t d = lds_read8(stage + kS + row * 16 + 4 * h);
+      t[ni].sc[0] = __builtin_amdgcn_alignbyte(d.y, d.x, shift);
       if ((u + 1) * kMx4UnitBlocks > kb) {  // what follows a row's end is the next row's
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-          if (u * kMx4UnitBlocks + b >= kb)
-            w[ni].sc[b / 4] = (w[ni].sc[b / 4] & ~(0xFFu << (8 * (b % 4)))) | (kMx4One << (8 * (b % 4)));
+        for (int b = 0; b < 4; ++b)
+          if (u * kMx4UnitBlocks + 4 * h + b >= kb)
+            t[ni].sc[0] = (t[ni].sc[0] & ~(0xFFu << (8 * b))) | (kMx4One << (8 * b));
       }
     }
+  };
+  auto read_x = [&](int j, uint32_t stage) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f16x8_t x[MG][4];
-#pragma unroll
-      for (int mg = 0; mg < MG; ++mg)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[mg][j] = __builtin_bit_cast(
-              f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine + (((4 * (4 * h + g) + j) ^ (r & 3)) * 16)));
-#pragma unroll
-      for (int ni = 0; ni < kWideNI; ++ni) mx4_mma_f16<MG, 1>(x, w[ni], h, g, acc[ni]);
-    }
+    for (int mg = 0; mg < MG; ++mg)
+      x[mg][j] = __builtin_bit_cast(
+          f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine + (((4 * (4 * h + g) + j) ^ (r & 3)) * 16)));
   };
 
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) copy(lds0 + s * kBytes, begin + s, begin + s < end);
-  uint32_t stage = 0;
-  for (int u = begin; u < end; ++u) {
-    // this wave's copies of the stage are in (those of kAhead - 1 later ones may
-    // not be) and its reads of the stage before are done; then everybody's
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kCopies * (kAhead - 1)) : "memory");
-    copy(lds0 + (stage == 0 ? kAhead * kBytes : stage - kBytes), u + kAhead, u + kAhead < end);
-    multiply(lds0 + stage, u);
-    stage = stage == kAhead * kBytes ? 0 : stage + kBytes;
+  for (int s = 0; s < kStages; ++s) {
+    const Copy c = plan(begin + s);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) copy(c, p, lds0 + s * kBytes);
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the workgroup's LDS
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kCopies * (kStages - 1)) : "memory");
+  read_w(w, lds0, begin);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) read_x(j, lds0);
+  uint32_t stage = lds0;  // of unit u
+  for (int u = begin; u < end; ++u) {
+    // this wave's copies of the next stage are in (those of kStages - 2 later
+    // ones may not be) and its reads of stage u are done; then everybody's
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kCopies * (kStages - 2)) : "memory");
+    const uint32_t next = stage == lds0 + (kStages - 1) * kBytes ? lds0 : stage + kBytes;
+    const Copy c = plan(u + kStages);
+    float s[kWideNI];
+    bool plain = true;
+#pragma unroll
+    for (int ni = 0; ni < kWideNI; ++ni) plain = mx4_plain_scale(w[ni], 0, g, s[ni]) && plain;
+    if (__builtin_expect(!__all(plain), 0)) {
+#pragma unroll
+      for (int ni = 0; ni < kWideNI; ++ni) {
+        mx4_mma_f16_blocks<MG, 1>(x, w[ni], 0, g, acc[ni]);
+        w[ni].half[0] = u32x4_t{0u, 0u, 0u, 0u};
+        s[ni] = 1.0f;
+      }
+    }
+    read_w(wn, next, u + 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int ni = 0; ni < kWideNI; ++ni) {
+        const f16x8_t v = mx4_to_f16(w[ni].half[0][j], s[ni]);
+#pragma unroll
+        for (int mg = 0; mg < MG; ++mg)
+          acc[ni][mg][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j], v, acc[ni][mg][0], 0, 0, 0);
+      }
+      copy(c, j, stage);
+      read_x(j, next);
+    }
+#pragma unroll
+    for (int ni = 0; ni < kWideNI; ++ni) w[ni] = wn[ni];
+    stage = next;
+  }
 
+  // the second half's sums to the waves of the first, through LDS
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  float4_t* sums = reinterpret_cast<float4_t*>(smem) + (wave & 3) * (kWideNI * MG * 64) + lane;
+  static_assert(4 * kWideNI * MG * 1024 <= kStages * kBytes, "the sums fit");
+  if (h == 1) {
+#pragma unroll
+    for (int i = 0; i < kWideNI * MG; ++i) sums[i * 64] = acc[i / MG][i % MG][0];
+  }
+  __syncthreads();
+  if (h == 1) return;
+#pragma unroll
+  for (int i = 0; i < kWideNI * MG; ++i) acc[i / MG][i % MG][0] += sums[i * 64];
 #pragma unroll
   for (int ni = 0; ni < kWideNI; ++ni) {
-    const int64_t col = n0 + wave * 32 + 16 * ni + r;
+    const int64_t col = n0 + cols + 16 * ni + r;
     if (col >= q.n) continue;
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg)
