@@ -26,6 +26,11 @@ namespace exl3 {
 constexpr int kWideWaves = 8, kWideCols = 128, kWideNI = 2;
 constexpr int kWideLine = kMx4UnitK * 2;  // bytes of a row of x in a stage
 
+// What the places of a row's chunks in LDS are turned by: a 16-byte read of one
+// chunk of eight rows and the next but three of the same rows then falls on 16
+// different places of 256 bytes.
+__device__ __forceinline__ uint32_t wide_turn(int row) { return (uint32_t)((row & 3) | ((row & 4) << 1)); }
+
 template <int MG>
 __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q) {
   // a stage: rows of x, lines of codes, and of each weight row four dwords, the
@@ -46,32 +51,34 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   const int begin = (int)((int64_t)units * split / q.splits), end = (int)((int64_t)units * (split + 1) / q.splits);
 
-  // x: two rows an instruction; chunk c of row i at place c ^ (i & 3), so that
-  // the lanes a 16-byte read serves together fall on different banks.  Rows past
-  // the last lie past the buffers' ends and read as zeros.
+  // x: two rows an instruction; chunk c of row i at place c ^ wide_turn(i).  Rows
+  // past the last lie past the buffers' ends and read as zeros.
   const int64_t left = q.n - n0 < kWideCols ? q.n - n0 : kWideCols;
   const u32x4_t rx = buffer_words(static_cast<const uint8_t*>(q.a), (uint64_t)(q.m - 1) * xpitch + (uint64_t)kb * 64);
   const u32x4_t rb = buffer_words(q.b + n0 * pitch, (uint64_t)left * pitch);
   const u32x4_t rs = buffer_words(q.b_scales + ((n0 * kb) & ~(int64_t)3), ((uint64_t)left * kb + (n0 * kb & 3) + 3) & ~3ull);
-  // a lane's chunk in this wave's even and odd instructions: pair CX wave + i
-  const uint32_t turn = 2 * ((CX * wave) & 1) + (lane >> 5);
-  const uint32_t x_chunk[2] = {(uint32_t)(lane & 31) ^ turn, (uint32_t)(lane & 31) ^ turn ^ 2u};
-  const uint32_t x_off[2] = {xpitch * (lane >> 5) + 16 * x_chunk[0], xpitch * (lane >> 5) + 16 * x_chunk[1]};
+  constexpr int kTurns = CX < 4 ? CX : 4;  // the turn of row 2 (CX wave + i) + lane / 32 repeats after four i
+  uint32_t x_chunk[kTurns], x_off[kTurns];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    x_chunk[i] = (uint32_t)(lane & 31) ^ wide_turn(2 * (CX * wave + i) + (lane >> 5));
+    x_off[i] = xpitch * (lane >> 5) + 16 * x_chunk[i];
+  }
   const uint32_t b_chunk = (lane & 7) ^ ((lane >> 3) & 7), b_off = pitch * (lane >> 3) + 16 * b_chunk;
   const uint32_t s_off = ((uint32_t)(n0 * kb & 3) + (uint32_t)(wave * 16 + r) * kb) & ~3u;  // dword of its first scale
   // Copies of unit u, in quarters (0 .. 3; the scales in the last); none of a
   // unit past the end: zeros, from a buffer without bytes.
   struct Copy {
     u32x4_t rx, rb, rs;
-    uint32_t x[2], b;
+    uint32_t x[kTurns], b;
     int u;
   };
   auto plan = [&](int u) {
-    Copy c{rx, rb, rs, {0u, 0u}, 0u, u};
+    Copy c{rx, rb, rs, {}, 0u, u};
     if (u >= end) c.rx.z = c.rb.z = c.rs.z = 0u;
     const int left = kb - u * kMx4UnitBlocks;  // chunks past a row's end: zeros
 #pragma unroll
-    for (int p = 0; p < 2; ++p) c.x[p] = (int)(x_chunk[p] >> 2) < left ? x_off[p] : kPastEnd;
+    for (int p = 0; p < kTurns; ++p) c.x[p] = (int)(x_chunk[p] >> 2) < left ? x_off[p] : kPastEnd;
     c.b = (int)b_chunk < left ? b_off : kPastEnd;
     return c;
   };
@@ -80,7 +87,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
     for (int i = 0; i < CX; ++i)
       if (i % 4 == part) {
         const int pair = wave * CX + i;
-        lds_copy16(c.rx, stage + kX + pair * 1024, c.x[i & 1],
+        lds_copy16(c.rx, stage + kX + pair * 1024, c.x[i % 4],
                    xpitch * 2 * pair + (uint32_t)c.u * kWideLine);
       }
 #pragma unroll
@@ -120,7 +127,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg)
       x[mg][j] = __builtin_bit_cast(
-          f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine + (((4 * (4 * h + g) + j) ^ (r & 3)) * 16)));
+          f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine + ((uint32_t)(4 * (4 * h + g) + j) ^ wide_turn(r)) * 16));
   };
 
 #pragma unroll
