@@ -321,11 +321,7 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
                      StageScales{b_scales, reinterpret_cast<uint32_t*>(sb), n, gb}, kb, steps);
   const int wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && ldy % (y_f32 ? 4 : 8) == 0;
   const Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, bias, y, ldy, m, n, kb, steps, y_f32, wide, 0, 0};
-#ifdef SMALL_TILE
-  launch_gemm_tiles<128, 128, 2, 2>(q, s);
-#else
   launch_gemm_tiles<256, 256, 2, 4>(q, s);
-#endif
   return hipGetLastError();
 }
 

@@ -80,17 +80,18 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
         for (int i = 0; i < kLoads; ++i)
           x[mg][i] = mx4_load_x<P>(xr[mg], there[mg], kb, u, h, g, r, i);
     };
+    bool exact = true;
     for (int u = first; u < units; u += stride) {
       Mx4Unit w[NG];
       f16x8_t x[2][MG][kLoads];
       load_w(w, u);
       load_x(x[0], 0, u);
-      if constexpr (P < 8) load_x(x[1], 1, u);
+      load_x(x[1], 1, u);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng) mx4_mma_f16<MG, P>(x[P < 8 ? h : 0], w[ng], h, g, acc[ng]);
+      for (int h = 0; h < 2; ++h) exact = mx4_mma_f16<MG, P, NG>(x[h], w, h, g, acc) && exact;
     }
+    if (__builtin_expect(!__all(exact), 0))
+      mx4_sum_blocks<MG, P, NG>(xr, there, rb, kb, first, units, stride, 0, 2, g, r, acc);
   }
 
   // Sum over the waves in wave order, R output tiles a round.  Lane l of a 16 x
@@ -171,7 +172,7 @@ static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s
 static int wide_splits(int64_t n, int64_t k) {
   const int64_t tiles = (n + 127) / 128, units = (k + kMx4UnitK - 1) / kMx4UnitK;
   int64_t s = 256 / tiles;
-  if (s > units / 4) s = units / 4;
+  if (s > units / 2) s = units / 2;
   return s < 1 ? 1 : (int)s;
 }
 size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {

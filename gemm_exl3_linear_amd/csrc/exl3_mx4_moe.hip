@@ -328,13 +328,14 @@ __global__ __launch_bounds__(NW * 64) void mx4_moe_router(MoeArgs q) {
 // ---------------------------------------------------------------------------
 // gate and up
 // ---------------------------------------------------------------------------
-// v as three bf16 pieces by truncation; their sum is v (24 significant bits).
+// v as three bf16 pieces by truncation; their sum is v (24 significant bits; an
+// infinity or a NaN is all in the first).
 __device__ __forceinline__ void split_bf16(float v, uint16_t (&p)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const uint32_t b = __float_as_uint(v) & 0xFFFF0000u;
     p[i] = (uint16_t)(b >> 16);
-    v -= __uint_as_float(b);
+    v = __builtin_isfinite(v) ? v - __uint_as_float(b) : 0.f;
   }
 }
 
@@ -363,22 +364,25 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
   const int i = r % Mx4X<P>::kRows;
   const bool there = i < en.count;
   const uint16_t* x = q.x + (there ? en.token(i) : 0) * q.ldx;
-  float4_t acc[1][P];
+  float4_t acc[1][1][P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) acc[0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < P; ++p) acc[0][0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
+  bool exact = true;
   for (int u = first; u < units; u += kMoeGateUpShares) {
-    Mx4Unit w;
-    mx4_load_unit(row, kb, u, g, w);
+    Mx4Unit w[1];
+    mx4_load_unit(row, kb, u, g, w[0]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f16x8_t f[1][kLoads];
 #pragma unroll
       for (int l = 0; l < kLoads; ++l) f[0][l] = mx4_load_x<P>(x, there, kb, u, h, g, r, l);
-      mx4_mma_f16<1, P>(f, w, h, g, acc);
+      exact = mx4_mma_f16<1, P, 1>(f, w, h, g, acc) && exact;
     }
   }
-  return mx4_pick<P>(acc[0], g);
+  if (__builtin_expect(!__all(exact), 0))
+    mx4_sum_blocks<1, P, 1>({x}, {there}, {row}, kb, first, units, kMoeGateUpShares, 0, 2, g, r, acc);
+  return mx4_pick<P>(acc[0][0], g);
 }
 
 __global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeArgs q) {

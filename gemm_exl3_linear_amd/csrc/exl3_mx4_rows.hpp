@@ -72,22 +72,21 @@ __device__ __forceinline__ void mx4_load_unit(const Mx4Row& row, int kb, int u, 
 // Scale byte of block g of half h, in the low byte.
 __device__ __forceinline__ uint32_t mx4_own_scale(const Mx4Unit& t, int h, int g) { return t.sc[h] >> (8 * g); }
 
-// Operand rows of fp16 activations: P pieces of 16 / P rows.
+// Operand rows of fp16 activations: P pieces (1, 2 or 4) of 16 / P rows.
 template <int P>
 struct Mx4X {
-  static constexpr int kRows = 16 / P;            // rows of x
-  static constexpr int kLoads = P >= 4 ? 1 : 4 / P;  // operands of one 128-k half (P = 8: of a whole unit)
+  static constexpr int kRows = 16 / P;  // rows of x
+  static constexpr int kLoads = 4 / P;  // operands of one 128-k half
 };
 
-// Operand `q` of half h of unit u: lane (r, g) holds 8 elements of block 4 h + g
-// (P = 8: of both halves), piece q P + r / kRows, of row r % kRows; zeros past
-// the row's end or where the row is not there.  x: this lane's row.
+// Operand `q` of half h of unit u: lane (r, g) holds 8 elements of block 4 h + g,
+// piece q P + r / kRows, of row r % kRows; zeros past the row's end or where the
+// row is not there.  x: this lane's row.
 template <int P>
 __device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g, int r, int q) {
-  const int piece = q * P + r / Mx4X<P>::kRows;  // 0 .. 3, or 0 .. 7 over two halves
-  const int b = u * kMx4UnitBlocks + 4 * (P == 8 ? piece >> 2 : h) + g;
+  const int b = u * kMx4UnitBlocks + 4 * h + g;
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * (piece & 3));
+  if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * (q * P + r / Mx4X<P>::kRows));
   return __builtin_bit_cast(f16x8_t, v);
 }
 
@@ -95,68 +94,95 @@ __device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int
 // least subnormal, to 6 * 2^(140 - 127) < 65504.
 constexpr uint32_t kMx4ScaleLow = 104, kMx4ScaleHigh = 140;
 
-// Whether this lane's block of half h is exact in fp16, and the factor then; a
-// block of zeros is zero at any scale (but NaN).
-__device__ __forceinline__ bool mx4_plain_scale(const Mx4Unit& w, int h, int g, float& s) {
+// Whether this lane's block of half h is exact in fp16, and the factor then.
+__device__ __forceinline__ bool mx4_fp16_scale(const Mx4Unit& w, int h, int g, float& s) {
   const uint32_t own = mx4_own_scale(w, h, g) & 0xFFu;
   const u32x4_t d = w.half[h];
-  bool plain = own - kMx4ScaleLow <= kMx4ScaleHigh - kMx4ScaleLow;
-  s = __uint_as_float(own << 23);
-  if (__builtin_expect(!__all(plain), 0)) {
-    if (!plain && own != 255u && ((d.x | d.y | d.z | d.w) & 0x77777777u) == 0) {
-      plain = true;
-      s = 1.0f;
-    }
-  }
-  return plain;
+  const bool zero = ((d.x | d.y | d.z | d.w) & 0x77777777u) == 0;
+  const bool exact = own - kMx4ScaleLow <= kMx4ScaleHigh - kMx4ScaleLow;
+  s = exact ? __uint_as_float(own << 23) : 1.0f;
+  return exact || (zero && own != 255u);
 }
 
-// acc += x times the half h of a unit, block by block: the unscaled codes, then
-// the sums by the block's scale.  x[mg][q] as loaded by mx4_load_x, acc[mg][p] the
-// sums of piece p (mod P).
-template <int MG, int P>
-__device__ __forceinline__ void mx4_mma_f16_blocks(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h,
-                                                   int g, float4_t (&acc)[MG][P]) {
-  constexpr int kPer = P < 4 ? P : 4;  // pieces of an operand in one half
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    const float sb = mx4_scale((w.sc[h] >> (8 * b)) & 0xFFu);
-    const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;
+// acc += x times the half h of a unit of NG x 16 weight rows; false where this
+// lane's blocks are not all exact in fp16, and what was added is of no use.  (A
+// block of zeros is, at any scale but NaN.)
+template <int MG, int P, int NG>
+__device__ __forceinline__ bool mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG], int h, int g,
+                                            float4_t (&acc)[NG][MG][P]) {
+  bool exact = true;
+#pragma unroll
+  for (int ng = 0; ng < NG; ++ng) {
+    float s;
+    exact = mx4_fp16_scale(w[ng], h, g, s) && exact;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const f16x8_t c = mx4_to_f16(w.half[h][j] & keep);
+      const f16x8_t c = mx4_to_f16(w[ng].half[h][j], s);
 #pragma unroll
-      for (int mg = 0; mg < MG; ++mg) {
-        const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
+      for (int mg = 0; mg < MG; ++mg)
+        acc[ng][mg][j % P] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / P], c, acc[ng][mg][j % P], 0, 0, 0);
+    }
+  }
+  return exact;
+}
+
+// acc += the same, whatever the scales: block by block the unscaled codes, then
+// the sums by the block's scale.  The other blocks are taken out of both operands:
+// an infinite x times their zeros would be NaN.
+template <int MG, int P, int NG>
+__device__ __forceinline__ void mx4_mma_f16_blocks(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG], int h,
+                                                   int g, float4_t (&acc)[NG][MG][P]) {
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], sb, a[i]);
+    for (int ng = 0; ng < NG; ++ng) {
+      const float sb = mx4_scale((w[ng].sc[h] >> (8 * b)) & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f16x8_t c = mx4_to_f16(w[ng].half[h][j] & keep);
+#pragma unroll
+        for (int mg = 0; mg < MG; ++mg) {
+          const u32x4_t xb = __builtin_bit_cast(u32x4_t, x[mg][j / P]) & keep;
+          const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xb), c,
+                                                                    float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          float4_t& a = acc[ng][mg][j % P];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(v[i], sb, a[i]);
+        }
       }
     }
   }
 }
 
-// acc += x times the half h of a unit of 16 weight rows.  A wave that cannot take
-// the scales into fp16 takes the blocks one by one and then zeros: a second path
-// to the end would cost the first one copies of its registers.
-template <int MG, int P>
-__device__ __forceinline__ void mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit& w, int h, int g,
-                                            float4_t (&acc)[MG][P]) {
-  constexpr int kPer = P < 4 ? P : 4;
-  u32x4_t d = w.half[h];
-  float s;
-  if (__builtin_expect(!__all(mx4_plain_scale(w, h, g, s)), 0)) {
-    mx4_mma_f16_blocks<MG, P>(x, w, h, g, acc);
-    d = u32x4_t{0u, 0u, 0u, 0u};
-    s = 1.0f;
-  }
+// acc = the sums over every `stride`th unit of [first, end) and its halves
+// [h0, h1) by that second way, from memory again.  A wave that met a scale
+// outside fp16 takes its whole share so: a choice inside the loop cost the common
+// case 5 to 10 % (5120 -> 17408, one row: 15.3 us against 14.5).
+template <int MG, int P, int NG>
+__device__ __forceinline__ void mx4_sum_blocks(const uint16_t* const (&x)[MG], const bool (&there)[MG],
+                                               const Mx4Row (&rows)[NG], int kb, int first, int end, int stride, int h0,
+                                               int h1, int g, int r, float4_t (&acc)[NG][MG][P]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const f16x8_t c = mx4_to_f16(d[j], s);
+  for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-    for (int mg = 0; mg < MG; ++mg) {
-      float4_t& a = acc[mg][P == 8 ? 4 * h + j : j % P];
-      a = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[mg][j / kPer], c, a, 0, 0, 0);
+    for (int mg = 0; mg < MG; ++mg)
+#pragma unroll
+      for (int p = 0; p < P; ++p) acc[ng][mg][p] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int u = first; u < end; u += stride) {
+    Mx4Unit w[NG];
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) mx4_load_unit(rows[ng], kb, u, g, w[ng]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h < h0 || h >= h1) continue;
+      f16x8_t f[MG][Mx4X<P>::kLoads];
+#pragma unroll
+      for (int mg = 0; mg < MG; ++mg)
+#pragma unroll
+        for (int i = 0; i < Mx4X<P>::kLoads; ++i) f[mg][i] = mx4_load_x<P>(x[mg], there[mg], kb, u, h, g, r, i);
+      mx4_mma_f16_blocks<MG, P, NG>(f, w, h, g, acc);
     }
   }
 }

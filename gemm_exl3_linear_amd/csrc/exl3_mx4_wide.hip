@@ -141,6 +141,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
 #pragma unroll
   for (int j = 0; j < 4; ++j) read_x(j, lds0);
   uint32_t stage = lds0;  // of unit u
+  bool exact = true;      // every scale in fp16
   for (int u = begin; u < end; ++u) {
     // this wave's copies of the next stage are in (those of kStages - 2 later
     // ones may not be) and its reads of stage u are done; then everybody's
@@ -148,17 +149,8 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
     const uint32_t next = stage == lds0 + (kStages - 1) * kBytes ? lds0 : stage + kBytes;
     const Copy c = plan(u + kStages);
     float s[kWideNI];
-    bool plain = true;
 #pragma unroll
-    for (int ni = 0; ni < kWideNI; ++ni) plain = mx4_plain_scale(w[ni], 0, g, s[ni]) && plain;
-    if (__builtin_expect(!__all(plain), 0)) {
-#pragma unroll
-      for (int ni = 0; ni < kWideNI; ++ni) {
-        mx4_mma_f16_blocks<MG, 1>(x, w[ni], 0, g, acc[ni]);
-        w[ni].half[0] = u32x4_t{0u, 0u, 0u, 0u};
-        s[ni] = 1.0f;
-      }
-    }
+    for (int ni = 0; ni < kWideNI; ++ni) exact = mx4_fp16_scale(w[ni], 0, g, s[ni]) && exact;
     read_w(wn, next, u + 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -175,6 +167,23 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
 #pragma unroll
     for (int ni = 0; ni < kWideNI; ++ni) w[ni] = wn[ni];
     stage = next;
+  }
+
+  if (__builtin_expect(!__all(exact), 0)) {
+    const uint16_t* xr[MG];
+    bool there[MG];
+    Mx4Row rows[kWideNI];
+#pragma unroll
+    for (int mg = 0; mg < MG; ++mg) {
+      there[mg] = 16 * mg + r < q.m;
+      xr[mg] = static_cast<const uint16_t*>(q.a) + (there[mg] ? 16 * mg + r : 0) * q.lda;
+    }
+#pragma unroll
+    for (int ni = 0; ni < kWideNI; ++ni) {
+      const int row = cols + 16 * ni + r;
+      rows[ni] = mx4_row(q.b, q.b_scales, n0, row < left ? row : (uint32_t)(left - 1), kb);
+    }
+    mx4_sum_blocks<MG, 1, kWideNI>(xr, there, rows, kb, begin, end, 1, h, h + 1, g, r, acc);
   }
 
   // the second half's sums to the waves of the first, through LDS

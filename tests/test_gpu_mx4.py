@@ -558,3 +558,65 @@ def test_two_streams_with_their_own_workspaces():
     for rs, rr in zip(runs, refs):
         for (_, outs), ref in zip(rs, rr):
             assert all(torch.equal(o, r) for o, r in zip(outs, ref))
+
+
+# ---------------------------------------------------------------------------
+# scales outside fp16 next to infinities
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("m,n", [(1, 40), (4, 2064), (7, 40), (8, 2064), (12, 40), (16, 2064), (20, 140), (40, 140), (64, 140)])
+def test_linear_infinity_next_to_far_scales(m, n):
+    # every code is 1.0 (and x positive), so an infinite x gives an infinity
+    # whatever the scales of its block and of the others
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(15)
+    codes = np.full((n, 160), 0x22, dtype=np.uint8)
+    scales = rng.integers(110, 130, (n, 10)).astype(np.uint8)
+    scales[: n // 2, 2] = 160
+    scales[n // 3:, 7] = 60
+    x = np.abs(rng.standard_normal((m, 320))).astype(np.float16)
+    x[0, 70] = x[m // 2, 239] = x[m - 1, 5] = np.inf
+    y = X.exl3_mx4_linear(G.to_dev(x), mx((codes, scales)), out_dtype=torch.float32).cpu().numpy()
+    rows = np.unique([0, m // 2, m - 1])
+    assert np.isposinf(y[rows]).all()
+    rest = np.delete(np.arange(m), rows)
+    ref, mag = M.product(x[rest], M.decode(codes, scales))
+    assert_within(y[rest], ref, bound(ref, mag, 320, True))
+
+
+@pytest.mark.parametrize("t", [1, 3, 6, 16])
+def test_moe_activations_past_fp32(t):
+    # silu(g) u passes fp32's range for token 0 only, and stays an infinity
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = moe_case(41, t, 3, 64, 64)
+    for k, s in (("gate_up", 190), ("down", 127)):
+        l[k][0][:] = 0x22
+        l[k][1][:] = s
+    x[:] = 0
+    x[0] = 1
+    y = X.exl3_mx4_moe(G.to_dev(x), moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
+    assert np.isposinf(y[0]).all() and (y[1:] == 0).all()
+
+
+@pytest.mark.parametrize("t", [1, 5, 6, 16])
+def test_moe_any_scale_byte(t):
+    # gate and up blocks on either side of fp16's range, a NaN block of one
+    # expert, far and NaN scales of down
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = moe_case(43, t, 4, 288, 96, si=64)
+    x = (x * np.float16(2.0 ** -3)).astype(np.float16)
+    gs, ds = l["gate_up"][1], l["down"][1]
+    gs[1, :, 5] = 90
+    gs[2, 0, 7, 3], gs[2, 1, 7, 3] = 150, 95
+    x[:, 96:128] = 0  # the block of scale 150
+    ds[0, 0, 3], ds[0, 0, 4] = 60, 190
+    gs[3, 0, 9, 8] = ds[3, 0, 11, 1] = 255
+    y = X.exl3_mx4_moe(G.to_dev(x), moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
+    ref, ids, w = M.moe(x, l, 2)
+    clean = dict(l)
+    for name in ("gate_up", "down"):
+        clean[name] = (l[name][0], np.where(l[name][1] == 255, 127, l[name][1]))
+    lim = moe_limit(x, clean, 2, ref, w, True)
+    assert_within(y, ref, lim)
