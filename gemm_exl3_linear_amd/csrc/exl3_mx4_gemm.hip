@@ -6,7 +6,7 @@
 // copied straight from memory to LDS while the other stage is multiplied.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_lds.hpp"
-#include "exl3_mx4_rows.hpp"
+#include "exl3_mx4_linear.hpp"
 
 namespace exl3 {
 
@@ -36,6 +36,7 @@ struct Mx4GemmArgs {
   int y_f32;
   int wide;                 // 16-byte stores of y fit its alignment
   uint32_t tiles_m, tiles_n;
+  int splits;               // workgroups that share a tile's steps: y is [split][m][n] then
 };
 
 // Scales as the matrix instructions take them: per step and group of 64 rows
@@ -113,9 +114,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   // tiles in XCD order: workgroups b, b + 8, ... share an XCD and its L2
-  const uint32_t total = q.tiles_m * q.tiles_n;
+  const uint32_t total = gridDim.x;
   const uint32_t x = blockIdx.x & 7, per = total >> 3, rest = total & 7;
-  const uint32_t tile = x * per + (x < rest ? x : rest) + (blockIdx.x >> 3);
+  const uint32_t at = x * per + (x < rest ? x : rest) + (blockIdx.x >> 3);
+  const uint32_t split = at / (q.tiles_m * q.tiles_n), tile = at - split * (q.tiles_m * q.tiles_n);
+  const int begin = (int)((uint32_t)q.steps * split / (uint32_t)q.splits);
+  const int end = (int)((uint32_t)q.steps * (split + 1) / (uint32_t)q.splits);
   constexpr uint32_t kGroup = 8;  // row tiles walked together
   const uint32_t group = tile / (kGroup * q.tiles_n);
   const uint32_t gm = q.tiles_m - group * kGroup < kGroup ? q.tiles_m - group * kGroup : kGroup;
@@ -142,7 +146,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
                                      : (uint32_t)(m0 * kStageBlocks) + wave * 512;
   auto copy = [&](uint32_t stage, int step) {
     // chunks past a row's end, and steps past the last, read past the buffer: zeros
-    const uint32_t at_lane = step * kStageBlocks + lane_chunk < q.kb ? lane_off : kPastEnd;
+    const uint32_t at_lane = step < end && step * kStageBlocks + lane_chunk < q.kb ? lane_off : kPastEnd;
     const uint32_t k_off = (uint32_t)step * kStageLine;
 #pragma unroll
     for (int c = 0; c < CA; ++c)
@@ -152,7 +156,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
       lds_copy16(rb, stage + kB + (wave * CB + c) * 1024, at_lane, pitch * 8 * (wave * CB + c) + k_off);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      lds_copy4(rss, stage + kSA + wave * 512 + c * 256, step < q.steps ? lane * 4 : kPastEnd,
+      lds_copy4(rss, stage + kSA + wave * 512 + c * 256, step < end ? lane * 4 : kPastEnd,
                 s_off + (uint32_t)step * s_step + c * 256);
   };
 
@@ -193,9 +197,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
     });
   };
 
-  copy(lds0, 0);
+  copy(lds0, begin);
   uint32_t stage = 0;
-  for (int s = 0; s < q.steps; ++s) {
+  for (int s = begin; s < end; ++s) {
     // this wave's copies of stage s are in, its LDS reads of the stage before
     // are done; then everybody's
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -251,7 +255,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
       }
     }
   } else if (q.wide) {
-    float* y = static_cast<float*>(q.y);
+    float* y = static_cast<float*>(q.y) + split * q.m * q.n;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // 32 columns: 128 bytes a row
 #pragma unroll
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
           const int64_t col = wave_n + 16 * j + 4 * g + c;
           if (col >= q.n) continue;
           if (q.y_f32)
-            static_cast<float*>(q.y)[row * q.ldy + col] = acc[j][k][c];
+            static_cast<float*>(q.y)[split * q.m * q.n + row * q.ldy + col] = acc[j][k][c];
           else
             static_cast<uint16_t*>(q.y)[row * q.ldy + col] = f2h(acc[j][k][c]);
         }
@@ -298,30 +302,69 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
 
 static uint32_t scale_groups(int64_t rows) { return (uint32_t)((rows + 255) / 256 * (256 / kScaleTile)); }
 
+// How a product is cut.  A round of the chip is 256 tiles of 256 x 256 or 512 of
+// 128 x 128 and takes 1.6 times as long with the large ones (5120 -> 17408, us,
+// large / small: 4096 rows 212 / 228, 1024 rows 79 / 74; 1024 rows 5120 -> 5120
+// 39 / 27; 4096 rows 2048 -> 4096 27 / 29).  Small tiles that would leave CUs
+// empty share k, six steps a workgroup at least (64 rows 17408 -> 5120: 48 unshared,
+// 21 shared; eight steps shared by two and added up, 4096 rows 2048 -> 512: 12
+// unshared, 18 shared).
+struct GemmPlan {
+  bool large;
+  int splits;  // of k
+  size_t scales, part;
+};
+static GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k) {
+  const int64_t steps = (k + kStageK - 1) / kStageK;
+  const int64_t large = ((m + 255) / 256) * ((n + 255) / 256), small = ((m + 127) / 128) * ((n + 127) / 128);
+  GemmPlan p{8 * ((large + 255) / 256) <= 5 * ((small + 511) / 512), 1,
+             (size_t)steps * ((size_t)scale_groups(m) + scale_groups(n)) * 512, 0};
+  if (!p.large) {
+    int64_t s = 256 / small;
+    if (s > steps / 6) s = steps / 6;
+    if (s > 1) p.splits = (int)s, p.part = (size_t)s * m * n * sizeof(float);
+  }
+  return p;
+}
+
+// Offsets into the staged scales are 32-bit.
+bool mx4_gemm_fits(int64_t m, int64_t n, int64_t k) { return gemm_plan(m, n, k).scales < ((size_t)1 << 32); }
+
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
-  return (size_t)((k + kStageK - 1) / kStageK) * ((size_t)scale_groups(m) + scale_groups(n)) * 512;
+  const GemmPlan p = gemm_plan(m, n, k);
+  return p.scales + p.part;
 }
 
 template <int TM, int TN, int WM, int WN>
 static void launch_gemm_tiles(Mx4GemmArgs q, hipStream_t s) {
   q.tiles_m = (uint32_t)((q.m + TM - 1) / TM);
   q.tiles_n = (uint32_t)((q.n + TN - 1) / TN);
-  hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN>), dim3(q.tiles_m * q.tiles_n), dim3(WM * WN * 64), 0, s, q);
+  hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN>), dim3(q.tiles_m * q.tiles_n * (uint32_t)q.splits),
+                     dim3(WM * WN * 64), 0, s, q);
 }
 
 hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
                            const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y, int64_t ldy,
                            bool y_f32, void* ws, hipStream_t s) {
   const int kb = (int)(k / kMx4Block), steps = (int)((k + kStageK - 1) / kStageK);
+  const GemmPlan p = gemm_plan(m, n, k);
   const uint32_t ga = scale_groups(m), gb = scale_groups(n);
   uint8_t* sa = static_cast<uint8_t*>(ws);
   uint8_t* sb = sa + (size_t)steps * ga * 512;
+  float* part = reinterpret_cast<float*>(sa + p.scales);
   hipLaunchKernelGGL(mx4_stage_scales, dim3(ga + gb, (2 * steps + 15) / 16), dim3(256), 0, s,
                      StageScales{a_scales, reinterpret_cast<uint32_t*>(sa), m, ga},
                      StageScales{b_scales, reinterpret_cast<uint32_t*>(sb), n, gb}, kb, steps);
-  const int wide = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && ldy % (y_f32 ? 4 : 8) == 0;
-  const Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, bias, y, ldy, m, n, kb, steps, y_f32, wide, 0, 0};
-  launch_gemm_tiles<256, 256, 2, 4>(q, s);
+  const bool shared = p.splits > 1;
+  Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, shared ? nullptr : bias, y, ldy, m, n, kb, steps, y_f32, 0, 0, 0, p.splits};
+  if (shared) q.y = part, q.ldy = n, q.y_f32 = 1;
+  q.wide = (reinterpret_cast<uintptr_t>(q.y) & 15) == 0 && q.ldy % (q.y_f32 ? 4 : 8) == 0 && (!shared || n % 4 == 0);
+  if (p.large)
+    launch_gemm_tiles<256, 256, 2, 4>(q, s);
+  else
+    launch_gemm_tiles<128, 128, 2, 2>(q, s);
+  if (shared)
+    launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, p.splits, part}, s);
   return hipGetLastError();
 }
 

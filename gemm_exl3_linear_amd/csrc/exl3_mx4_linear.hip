@@ -18,8 +18,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   __shared__ float4_t part[NW * R * 64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
-  const uint32_t tile = blockIdx.x / (uint32_t)q.splits, split = blockIdx.x - tile * (uint32_t)q.splits;
-  const uint32_t tm = tile / q.col_tiles, tn = tile - tm * q.col_tiles;
+  const uint32_t tm = blockIdx.x / q.col_tiles, tn = blockIdx.x - tm * q.col_tiles;
   const int64_t m0 = (int64_t)tm * (16 * MG), n0 = (int64_t)tn * (16 * NG);
   const int kb = q.kb;
 
@@ -52,13 +51,12 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
       for (int p = 0; p < P; ++p) acc[ng][mg][p] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
-  const int first = (int)split * NW + wave, stride = NW * q.splits;
   auto load_w = [&](Mx4Unit (&w)[NG], int u) {
 #pragma unroll
     for (int ng = 0; ng < NG; ++ng) mx4_load_unit(rb[ng], kb, u, g, w[ng]);
   };
   if constexpr (A4) {
-    for (int u = first; u < units; u += stride) {
+    for (int u = wave; u < units; u += NW) {
       Mx4Unit w[NG], x[MG];
       load_w(w, u);
 #pragma unroll
@@ -81,7 +79,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
           x[mg][i] = mx4_load_x<P>(xr[mg], there[mg], kb, u, h, g, r, i);
     };
     bool exact = true;
-    for (int u = first; u < units; u += stride) {
+    for (int u = wave; u < units; u += NW) {
       Mx4Unit w[NG];
       f16x8_t x[2][MG][kLoads];
       load_w(w, u);
@@ -91,7 +89,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
       for (int h = 0; h < 2; ++h) exact = mx4_mma_f16<MG, P, NG>(x[h], w, h, g, acc) && exact;
     }
     if (__builtin_expect(!__all(exact), 0))
-      mx4_sum_blocks<MG, P, NG>(xr, there, rb, kb, first, units, stride, 0, 2, g, r, acc);
+      mx4_sum_blocks<MG, P, NG>(xr, there, rb, kb, wave, units, NW, 0, 2, g, r, acc);
   }
 
   // Sum over the waves in wave order, R output tiles a round.  Lane l of a 16 x
@@ -129,10 +127,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (row + i >= q.m) break;
-        if (q.splits == 1)
-          mx4_store(q, row + i, col, v[i]);
-        else
-          q.part[((int64_t)split * q.m + row + i) * q.n + col] = v[i];
+        mx4_store(q, row + i, col, v[i]);
       }
     }
   }
@@ -140,26 +135,24 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
 
 // y = sum of the splits in order (+ bias).
 __global__ __launch_bounds__(256) void mx4_rows_finish(Mx4RowsArgs q) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = q.m * q.n;
-  if (i >= size) return;
-  float v = q.part[i];
-  for (int s = 1; s < q.splits; ++s) v += q.part[s * size + i];
-  const int64_t row = i / q.n;
-  mx4_store(q, row, i - row * q.n, v);
+  const int64_t row = blockIdx.y, col = (int64_t)blockIdx.x * 256 + threadIdx.x, size = q.m * q.n;
+  if (col >= q.n) return;
+  const float* p = q.part + row * q.n + col;
+  float v = *p;
+#pragma unroll 4
+  for (int s = 1; s < q.splits; ++s) v += p[s * size];
+  mx4_store(q, row, col, v);
 }
 
 void launch_mx4_rows_finish(const Mx4RowsArgs& q, hipStream_t s) {
-  hipLaunchKernelGGL(mx4_rows_finish, dim3((uint32_t)((q.m * q.n + 255) / 256)), dim3(256), 0, s, q);
+  hipLaunchKernelGGL(mx4_rows_finish, dim3((uint32_t)((q.n + 255) / 256), (uint32_t)q.m), dim3(256), 0, s, q);
 }
 
 template <bool A4, int MG, int P, int NG, int NW>
-static hipError_t launch_rows(Mx4RowsArgs q, int splits, void* ws, hipStream_t s) {
+static hipError_t launch_rows(Mx4RowsArgs q, hipStream_t s) {
   q.col_tiles = (uint32_t)((q.n + 16 * NG - 1) / (16 * NG));
   const uint32_t tiles = q.col_tiles * (uint32_t)((q.m + 16 * MG - 1) / (16 * MG));
-  q.splits = splits;
-  q.part = static_cast<float*>(ws);
-  hipLaunchKernelGGL((mx4_rows_kernel<A4, MG, P, NG, NW>), dim3(tiles * (uint32_t)splits), dim3(NW * 64), 0, s, q);
-  if (splits > 1) launch_mx4_rows_finish(q, s);
+  hipLaunchKernelGGL((mx4_rows_kernel<A4, MG, P, NG, NW>), dim3(tiles), dim3(NW * 64), 0, s, q);
   return hipGetLastError();
 }
 
@@ -185,16 +178,21 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
                              hipStream_t s) {
   const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
   const bool wide = n >= 2048;  // 32 columns a workgroup still fill the chip's half
-  if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, 1, ws, s);
-  if (m <= 8) return wide ? launch_rows<false, 1, 2, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 2, 1, 8>(q, 1, ws, s);
-  if (m <= 16) return wide ? launch_rows<false, 1, 1, 2, 8>(q, 1, ws, s) : launch_rows<false, 1, 1, 1, 8>(q, 1, ws, s);
+  if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, s);
+  if (m <= 8) return wide ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
+  if (m <= 16) return wide ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
   // rows too far apart for 32-bit offsets: 16 at a time
-  if (ldx > kMx4WideMaxStride) return launch_rows<false, 1, 1, 1, 8>(q, 1, ws, s);
+  if (ldx > kMx4WideMaxStride) return launch_rows<false, 1, 1, 1, 8>(q, s);
   return launch_mx4_wide(q, wide_splits(n, k), ws, s);
 }
 
+// Tiles through LDS (exl3_mx4_gemm.hip: two launches, three where k is shared)
+// from about 3e9 products on, the rows counted in the 64s of a tile here (us, here /
+// there: 64 rows 17408 -> 5120 29 / 21, 256 rows 5120 -> 5120 26 / 20, 256 rows 5120
+// -> 17408 57 / 27, 128 rows 5120 -> 5120 16 / 16, 100 rows 5120 -> 2048 11 / 13,
+// 256 rows 2048 -> 512 6.4 / 10.5).
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
-  return m >= 512 && n >= 512 && mx4_gemm_workspace(m, n, k) < ((size_t)1 << 32);
+  return m > 16 && (double)((m + 63) / 64 * 64) * (double)n * (double)k >= 3.3e9 && mx4_gemm_fits(m, n, k);
 }
 size_t mx4_matmul_workspace(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? mx4_gemm_workspace(m, n, k) : 0;
@@ -205,9 +203,15 @@ hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t 
                              bool y_f32, void* ws, hipStream_t s) {
   if (use_gemm(m, n, k)) return launch_mx4_gemm(a, a_scales, m, b, b_scales, n, k, bias, y, ldy, y_f32, ws, s);
   const Mx4RowsArgs q{a, a_scales, 0, b, b_scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
-  if (m <= 16) return launch_rows<true, 1, 1, 1, 8>(q, 1, ws, s);
-  if (((m + 63) / 64) * ((n + 63) / 64) >= 160) return launch_rows<true, 4, 1, 4, 4>(q, 1, ws, s);
-  return launch_rows<true, 4, 1, 2, 8>(q, 1, ws, s);
+  // 16 rows or fewer in 32 columns a workgroup where the chip stays full, for
+  // fewer loads of a; not for a row or two, whose a comes from cache, over very many
+  // columns (us, 16 / 32 columns: 16 rows 17408 -> 5120 20.0 / 16.0, 17408 -> 2048
+  // 11.4 / 15.7, 2048 -> 8192 5.1 / 4.6; one row 17408 -> 5120 15.0 / 12.8, 5120 ->
+  // 17408 11.5 / 12.2)
+  if (m <= 16)
+    return n >= 4096 && (m > 4 || n < 16384) ? launch_rows<true, 1, 1, 2, 8>(q, s) : launch_rows<true, 1, 1, 1, 8>(q, s);
+  if (((m + 63) / 64) * ((n + 63) / 64) >= 160) return launch_rows<true, 4, 1, 4, 4>(q, s);
+  return launch_rows<true, 4, 1, 2, 8>(q, s);
 }
 
 }  // namespace exl3

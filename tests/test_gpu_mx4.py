@@ -620,3 +620,89 @@ def test_moe_any_scale_byte(t):
         clean[name] = (l[name][0], np.where(l[name][1] == 255, 127, l[name][1]))
     lim = moe_limit(x, clean, 2, ref, w, True)
     assert_within(y, ref, lim)
+
+
+# ---------------------------------------------------------------------------
+# products large enough for the tiles in LDS
+# ---------------------------------------------------------------------------
+# 128 x 128 tiles with k shared by 28 workgroups, by two, and not; 256 x 256 tiles
+TILES = [(65, 1111, 46496), (128, 1028, 26080), (700, 1290, 4128), (1000, 2602, 1312), (2040, 7700, 288), (4097, 4100, 224)]
+
+
+@pytest.mark.parametrize("aligned", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_matmul_tiles(m, n, k, f32, aligned):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n + k + aligned)
+    a, b = rand_mx(rng, m, k), rand_mx(rng, n, k, lo=112, hi=122)
+    a[1][m - 1, -1] = b[1][n // 2, 0] = 255
+    bias = rng.standard_normal(n).astype(np.float16) if f32 == aligned else None
+    dt = torch.float32 if f32 else torch.float16
+    first, pitch = (8, (n + 7) // 8 * 8 + 16) if aligned else (1, n + 2)
+    buf = torch.full((m, pitch), 7.0, dtype=dt, device=G.dev())
+    y = X.exl3_mx4_matmul(mx(a), mx(b), bias=None if bias is None else G.to_dev(bias), out=buf[:, first:first + n])
+    da, db = M.decode(*a).astype(np.float32), M.decode(*b).astype(np.float32)  # exact
+    rows = np.unique(np.concatenate([np.arange(0, m, max(1, m // 90)), np.arange(max(0, m - 20), m)]))
+    ref, _ = M.product(da[rows], db, bias)
+    mag = M.product(np.nan_to_num(da[rows]), np.nan_to_num(db), bias)[1]
+    assert_within(y.cpu().numpy()[rows], ref, bound(ref, mag, k, f32), f"{m}x{n}x{k}")
+    rest = np.isnan(y.cpu().numpy())
+    assert rest[:, n // 2].all() and rest[m - 1].all() and rest.sum() == m + n - 1
+    assert (buf[:, :first] == 7.0).all() and (buf[:, first + n:] == 7.0).all()
+
+
+def test_matmul_tiles_of_one_scale_are_exact():
+    # multiples of 1/4 below 36 k < 2^20, every element, in any order
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(3)
+    for m, n, k in ((192, 900, 26080), (1300, 1500, 2080), (2048, 7680, 320)):
+        a, b = rand_mx(rng, m, k, lo=127, hi=127), rand_mx(rng, n, k, lo=127, hi=127)
+        y = X.exl3_mx4_matmul(mx(a), mx(b), out_dtype=torch.float32)
+        np.testing.assert_array_equal(y.double().cpu().numpy(), M.product(M.decode(*a), M.decode(*b))[0])
+
+
+def test_matmul_workspace_serves_other_sizes():
+    # the same scratch, full of NaNs at first, for products cut differently, two in a row
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(4)
+    sizes = [(65, 1111, 46496), (700, 1290, 4128), (4097, 4100, 224), (1000, 2602, 1312), (20, 5000, 4096)]
+    built = [(mx(rand_mx(rng, m, k)), mx(rand_mx(rng, n, k))) for m, n, k in sizes]
+    own = [X.exl3_mx4_matmul(a, b) for a, b in built]
+    ws = torch.full((max(X.exl3_mx4_matmul_workspace_size(a, b) for a, b in built),), 255, dtype=torch.uint8, device=G.dev())
+    for i in (0, 1, 2, 3, 4, 2, 0, 3, 0, 0):
+        assert torch.equal(X.exl3_mx4_matmul(*built[i], workspace=ws), own[i])
+
+
+# the rows of a k that is not whole units, of weight rows that start at any byte of
+# a dword of scales, with k shared and not, one column over a tile; and rows too far
+# apart for 32-bit offsets
+@pytest.mark.parametrize("m,n,k,pitch", [(17, 129, 5152, 0), (33, 257, 4160, 8), (49, 128, 2080, 8), (64, 1, 32, 0),
+                                         (32, 2, 17440, 0), (48, 40000, 96, 0), (18, 33, 320, (1 << 24) + 8)])
+def test_linear_shared_rows(m, n, k, pitch):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n + k)
+    w = rand_mx(rng, n, k, lo=112, hi=122)
+    w[1][n - 1, -1] = 90   # outside fp16
+    w[0][0, 16:32], w[1][0, 1 % (k // 32)] = (w[0][0, 16:32], w[1][0, 0]) if k == 32 else (0, 0)  # zeros at 2^-127
+    x = rng.standard_normal((m, k)).astype(np.float16)
+    bias = rng.standard_normal(n).astype(np.float16)
+    if pitch > k:
+        big = torch.empty((m - 1) * pitch + k, dtype=torch.float16, device=G.dev())
+        xd = big.as_strided((m, k), (pitch, 1))
+        xd.copy_(G.to_dev(x))
+    else:
+        xd = torch.full((m, k + pitch), float("nan"), dtype=torch.float16, device=G.dev())[:, :k]
+        xd.copy_(G.to_dev(x))
+    y = X.exl3_mx4_linear(xd, mx(w), bias=G.to_dev(bias), out_dtype=torch.float32)
+    ref, mag = M.product(x, M.decode(*w), bias)
+    assert_within(y.cpu().numpy(), ref, bound(ref, mag, k, True), f"{m}x{n}x{k}")
+    ws = X.exl3_mx4_linear_workspace_size(mx(w), m)
+    ws = torch.full((ws + 16,), 255, dtype=torch.uint8, device=G.dev())
+    for _ in range(2):
+        again = X.exl3_mx4_linear(xd, mx(w), bias=G.to_dev(bias), out_dtype=torch.float32, workspace=ws)
+        assert torch.equal(again, y)
