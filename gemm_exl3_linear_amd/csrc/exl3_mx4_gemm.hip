@@ -305,21 +305,29 @@ static uint32_t scale_groups(int64_t rows) { return (uint32_t)((rows + 255) / 25
 // How a product is cut.  A round of the chip is 256 tiles of 256 x 256 or 512 of
 // 128 x 128 and takes 1.6 times as long with the large ones (5120 -> 17408, us,
 // large / small: 4096 rows 212 / 228, 1024 rows 79 / 74; 1024 rows 5120 -> 5120
-// 39 / 27; 4096 rows 2048 -> 4096 27 / 29).  Small tiles that would leave CUs
-// empty share k, six steps a workgroup at least (64 rows 17408 -> 5120: 48 unshared,
-// 21 shared; eight steps shared by two and added up, 4096 rows 2048 -> 512: 12
-// unshared, 18 shared).
+// 39 / 27; 4096 rows 2048 -> 4096 27 / 29).  A last round of large tiles that would
+// be short is left to small ones, as columns of their own (4096 rows 5120 -> 17408
+// 212 without, 201 with; 1024 rows 75 / 68).  Small tiles that would
+// leave CUs empty share k, six steps a workgroup at least (64 rows 17408 -> 5120:
+// 48 unshared, 21 shared; eight steps shared by two and added up, 4096 rows 2048 ->
+// 512: 12 unshared, 18 shared).
 struct GemmPlan {
-  bool large;
-  int splits;  // of k
+  int64_t large;  // columns of large tiles, the first ones
+  int splits;     // of k, of small tiles where there are no large ones
   size_t scales, part;
 };
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static int64_t rounds_small(int64_t m, int64_t n) { return cdiv(cdiv(m, 128) * cdiv(n, 128), 512); }
 static GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k) {
-  const int64_t steps = (k + kStageK - 1) / kStageK;
-  const int64_t large = ((m + 255) / 256) * ((n + 255) / 256), small = ((m + 127) / 128) * ((n + 127) / 128);
-  GemmPlan p{8 * ((large + 255) / 256) <= 5 * ((small + 511) / 512), 1,
-             (size_t)steps * ((size_t)scale_groups(m) + scale_groups(n)) * 512, 0};
-  if (!p.large) {
+  const int64_t steps = cdiv(k, kStageK), tiles_m = cdiv(m, 256), all = tiles_m * cdiv(n, 256);
+  GemmPlan p{0, 1, (size_t)steps * ((size_t)scale_groups(m) + scale_groups(n)) * 512, 0};
+  int64_t best = 5 * rounds_small(m, n);
+  if (8 * cdiv(all, 256) <= best) best = 8 * cdiv(all, 256), p.large = n;
+  const int64_t cols = all / 256 * 256 / tiles_m * 256;  // of whole rounds
+  if (cols > 0 && cols < n && 8 * cdiv(tiles_m * (cols / 256), 256) + 5 * rounds_small(m, n - cols) < best)
+    p.large = cols;
+  if (p.large == 0) {
+    const int64_t small = cdiv(m, 128) * cdiv(n, 128);
     int64_t s = 256 / small;
     if (s > steps / 6) s = steps / 6;
     if (s > 1) p.splits = (int)s, p.part = (size_t)s * m * n * sizeof(float);
@@ -359,10 +367,16 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
   Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, shared ? nullptr : bias, y, ldy, m, n, kb, steps, y_f32, 0, 0, 0, p.splits};
   if (shared) q.y = part, q.ldy = n, q.y_f32 = 1;
   q.wide = (reinterpret_cast<uintptr_t>(q.y) & 15) == 0 && q.ldy % (q.y_f32 ? 4 : 8) == 0 && (!shared || n % 4 == 0);
-  if (p.large)
+  if (p.large > 0) {
+    q.n = p.large;
     launch_gemm_tiles<256, 256, 2, 4>(q, s);
-  else
-    launch_gemm_tiles<128, 128, 2, 2>(q, s);
+    q.b += p.large * kb * 16;
+    q.b_scales += p.large * kStageBlocks;
+    if (q.bias) q.bias += p.large;
+    q.y = static_cast<uint8_t*>(q.y) + p.large * (q.y_f32 ? 4 : 2);
+    q.n = n - p.large;
+  }
+  if (q.n > 0) launch_gemm_tiles<128, 128, 2, 2>(q, s);
   if (shared)
     launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, p.splits, part}, s);
   return hipGetLastError();
