@@ -1,5 +1,5 @@
 // exl3_mx4_moe: a whole mixture-of-experts layer for 1 to 16 tokens, in three
-// launches (four for many listed experts).
+// launches.
 //
 //   1. mx4_moe_router  logits x W_r^T (the shared expert's gate as one more
 //      row): workgroup (16 experts, k share), fp16 matrix instructions.  The last
@@ -9,7 +9,7 @@
 //      the waves' shares of k, a = silu(g) * u.
 //   3. mx4_moe_down    workgroup (16 columns): the waves share the (expert, 256
 //      k) units, sums are weighted per expert and meet in LDS; many experts are
-//      shared among workgroups, whose sums mx4_moe_finish adds.
+//      shared among workgroups, the last of which adds their sums.
 //
 // A token chooses an expert at most once, so 16 tokens fill at most one 16-row
 // matrix operand per expert and each expert's weights are read once, whatever
@@ -25,6 +25,7 @@
 namespace exl3 {
 
 constexpr int kMoeTokens = 16;
+constexpr int kMoeMaxDim = 65536;  // of hidden and of an expert
 constexpr int kMoeGateUpWaves = 8, kMoeDownWaves = 16;
 
 // A listed expert: its tokens, in order, and the first of their rows in the
@@ -54,7 +55,7 @@ struct MoeArgs {
   int splits;         // k shares of the router
   int lstride;        // floats of a token's partial logits
   // workspace
-  uint32_t* arrived;  // router workgroups done, 0 between calls
+  uint32_t* arrived;  // workgroups done, 0 between calls: the router's, then those of each 16 columns of down
   float* logits;      // [splits][16][lstride] partial sums, the shared gate's after the experts'
   MoeEntry* entries;  // [most + 1]; the last is the shared expert
   int* count;         // routed entries
@@ -63,6 +64,24 @@ struct MoeArgs {
   int down_splits;    // workgroups that share the entries of 16 columns
   float* down;        // their sums [split][t][hidden], where there are several
 };
+
+// Sums that the last workgroup to arrive takes from the others, which run on
+// other XCDs, pass by stores and loads of device scope: those do not stay in an
+// XCD's L2, so a wave that has waited for its stores may count itself in.  (Fences
+// of device scope write the L2 back and drop it: 1 to 2 us.)
+__device__ __forceinline__ void store_shared(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float load_shared(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void wait_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Counts one of n in; true for the last, which leaves 0.
+__device__ __forceinline__ bool last_in(uint32_t* count, uint32_t n) {
+  const bool last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+  if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return last;
+}
 
 // ---------------------------------------------------------------------------
 // router
@@ -178,7 +197,7 @@ __device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s)
       const float* p = q.logits + (int64_t)t * q.lstride + e;
       float l = 0.f;
 #pragma unroll 4
-      for (int k = 0; k < q.splits; ++k) l += p[(int64_t)k * kMoeTokens * q.lstride];
+      for (int k = 0; k < q.splits; ++k) l += load_shared(p + (int64_t)k * kMoeTokens * q.lstride);
       const float b = q.d.router_bias ? q.d.router_bias[e] : 0.f;
       const float score = q.d.scoring == 0 ? l + b : 1.f / (1.f + exp_f(-l));
       // without a bias the sigmoid's order is the logit's, where it has not saturated
@@ -189,7 +208,7 @@ __device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s)
   }
   if (q.d.shared_gate && tid < q.t) {
     float l = 0.f;
-    for (int k = 0; k < q.splits; ++k) l += q.logits[((int64_t)k * kMoeTokens + tid) * q.lstride + E];
+    for (int k = 0; k < q.splits; ++k) l += load_shared(q.logits + ((int64_t)k * kMoeTokens + tid) * q.lstride + E);
     s.gates[tid] = l;
   }
   __syncthreads();
@@ -279,7 +298,7 @@ __global__ __launch_bounds__(NW * 64) void mx4_moe_router(MoeArgs q) {
     float4_t part[NW * 64];
     MoeRouteLds<EPL> route;
   } s;
-  __shared__ uint32_t before;
+  __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int E = q.d.experts, H = q.d.hidden;
@@ -311,17 +330,12 @@ __global__ __launch_bounds__(NW * 64) void mx4_moe_router(MoeArgs q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (there && 4 * g + i < q.t)
-        __hip_atomic_store(q.logits + ((int64_t)split * kMoeTokens + 4 * g + i) * q.lstride + e, acc[i],
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // device scope: the workgroups run on different XCDs.  One wave acquires for
-    // all (sixteen took 2 us), the barrier passes it on.
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    if (lane == 0) before = __hip_atomic_fetch_add(q.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        store_shared(q.logits + ((int64_t)split * kMoeTokens + 4 * g + i) * q.lstride + e, acc[i]);
+    wait_stores();
+    if (lane == 0) last = last_in(q.arrived, gridDim.x);
   }
   __syncthreads();
-  if (before != gridDim.x - 1) return;
-  if (threadIdx.x == 0) __hip_atomic_store(q.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (!last) return;
   moe_route<EPL, NW>(q, s.route);
 }
 
@@ -557,24 +571,26 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, 8) void mx4_moe_down(MoeArgs q)
   }
   __syncthreads();
   const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
-  if (t >= q.t) return;
   float v = 0.f;
+  if (t < q.t) {
 #pragma unroll
-  for (int o = 0; o < kMoeDownWaves; ++o) v += tiles[o][t][c];
-  if (q.down_splits == 1)
-    moe_store(q, t, h0 + c, v);
-  else
-    q.down[((int64_t)blockIdx.y * q.t + t) * H + h0 + c] = v;
-}
-
-// y = sum of the down splits in order.
-__global__ __launch_bounds__(256) void mx4_moe_finish(MoeArgs q) {
-  const int t = blockIdx.y, h = blockIdx.x * 256 + threadIdx.x, H = q.d.hidden;
-  if (h >= H) return;
-  float v = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < q.down_splits; ++s) v += q.down[((int64_t)s * q.t + t) * H + h];
-  moe_store(q, t, h, v);
+    for (int o = 0; o < kMoeDownWaves; ++o) v += tiles[o][t][c];
+  }
+  if (q.down_splits > 1) {
+    __shared__ int last;
+    const int64_t plane = (int64_t)q.t * H;
+    float* p = q.down + t * H + h0 + c;
+    if (t < q.t) store_shared(p + blockIdx.y * plane, v);
+    wait_stores();
+    __syncthreads();
+    if (threadIdx.x == 0) last = last_in(q.arrived + 1 + blockIdx.x, (uint32_t)q.down_splits);
+    __syncthreads();
+    if (!last) return;
+    v = 0.f;
+    if (t < q.t)
+      for (int i = 0; i < q.down_splits; ++i) v += load_shared(p + i * plane);
+  }
+  if (t < q.t) moe_store(q, t, h0 + c, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -592,12 +608,12 @@ int moe_splits(const Mx4MoeDesc& d) {
   return s < 1 ? 1 : (s > 8 ? 8 : s);
 }
 
-// Shares of the down product's entries: about four tasks a wave where there
+// Shares of the down product's entries: a task a wave at least, where there
 // may be so many, and no more than the chip takes at once (two workgroups a CU).
 int moe_down_splits(const Mx4MoeDesc& d, int64_t t, int topk) {
   const int units = (d.inter + kMx4UnitK - 1) / kMx4UnitK, tasks = moe_most(d, t, topk) * units;
   const int room = 512 / (d.hidden / 16);
-  int s = tasks / (4 * kMoeDownWaves);
+  int s = tasks / kMoeDownWaves;
   if (s > room) s = room;
   return s < 1 ? 1 : s;
 }
@@ -616,7 +632,7 @@ MoeLayout moe_layout(const Mx4MoeDesc& d, int64_t t, int topk) {
     return at;
   };
   L.lstride = (d.experts + 16) / 16 * 16;
-  L.arrived = take(4);  // first in every layout: a workspace serves all sizes
+  L.arrived = take((1 + kMoeMaxDim / 16) * 4);  // first and as long in every layout: a workspace serves all sizes
   L.logits = take((size_t)moe_splits(d) * kMoeTokens * L.lstride * 4);
   L.entries = take(most * sizeof(MoeEntry));
   L.count = take(4);
@@ -660,8 +676,6 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
   hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s, q);
   hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
-  if (q.down_splits > 1)
-    hipLaunchKernelGGL(mx4_moe_finish, dim3((d.hidden + 255) / 256, (uint32_t)t), dim3(256), 0, s, q);
   return hipGetLastError();
 }
 
