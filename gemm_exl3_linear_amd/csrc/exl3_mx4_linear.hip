@@ -156,12 +156,15 @@ static hipError_t launch_rows(Mx4RowsArgs q, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Kernel by size, as measured (us; graph replays, weights alternating among
-// three copies):
-//   fp16 rows, few: pieces (see exl3_mx4_rows.hpp)
-//     5120 -> 17408, one row: P = 4 12.8, P = 2 13.1, P = 1 16
-//   more than 16 rows: exl3_mx4_wide.hip, k in as many shares as fill the chip
-//   once (one workgroup a CU)
+// fp16 rows shared through LDS (exl3_mx4_wide.hip) where they are many, or 9 to 16
+// of large weights (us, here / there: 16 rows 17408 -> 5120 29 / 20, 5120 -> 17408
+// 26 / 22, 5120 -> 5120 11 / 13, 2048 -> 8192 6 / 10; 6 rows 17408 -> 5120 18 / 19).
+// Rows too far apart for its 32-bit offsets are taken here, 16 at a time.
+static bool use_wide(int64_t m, int64_t n, int64_t k) { return m > 16 || (m > 8 && n * k >= 80000000); }
+
+// Shares of k there: as many as fill the chip's CUs once, two units each at least
+// (us, for 2 / 3 / 4 / 5 / 6 / 8 shares: 37 rows 17408 -> 5120, 40 tiles, 42 / 32 / 27 /
+// 25 / 24 / 33; 20 rows 8192 -> 8192, 64 tiles, 22 / 19 / 17 / 25 / 24 / 23).
 static int wide_splits(int64_t n, int64_t k) {
   const int64_t tiles = (n + 127) / 128, units = (k + kMx4UnitK - 1) / kMx4UnitK;
   int64_t s = 256 / tiles;
@@ -169,7 +172,7 @@ static int wide_splits(int64_t n, int64_t k) {
   return s < 1 ? 1 : (int)s;
 }
 size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  const int s = m > 16 ? wide_splits(n, k) : 1;
+  const int s = use_wide(m, n, k) ? wide_splits(n, k) : 1;
   return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
 }
 
@@ -177,13 +180,13 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
                              const uint16_t* x, int64_t m, int64_t ldx, void* y, int64_t ldy, bool y_f32, void* ws,
                              hipStream_t s) {
   const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
-  const bool wide = n >= 2048;  // 32 columns a workgroup still fill the chip's half
+  if (use_wide(m, n, k) && ldx <= kMx4WideMaxStride) return launch_mx4_wide(q, wide_splits(n, k), ws, s);
+  // pieces for few rows (exl3_mx4_rows.hpp; one row 5120 -> 17408: 12.8 us with four,
+  // 13.1 with two, 16 with one); 32 columns a workgroup where those fill half the chip
+  const bool cols32 = n >= 2048;
   if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, s);
-  if (m <= 8) return wide ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
-  if (m <= 16) return wide ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
-  // rows too far apart for 32-bit offsets: 16 at a time
-  if (ldx > kMx4WideMaxStride) return launch_rows<false, 1, 1, 1, 8>(q, s);
-  return launch_mx4_wide(q, wide_splits(n, k), ws, s);
+  if (m <= 8) return cols32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
+  return m <= 16 && cols32 ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
 }
 
 // Tiles through LDS (exl3_mx4_gemm.hip: two launches, three where k is shared)

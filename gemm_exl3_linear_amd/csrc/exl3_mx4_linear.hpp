@@ -32,7 +32,8 @@ __device__ __forceinline__ void mx4_store(const Mx4RowsArgs& q, int64_t row, int
 
 // y = sum of the splits in order (+ bias).
 void launch_mx4_rows_finish(const Mx4RowsArgs& q, hipStream_t s);
-// 17 to 64 fp16 rows, at most kMx4WideMaxStride elements apart; splits > 1: partial sums fp32 [splits][m][n] in ws
+// Up to 64 fp16 rows, at most kMx4WideMaxStride elements apart;
+// splits > 1: partial sums fp32 [splits][m][n] in ws
 constexpr int64_t kMx4WideMaxStride = (int64_t)1 << 24;
 hipError_t launch_mx4_wide(Mx4RowsArgs q, int splits, void* ws, hipStream_t s);
 

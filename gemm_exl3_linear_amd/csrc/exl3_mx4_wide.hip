@@ -1,4 +1,4 @@
-// exl3_mx4_linear for 17 to 64 rows: fp16 rows shared by a workgroup through
+// exl3_mx4_linear for 17 to 64 rows, and from 9 on of large weights: fp16 rows shared by a workgroup through
 // LDS.
 //
 // With so many rows the waves can no longer each fetch the rows for their share
@@ -11,7 +11,7 @@
 // LDS reads, conversions and matrix instructions one after the other (25 us).
 //
 // A stage is 256 k of everything, copied from memory straight to LDS, kept in a
-// ring of three or four: a step waits for the next stage only, so that the bytes
+// ring of three to six: a step waits for the next stage only, so that the bytes
 // of the others are in flight meanwhile.  The waves run in step, so what a step
 // does one after the other leaves the rest of the CU idle (copies 500 cycles, LDS
 // reads 900, product 1000, of 3000): a quarter of the product is followed by a
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   // first three of which hold its eight scale bytes
   constexpr uint32_t kX = 0, kB = kX + MG * 16 * kWideLine, kS = kB + kWideCols * kMx4UnitBytes,
                      kBytes = kS + kWideCols * 16;
-  constexpr int kStages = 160 * 1024 / kBytes < 4 ? 160 * 1024 / kBytes : 4;
+  constexpr int kStages = 160 * 1024 / kBytes;
   constexpr int CX = MG * 8 / kWideWaves, CB = kWideCols / 8 / kWideWaves, kCopies = CX + CB + 1;  // a wave's, a stage
   __shared__ __align__(128) uint8_t smem[kStages * kBytes];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   const int64_t left = q.n - n0 < kWideCols ? q.n - n0 : kWideCols;
   const u32x4_t rx = buffer_words(static_cast<const uint8_t*>(q.a), (uint64_t)(q.m - 1) * xpitch + (uint64_t)kb * 64);
   const u32x4_t rb = buffer_words(q.b + n0 * pitch, (uint64_t)left * pitch);
-  const u32x4_t rs = buffer_words(q.b_scales + ((n0 * kb) & ~(int64_t)3), ((uint64_t)left * kb + (n0 * kb & 3) + 3) & ~3ull);
+  const u32x4_t rs = buffer_words(q.b_scales + n0 * kb, ((uint64_t)left * kb + 3) & ~3ull);
   constexpr int kTurns = CX < 4 ? CX : 4;  // the turn of row 2 (CX wave + i) + lane / 32 repeats after four i
   uint32_t x_chunk[kTurns], x_off[kTurns];
 #pragma unroll
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
     x_off[i] = xpitch * (lane >> 5) + 16 * x_chunk[i];
   }
   const uint32_t b_chunk = (lane & 7) ^ ((lane >> 3) & 7), b_off = pitch * (lane >> 3) + 16 * b_chunk;
-  const uint32_t s_off = ((uint32_t)(n0 * kb & 3) + (uint32_t)(wave * 16 + r) * kb) & ~3u;  // dword of its first scale
+  const uint32_t s_off = ((uint32_t)(wave * 16 + r) * kb) & ~3u;  // dword of its first scale
   // Copies of unit u, in quarters (0 .. 3; the scales in the last); none of a
   // unit past the end: zeros, from a buffer without bytes.
   struct Copy {
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
       const int row = cols + 16 * ni + r;
       t[ni].half[0] = lds_read16(stage + kB + row * kMx4UnitBytes + (((4 * h + g) ^ (r & 7)) * 16));
       // scale bytes 4 h .. 4 h + 3, of three dwords that hold all eight
-      const uint32_t shift = ((uint32_t)(n0 * kb & 3) + (uint32_t)row * kb) & 3u;
+      const uint32_t shift = ((uint32_t)row * kb) & 3u;
       const u32x2_t d = lds_read8(stage + kS + row * 16 + 4 * h);
       t[ni].sc[0] = __builtin_amdgcn_alignbyte(d.y, d.x, shift);
       if ((u + 1) * kMx4UnitBlocks > kb) {  // what follows a row's end is the next row's
@@ -172,18 +172,20 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
   if (__builtin_expect(!__all(exact), 0)) {
     const uint16_t* xr[MG];
     bool there[MG];
-    Mx4Row rows[kWideNI];
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg) {
       there[mg] = 16 * mg + r < q.m;
       xr[mg] = static_cast<const uint16_t*>(q.a) + (there[mg] ? 16 * mg + r : 0) * q.lda;
     }
 #pragma unroll
-    for (int ni = 0; ni < kWideNI; ++ni) {
+    for (int ni = 0; ni < kWideNI; ++ni) {  // one by one, for fewer registers
       const int row = cols + 16 * ni + r;
-      rows[ni] = mx4_row(q.b, q.b_scales, n0, row < left ? row : (uint32_t)(left - 1), kb);
+      const Mx4Row rows[1] = {mx4_row(q.b, q.b_scales, n0, row < left ? row : (uint32_t)(left - 1), kb)};
+      float4_t sums[1][MG][1];
+      mx4_sum_blocks<MG, 1, 1>(xr, there, rows, kb, begin, end, 1, h, h + 1, g, r, sums);
+#pragma unroll
+      for (int mg = 0; mg < MG; ++mg) acc[ni][mg][0] = sums[0][mg][0];
     }
-    mx4_sum_blocks<MG, 1, kWideNI>(xr, there, rows, kb, begin, end, 1, h, h + 1, g, r, acc);
   }
 
   // the second half's sums to the waves of the first, through LDS
@@ -221,7 +223,8 @@ hipError_t launch_mx4_wide(Mx4RowsArgs q, int splits, void* ws, hipStream_t s) {
   q.splits = splits;
   q.part = static_cast<float*>(ws);
   const dim3 grid(tiles * (uint32_t)splits), block(kWideWaves * 64);
-  if (q.m <= 32) hipLaunchKernelGGL(mx4_wide_kernel<2>, grid, block, 0, s, q);
+  if (q.m <= 16) hipLaunchKernelGGL(mx4_wide_kernel<1>, grid, block, 0, s, q);
+  else if (q.m <= 32) hipLaunchKernelGGL(mx4_wide_kernel<2>, grid, block, 0, s, q);
   else if (q.m <= 48) hipLaunchKernelGGL(mx4_wide_kernel<3>, grid, block, 0, s, q);
   else hipLaunchKernelGGL(mx4_wide_kernel<4>, grid, block, 0, s, q);
   if (splits > 1) launch_mx4_rows_finish(q, s);

@@ -706,3 +706,19 @@ def test_linear_shared_rows(m, n, k, pitch):
     for _ in range(2):
         again = X.exl3_mx4_linear(xd, mx(w), bias=G.to_dev(bias), out_dtype=torch.float32, workspace=ws)
         assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("m,n,k", [(9, 4613, 17440), (16, 17408, 4640)])
+def test_linear_shared_rows_of_large_weights(m, n, k):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n)
+    w = rand_mx(rng, n, k, lo=112, hi=122)
+    w[1][n // 2, 7], w[1][5, k // 32 - 1] = 90, 255
+    x = rng.standard_normal((m, k)).astype(np.float16)
+    y = X.exl3_mx4_linear(G.to_dev(x), mx(w), out_dtype=torch.float32).cpu().numpy()
+    cols = np.unique(np.concatenate([np.arange(0, n, 37), [5, n // 2], np.arange(n - 140, n)]))
+    wc = M.decode(w[0][cols], w[1][cols])
+    ref, _ = M.product(x, wc)
+    assert_within(y[:, cols], ref, bound(ref, M.product(x, np.nan_to_num(wc))[1], k, True))
+    assert np.isnan(y).sum() == m
