@@ -522,7 +522,11 @@ def _stream_for(t, what: str, stream) -> int:
     i = t.get_device()
     if i != torch._C._cuda_getDevice():
         _refuse(f"{what} is on GPU {i}, not on the current device")
-    return torch._C._cuda_getCurrentRawStream(i) if stream is None else int(stream.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(i)
+    if stream.device_index != i:
+        _refuse(f"the stream is of GPU {stream.device_index}, {what} is on GPU {i}")
+    return int(stream.cuda_stream)
 
 
 def _tensor(t, what: str, dtype, shape):
@@ -559,15 +563,25 @@ def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
     return ld if m > 1 else -(-n // 8) * 8
 
 
-def _scratch(workspace, need, args, device):
-    """Address and bytes of the caller's workspace, or of a zero-filled one (of
-    need(*args) bytes) and the tensor that holds it."""
+def _new(make, shape, dtype, device, stream):
+    """make(shape, ...): a tensor of the stream that the call runs on, so that
+    its memory is not another stream's, cleared or handed on too early."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace, make, need, args, device, stream):
+    """Address and bytes of the caller's workspace, or of one that make() gives
+    (need(*args) bytes), and the tensor that holds it."""
     import torch
     if workspace is None:
         n = need(*args)
         if not n:
             return 0, 0, None
-        workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+        workspace = _new(make, n, torch.uint8, device, stream)
     elif workspace.numel() and (workspace.device != device or not workspace.is_contiguous()):
         _refuse("the workspace is on another device than the operands, or not contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -683,8 +697,10 @@ class Exl3Mx4Moe:
         object.__setattr__(self, "_record", record)
         object.__setattr__(self, "_ref", ctypes.byref(record))
 
+
 def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     """MXFP4 of fp16 or fp32 rows x [rows, k], k a multiple of 32."""
+    import torch
     ldx = _row_stride(x, "x", None, None)
     dtype = _f16_f32(x, "x")
     on = _stream_for(x, "x", stream)
@@ -692,7 +708,8 @@ def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     if out is None:
         if k == 0 or k % MX4_BLOCK:
             _refuse(f"x has {k} columns, not a multiple of {MX4_BLOCK}")
-        out = Exl3Mx4.empty(rows, k, device=x.device)
+        out = Exl3Mx4(_new(torch.empty, (rows, k // 2), torch.uint8, x.device, stream),
+                      _new(torch.empty, (rows, k // MX4_BLOCK), torch.uint8, x.device, stream))
     r = out._record
     if r.rows != rows or r.k != k or out.codes.device != x.device:
         _refuse("out does not match x")
@@ -707,7 +724,7 @@ def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     on = _stream_for(w.codes, "w", stream)
     r = w._record
     if out is None:
-        out = torch.empty((r.rows, r.k), dtype=dtype or torch.float16, device=w.codes.device)
+        out = _new(torch.empty, (r.rows, r.k), dtype or torch.float16, w.codes.device, stream)
     elif out.device != w.codes.device:
         _refuse("out is on another device than w")
     ldo = _row_stride(out, "out", r.rows, r.k)
@@ -716,11 +733,11 @@ def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     return out
 
 
-def _product_out(out, out_dtype, m: int, n: int, device, bias):
+def _product_out(out, out_dtype, m: int, n: int, device, bias, stream):
     """The output of a product (a new one if none is given), its row stride and type."""
     import torch
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype or torch.float16, device=device)
+        out = _new(torch.empty, (m, n), out_dtype or torch.float16, device, stream)
     elif out.device != device:
         _refuse("out is on another device than the operands")
     ldy = _row_stride(out, "out", m, n)
@@ -736,14 +753,14 @@ def exl3_mx4_matmul_workspace_size(a: Exl3Mx4, b: Exl3Mx4) -> int:
 
 
 def exl3_mx4_matmul(a: Exl3Mx4, b: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
-    """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4.  A
-    workspace passed in has to be zero-filled before its first use."""
+    """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4."""
+    import torch
     device = a.codes.device
     on = _stream_for(a.codes, "a", stream)
     if b.codes.device != device:
         _refuse("a and b are on different devices")
-    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, device, bias)
-    ws, nws, _keep = _scratch(workspace, exl3_mx4_matmul_workspace_size, (a, b), device)
+    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, device, bias, stream)
+    ws, nws, _keep = _scratch(workspace, torch.empty, exl3_mx4_matmul_workspace_size, (a, b), device, stream)
     _check(lib().exl3_mx4_matmul(a._ref, b._ref, _ptr(bias), out.data_ptr(), ldy, ydt, ws, nws, on),
            "exl3_mx4_matmul")
     return out
@@ -755,8 +772,7 @@ def exl3_mx4_linear_workspace_size(w: Exl3Mx4, m: int) -> int:
 
 def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = x w^T (+ bias fp16 [n]): fp16 rows x [m, k], m up to 64,
-    against MXFP4 weights w [n, k].  A workspace passed in has to be
-    zero-filled before its first use."""
+    against MXFP4 weights w [n, k]."""
     import torch
     r = w._record
     ldx = _row_stride(x, "x", None, r.k)
@@ -767,8 +783,8 @@ def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspac
     if w.codes.device != device:
         _refuse("x and w are on different devices")
     m = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, device, bias)
-    ws, nws, _keep = _scratch(workspace, exl3_mx4_linear_workspace_size, (w, m), device)
+    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, device, bias, stream)
+    ws, nws, _keep = _scratch(workspace, torch.empty, exl3_mx4_linear_workspace_size, (w, m), device, stream)
     _check(lib().exl3_mx4_linear(w._ref, _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt, ws, nws,
                                  on), "exl3_mx4_linear")
     return out
@@ -795,11 +811,11 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
     if layer.gate_up.codes.device != device:
         _refuse("x and the layer are on different devices")
     t = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, device, None)
+    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, device, None, stream)
     for v, what, dt in ((topk_ids, "topk_ids", torch.int32), (topk_weights, "topk_weights", torch.float32)):
         if v is not None and _tensor(v, what, dt, (t, topk)).device != device:
             _refuse(f"{what} is on another device than x")
-    ws, nws, _keep = _scratch(workspace, exl3_mx4_moe_workspace_size, (layer, t, topk), device)
+    ws, nws, _keep = _scratch(workspace, torch.zeros, exl3_mx4_moe_workspace_size, (layer, t, topk), device, stream)
     _check(lib().exl3_mx4_moe(layer._ref, x.data_ptr(), t, ldx, topk, out.data_ptr(), ldy, ydt, _ptr(topk_ids),
                               _ptr(topk_weights), ws, nws, on), "exl3_mx4_moe")
     return out

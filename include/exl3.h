@@ -382,8 +382,8 @@ typedef struct exl3_mx4 {
  *   code = x / S rounded to the nearest E2M1 value, ties to the even code,
  *   magnitudes above 6 to 6; the sign bit is x's, also where x / S rounds to 0
  *   x       [rows][ldx] of `dtype` (EXL3_F16 or EXL3_F32), ldx >= k, multiple
- *           of 8
- *   codes, scales  as above, written whole
+ *           of 8, 16-byte aligned
+ *   codes, scales  as above, written whole; they may not overlap x
  * A block of zeros gets scale byte 0.  A block that holds a NaN or an
  * infinity becomes a NaN block: scale byte 255, codes 0.  Every decision is
  * exact, so the output is bit-exact by definition.  rows == 0 returns
@@ -393,11 +393,11 @@ exl3_status exl3_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_
 
 /* exl3_mx4_reconstruct - the values an MXFP4 matrix stands for.
  *   out     [rows][ld_out] of `dtype` (EXL3_F16 or EXL3_F32), ld_out >= k,
- *           multiple of 8
+ *           multiple of 8, 16-byte aligned
  * Values are exact in fp32 except past its range (scale bytes 253 and 254:
  * magnitudes from 2^128 become infinity); fp16 rounds to nearest once.  What
  * exl3_mx4_quantize made of fp16 rows is exact in fp16.  NaN blocks give NaN.
- * rows * k must stay below 2^39.                                           */
+ * rows * k must stay below 2^35.                                           */
 exl3_status exl3_mx4_reconstruct(const exl3_mx4* w, void* out, int32_t dtype, int64_t ld_out,
                                  exl3_stream_t stream);
 
@@ -411,11 +411,10 @@ size_t exl3_mx4_matmul_workspace_size(const exl3_mx4* a, const exl3_mx4* b);
  *   a      [m][k] (rows = m), b [n][k] (rows = n), the same k; m and n any
  *   bias   fp16 [n] device pointer or NULL (added last, in fp32)
  *   y      [m][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= n; rows need no
- *          alignment beyond the element's own
+ *          alignment beyond the element's own.  y may not overlap an operand
  *   ws     device workspace of at least the queried size (may be NULL when
- *          that is 0), zero-filled before its first use; calls leave its
- *          arrival counts at zero, so it serves later calls without clearing.
- *          Calls that overlap in time on one workspace race.
+ *          that is 0), 16-byte aligned: scratch, whatever it holds before and
+ *          after.  Calls that overlap in time on one workspace race.
  * m == 0 or n == 0 returns EXL3_OK.  Calls whose launch would not fit the
  * hardware's grid (ceil(m/16) * ceil(n/16) >= 2^26) return EXL3_E_INVALID.
  * Results are the same bits on every run of one shape; a row's result may
@@ -435,8 +434,9 @@ size_t exl3_mx4_linear_workspace_size(const exl3_mx4* w, int64_t m);
  * activations, unrounded, against MXFP4 weights; products exact in fp32, sums
  * fp32.  For more than EXL3_MX4_LINEAR_MAX_ROWS rows the weights' bytes no
  * longer bound the product: quantize the rows and call exl3_mx4_matmul.
- *   w      [n][k] (rows = n)
- *   x      fp16 [m][ldx], ldx >= k, multiple of 8
+ *   w      [n][k] (rows = n).  Blocks with scale bytes outside 104 .. 140, whose
+ *          values fp16 cannot hold, are taken in a second, slower way
+ *   x      fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
  *   bias, y, ldy, y_dtype, ws   as for exl3_mx4_matmul
  * 0 <= m <= EXL3_MX4_LINEAR_MAX_ROWS; m == 0 or n == 0 returns EXL3_OK.    */
 exl3_status exl3_mx4_linear(const exl3_mx4* w, const uint16_t* bias, const void* x, int64_t m,
@@ -504,15 +504,17 @@ size_t exl3_mx4_moe_workspace_size(const exl3_mx4_moe_layer* layer, int64_t t, i
  *          (+ w_s[i] * down_s(a_s)),   a = silu(gate(x_i)) * up(x_i)
  * Activations are not rounded to 4 bits: x enters as fp16, a is held to 24
  * bits, every sum and the routing in fp32.
- *   x             fp16 [t][ldx], ldx >= hidden, multiple of 8
+ *   x             fp16 [t][ldx], ldx >= hidden, multiple of 8, 16-byte aligned
  *   topk          experts per token, 1..min(EXL3_MAX_TOPK, experts); equal
  *                 scores go to the lower expert
- *   y             [t][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= hidden
+ *   y             [t][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= hidden;
+ *                 it may not overlap x
  *   topk_ids      int32 [t][topk] device pointer or NULL: the choices, best
  *                 first
  *   topk_weights  fp32 [t][topk] device pointer or NULL: their weights
- *   ws            device workspace of at least the queried size, zero-filled
- *                 before its first use and then left to this entry point
+ *   ws            device workspace of at least the queried size, 16-byte
+ *                 aligned, zero-filled before its first use and then left to
+ *                 this entry point, which leaves its arrival counts at zero
  *                 (calls of any layer and size may share it, one after the
  *                 other); calls that overlap on it race
  * 0 <= t <= EXL3_MX4_MOE_MAX_TOKENS, experts <= EXL3_MX4_MOE_MAX_EXPERTS;

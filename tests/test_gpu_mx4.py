@@ -722,3 +722,35 @@ def test_linear_shared_rows_of_large_weights(m, n, k):
     ref, _ = M.product(x, wc)
     assert_within(y[:, cols], ref, bound(ref, M.product(x, np.nan_to_num(wc))[1], k, True))
     assert np.isnan(y).sum() == m
+
+
+def test_calls_on_another_stream_take_their_memory_there():
+    # outputs and workspaces that the call makes itself belong to its stream:
+    # while the current stream is busy, its freed blocks are not taken over
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(50)
+    x, l = moe_case(51, 16, 32, 512, 256, si=64)
+    layer, xd = moe_layer(l), G.to_dev(x)
+    w = mx(rand_mx(rng, 512, 8192))
+    rows = G.to_dev(rng.standard_normal((40, 8192)).astype(np.float16))
+    q = X.exl3_mx4_quantize(rows)
+    a, b = mx(rand_mx(rng, 700, 4128)), mx(rand_mx(rng, 1290, 4128))
+    calls = [lambda s: X.exl3_mx4_moe(xd, layer, 6, stream=s), lambda s: X.exl3_mx4_linear(rows, w, stream=s),
+             lambda s: X.exl3_mx4_matmul(a, b, stream=s), lambda s: X.exl3_mx4_quantize(rows, stream=s).codes,
+             lambda s: X.exl3_mx4_reconstruct(q, stream=s)]
+    want = [c(None) for c in calls]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    big = torch.randn(4096, 4096, device=G.dev())
+    for _ in range(3):
+        for c, y in zip(calls, want):
+            for _ in range(4):
+                junk = [torch.full((n,), 255, dtype=torch.uint8, device=G.dev()) for n in (1 << 14, 1 << 20, 1 << 22)]
+                big = torch.tanh(big)
+                del junk
+            got = c(s)
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device=G.dev()) for n in (1 << 14, 1 << 20, 1 << 22)]
+            s.synchronize()
+            assert torch.equal(got, y)
+            del junk
