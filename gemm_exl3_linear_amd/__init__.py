@@ -512,18 +512,26 @@ def _refuse(what: str):
     raise ValueError(what)
 
 
+# Host time counts for single tokens (a launch takes 3.7 us): what the calls below
+# look up each time is kept here, since an import inside a function costs 0.2 us.
+_dtype_codes = {}    # torch dtype -> EXL3_F16, EXL3_F32
+_cuda_queries = []   # current device, current stream of a device
+
+
 def _stream_for(t, what: str, stream) -> int:
     """The stream's handle (the current one if None) for a call on t, which has
     to be on the current device: the library launches there.  The raw query
     costs 0.1 us of host time where torch.cuda.current_stream() costs 2.9."""
-    import torch
     if not t.is_cuda:
         _refuse(f"{what} is not on a GPU")
+    if not _cuda_queries:
+        import torch
+        _cuda_queries.extend((torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream))
     i = t.get_device()
-    if i != torch._C._cuda_getDevice():
+    if i != _cuda_queries[0]():
         _refuse(f"{what} is on GPU {i}, not on the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(i)
+        return _cuda_queries[1](i)
     if stream.device_index != i:
         _refuse(f"the stream is of GPU {stream.device_index}, {what} is on GPU {i}")
     return int(stream.cuda_stream)
@@ -541,12 +549,20 @@ def _tensor(t, what: str, dtype, shape):
 
 
 def _f16_f32(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.float16:
-        return EXL3_F16
-    if t.dtype != torch.float32:
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float16: EXL3_F16, torch.float32: EXL3_F32})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         _refuse(f"{what} is {t.dtype}, not fp16 or fp32")
-    return EXL3_F32
+    return code
+
+
+def _f16_rows(x, cols: int) -> int:
+    """Row stride of the fp16 matrix x, checked."""
+    if _f16_f32(x, "x") != EXL3_F16:
+        _refuse(f"x is {x.dtype}, not fp16")
+    return _row_stride(x, "x", None, cols)
 
 
 def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
@@ -573,18 +589,20 @@ def _new(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
-def _scratch(workspace, make, need, args, device, stream):
-    """Address and bytes of the caller's workspace, or of one that make() gives
-    (need(*args) bytes), and the tensor that holds it."""
-    import torch
+def _scratch(workspace, zeroed: bool, need, args, like, stream):
+    """Address and bytes of the caller's workspace, or of a new one (need(*args)
+    bytes), and the tensor that holds it; on the device of `like`."""
     if workspace is None:
         n = need(*args)
         if not n:
             return 0, 0, None
-        workspace = _new(make, n, torch.uint8, device, stream)
-    elif workspace.numel() and (workspace.device != device or not workspace.is_contiguous()):
+        import torch
+        workspace = _new(torch.zeros if zeroed else torch.empty, n, torch.uint8, like.device, stream)
+        return workspace.data_ptr(), n, workspace
+    n = workspace.numel() * workspace.element_size()
+    if n and (workspace.get_device() != like.get_device() or not workspace.is_contiguous()):
         _refuse("the workspace is on another device than the operands, or not contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), n, workspace
 
 
 @dataclass(frozen=True)
@@ -700,7 +718,6 @@ class Exl3Mx4Moe:
 
 def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     """MXFP4 of fp16 or fp32 rows x [rows, k], k a multiple of 32."""
-    import torch
     ldx = _row_stride(x, "x", None, None)
     dtype = _f16_f32(x, "x")
     on = _stream_for(x, "x", stream)
@@ -708,10 +725,11 @@ def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     if out is None:
         if k == 0 or k % MX4_BLOCK:
             _refuse(f"x has {k} columns, not a multiple of {MX4_BLOCK}")
+        import torch
         out = Exl3Mx4(_new(torch.empty, (rows, k // 2), torch.uint8, x.device, stream),
                       _new(torch.empty, (rows, k // MX4_BLOCK), torch.uint8, x.device, stream))
     r = out._record
-    if r.rows != rows or r.k != k or out.codes.device != x.device:
+    if r.rows != rows or r.k != k or out.codes.get_device() != x.get_device():
         _refuse("out does not match x")
     _check(lib().exl3_mx4_quantize(x.data_ptr(), dtype, rows, k, ldx, r.codes, r.scales, on),
            "exl3_mx4_quantize")
@@ -720,12 +738,12 @@ def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
 
 def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     """The values w stands for, fp16 (the default) or fp32 [rows, k]."""
-    import torch
     on = _stream_for(w.codes, "w", stream)
     r = w._record
     if out is None:
+        import torch
         out = _new(torch.empty, (r.rows, r.k), dtype or torch.float16, w.codes.device, stream)
-    elif out.device != w.codes.device:
+    elif out.get_device() != w.codes.get_device():
         _refuse("out is on another device than w")
     ldo = _row_stride(out, "out", r.rows, r.k)
     _check(lib().exl3_mx4_reconstruct(w._ref, out.data_ptr(), _f16_f32(out, "out"), ldo, on),
@@ -733,17 +751,19 @@ def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     return out
 
 
-def _product_out(out, out_dtype, m: int, n: int, device, bias, stream):
-    """The output of a product (a new one if none is given), its row stride and type."""
-    import torch
+def _product_out(out, out_dtype, m: int, n: int, like, bias, stream):
+    """The output of a product (a new one if none is given), its row stride and
+    type; on the device of `like`."""
     if out is None:
-        out = _new(torch.empty, (m, n), out_dtype or torch.float16, device, stream)
-    elif out.device != device:
+        import torch
+        out = _new(torch.empty, (m, n), out_dtype or torch.float16, like.device, stream)
+    elif out.get_device() != like.get_device():
         _refuse("out is on another device than the operands")
     ldy = _row_stride(out, "out", m, n)
     if bias is not None:
+        import torch
         _tensor(bias, "bias", torch.float16, (n,))
-        if bias.device != device:
+        if bias.get_device() != like.get_device():
             _refuse("bias is on another device than the operands")
     return out, ldy, _f16_f32(out, "out")
 
@@ -754,13 +774,12 @@ def exl3_mx4_matmul_workspace_size(a: Exl3Mx4, b: Exl3Mx4) -> int:
 
 def exl3_mx4_matmul(a: Exl3Mx4, b: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4."""
-    import torch
-    device = a.codes.device
-    on = _stream_for(a.codes, "a", stream)
-    if b.codes.device != device:
+    like = a.codes
+    on = _stream_for(like, "a", stream)
+    if b.codes.get_device() != like.get_device():
         _refuse("a and b are on different devices")
-    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, device, bias, stream)
-    ws, nws, _keep = _scratch(workspace, torch.empty, exl3_mx4_matmul_workspace_size, (a, b), device, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, like, bias, stream)
+    ws, nws, _keep = _scratch(workspace, False, exl3_mx4_matmul_workspace_size, (a, b), like, stream)
     _check(lib().exl3_mx4_matmul(a._ref, b._ref, _ptr(bias), out.data_ptr(), ldy, ydt, ws, nws, on),
            "exl3_mx4_matmul")
     return out
@@ -773,18 +792,14 @@ def exl3_mx4_linear_workspace_size(w: Exl3Mx4, m: int) -> int:
 def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = x w^T (+ bias fp16 [n]): fp16 rows x [m, k], m up to 64,
     against MXFP4 weights w [n, k]."""
-    import torch
     r = w._record
-    ldx = _row_stride(x, "x", None, r.k)
-    if x.dtype != torch.float16:
-        _refuse(f"x is {x.dtype}, not fp16")
+    ldx = _f16_rows(x, r.k)
     on = _stream_for(x, "x", stream)
-    device = x.device
-    if w.codes.device != device:
+    if w.codes.get_device() != x.get_device():
         _refuse("x and w are on different devices")
     m = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, device, bias, stream)
-    ws, nws, _keep = _scratch(workspace, torch.empty, exl3_mx4_linear_workspace_size, (w, m), device, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, x, bias, stream)
+    ws, nws, _keep = _scratch(workspace, False, exl3_mx4_linear_workspace_size, (w, m), x, stream)
     _check(lib().exl3_mx4_linear(w._ref, _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt, ws, nws,
                                  on), "exl3_mx4_linear")
     return out
@@ -803,19 +818,16 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
     this function."""
     import torch
     hidden = layer._record.gate_up.k
-    ldx = _row_stride(x, "x", None, hidden)
-    if x.dtype != torch.float16:
-        _refuse(f"x is {x.dtype}, not fp16")
+    ldx = _f16_rows(x, hidden)
     on = _stream_for(x, "x", stream)
-    device = x.device
-    if layer.gate_up.codes.device != device:
+    if layer.gate_up.codes.get_device() != x.get_device():
         _refuse("x and the layer are on different devices")
     t = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, device, None, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, x, None, stream)
     for v, what, dt in ((topk_ids, "topk_ids", torch.int32), (topk_weights, "topk_weights", torch.float32)):
-        if v is not None and _tensor(v, what, dt, (t, topk)).device != device:
+        if v is not None and _tensor(v, what, dt, (t, topk)).get_device() != x.get_device():
             _refuse(f"{what} is on another device than x")
-    ws, nws, _keep = _scratch(workspace, torch.zeros, exl3_mx4_moe_workspace_size, (layer, t, topk), device, stream)
+    ws, nws, _keep = _scratch(workspace, True, exl3_mx4_moe_workspace_size, (layer, t, topk), x, stream)
     _check(lib().exl3_mx4_moe(layer._ref, x.data_ptr(), t, ldx, topk, out.data_ptr(), ldy, ydt, _ptr(topk_ids),
                               _ptr(topk_weights), ws, nws, on), "exl3_mx4_moe")
     return out
