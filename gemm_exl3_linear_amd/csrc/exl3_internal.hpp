@@ -130,7 +130,7 @@ hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t 
                              const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y,
                              int64_t ldy, bool y_f32, void* ws, hipStream_t s);
 // the LDS-tiled kernel for many rows
-bool mx4_gemm_fits(int64_t m, int64_t n, int64_t k);
+double mx4_gemm_cost(int64_t m, int64_t n, int64_t k);
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
                            const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y,

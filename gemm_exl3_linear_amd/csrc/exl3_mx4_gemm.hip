@@ -335,8 +335,14 @@ static GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-// Offsets into the staged scales are 32-bit.
-bool mx4_gemm_fits(int64_t m, int64_t n, int64_t k) { return gemm_plan(m, n, k).scales < ((size_t)1 << 32); }
+// Estimated us: two launches, a step, rounds, a third launch.  Offsets into the
+// staged scales are 32-bit: products past them are not for this kernel.
+double mx4_gemm_cost(int64_t m, int64_t n, int64_t k) {
+  const GemmPlan p = gemm_plan(m, n, k);
+  if (p.scales >= ((size_t)1 << 32)) return 1e30;
+  const double steps = (double)cdiv(cdiv(k, kStageK), p.splits);
+  return 6.8 + 0.55 * steps * (double)rounds_small(m, n) + (p.splits > 1 ? 4.0 : 0.0);
+}
 
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
   const GemmPlan p = gemm_plan(m, n, k);
@@ -378,7 +384,7 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
   }
   if (q.n > 0) launch_gemm_tiles<128, 128, 2, 2>(q, s);
   if (shared)
-    launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, p.splits, part}, s);
+    launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, 0, p.splits, part}, s);
   return hipGetLastError();
 }
 

@@ -179,7 +179,7 @@ size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, const uint16_t* bias,
                              const uint16_t* x, int64_t m, int64_t ldx, void* y, int64_t ldy, bool y_f32, void* ws,
                              hipStream_t s) {
-  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
+  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 0, 1, nullptr};
   if (use_wide(m, n, k) && ldx <= kMx4WideMaxStride) return launch_mx4_wide(q, wide_splits(n, k), ws, s);
   // pieces for few rows (exl3_mx4_rows.hpp; one row 5120 -> 17408: 12.8 us with four,
   // 13.1 with two, 16 with one); 32 columns a workgroup where those fill half the chip
@@ -189,13 +189,37 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
   return m <= 16 && cols32 ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
 }
 
-// Tiles through LDS (exl3_mx4_gemm.hip: two launches, three where k is shared)
-// from about 3e9 products on, the rows counted in the 64s of a tile here (us, here /
-// there: 64 rows 17408 -> 5120 29 / 21, 256 rows 5120 -> 5120 26 / 20, 256 rows 5120
-// -> 17408 57 / 27, 128 rows 5120 -> 5120 16 / 16, 100 rows 5120 -> 2048 11 / 13,
-// 256 rows 2048 -> 512 6.4 / 10.5).
+// How a product of more than 16 rows and columns is cut: tiles of 16 x 16, 32 x 32
+// or 64 x 32 by eight waves that share k here, or tiles through LDS
+// (exl3_mx4_gemm.hip).  Small tiles load more for a product and are more; the
+// estimates, in us, count the launch, a wave's turns over k and what further
+// rounds of the CUs add, which is less where k is too short for all waves.  As
+// measured (us, 16 / 32 / 64 x 32 / LDS, - not measured):
+//   100 rows 17408 ->   50   10.9   19.5   27.8    -
+//   333 rows  2080 -> 1111    8.7    7.6    7.5    -
+//   500 rows  5120 ->  500   13.3    8.4   11.0   14.7
+//   500 rows  2048 -> 1000   12.5    7.7    6.9   11.2
+//    32 rows 17408 -> 5120   28.5   20.3   25.6   19.8
+//  1000 rows  1024 -> 4000   35.9   21.8    -     10.1
+//  4000 rows    96 -> 5000  154.7  106.7    -     20.9
+enum class Mx4Cut { k16, k32, k64x32, kLds };
+static Mx4Cut matmul_cut(int64_t m, int64_t n, int64_t k) {
+  const double units = (double)((k + kMx4UnitK - 1) / kMx4UnitK), eighth = units / 8;
+  const double turns = __builtin_ceil(eighth), more = eighth < 0.35 ? 0.35 : (eighth < 1 ? eighth : turns);
+  auto cost = [&](int64_t rows, int64_t cols, double turn) {
+    const int64_t tiles = ((m + rows - 1) / rows) * ((n + cols - 1) / cols), rounds = (tiles + 255) / 256;
+    return 2.2 + turn * (turns + (double)(rounds - 1) * more);
+  };
+  Mx4Cut best = Mx4Cut::k16;
+  double least = cost(16, 16, 0.95);
+  const double others[3] = {cost(32, 32, 1.95), cost(64, 32, 2.9), mx4_gemm_cost(m, n, k)};
+  const Mx4Cut cuts[3] = {Mx4Cut::k32, Mx4Cut::k64x32, Mx4Cut::kLds};
+  for (int i = 0; i < 3; ++i)
+    if (others[i] < least) least = others[i], best = cuts[i];
+  return best;
+}
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
-  return m > 16 && (double)((m + 63) / 64 * 64) * (double)n * (double)k >= 3.3e9 && mx4_gemm_fits(m, n, k);
+  return m > 16 && n > 16 && matmul_cut(m, n, k) == Mx4Cut::kLds;
 }
 size_t mx4_matmul_workspace(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? mx4_gemm_workspace(m, n, k) : 0;
@@ -205,16 +229,25 @@ hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t 
                              const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y, int64_t ldy,
                              bool y_f32, void* ws, hipStream_t s) {
   if (use_gemm(m, n, k)) return launch_mx4_gemm(a, a_scales, m, b, b_scales, n, k, bias, y, ldy, y_f32, ws, s);
-  const Mx4RowsArgs q{a, a_scales, 0, b, b_scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 1, nullptr};
+  Mx4RowsArgs q{a, a_scales, 0, b, b_scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 0, 1, nullptr};
+  if (m > 16 && n > 16) {
+    const Mx4Cut cut = matmul_cut(m, n, k);
+    if (cut == Mx4Cut::k16) return launch_rows<true, 1, 1, 1, 8>(q, s);
+    if (cut == Mx4Cut::k32) return launch_rows<true, 2, 1, 2, 8>(q, s);
+    return launch_rows<true, 4, 1, 2, 8>(q, s);
+  }
+  if (m > 16 && m > n) {  // few columns: as few rows, the operands' places changed
+    q.a = b, q.a_scales = b_scales, q.m = n;
+    q.b = a, q.b_scales = a_scales, q.n = m;
+    q.swapped = 1;
+  }
   // 16 rows or fewer in 32 columns a workgroup where the chip stays full, for
   // fewer loads of a; not for a row or two, whose a comes from cache, over very many
   // columns (us, 16 / 32 columns: 16 rows 17408 -> 5120 20.0 / 16.0, 17408 -> 2048
   // 11.4 / 15.7, 2048 -> 8192 5.1 / 4.6; one row 17408 -> 5120 15.0 / 12.8, 5120 ->
   // 17408 11.5 / 12.2)
-  if (m <= 16)
-    return n >= 4096 && (m > 4 || n < 16384) ? launch_rows<true, 1, 1, 2, 8>(q, s) : launch_rows<true, 1, 1, 1, 8>(q, s);
-  if (((m + 63) / 64) * ((n + 63) / 64) >= 160) return launch_rows<true, 4, 1, 4, 4>(q, s);
-  return launch_rows<true, 4, 1, 2, 8>(q, s);
+  return q.n >= 4096 && (q.m > 4 || q.n < 16384) ? launch_rows<true, 1, 1, 2, 8>(q, s)
+                                                 : launch_rows<true, 1, 1, 1, 8>(q, s);
 }
 
 }  // namespace exl3

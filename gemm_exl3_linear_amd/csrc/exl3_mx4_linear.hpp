@@ -17,17 +17,19 @@ struct Mx4RowsArgs {
   int64_t m, n;
   int kb;                 // blocks of 32 in a row
   int y_f32;
+  int swapped;            // y is [n][ldy], bias [m]: the product's operands changed places
   uint32_t col_tiles;     // tiles of 16 NG columns
   int splits;             // workgroups that share a tile's k
   float* part;            // their sums [split][m][n], where there are several
 };
 
 __device__ __forceinline__ void mx4_store(const Mx4RowsArgs& q, int64_t row, int64_t col, float v) {
-  const float y = v + (q.bias ? h2f(q.bias[col]) : 0.f);
+  const float y = v + (q.bias ? h2f(q.bias[q.swapped ? row : col]) : 0.f);
+  const int64_t at = q.swapped ? col * q.ldy + row : row * q.ldy + col;
   if (q.y_f32)
-    static_cast<float*>(q.y)[row * q.ldy + col] = y;
+    static_cast<float*>(q.y)[at] = y;
   else
-    static_cast<uint16_t*>(q.y)[row * q.ldy + col] = f2h(y);
+    static_cast<uint16_t*>(q.y)[at] = f2h(y);
 }
 
 // y = sum of the splits in order (+ bias).

@@ -754,3 +754,29 @@ def test_calls_on_another_stream_take_their_memory_there():
             s.synchronize()
             assert torch.equal(got, y)
             del junk
+
+
+# every cut of a product: 16 x 16, 32 x 32 and 64 x 32 tiles at lengths with and
+# without whole units, LDS tiles of a short k, and few columns, where the operands
+# change places
+CUTS = [(100, 50, 5152), (30, 30, 10240), (300, 300, 2048), (500, 500, 5120), (24, 2100, 2080), (17, 6000, 1024),
+        (333, 1111, 2080), (500, 1000, 2048), (1500, 1400, 96), (2050, 1930, 32), (600, 1, 96), (129, 16, 2080),
+        (5000, 3, 544), (4100, 16, 288), (17, 16, 64)]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m,n,k", CUTS)
+def test_matmul_cuts(m, n, k, f32):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + 3 * n + k)
+    a, b = rand_mx(rng, m, k), rand_mx(rng, n, k, lo=112, hi=122)
+    a[1][m // 3, 0] = b[1][n - 1, -1] = 255
+    bias = rng.standard_normal(n).astype(np.float16)
+    buf = torch.full((m, n + 3), 7.0, dtype=torch.float32 if f32 else torch.float16, device=G.dev())
+    y = X.exl3_mx4_matmul(mx(a), mx(b), bias=G.to_dev(bias), out=buf[:, 1:n + 1])
+    da, db = M.decode(*a), M.decode(*b)
+    ref, _ = M.product(da, db, bias)
+    mag = M.product(np.nan_to_num(da), np.nan_to_num(db), bias)[1]
+    assert_within(y.cpu().numpy(), ref, bound(ref, mag, k, f32), f"{m}x{n}x{k}")
+    assert (buf[:, 0] == 7.0).all() and (buf[:, n + 1:] == 7.0).all()
