@@ -156,37 +156,69 @@ static hipError_t launch_rows(Mx4RowsArgs q, hipStream_t s) {
   return hipGetLastError();
 }
 
-// fp16 rows shared through LDS (exl3_mx4_wide.hip) where they are many, or 9 to 16
-// of large weights (us, here / there: 16 rows 17408 -> 5120 29 / 20, 5120 -> 17408
-// 26 / 22, 5120 -> 5120 11 / 13, 2048 -> 8192 6 / 10; 6 rows 17408 -> 5120 18 / 19).
-// Rows too far apart for its 32-bit offsets are taken here, 16 at a time.
-static bool use_wide(int64_t m, int64_t n, int64_t k) { return m > 16 || (m > 8 && n * k >= 80000000); }
-
-// Shares of k there: as many as fill the chip's CUs once, two units each at least
-// (us, for 2 / 3 / 4 / 5 / 6 / 8 shares: 37 rows 17408 -> 5120, 40 tiles, 42 / 32 / 27 /
-// 25 / 24 / 33; 20 rows 8192 -> 8192, 64 tiles, 22 / 19 / 17 / 25 / 24 / 23).
+// Shares of k of the rows shared through LDS: as many as fill the chip's CUs once,
+// two units each at least (us, for 2 / 3 / 4 / 5 / 6 / 8 shares: 37 rows 17408 -> 5120,
+// 40 tiles, 42 / 32 / 27 / 25 / 24 / 33; 20 rows 8192 -> 8192, 64 tiles, 22 / 19 / 17 /
+// 25 / 24 / 23).
 static int wide_splits(int64_t n, int64_t k) {
   const int64_t tiles = (n + 127) / 128, units = (k + kMx4UnitK - 1) / kMx4UnitK;
   int64_t s = 256 / tiles;
   if (s > units / 2) s = units / 2;
   return s < 1 ? 1 : (int)s;
 }
+
+// How nine rows and more are cut: 16 rows and 16 or 32 columns a workgroup here, or
+// all rows shared through LDS for 128 columns (exl3_mx4_wide.hip).  The estimates,
+// in us, count the launch, a wave's turns over k and what further rounds of the CUs
+// add; there, a start and steps that grow with the rows, and a second launch for
+// shares of k.  As measured (us, 16 / 32 / LDS):
+//   64 rows  2048 ->   512    5.2    5.9   11.0
+//   64 rows  5120 ->  2048   14.9   10.9   13.6
+//   20 rows   512 ->  8192    5.5    4.6    7.8
+//   40 rows 17408 ->    64   21.7   26.2   11.9
+//   32 rows  5120 ->  5120   21.0   17.8   14.2
+//   16 rows 17408 ->  5120    -     28.9   20.0
+//   16 rows  5120 ->  5120    -     11.1   12.7
+enum class Mx4RowsCut { k16, k32, kLds };
+static Mx4RowsCut rows_cut(int64_t m, int64_t n, int64_t k) {
+  const int64_t units = (k + kMx4UnitK - 1) / kMx4UnitK, row_tiles = (m + 15) / 16;
+  const double turns = (double)((units + 7) / 8), more = units < 2 ? 0.25 : (units < 8 ? (double)units / 8 : turns);
+  auto cost = [&](int64_t cols, double start, double turn) {
+    const int64_t rounds = (row_tiles * ((n + cols - 1) / cols) + 255) / 256;
+    return start + turn * (turns + (double)(rounds - 1) * more);
+  };
+  const int64_t tiles = (n + 127) / 128, shares = wide_splits(n, k);
+  const double steps = (double)((units + shares - 1) / shares * ((tiles * shares + 255) / 256));
+  const double c16 = cost(16, 2.9, 2.2), c32 = cost(32, 3.2, 2.6);
+  const double lds = 4.6 + 0.8 * (double)row_tiles + (0.8 + 0.1 * (double)row_tiles) * steps + (shares > 1 ? 2.2 : 0.0);
+  if (lds < c16 && lds < c32) return Mx4RowsCut::kLds;
+  return c16 <= c32 ? Mx4RowsCut::k16 : Mx4RowsCut::k32;
+}
 size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  const int s = use_wide(m, n, k) ? wide_splits(n, k) : 1;
+  if (m <= 8 || rows_cut(m, n, k) != Mx4RowsCut::kLds) return 0;
+  const int s = wide_splits(n, k);
   return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
 }
 
 hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, const uint16_t* bias,
                              const uint16_t* x, int64_t m, int64_t ldx, void* y, int64_t ldy, bool y_f32, void* ws,
                              hipStream_t s) {
-  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, (int)(k / kMx4Block), y_f32, 0, 0, 1, nullptr};
-  if (use_wide(m, n, k) && ldx <= kMx4WideMaxStride) return launch_mx4_wide(q, wide_splits(n, k), ws, s);
-  // pieces for few rows (exl3_mx4_rows.hpp; one row 5120 -> 17408: 12.8 us with four,
-  // 13.1 with two, 16 with one); 32 columns a workgroup where those fill half the chip
-  const bool cols32 = n >= 2048;
-  if (m <= 4) return launch_rows<false, 1, 4, 1, 8>(q, s);
-  if (m <= 8) return cols32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
-  return m <= 16 && cols32 ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
+  const int kb = (int)(k / kMx4Block);
+  const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, kb, y_f32, 0, 0, 1, nullptr};
+  // up to 8 rows: pieces (exl3_mx4_rows.hpp), four where k is long enough for the
+  // fewer loads to show, and 32 columns a workgroup where those fill half the chip
+  // and x has more than a row to fetch (us: one row 5120 -> 17408 four pieces 12.8, two
+  // 13.6, one 16; 2048 -> 2048 4.0 / 3.7; 16 / 32 columns: 4 rows 17408 -> 5120 21.3 /
+  // 16.7, 5120 -> 2048 5.9 / 7.3, 8 rows 5120 -> 5120 10.9 / 8.6, 5120 -> 2048 6.7 / 8.0,
+  // one row 5120 -> 17408 12.8 / 14.7)
+  const bool cols32 = n >= 4096;
+  if (m <= 4 && k >= 4096)
+    return m > 1 && cols32 ? launch_rows<false, 1, 4, 2, 8>(q, s) : launch_rows<false, 1, 4, 1, 8>(q, s);
+  if (m <= 8) return m > 1 && cols32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
+  const Mx4RowsCut cut = rows_cut(m, n, k);
+  // rows too far apart for 32-bit offsets are taken here, 16 at a time
+  if (cut == Mx4RowsCut::kLds && ldx <= kMx4WideMaxStride) return launch_mx4_wide(q, wide_splits(n, k), ws, s);
+  return cut == Mx4RowsCut::k32 ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
 }
 
 // How a product of more than 16 rows and columns is cut: tiles of 16 x 16, 32 x 32

@@ -780,3 +780,53 @@ def test_matmul_cuts(m, n, k, f32):
     mag = M.product(np.nan_to_num(da), np.nan_to_num(db), bias)[1]
     assert_within(y.cpu().numpy(), ref, bound(ref, mag, k, f32), f"{m}x{n}x{k}")
     assert (buf[:, 0] == 7.0).all() and (buf[:, n + 1:] == 7.0).all()
+
+
+# rows shared through LDS: two, three and four groups of 16, k shared by many and
+# whole, lengths that end inside a unit, weight rows that start at any byte of a dword
+# of scales, a column over a tile, and rows too far apart for that
+@pytest.mark.parametrize("m,n,k,pitch", [(17, 129, 17440, 0), (32, 2, 12320, 8), (33, 257, 13344, 8), (49, 128, 10336, 0),
+                                         (64, 130, 17440, 16), (64, 5000, 2080, 0), (23, 17000, 416, 8),
+                                         (18, 33, 17440, (1 << 24) + 8)])
+def test_linear_long_shared_rows(m, n, k, pitch):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n + k)
+    w = rand_mx(rng, n, k, lo=112, hi=122)
+    w[1][n - 1, -1], w[1][n // 2, 3] = 90, 255      # outside fp16, NaN
+    w[0][0, 16:32], w[1][0, 1] = 0, 0               # zeros at 2^-127
+    x = rng.standard_normal((m, k)).astype(np.float16)
+    bias = rng.standard_normal(n).astype(np.float16)
+    if pitch > k:
+        xd = torch.empty((m - 1) * pitch + k, dtype=torch.float16, device=G.dev()).as_strided((m, k), (pitch, 1))
+    else:
+        xd = torch.full((m, k + pitch), float("nan"), dtype=torch.float16, device=G.dev())[:, :k]
+    xd.copy_(G.to_dev(x))
+    wd, bd = mx(w), G.to_dev(bias)
+    y = X.exl3_mx4_linear(xd, wd, bias=bd, out_dtype=torch.float32)
+    cols = np.unique(np.concatenate([np.arange(0, n, max(1, n // 200)), [0, n // 2], np.arange(max(0, n - 140), n)]))
+    wc = M.decode(w[0][cols], w[1][cols])
+    ref, _ = M.product(x, wc, bias[cols])
+    got = y.cpu().numpy()
+    assert_within(got[:, cols], ref, bound(ref, M.product(x, np.nan_to_num(wc), bias[cols])[1], k, True), f"{m}x{n}x{k}")
+    assert np.isnan(got).sum() == m
+    ws = torch.full((X.exl3_mx4_linear_workspace_size(wd, m) + 16,), 255, dtype=torch.uint8, device=G.dev())
+    for _ in range(2):
+        assert torch.equal(torch.nan_to_num(X.exl3_mx4_linear(xd, wd, bias=bd, out_dtype=torch.float32, workspace=ws)),
+                           torch.nan_to_num(y))
+
+
+@pytest.mark.parametrize("m,n,k", [(2, 4100, 4128), (4, 5000, 4640), (3, 70, 4128), (4, 4100, 96), (8, 4097, 288),
+                                   (5, 4000, 2080), (9, 2000, 2080), (12, 9000, 544), (40, 600, 2080), (64, 8200, 288)])
+def test_linear_cuts(m, n, k):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n + k)
+    w = rand_mx(rng, n, k, lo=112, hi=122)
+    w[1][n - 1, -1], w[1][n // 2, 0] = 90, 255
+    x = rng.standard_normal((m, k)).astype(np.float16)
+    bias = rng.standard_normal(n).astype(np.float16)
+    y = X.exl3_mx4_linear(G.to_dev(x), mx(w), bias=G.to_dev(bias), out_dtype=torch.float32).cpu().numpy()
+    wd = M.decode(*w)
+    ref, _ = M.product(x, wd, bias)
+    assert_within(y, ref, bound(ref, M.product(x, np.nan_to_num(wd), bias)[1], k, True), f"{m}x{n}x{k}")
