@@ -608,12 +608,12 @@ int moe_splits(const Mx4MoeDesc& d) {
   return s < 1 ? 1 : (s > 8 ? 8 : s);
 }
 
-// Shares of the down product's entries: a task a wave at least, where there
+// Shares of the down product's entries: about a task a wave, where there
 // may be so many, and no more than the chip takes at once (two workgroups a CU).
 int moe_down_splits(const Mx4MoeDesc& d, int64_t t, int topk) {
   const int units = (d.inter + kMx4UnitK - 1) / kMx4UnitK, tasks = moe_most(d, t, topk) * units;
   const int room = 512 / (d.hidden / 16);
-  int s = tasks / kMoeDownWaves;
+  int s = (tasks + kMoeDownWaves / 2) / kMoeDownWaves;
   if (s > room) s = room;
   return s < 1 ? 1 : s;
 }
