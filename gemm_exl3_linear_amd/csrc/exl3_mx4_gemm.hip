@@ -262,7 +262,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
       for (int k = 0; k < MI; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4_t*>(out + (16 * k + r) * 128 + (((4 * j + g) ^ (r & 7)) * 16)) = acc[2 * half + j][k];
+          *reinterpret_cast<float4_t*>(out + (16 * k + r) * 128 + (((4 * j + g) ^ (r & 7)) * 16)) =
+              acc[2 * half + j][k];
       const int c = lane & 7;
       const int64_t col = wave_n + 32 * half + 4 * c;
 #pragma unroll 4
@@ -310,7 +311,9 @@ static uint32_t scale_groups(int64_t rows) { return (uint32_t)((rows + 255) / 25
 // 212 without, 201 with; 1024 rows 75 / 68).  Small tiles that would
 // leave CUs empty share k, six steps a workgroup at least (64 rows 17408 -> 5120:
 // 48 unshared, 21 shared; eight steps shared by two and added up, 4096 rows 2048 ->
-// 512: 12 unshared, 18 shared).
+// 512: 12 unshared, 18 shared), and long k by two workgroups a CU where one each
+// would leave many without (1500 rows 17408 -> 1500: 55 / 41; ten steps each, 512
+// rows 5120 -> 5120: 21 / 27).
 struct GemmPlan {
   int64_t large;  // columns of large tiles, the first ones
   int splits;     // of k, of small tiles where there are no large ones
@@ -328,8 +331,9 @@ static GemmPlan gemm_plan(int64_t m, int64_t n, int64_t k) {
     p.large = cols;
   if (p.large == 0) {
     const int64_t small = cdiv(m, 128) * cdiv(n, 128);
-    int64_t s = 256 / small;
-    if (s > steps / 6) s = steps / 6;
+    int64_t s = 256 / small < steps / 6 ? 256 / small : steps / 6;
+    const int64_t two = 512 / small < steps / 14 ? 512 / small : steps / 14;
+    if (s < 3 && two > s) s = two;
     if (s > 1) p.splits = (int)s, p.part = (size_t)s * m * n * sizeof(float);
   }
   return p;
@@ -370,7 +374,8 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
                      StageScales{a_scales, reinterpret_cast<uint32_t*>(sa), m, ga},
                      StageScales{b_scales, reinterpret_cast<uint32_t*>(sb), n, gb}, kb, steps);
   const bool shared = p.splits > 1;
-  Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, shared ? nullptr : bias, y, ldy, m, n, kb, steps, y_f32, 0, 0, 0, p.splits};
+  Mx4GemmArgs q{a, b, sa, sb, ga * 512, gb * 512, shared ? nullptr : bias, y, ldy, m, n, kb, steps, y_f32, 0, 0, 0,
+                p.splits};
   if (shared) q.y = part, q.ldy = n, q.y_f32 = 1;
   q.wide = (reinterpret_cast<uintptr_t>(q.y) & 15) == 0 && q.ldy % (q.y_f32 ? 4 : 8) == 0 && (!shared || n % 4 == 0);
   if (p.large > 0) {
@@ -384,7 +389,8 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
   }
   if (q.n > 0) launch_gemm_tiles<128, 128, 2, 2>(q, s);
   if (shared)
-    launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, 0, p.splits, part}, s);
+    launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, 0, p.splits, part},
+                           s);
   return hipGetLastError();
 }
 

@@ -161,7 +161,8 @@ __device__ __forceinline__ void moe_route_token(const MoeArgs& q, const uint32_t
   }
   weight = scores[id];
   if (q.d.scoring == 0) {
-    const float high = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);  // the highest l + b (NaN if every one is)
+    // the highest l + b (NaN if every one is)
+    const float high = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum += lane + 64 * i < q.d.experts ? exp_f(scores[lane + 64 * i] - high) : 0.f;
@@ -662,7 +663,8 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
   const MoeLayout L = moe_layout(d, t, topk);
   unsigned char* w = static_cast<unsigned char*>(ws);
   const int most = moe_most(d, t, topk), splits = moe_splits(d);
-  const MoeArgs q{d, x, ldx, (int)t, topk, y, ldy, y_f32, ids, weights, most, {(int)t * topk, (int)t}, splits, L.lstride,
+  const MoeArgs q{d, x, ldx, (int)t, topk, y, ldy, y_f32, ids, weights, most, {(int)t * topk, (int)t}, splits,
+                  L.lstride,
                   reinterpret_cast<uint32_t*>(w + L.arrived), reinterpret_cast<float*>(w + L.logits),
                   reinterpret_cast<MoeEntry*>(w + L.entries), reinterpret_cast<int*>(w + L.count),
                   reinterpret_cast<float*>(w + L.wtab),
@@ -674,7 +676,8 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
   else if (d.experts <= 512) launch_router<8>(q, s);
   else launch_router<16>(q, s);
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
-  hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s, q);
+  hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s,
+                     q);
   hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
   return hipGetLastError();
 }

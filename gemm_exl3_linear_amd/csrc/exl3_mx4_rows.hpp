@@ -41,7 +41,8 @@ struct Mx4Row {
   const uint8_t* scales;
   uint32_t code_off, scale_off;
 };
-__device__ __forceinline__ Mx4Row mx4_row(const uint8_t* codes, const uint8_t* scales, int64_t first, uint32_t row, int kb) {
+__device__ __forceinline__ Mx4Row mx4_row(const uint8_t* codes, const uint8_t* scales, int64_t first, uint32_t row,
+                                          int kb) {
   return Mx4Row{codes + first * kb * 16, scales + first * kb, row * (uint32_t)kb * 16u, row * (uint32_t)kb};
 }
 
@@ -83,7 +84,8 @@ struct Mx4X {
 // piece q P + r / kRows, of row r % kRows; zeros past the row's end or where the
 // row is not there.  x: this lane's row.
 template <int P>
-__device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g, int r, int q) {
+__device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g, int r,
+                                              int q) {
   const int b = u * kMx4UnitBlocks + 4 * h + g;
   u32x4_t v = {0u, 0u, 0u, 0u};
   if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * (q * P + r / Mx4X<P>::kRows));
@@ -108,8 +110,8 @@ __device__ __forceinline__ bool mx4_fp16_scale(const Mx4Unit& w, int h, int g, f
 // lane's blocks are not all exact in fp16, and what was added is of no use.  (A
 // block of zeros is, at any scale but NaN.)
 template <int MG, int P, int NG>
-__device__ __forceinline__ bool mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG], int h, int g,
-                                            float4_t (&acc)[NG][MG][P]) {
+__device__ __forceinline__ bool mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG], int h,
+                                            int g, float4_t (&acc)[NG][MG][P]) {
   bool exact = true;
 #pragma unroll
   for (int ng = 0; ng < NG; ++ng) {
@@ -130,8 +132,8 @@ __device__ __forceinline__ bool mx4_mma_f16(const f16x8_t (&x)[MG][Mx4X<P>::kLoa
 // the sums by the block's scale.  The other blocks are taken out of both operands:
 // an infinite x times their zeros would be NaN.
 template <int MG, int P, int NG>
-__device__ __forceinline__ void mx4_mma_f16_blocks(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG], int h,
-                                                   int g, float4_t (&acc)[NG][MG][P]) {
+__device__ __forceinline__ void mx4_mma_f16_blocks(const f16x8_t (&x)[MG][Mx4X<P>::kLoads], const Mx4Unit (&w)[NG],
+                                                   int h, int g, float4_t (&acc)[NG][MG][P]) {
 #pragma unroll 1
   for (int b = 0; b < 4; ++b) {
     const uint32_t keep = g == b ? 0xFFFFFFFFu : 0u;

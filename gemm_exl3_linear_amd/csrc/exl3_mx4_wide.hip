@@ -127,7 +127,8 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
 #pragma unroll
     for (int mg = 0; mg < MG; ++mg)
       x[mg][j] = __builtin_bit_cast(
-          f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine + ((uint32_t)(4 * (4 * h + g) + j) ^ wide_turn(r)) * 16));
+          f16x8_t, lds_read16(stage + kX + (16 * mg + r) * kWideLine +
+                              ((uint32_t)(4 * (4 * h + g) + j) ^ wide_turn(r)) * 16));
   };
 
 #pragma unroll

@@ -830,3 +830,16 @@ def test_linear_cuts(m, n, k):
     wd = M.decode(*w)
     ref, _ = M.product(x, wd, bias)
     assert_within(y, ref, bound(ref, M.product(x, np.nan_to_num(wd), bias)[1], k, True), f"{m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 1300, 4640), (1417, 17, 13664), (2100, 700, 7200)])
+def test_matmul_long_k_shared_by_two(m, n, k):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m)
+    a, b = rand_mx(rng, m, k), rand_mx(rng, n, k, lo=112, hi=122)
+    bias = rng.standard_normal(n).astype(np.float16)
+    y = X.exl3_mx4_matmul(mx(a), mx(b), bias=G.to_dev(bias), out_dtype=torch.float32).cpu().numpy()
+    rows = np.unique(np.concatenate([np.arange(0, m, 17), np.arange(m - 130, m)]))
+    ref, mag = M.product(M.decode(a[0][rows], a[1][rows]), M.decode(*b), bias)
+    assert_within(y[rows], ref, bound(ref, mag, k, True), f"{m}x{n}x{k}")
