@@ -10,7 +10,10 @@
 //
 // Both kernels are bound by HBM.  A thread takes eight elements, so a wave's
 // loads, its 4-byte code stores and its value stores are contiguous; the four
-// lanes of a block meet in two quad permutations.
+// lanes of a block meet in two quad permutations.  Measured: 4096 x 5120 fp16
+// 11.6 us there and 8.7 back (52 MB each), 10007 x 6880 fp32 75 and 63 us (312 MB
+// each, 4.2 and 5.0 TB/s; a 2 GiB copy reaches 4.9).  One row of 5120: 1.6 us each,
+// a launch.
 #include "exl3_internal.hpp"
 #include "exl3_mx4.hpp"
 

@@ -1,5 +1,5 @@
-// exl3_mx4_linear for 17 to 64 rows, and from 9 on of large weights: fp16 rows shared by a workgroup through
-// LDS.
+// exl3_mx4_linear for more rows and large weights: fp16 rows shared by a
+// workgroup through LDS.
 //
 // With so many rows the waves can no longer each fetch the rows for their share
 // of k (exl3_mx4_rows.hpp): a wave's 16 columns bring 2 KB of weights for 8 KB of
@@ -16,7 +16,13 @@
 // does one after the other leaves the rest of the CU idle (copies 500 cycles, LDS
 // reads 900, product 1000, of 3000): a quarter of the product is followed by a
 // quarter of the copies and by the reads of the next stage into the registers
-// that it has freed.
+// that it has freed.  (Quarters of a unit for 64 columns a wave, with fewer LDS
+// reads, were 12 % slower; shares of k across the tiles' ends, to fill the chip for
+// any number of tiles, 10 %.)
+//
+// Measured: 37 rows 17408 -> 5120 (49 MB) 23.6 us: 11.3 steps of 1.25 us, 3.4 TB/s of
+// weights, then start, end and the second launch.  The copies bound a step: alone
+// they take 1.1 us with 16 rows and 1.5 with 48, the rest without them 0.95.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_lds.hpp"
 #include "exl3_mx4_linear.hpp"
