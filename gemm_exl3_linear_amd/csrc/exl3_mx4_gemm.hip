@@ -9,11 +9,10 @@
 // 128 x 64 a wave of 256 x 256 is as large as its registers allow.
 //
 // What bounds it: 4096 rows 5120 -> 17408, 201 us, 3.6 PFLOP/s.  The 256 x 256
-// kernel takes 181 of them; its matrix cores are busy 0.47 of the time of a CU's
-// workgroups (0.38 with the fifth round cut off the whole).  A loop of these
-// instructions from registers alone runs at 7.0 to 7.2 PFLOP/s with random codes
-// and at 9.5 with zeros: the clock falls with what the matrix cores switch, and
-// this kernel, too, is a fifth faster a step on zeros (1.49 against 1.83 us).
+// kernel takes 181 of them, with the matrix cores busy 0.44 of the time.  A loop of
+// these instructions from registers alone runs at 7.0 to 7.2 PFLOP/s with random
+// codes and at 9.5 with zeros: the clock falls with what the matrix cores switch,
+// and this kernel, too, is a fifth faster a step on zeros (1.49 against 1.83 us).
 // Without the copies a step takes 1.52 us, with all tiles the same (nothing but L2
 // hits) still 1.83.  Reading operands one fragment ahead of the products across
 // the barrier (4 % slower), and copies through registers (9 % slower), did not pay.
