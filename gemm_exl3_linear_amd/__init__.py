@@ -568,15 +568,15 @@ def _f16_rows(x, cols: int) -> int:
 def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
     """Row stride of t, checked as a matrix of contiguous rows.  With fewer than
     two rows the stride says nothing and the width, rounded up to 8, stands in."""
-    if t.dim() != 2:
+    stride = t.stride()
+    if len(stride) != 2:
         _refuse(f"{what} is not a matrix")
     m, n = t.shape
     if (rows is not None and m != rows) or (cols is not None and n != cols):
         _refuse(f"{what} has shape {(m, n)}, not {(rows, cols)}")
-    ld, one = t.stride()
-    if one != 1 and n > 1:
+    if stride[1] != 1 and n > 1:
         _refuse(f"{what} does not have contiguous rows")
-    return ld if m > 1 else -(-n // 8) * 8
+    return stride[0] if m > 1 else -(-n // 8) * 8
 
 
 def _new(make, shape, dtype, device, stream):
@@ -599,7 +599,7 @@ def _scratch(workspace, zeroed: bool, need, args, like, stream):
         import torch
         workspace = _new(torch.zeros if zeroed else torch.empty, n, torch.uint8, like.device, stream)
         return workspace.data_ptr(), n, workspace
-    n = workspace.numel() * workspace.element_size()
+    n = workspace.nbytes
     if n and (workspace.get_device() != like.get_device() or not workspace.is_contiguous()):
         _refuse("the workspace is on another device than the operands, or not contiguous")
     return workspace.data_ptr(), n, workspace

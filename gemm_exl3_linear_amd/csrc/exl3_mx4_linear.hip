@@ -137,14 +137,27 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   }
 }
 
-// y = sum of the splits in order (+ bias).
+// y = sum of the splits in order (+ bias), eight splits' loads at a time where
+// there are so many (20 rows 17408 -> 1001, 17 splits: 13.2 us, 14.4 with four).
+template <int N>
+__device__ __forceinline__ void add_splits(const float* p, int64_t size, int& s, int splits, float& v) {
+  for (; s + N <= splits; s += N) {
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = p[(s + i) * size];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v += w[i];
+  }
+}
 __global__ __launch_bounds__(256) void mx4_rows_finish(Mx4RowsArgs q) {
   const int64_t row = blockIdx.y, col = (int64_t)blockIdx.x * 256 + threadIdx.x, size = q.m * q.n;
   if (col >= q.n) return;
   const float* p = q.part + row * q.n + col;
-  float v = *p;
-#pragma unroll 4
-  for (int s = 1; s < q.splits; ++s) v += p[s * size];
+  float v = 0.f;
+  int s = 0;
+  add_splits<8>(p, size, s, q.splits, v);
+  add_splits<3>(p, size, s, q.splits, v);
+  add_splits<1>(p, size, s, q.splits, v);
   mx4_store(q, row, col, v);
 }
 
