@@ -34,7 +34,7 @@ namespace exl3 {
 
 constexpr int kMoeTokens = 16;
 constexpr int kMoeMaxDim = 65536;  // of hidden and of an expert
-constexpr int kMoeGateUpWaves = 8, kMoeDownWaves = 16;
+constexpr int kMoeDownWaves = 16;
 
 // A listed expert: its tokens, in order, and the first of their rows in the
 // activations.
@@ -376,10 +376,9 @@ __device__ __forceinline__ int load_uniform(const int* p) {
   return *(__attribute__((address_space(4))) const int*)(uintptr_t)p;
 }
 
-// Sums of 16 weight rows over every fourth unit of k from `first`; operand rows
+// Sums of 16 weight rows over every SHARES-th unit of k from `first`; operand rows
 // are the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
-constexpr int kMoeGateUpShares = kMoeGateUpWaves / 2;
-template <int P>
+template <int P, int SHARES>
 __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const Mx4Row& row,
                                                      int first, int g, int r) {
   constexpr int kLoads = Mx4X<P>::kLoads;
@@ -392,7 +391,7 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
   for (int p = 0; p < P; ++p) acc[0][0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   bool exact = true;
-  for (int u = first; u < units; u += kMoeGateUpShares) {
+  for (int u = first; u < units; u += SHARES) {
     Mx4Unit w[1];
     mx4_load_unit(row, kb, u, g, w[0]);
 #pragma unroll
@@ -404,12 +403,15 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
     }
   }
   if (__builtin_expect(!__all(exact), 0))
-    mx4_sum_blocks<1, P, 1>({x}, {there}, {row}, kb, first, units, kMoeGateUpShares, 0, 2, g, r, acc);
+    mx4_sum_blocks<1, P, 1>({x}, {there}, {row}, kb, first, units, SHARES, 0, 2, g, r, acc);
   return mx4_pick<P>(acc[0][0], g);
 }
 
-__global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeArgs q) {
-  __shared__ float part[kMoeGateUpWaves][16][16];  // [wave][operand row][column]; the first half of the waves: gate
+// NW waves: half gate, half up.
+template <int NW>
+__global__ __launch_bounds__(NW * 64, 8) void mx4_moe_gate_up(MoeArgs q) {
+  constexpr int kShares = NW / 2;
+  __shared__ float part[NW][16][16];  // [wave][operand row][column]; the first half of the waves: gate
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int entry = blockIdx.y;
@@ -419,13 +421,13 @@ __global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeAr
   const int inter = shared ? q.d.shared_inter : q.d.inter;
   const int i0 = blockIdx.x * 16;
   if (i0 >= inter) return;
-  const int64_t top = (shared ? 0 : (int64_t)en.e * 2 * inter) + (wave >= kMoeGateUpShares ? inter : 0) + i0;
+  const int64_t top = (shared ? 0 : (int64_t)en.e * 2 * inter) + (wave >= kShares ? inter : 0) + i0;
   const Mx4Row row = mx4_row(shared ? q.d.sgu_codes : q.d.gu_codes, shared ? q.d.sgu_scales : q.d.gu_scales, top, r,
                              q.d.hidden / kMx4Block);
-  const int first = wave % kMoeGateUpShares;
+  const int first = wave % kShares;
   const bool few = en.count <= 4;
-  const float4_t v = few ? moe_gate_up_wave<4>(q, en, row, first, g, r)
-                         : moe_gate_up_wave<1>(q, en, row, first, g, r);
+  const float4_t v = few ? moe_gate_up_wave<4, kShares>(q, en, row, first, g, r)
+                         : moe_gate_up_wave<1, kShares>(q, en, row, first, g, r);
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][4 * g + i][r] = v[i];
   __syncthreads();
@@ -434,10 +436,10 @@ __global__ __launch_bounds__(kMoeGateUpWaves * 64, 8) void mx4_moe_gate_up(MoeAr
   if (i >= en.count) return;
   float sg = 0.f, su = 0.f;
 #pragma unroll
-  for (int w = 0; w < kMoeGateUpShares; ++w)
+  for (int w = 0; w < kShares; ++w)
     for (int o = i; o < 16; o += few ? 4 : 16) {
       sg += part[w][o][c];
-      su += part[kMoeGateUpShares + w][o][c];
+      su += part[kShares + w][o][c];
     }
   uint16_t p[3];
   split_bf16(sg / (1.0f + exp_f(-sg)) * su, p);
@@ -684,8 +686,15 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
   else if (d.experts <= 512) launch_router<8>(q, s);
   else launch_router<16>(q, s);
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
-  hipLaunchKernelGGL(mx4_moe_gate_up, dim3(wide / 16, most + (d.shared_inter ? 1 : 0)), dim3(kMoeGateUpWaves * 64), 0, s,
-                     q);
+  // four waves where workgroups are many or k is short, else eight, for fewer turns
+  // over k (us a call, four / eight: 16 tokens, 128 entries of 512, hidden 2048 66.8 /
+  // 68.7; 1 token, 7 of 256, hidden 576 13.9 / 14.8; 1 token, 8 of 512, hidden 2048 18.5
+  // / 17.9; 13 tokens, 13 of 160, hidden 2976 22.9 / 21.6)
+  const dim3 grid(wide / 16, most + (d.shared_inter ? 1 : 0));
+  if ((int)(grid.x * grid.y) >= 1536 || d.hidden <= 1280)
+    hipLaunchKernelGGL(mx4_moe_gate_up<4>, grid, dim3(256), 0, s, q);
+  else
+    hipLaunchKernelGGL(mx4_moe_gate_up<8>, grid, dim3(512), 0, s, q);
   hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
   return hipGetLastError();
 }
