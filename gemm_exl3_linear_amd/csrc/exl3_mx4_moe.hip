@@ -17,7 +17,7 @@
 //
 // Measured (us, router / gate and up / down, of kernels; a call): 1 token, 8 of 256
 // experts 2048 x 512 7.4 / 6.7 / 5.0, 17.8; 16 tokens, about 101 experts of them and a
-// shared one 11 / 33 / 25, 68 (116 and 58 MB: 3.5 and 2.4 TB/s); 5 tokens, 4 of 60
+// shared one 11 / 31 / 25, 66.5 (116 and 58 MB: 3.8 and 2.4 TB/s); 5 tokens, 4 of 60
 // experts 1440 x 352 6.4 / 7.2 / 9.8, 22.  Few tokens are bound by the three launches,
 // each with its loads, sums and routing one after the other; many experts by what
 // eight waves a SIMD have in flight: more loads a wave at the price of waves were
