@@ -843,3 +843,18 @@ def test_matmul_long_k_shared_by_two(m, n, k):
     rows = np.unique(np.concatenate([np.arange(0, m, 17), np.arange(m - 130, m)]))
     ref, mag = M.product(M.decode(a[0][rows], a[1][rows]), M.decode(*b), bias)
     assert_within(y[rows], ref, bound(ref, mag, k, True), f"{m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("dtype,rows,k,pad", [(np.float32, 3277, 5152, 0), (np.float32, 3300, 5120, 8),
+                                              (np.float16, 6601, 5120, 16), (np.float16, 6701, 5024, 0)])
+def test_reconstruct_past_the_caches(dtype, rows, k, pad):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(rows)
+    q = rand_mx(rng, rows, k, lo=100, hi=140)
+    q[1][rows - 1, -1] = 255
+    buf = torch.full((rows, k + pad), 7.0, dtype=torch.float32 if dtype == np.float32 else torch.float16, device=G.dev())
+    out = X.exl3_mx4_reconstruct(mx(q), out=buf[:, :k])
+    want = M.decode(*q).astype(dtype)  # one rounding
+    np.testing.assert_array_equal(out.cpu().numpy(), want)
+    assert (buf[:, k:] == 7.0).all()
