@@ -8,15 +8,16 @@
 // instruction applies the scales itself, so a wave only reads and multiplies:
 // 128 x 64 a wave of 256 x 256 is as large as its registers allow.
 //
-// What bounds it: 4096 rows 5120 -> 17408, 201 us, 3.6 PFLOP/s.  The 256 x 256
-// kernel takes 181 of them, with the matrix cores busy 0.44 of the time.  A loop of
-// these instructions from registers alone runs at 7.0 to 7.2 PFLOP/s with random
-// codes and at 9.5 with zeros: the clock falls with what the matrix cores switch,
-// and this kernel, too, is a fifth faster a step on zeros (1.49 against 1.83 us).
+// What bounds it: 4096 rows 5120 -> 17408, 187 us, 3.9 PFLOP/s: about 160 for four
+// rounds of 256 x 256 tiles, with the matrix cores busy nearly half of the time, 20 for
+// the small tiles of the rest, 5 for the scales.  A loop of these instructions from
+// registers alone runs at 7.0 to 7.2 PFLOP/s with random codes and at 9.5 with zeros:
+// the clock falls with what the matrix cores switch, and this kernel, too, is a fifth
+// faster a step on zeros (1.49 against 1.83 us).
 // Without the copies a step takes 1.52 us, with all tiles the same (nothing but L2
 // hits) still 1.83.  Reading operands one fragment ahead of the products across
 // the barrier (4 % slower), and copies through registers (9 % slower), did not pay.
-// A round's output, 128 KB a CU, takes 4 us that nothing overlaps.
+// A round's output, 128 KB a CU, is not overlapped.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_lds.hpp"
 #include "exl3_mx4_linear.hpp"
@@ -111,7 +112,8 @@ __device__ __forceinline__ void unrolled(F&& f) {
   }
 }
 
-template <int TM, int TN, int WM, int WN>
+// STREAM: y is whole lines past what the caches keep (launch_mx4_gemm).
+template <int TM, int TN, int WM, int WN, bool STREAM>
 __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q) {
   constexpr int NW = WM * WN;
   constexpr int MI = TM / WM / 16, NI = TN / WN / 16;  // 16 x 16 tiles of a wave
@@ -260,7 +262,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
       if (wave_m + row >= q.m) continue;
       uint16_t* o = y + (wave_m + row) * q.ldy + col;
       if (col + 8 <= q.n) {
-        *reinterpret_cast<u32x4_t*>(o) = v;
+        u32x4_t* to = reinterpret_cast<u32x4_t*>(o);
+        if constexpr (STREAM) __builtin_nontemporal_store(v, to);
+        else *to = v;
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -286,7 +290,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void mx4_gemm_kernel(Mx4GemmArgs q)
         if (wave_m + row >= q.m) continue;
         float* o = y + (wave_m + row) * q.ldy + col;
         if (col + 4 <= q.n) {
-          *reinterpret_cast<float4_t*>(o) = v;
+          float4_t* to = reinterpret_cast<float4_t*>(o);
+          if constexpr (STREAM) __builtin_nontemporal_store(v, to);
+          else *to = v;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -321,7 +327,7 @@ static uint32_t scale_groups(int64_t rows) { return (uint32_t)((rows + 255) / 25
 // large / small: 4096 rows 212 / 228, 1024 rows 79 / 74; 1024 rows 5120 -> 5120
 // 39 / 27; 4096 rows 2048 -> 4096 27 / 29).  A last round of large tiles that would
 // be short is left to small ones, as columns of their own (4096 rows 5120 -> 17408
-// 212 without, 201 with; 1024 rows 75 / 68).  Small tiles that would
+// 212 without, 201 with; 1024 rows 75 / 68; these figures with y in the caches).  Small tiles that would
 // leave CUs empty share k, six steps a workgroup at least (64 rows 17408 -> 5120:
 // 48 unshared, 21 shared; eight steps shared by two and added up, 4096 rows 2048 ->
 // 512: 12 unshared, 18 shared), and long k by two workgroups a CU where one each
@@ -367,11 +373,14 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
 }
 
 template <int TM, int TN, int WM, int WN>
-static void launch_gemm_tiles(Mx4GemmArgs q, hipStream_t s) {
+static void launch_gemm_tiles(Mx4GemmArgs q, bool stream, hipStream_t s) {
   q.tiles_m = (uint32_t)((q.m + TM - 1) / TM);
   q.tiles_n = (uint32_t)((q.n + TN - 1) / TN);
-  hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN>), dim3(q.tiles_m * q.tiles_n * (uint32_t)q.splits),
-                     dim3(WM * WN * 64), 0, s, q);
+  const dim3 grid(q.tiles_m * q.tiles_n * (uint32_t)q.splits), block(WM * WN * 64);
+  if (stream)
+    hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN, true>), grid, block, 0, s, q);
+  else
+    hipLaunchKernelGGL((mx4_gemm_kernel<TM, TN, WM, WN, false>), grid, block, 0, s, q);
 }
 
 hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
@@ -391,16 +400,22 @@ hipError_t launch_mx4_gemm(const uint8_t* a, const uint8_t* a_scales, int64_t m,
                 p.splits};
   if (shared) q.y = part, q.ldy = n, q.y_f32 = 1;
   q.wide = (reinterpret_cast<uintptr_t>(q.y) & 15) == 0 && q.ldy % (q.y_f32 ? 4 : 8) == 0 && (!shared || n % 4 == 0);
+  // 32 MB of y (the L2s together) and more, in whole lines, are stored without a place
+  // in the caches
+  // (us, with / without a place: 4096 rows 5120 -> 17408 199 / 187, 2048 rows 112 / 106;
+  // in parts of lines, 4000 rows 96 -> 5000 21 / 29)
+  const bool stream = !shared && (int64_t)m * n * (y_f32 ? 4 : 2) >= ((int64_t)32 << 20) &&
+                      (reinterpret_cast<uintptr_t>(y) & 127) == 0 && ldy * (y_f32 ? 4 : 2) % 128 == 0;
   if (p.large > 0) {
     q.n = p.large;
-    launch_gemm_tiles<256, 256, 2, 4>(q, s);
+    launch_gemm_tiles<256, 256, 2, 4>(q, stream, s);
     q.b += p.large * kb * 16;
     q.b_scales += p.large * kStageBlocks;
     if (q.bias) q.bias += p.large;
     q.y = static_cast<uint8_t*>(q.y) + p.large * (q.y_f32 ? 4 : 2);
     q.n = n - p.large;
   }
-  if (q.n > 0) launch_gemm_tiles<128, 128, 2, 2>(q, s);
+  if (q.n > 0) launch_gemm_tiles<128, 128, 2, 2>(q, stream, s);
   if (shared)
     launch_mx4_rows_finish({nullptr, nullptr, 0, nullptr, nullptr, bias, y, ldy, m, n, kb, y_f32, 0, 0, p.splits, part},
                            s);

@@ -858,3 +858,20 @@ def test_reconstruct_past_the_caches(dtype, rows, k, pad):
     want = M.decode(*q).astype(dtype)  # one rounding
     np.testing.assert_array_equal(out.cpu().numpy(), want)
     assert (buf[:, k:] == 7.0).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_matmul_output_past_the_caches(f32):
+    # 64 MB and more in whole lines, ragged at the end of rows and columns
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(60)
+    m, n, k = (2100, 8090, 224) if f32 else (4099, 8250, 96)
+    a, b = rand_mx(rng, m, k), rand_mx(rng, n, k, lo=112, hi=122)
+    bias = rng.standard_normal(n).astype(np.float16)
+    buf = torch.full((m, (n + 63) // 64 * 64), 7.0, dtype=torch.float32 if f32 else torch.float16, device=G.dev())
+    y = X.exl3_mx4_matmul(mx(a), mx(b), bias=G.to_dev(bias), out=buf[:, :n]).cpu().numpy()
+    rows = np.unique(np.concatenate([np.arange(0, m, 41), np.arange(m - 140, m)]))
+    ref, mag = M.product(M.decode(a[0][rows], a[1][rows]), M.decode(*b), bias)
+    assert_within(y[rows], ref, bound(ref, mag, k, f32))
+    assert (buf[:, n:] == 7.0).all() and np.isfinite(y).all()
