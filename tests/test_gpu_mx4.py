@@ -875,3 +875,85 @@ def test_matmul_output_past_the_caches(f32):
     ref, mag = M.product(M.decode(a[0][rows], a[1][rows]), M.decode(*b), bias)
     assert_within(y[rows], ref, bound(ref, mag, k, f32))
     assert (buf[:, n:] == 7.0).all() and np.isfinite(y).all()
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+def test_quantize_and_reconstruct_past_32_bits():
+    import torch
+    import gemm_exl3_linear_amd as X
+    rows, k = 270000, 16384  # 4.4e9 elements
+    x = torch.empty((rows, k), dtype=torch.float16, device=G.dev())
+    torch.manual_seed(1)
+    x.copy_(torch.randn(k, device=G.dev()))  # every row the same but for its own factor
+    x *= torch.exp2((torch.arange(rows, device=G.dev()) % 9 - 4).half())[:, None]
+    q = X.exl3_mx4_quantize(x)
+    for first in (0, 131070, 262143, rows - 3):
+        c, s = M.quantize(x[first:first + 3].cpu().numpy())
+        np.testing.assert_array_equal(q.codes[first:first + 3].cpu().numpy(), c)
+        np.testing.assert_array_equal(q.scales[first:first + 3].cpu().numpy(), s)
+    x.zero_()
+    X.exl3_mx4_reconstruct(q, out=x)
+    for first in (0, 131070, 262143, rows - 3):
+        want = M.decode(q.codes[first:first + 3].cpu().numpy(), q.scales[first:first + 3].cpu().numpy())
+        np.testing.assert_array_equal(x[first:first + 3].cpu().numpy(), want.astype(np.float16))
+
+
+@pytest.mark.parametrize("m", [1, 6, 14, 40])
+def test_linear_and_matmul_of_weights_past_32_bits(m):
+    import torch
+    import gemm_exl3_linear_amd as X
+    n, k = 540000, 16384  # 4.4 GB of codes
+    torch.manual_seed(m)
+    w = X.Exl3Mx4(torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=G.dev()),
+                  torch.randint(112, 122, (n, k // 32), dtype=torch.uint8, device=G.dev()))
+    x = torch.randn((m, k), device=G.dev()).half()
+    cols = np.unique(np.concatenate([np.arange(20), np.arange(262134, 262154), np.arange(524278, 524298),
+                                     np.arange(n - 130, n)]))
+    wc = M.decode(w.codes[cols].cpu().numpy(), w.scales[cols].cpu().numpy())
+    y = X.exl3_mx4_linear(x, w, out_dtype=torch.float32)[:, cols].cpu().numpy()
+    ref, mag = M.product(x.cpu().numpy(), wc)
+    assert_within(y, ref, bound(ref, mag, k, True))
+    a = X.exl3_mx4_quantize(x)
+    y = X.exl3_mx4_matmul(a, w, out_dtype=torch.float32)[:, cols].cpu().numpy()
+    ref, mag = M.product(M.decode(a.codes.cpu().numpy(), a.scales.cpu().numpy()), wc)
+    assert_within(y, ref, bound(ref, mag, k, True))
+
+
+def test_matmul_output_past_32_bits():
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(70)
+    m, n, k = 4100, 1050000, 64  # 4.3e9 elements
+    a, b = rand_mx(rng, m, k), rand_mx(rng, n, k, lo=112, hi=122)
+    y = X.exl3_mx4_matmul(mx(a), mx(b))
+    da, db = M.decode(*a), M.decode(*b)
+    for r in (0, 2047, 4090, m - 1):
+        ref, mag = M.product(da[r:r + 1], db)
+        assert_within(y[r:r + 1].cpu().numpy(), ref, bound(ref, mag, k, False), f"row {r}")
+
+
+@pytest.mark.parametrize("t", [1, 7])
+def test_moe_of_arenas_past_32_bits(t):
+    # the last four of 1024 experts are chosen; alone, they are a layer of four
+    import torch
+    import gemm_exl3_linear_amd as X
+    h, i, e = 2048, 2112, 1024  # 4.4 GB of gate and up codes
+    x, l = moe_case(80, t, 4, h, i, scoring="sigmoid", bias=True)
+    big = {}
+    for name, slots, n, k in (("gate_up", 2, i, h), ("down", 1, h, i)):
+        codes = torch.zeros((e, slots, n, k // 2), dtype=torch.uint8, device=G.dev())
+        scales = torch.full((e, slots, n, k // 32), 255, dtype=torch.uint8, device=G.dev())
+        codes[e - 4:], scales[e - 4:] = G.to_dev(l[name][0]), G.to_dev(l[name][1])
+        big[name] = X.Exl3Mx4Arena(codes, scales)
+    router = torch.zeros((e, h), dtype=torch.float16, device=G.dev())
+    router[e - 4:] = G.to_dev(l["router"])
+    bias = torch.full((e,), -9.0, dtype=torch.float32, device=G.dev())
+    bias[e - 4:] = G.to_dev(l["bias"])
+    layer = X.Exl3Mx4Moe(X.Exl3MoeRouter(router, bias=bias, scoring="sigmoid"), big["gate_up"], big["down"])
+    ids = torch.empty((t, 3), dtype=torch.int32, device=G.dev())
+    y = X.exl3_mx4_moe(G.to_dev(x), layer, 3, out_dtype=torch.float32, topk_ids=ids).cpu().numpy()
+    ref, rid, rw = M.moe(x, l, 3)
+    np.testing.assert_array_equal(ids.cpu().numpy(), rid + e - 4)
+    assert_within(y, ref, moe_limit(x, l, 3, ref, rw, True))
