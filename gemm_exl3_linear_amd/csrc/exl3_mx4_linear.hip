@@ -8,18 +8,14 @@
 
 namespace exl3 {
 
-// Output tiles that fit the LDS of one combine round, at a kilobyte a wave.
-constexpr int kMx4CombineTiles = 64;
-
 // 16 MG rows (A4: 4-bit, else fp16 in operands of P pieces, P = 1 unless
 // MG = 1), 16 NG columns, NW waves.
 template <bool A4, int MG, int P, int NG, int NW>
 __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
   static_assert(P == 1 || (MG == 1 && !A4), "pieces are for few fp16 rows");
   constexpr int T = MG * NG;
-  constexpr int R = T * NW <= kMx4CombineTiles ? T : kMx4CombineTiles / NW;  // tiles a round
   constexpr int kRows = Mx4X<P>::kRows, kLoads = Mx4X<P>::kLoads;
-  __shared__ float4_t part[NW * R * 64];
+  __shared__ float4_t part[NW * T * 64];  // 64 KB at most
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const uint32_t tm = blockIdx.x / q.col_tiles, tn = blockIdx.x - tm * q.col_tiles;
@@ -96,43 +92,36 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
       mx4_sum_blocks<MG, P, NG>(xr, there, rb, kb, wave, units, NW, 0, 2, g, r, acc);
   }
 
-  // Sum over the waves in wave order, R output tiles a round.  Lane l of a 16 x
-  // 16 tile holds operand rows 4 (l / 16) .. + 3 of column l % 16.
+  // Sum over the waves in wave order.  Lane l of a 16 x 16 tile holds operand rows
+  // 4 (l / 16) .. + 3 of column l % 16.
 #pragma unroll
-  for (int b = 0; b < T; b += R) {
-    if (b) __syncthreads();
-    const int some = T - b < R ? T - b : R;
+  for (int t = 0; t < T; ++t) part[(wave * T + t) * 64 + lane] = mx4_pick<P>(acc[t / MG][t % MG], g);
+  __syncthreads();
+  for (int e = threadIdx.x; e < T * 64; e += NW * 64) {
+    float4_t v = part[e];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (b + i < T) part[(wave * R + i) * 64 + lane] = mx4_pick<P>(acc[(b + i) / MG][(b + i) % MG], g);
-    __syncthreads();
-    for (int e = threadIdx.x; e < some * 64; e += NW * 64) {
-      float4_t v = part[e];
+    for (int w = 1; w < NW; ++w) v += part[w * T * 64 + e];
+    const int t = e >> 6, l = e & 63;
+    const int64_t col = n0 + 16 * (t / MG) + (l & 15), row = m0 + 16 * (t % MG) + 4 * (l >> 4);
+    if constexpr (P > 1) {  // the pieces' sums, in piece order, by the lanes of the first rows
+      part[e] = v;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += part[w * R * 64 + e];
-      const int t = b + (e >> 6), l = e & 63;
-      const int64_t col = n0 + 16 * (t / MG) + (l & 15);
-      int64_t row = m0 + 16 * (t % MG) + 4 * (l >> 4);
-      if constexpr (P > 1) {  // the pieces' sums, in piece order, by the lanes of the first rows
-        part[e] = v;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int p = 1; p < P; ++p) {
+        const int at = p * kRows;  // operand row of the piece's row 0
 #pragma unroll
-        for (int p = 1; p < P; ++p) {
-          const int at = p * kRows;  // operand row of the piece's row 0
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (4 * (l >> 4) + i < kRows) {
-              const int o = at + 4 * (l >> 4) + i;
-              v[i] += part[(e & ~63) + 16 * (o >> 2) + (l & 15)][o & 3];
-            }
-        }
+        for (int i = 0; i < 4; ++i)
+          if (4 * (l >> 4) + i < kRows) {
+            const int o = at + 4 * (l >> 4) + i;
+            v[i] += part[(e & ~63) + 16 * (o >> 2) + (l & 15)][o & 3];
+          }
       }
-      if (col >= q.n) continue;
+    }
+    if (col >= q.n) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (row + i >= q.m) break;
-        mx4_store(q, row + i, col, v[i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      if (row + i >= q.m) break;
+      mx4_store(q, row + i, col, v[i]);
     }
   }
 }
