@@ -173,11 +173,16 @@ static int wide_splits(int64_t n, int64_t k) {
   return s < 1 ? 1 : (int)s;
 }
 
-// How nine rows and more are cut: 16 rows and 16 or 32 columns a workgroup here, or
-// all rows shared through LDS for 128 columns (exl3_mx4_wide.hip).  The estimates,
-// in us, count the launch, a wave's turns over k and what further rounds of the CUs
-// add; there, a start and steps that grow with the rows, and a second launch for
-// shares of k.  As measured (us, 16 / 32 / LDS):
+// How five rows and more are cut: 16 rows (up to 8 in two pieces) and 16 or 32
+// columns a workgroup here, or all rows shared through LDS for 128 columns
+// (exl3_mx4_wide.hip).  The estimates, in us, count the launch, a wave's turns over k
+// and what further rounds of the CUs add; there, a start and steps that grow with
+// the rows, and a second launch for shares of k (up to 8 rows only where it is
+// clearly less).  As measured (us, 16 / 32 / LDS):
+//    8 rows  5120 ->  2048    6.6    8.0    -
+//    8 rows  5120 ->  5120   10.9    8.5   12.2
+//    8 rows 17408 ->   512   14.8   18.8   10.1
+//    6 rows 17408 ->  5120    -     18.2   19.4
 //   64 rows  2048 ->   512    5.2    5.9   11.0
 //   64 rows  5120 ->  2048   14.9   10.9   13.6
 //   20 rows   512 ->  8192    5.5    4.6    7.8
@@ -195,13 +200,15 @@ static Mx4RowsCut rows_cut(int64_t m, int64_t n, int64_t k) {
   };
   const int64_t tiles = (n + 127) / 128, shares = wide_splits(n, k);
   const double steps = (double)((units + shares - 1) / shares * ((tiles * shares + 255) / 256));
-  const double c16 = cost(16, 2.9, 2.2), c32 = cost(32, 3.2, 2.6);
-  const double lds = 4.6 + 0.8 * (double)row_tiles + (0.8 + 0.1 * (double)row_tiles) * steps + (shares > 1 ? 2.2 : 0.0);
+  const bool few = m <= 8;
+  const double c16 = few ? cost(16, 2.6, 1.35) : cost(16, 2.9, 2.2);
+  const double c32 = few ? cost(32, 2.6, 1.9) : cost(32, 3.2, 2.6);
+  const double lds = (few ? 1.15 : 1.0) * (4.6 + 0.8 * (double)row_tiles + (0.8 + 0.1 * (double)row_tiles) * steps + (shares > 1 ? 2.2 : 0.0));
   if (lds < c16 && lds < c32) return Mx4RowsCut::kLds;
   return c16 <= c32 ? Mx4RowsCut::k16 : Mx4RowsCut::k32;
 }
 size_t mx4_linear_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m <= 8 || rows_cut(m, n, k) != Mx4RowsCut::kLds) return 0;
+  if (m <= 4 || rows_cut(m, n, k) != Mx4RowsCut::kLds) return 0;
   const int s = wide_splits(n, k);
   return s > 1 ? (size_t)s * m * n * sizeof(float) : 0;
 }
@@ -211,19 +218,21 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
                              hipStream_t s) {
   const int kb = (int)(k / kMx4Block);
   const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, kb, y_f32, 0, 0, 1, nullptr};
-  // up to 8 rows: pieces (exl3_mx4_rows.hpp), four where k is long enough for the
-  // fewer loads to show, and 32 columns a workgroup where those fill half the chip
-  // and x has more than a row to fetch (us: one row 5120 -> 17408 four pieces 12.8, two
+  // up to 4 rows: four pieces (exl3_mx4_rows.hpp) where k is long enough for the fewer
+  // loads to show, else two; 32 columns a workgroup where those fill half the chip and
+  // x has more than a row to fetch (us: one row 5120 -> 17408 four pieces 12.8, two
   // 13.6, one 16; 2048 -> 2048 4.0 / 3.7; 16 / 32 columns: 4 rows 17408 -> 5120 21.3 /
-  // 16.7, 5120 -> 2048 5.9 / 7.3, 8 rows 5120 -> 5120 10.9 / 8.6, 5120 -> 2048 6.7 / 8.0,
-  // one row 5120 -> 17408 12.8 / 14.7)
-  const bool cols32 = n >= 4096;
-  if (m <= 4 && k >= 4096)
-    return m > 1 && cols32 ? launch_rows<false, 1, 4, 2, 8>(q, s) : launch_rows<false, 1, 4, 1, 8>(q, s);
-  if (m <= 8) return m > 1 && cols32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
+  // 16.7, 5120 -> 2048 5.9 / 7.3, one row 5120 -> 17408 12.8 / 14.7)
+  if (m <= 4) {
+    const bool cols32 = m > 1 && n >= 4096;
+    if (k >= 4096) return cols32 ? launch_rows<false, 1, 4, 2, 8>(q, s) : launch_rows<false, 1, 4, 1, 8>(q, s);
+    return cols32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
+  }
   const Mx4RowsCut cut = rows_cut(m, n, k);
   // rows too far apart for 32-bit offsets are taken here, 16 at a time
   if (cut == Mx4RowsCut::kLds && ldx <= kMx4WideMaxStride) return launch_mx4_wide(q, wide_splits(n, k), ws, s);
+  if (m <= 8)
+    return cut == Mx4RowsCut::k32 ? launch_rows<false, 1, 2, 2, 8>(q, s) : launch_rows<false, 1, 2, 1, 8>(q, s);
   return cut == Mx4RowsCut::k32 ? launch_rows<false, 1, 1, 2, 8>(q, s) : launch_rows<false, 1, 1, 1, 8>(q, s);
 }
 

@@ -957,3 +957,19 @@ def test_moe_of_arenas_past_32_bits(t):
     ref, rid, rw = M.moe(x, l, 3)
     np.testing.assert_array_equal(ids.cpu().numpy(), rid + e - 4)
     assert_within(y, ref, moe_limit(x, l, 3, ref, rw, True))
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 512, 17408), (8, 131, 17440), (7, 40, 13344)])
+def test_linear_few_long_rows(m, n, k):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n + k)
+    w = rand_mx(rng, n, k, lo=112, hi=122)
+    w[1][n - 1, -1], w[1][n // 2, 0] = 90, 255
+    x = np.full((m, k + 8), np.nan, dtype=np.float16)
+    x[:, :k] = rng.standard_normal((m, k))
+    bias = rng.standard_normal(n).astype(np.float16)
+    y = X.exl3_mx4_linear(G.to_dev(x)[:, :k], mx(w), bias=G.to_dev(bias), out_dtype=torch.float32).cpu().numpy()
+    wd = M.decode(*w)
+    ref, _ = M.product(x[:, :k], wd, bias)
+    assert_within(y, ref, bound(ref, M.product(x[:, :k], np.nan_to_num(wd), bias)[1], k, True), f"{m}x{n}x{k}")
