@@ -203,7 +203,8 @@ static Mx4RowsCut rows_cut(int64_t m, int64_t n, int64_t k) {
   const bool few = m <= 8;
   const double c16 = few ? cost(16, 2.6, 1.35) : cost(16, 2.9, 2.2);
   const double c32 = few ? cost(32, 2.6, 1.9) : cost(32, 3.2, 2.6);
-  const double lds = (few ? 1.15 : 1.0) * (4.6 + 0.8 * (double)row_tiles + (0.8 + 0.1 * (double)row_tiles) * steps + (shares > 1 ? 2.2 : 0.0));
+  const double lds = (few ? 1.15 : 1.0) * (4.6 + 0.8 * (double)row_tiles + (0.8 + 0.1 * (double)row_tiles) * steps +
+                                           (shares > 1 ? 2.2 : 0.0));
   if (lds < c16 && lds < c32) return Mx4RowsCut::kLds;
   return c16 <= c32 ? Mx4RowsCut::k16 : Mx4RowsCut::k32;
 }

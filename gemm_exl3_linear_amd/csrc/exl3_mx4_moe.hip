@@ -472,7 +472,10 @@ struct MoeDownTask {
   int inter, kb, u;
 };
 
-__global__ __launch_bounds__(kMoeDownWaves * 64, 8) void mx4_moe_down(MoeArgs q) {
+// ROOMY: a workgroup a CU at most, whose waves may have twice the registers and
+// fetch the activations of several tokens together.
+template <bool ROOMY>
+__global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_down(MoeArgs q) {
   __shared__ float tiles[kMoeDownWaves][kMoeTokens][16];  // weighted sums [token][column]
   __shared__ float dump[kMoeDownWaves][16][16];           // one unit's sums [operand row][column]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -547,18 +550,49 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, 8) void mx4_moe_down(MoeArgs q)
     } else {
       float4_t acc = {0.f, 0.f, 0.f, 0.f};
       const bool wide = n <= kMoeDownWide;  // operand row 3 i + p, else row i and one plane after the other
+      if constexpr (ROOMY) {
+        // PL planes of this lane's row, from `from` on, both halves of the unit
+        auto rows = [&](auto planes, bool there, const uint16_t* from) {
+          constexpr int PL = decltype(planes)::value;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float s = mx4_scale(mx4_own_scale(w, h, g) & 0xFFu);
+          for (int h = 0; h < 2; ++h) {
+            const float s = mx4_scale(mx4_own_scale(w, h, g) & 0xFFu);
+            const int b = now.u * kMx4UnitBlocks + 4 * h + g;
+            u32x4_t f[PL][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8_t c = mx4_to_bf16(w.half[h][j], s);
-          if (wide) {
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(act(r < 3 * n, r / 3, r % 3, h, j), c, acc, 0, 0, 0);
-          } else {
+            for (int i = 0; i < PL * 4; ++i) f[i / 4][i % 4] = u32x4_t{0u, 0u, 0u, 0u};
+            if (there && b < now.kb) {
 #pragma unroll
-            for (int p = 2; p >= 0; --p)
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(act(r < n, r, p, h, j), c, acc, 0, 0, 0);
+              for (int i = 0; i < PL * 4; ++i)
+                f[i / 4][i % 4] = load16(from + (i / 4) * now.plane + b * kMx4Block + 8 * (i % 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bf16x8_t c = mx4_to_bf16(w.half[h][j], s);
+#pragma unroll
+              for (int p = PL - 1; p >= 0; --p)  // smallest plane first
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[p][j]), c, acc, 0, 0, 0);
+            }
+          }
+        };
+        if (wide)
+          rows(PowC<1>{}, r < 3 * n, now.a + (r % 3) * now.plane + (int64_t)(r < 3 * n ? r / 3 : 0) * now.inter);
+        else
+          rows(PowC<3>{}, r < n, now.a + (int64_t)(r < n ? r : 0) * now.inter);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = mx4_scale(mx4_own_scale(w, h, g) & 0xFFu);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8_t c = mx4_to_bf16(w.half[h][j], s);
+            if (wide) {
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(act(r < 3 * n, r / 3, r % 3, h, j), c, acc, 0, 0, 0);
+            } else {
+#pragma unroll
+              for (int p = 2; p >= 0; --p)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(act(r < n, r, p, h, j), c, acc, 0, 0, 0);
+            }
           }
         }
       }
@@ -695,7 +729,14 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
     hipLaunchKernelGGL(mx4_moe_gate_up<4>, grid, dim3(256), 0, s, q);
   else
     hipLaunchKernelGGL(mx4_moe_gate_up<8>, grid, dim3(512), 0, s, q);
-  hipLaunchKernelGGL(mx4_moe_down, dim3(d.hidden / 16, q.down_splits), dim3(kMoeDownWaves * 64), 0, s, q);
+  // (us a call, with twice the registers / without: 14 tokens, 8 experts of 704, hidden
+  // 128 19.9 / 22.0; 10 tokens, 28 of 96, hidden 480 16.8 / 18.0; 15 tokens, 51 of 128,
+  // hidden 4320, more than a workgroup a CU, 40 / 37)
+  const dim3 down(d.hidden / 16, q.down_splits);
+  if (down.x * down.y <= 256)
+    hipLaunchKernelGGL(mx4_moe_down<true>, down, dim3(kMoeDownWaves * 64), 0, s, q);
+  else
+    hipLaunchKernelGGL(mx4_moe_down<false>, down, dim3(kMoeDownWaves * 64), 0, s, q);
   return hipGetLastError();
 }
 

@@ -438,7 +438,9 @@ size_t exl3_mx4_linear_workspace_size(const exl3_mx4* w, int64_t m);
  *          values fp16 cannot hold, are taken in a second, slower way
  *   x      fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
  *   bias, y, ldy, y_dtype, ws   as for exl3_mx4_matmul
- * 0 <= m <= EXL3_MX4_LINEAR_MAX_ROWS; m == 0 or n == 0 returns EXL3_OK.    */
+ * 0 <= m <= EXL3_MX4_LINEAR_MAX_ROWS; m == 0 or n == 0 returns EXL3_OK.
+ * Results are the same bits on every run of one shape; a row's result may
+ * depend on m, to rounding.                                                */
 exl3_status exl3_mx4_linear(const exl3_mx4* w, const uint16_t* bias, const void* x, int64_t m,
                             int64_t ldx, void* y, int64_t ldy, int32_t y_dtype, void* ws,
                             size_t ws_bytes, exl3_stream_t stream);
