@@ -16,12 +16,12 @@
 // the routing.  The weights' bytes bound the two products.
 //
 // Measured (us, router / gate and up / down, of kernels; a call): 1 token, 8 of 256
-// experts 2048 x 512 7.4 / 6.7 / 5.0, 17.8; 16 tokens, about 101 experts of them and a
-// shared one 11 / 31 / 25, 66.5 (116 and 58 MB: 3.8 and 2.4 TB/s); 5 tokens, 4 of 60
+// experts 2048 x 512 7.4 / 6.2 / 4.9, 17.2; 16 tokens, about 101 experts of them and a
+// shared one 11 / 30 / 25, 65.6 (116 and 58 MB: 3.9 and 2.4 TB/s); 5 tokens, 4 of 60
 // experts 1440 x 352 6.4 / 7.2 / 9.8, 22.  Few tokens are bound by the three launches,
 // each with its loads, sums and routing one after the other; many experts by what
 // eight waves a SIMD have in flight: more loads a wave at the price of waves were
-// slower (two units at a time 77 us, six waves 74).
+// slower (two units at a time 67 us, six waves 74).
 //
 // a is kept as three bf16 pieces (8 + 8 + 8 significand bits, exact to fp32's
 // 24), so the down product runs on bf16 matrix instructions against weights
@@ -376,9 +376,9 @@ __device__ __forceinline__ int load_uniform(const int* p) {
   return *(__attribute__((address_space(4))) const int*)(uintptr_t)p;
 }
 
-// Sums of 16 weight rows over every SHARES-th unit of k from `first`; operand rows
-// are the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
-template <int P, int SHARES>
+// Sums of 16 weight rows over every SHARES-th unit of k from `first`, fetched GU at a
+// time; operand rows are the entry's tokens, P pieces at a time (exl3_mx4_rows.hpp).
+template <int P, int SHARES, int GU>
 __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const MoeEntry& en, const Mx4Row& row,
                                                      int first, int g, int r) {
   constexpr int kLoads = Mx4X<P>::kLoads;
@@ -391,16 +391,18 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
   for (int p = 0; p < P; ++p) acc[0][0][p] = float4_t{0.f, 0.f, 0.f, 0.f};
   const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   bool exact = true;
-  for (int u = first; u < units; u += SHARES) {
-    Mx4Unit w[1];
-    mx4_load_unit(row, kb, u, g, w[0]);
+  for (int u = first; u < units; u += GU * SHARES) {
+    Mx4Unit w[GU][1];
+    f16x8_t f[GU][2][1][kLoads];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f16x8_t f[1][kLoads];
+    for (int i = 0; i < GU; ++i) mx4_load_unit(row, kb, u + i * SHARES, g, w[i][0]);
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) f[0][l] = mx4_load_x<P>(x, there, kb, u, h, g, r, l);
-      exact = mx4_mma_f16<1, P, 1>(f, w, h, g, acc) && exact;
+    for (int i = 0; i < GU * 2 * kLoads; ++i) {
+      const int k = i / (2 * kLoads), h = i / kLoads % 2, l = i % kLoads;
+      f[k][h][0][l] = mx4_load_x<P>(x, there, kb, u + k * SHARES, h, g, r, l);
     }
+#pragma unroll
+    for (int i = 0; i < GU * 2; ++i) exact = mx4_mma_f16<1, P, 1>(f[i / 2][i % 2], w[i / 2], i % 2, g, acc) && exact;
   }
   if (__builtin_expect(!__all(exact), 0))
     mx4_sum_blocks<1, P, 1>({x}, {there}, {row}, kb, first, units, SHARES, 0, 2, g, r, acc);
@@ -408,8 +410,11 @@ __device__ __forceinline__ float4_t moe_gate_up_wave(const MoeArgs& q, const Moe
 }
 
 // NW waves: half gate, half up.
-template <int NW>
-__global__ __launch_bounds__(NW * 64, 8) void mx4_moe_gate_up(MoeArgs q) {
+// ROOMY: a workgroup a CU at most, whose waves may have twice the registers and fetch
+// two units at a time.
+template <int NW, bool ROOMY>
+__global__ __launch_bounds__(NW * 64, ROOMY ? 4 : 8) void mx4_moe_gate_up(MoeArgs q) {
+  constexpr int GU = ROOMY ? 2 : 1;
   constexpr int kShares = NW / 2;
   __shared__ float part[NW][16][16];  // [wave][operand row][column]; the first half of the waves: gate
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -426,8 +431,8 @@ __global__ __launch_bounds__(NW * 64, 8) void mx4_moe_gate_up(MoeArgs q) {
                              q.d.hidden / kMx4Block);
   const int first = wave % kShares;
   const bool few = en.count <= 4;
-  const float4_t v = few ? moe_gate_up_wave<4, kShares>(q, en, row, first, g, r)
-                         : moe_gate_up_wave<1, kShares>(q, en, row, first, g, r);
+  const float4_t v = few ? moe_gate_up_wave<4, kShares, GU>(q, en, row, first, g, r)
+                         : moe_gate_up_wave<1, kShares, GU>(q, en, row, first, g, r);
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][4 * g + i][r] = v[i];
   __syncthreads();
@@ -721,17 +726,22 @@ hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int
   else launch_router<16>(q, s);
   const int wide = d.inter > d.shared_inter ? d.inter : d.shared_inter;
   // four waves where workgroups are many or k is short, else eight, for fewer turns
-  // over k (us a call, four / eight: 16 tokens, 128 entries of 512, hidden 2048 66.8 /
+  // over k (us a call, four / eight: 16 tokens, 128 entries of 512, hidden 2048 65.6 /
   // 68.7; 1 token, 7 of 256, hidden 576 13.9 / 14.8; 1 token, 8 of 512, hidden 2048 18.5
-  // / 17.9; 13 tokens, 13 of 160, hidden 2976 22.9 / 21.6)
+  // / 17.7, 17.2 with twice the registers; 13 tokens, 13 of 160, hidden 2976 22.9 /
+  // 21.6; 16 tokens, 80 of 128, hidden 1440, more than a workgroup a CU, 26.8 with eight,
+  // 28.4 with twice the registers)
   const dim3 grid(wide / 16, most + (d.shared_inter ? 1 : 0));
-  if ((int)(grid.x * grid.y) >= 1536 || d.hidden <= 1280)
-    hipLaunchKernelGGL(mx4_moe_gate_up<4>, grid, dim3(256), 0, s, q);
+  const int groups = (int)(grid.x * grid.y);
+  if (groups >= 1536 || d.hidden <= 1280)
+    hipLaunchKernelGGL((mx4_moe_gate_up<4, false>), grid, dim3(256), 0, s, q);
+  else if (groups > 256)
+    hipLaunchKernelGGL((mx4_moe_gate_up<8, false>), grid, dim3(512), 0, s, q);
   else
-    hipLaunchKernelGGL(mx4_moe_gate_up<8>, grid, dim3(512), 0, s, q);
-  // (us a call, with twice the registers / without: 14 tokens, 8 experts of 704, hidden
-  // 128 19.9 / 22.0; 10 tokens, 28 of 96, hidden 480 16.8 / 18.0; 15 tokens, 51 of 128,
-  // hidden 4320, more than a workgroup a CU, 40 / 37)
+    hipLaunchKernelGGL((mx4_moe_gate_up<8, true>), grid, dim3(512), 0, s, q);
+  // the same for down (us a call, with twice the registers / without: 14 tokens, 8
+  // experts of 704, hidden 128 19.9 / 22.0; 10 tokens, 28 of 96, hidden 480 16.8 / 18.0;
+  // 15 tokens, 51 of 128, hidden 4320, more than a workgroup a CU, 40 / 37)
   const dim3 down(d.hidden / 16, q.down_splits);
   if (down.x * down.y <= 256)
     hipLaunchKernelGGL(mx4_moe_down<true>, down, dim3(kMoeDownWaves * 64), 0, s, q);
