@@ -17,8 +17,8 @@
 //
 // Measured (us, router / gate and up / down, of kernels; a call): 1 token, 8 of 256
 // experts 2048 x 512 7.4 / 6.2 / 4.9, 17.2; 16 tokens, about 101 experts of them and a
-// shared one 11 / 30 / 25, 65.6 (116 and 58 MB: 3.9 and 2.4 TB/s); 5 tokens, 4 of 60
-// experts 1440 x 352 6.4 / 7.2 / 9.8, 22.  Few tokens are bound by the three launches,
+// shared one 11 / 30 / 23, 64.2 (116 and 58 MB: 3.9 and 2.5 TB/s); 5 tokens, 4 of 60
+// experts 1440 x 352 6.4 / 7.2 / 8.5, 21.  Few tokens are bound by the three launches,
 // each with its loads, sums and routing one after the other; many experts by what
 // eight waves a SIMD have in flight: more loads a wave at the price of waves were
 // slower (two units at a time 67 us, six waves 74).
@@ -659,10 +659,12 @@ int moe_splits(const Mx4MoeDesc& d) {
 }
 
 // Shares of the down product's entries: about a task a wave, where there
-// may be so many, and no more than the chip takes at once (two workgroups a CU).
+// may be so many, and no more than one workgroup a CU (us a call, one / two: 16 tokens,
+// 128 entries of 512, hidden 2048 64.2 / 65.6; 14 tokens, 52 of 1248, hidden 608 30.6 /
+// 34.8; 5 tokens, 20 of 352, hidden 1440 21.1 / 22.4).
 int moe_down_splits(const Mx4MoeDesc& d, int64_t t, int topk) {
   const int units = (d.inter + kMx4UnitK - 1) / kMx4UnitK, tasks = moe_most(d, t, topk) * units;
-  const int room = 512 / (d.hidden / 16);
+  const int room = 256 / (d.hidden / 16);
   int s = (tasks + kMoeDownWaves / 2) / kMoeDownWaves;
   if (s > room) s = room;
   return s < 1 ? 1 : s;
