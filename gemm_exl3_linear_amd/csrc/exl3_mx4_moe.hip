@@ -17,7 +17,7 @@
 //
 // Measured (us, router / gate and up / down, of kernels; a call): 1 token, 8 of 256
 // experts 2048 x 512 7.4 / 6.2 / 4.9, 17.2; 16 tokens, about 101 experts of them and a
-// shared one 11 / 30 / 23, 64.2 (116 and 58 MB: 3.9 and 2.5 TB/s); 5 tokens, 4 of 60
+// shared one 11 / 30 / 21, 62.0 (116 and 58 MB: 3.9 and 2.7 TB/s); 5 tokens, 4 of 60
 // experts 1440 x 352 6.4 / 7.2 / 8.5, 21.  Few tokens are bound by the three launches,
 // each with its loads, sums and routing one after the other; many experts by what
 // eight waves a SIMD have in flight: more loads a wave at the price of waves were
@@ -506,19 +506,35 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) tiles[wave][4 * g + i][r] = 0.f;
-  // the weights of the next task are fetched before this one's product
+  // the weights of the next task are fetched before this one's product, and (ROOMY)
+  // a single token's activations, operand row 3 j + p piece j of plane p: loads return
+  // in order, so one for this task would wait for the next one's weights.  (Its
+  // routing weight comes by a scalar load for the same reason.  Two tasks in turn,
+  // without the moves at the end, were slower for their longer code.)
   MoeDownTask now, next;
   Mx4Unit w, wn;
+  bf16x8_t one[2], one_n[2];
+  auto load_one = [&](const MoeDownTask& t, bf16x8_t (&f)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int b = t.u * kMx4UnitBlocks + 4 * h + g;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (r < 12 && b < t.kb) v = load16(t.a + (r % 3) * t.plane + b * kMx4Block + 8 * (r / 3));
+      f[h] = __builtin_bit_cast(bf16x8_t, v);
+    }
+  };
   const int first = (int)blockIdx.y * kMoeDownWaves + wave, stride = kMoeDownWaves * q.down_splits;
   if (first < tasks) {
     now = task(first);
     mx4_load_unit(now.row, now.kb, now.u, g, w);
+    if (ROOMY && now.en.count == 1) load_one(now, one);
   }
   for (int id = first; id < tasks; id += stride) {
     const bool more = id + stride < tasks;
     if (more) {
       next = task(id + stride);
       mx4_load_unit(next.row, next.kb, next.u, g, wn);
+      if (ROOMY && next.en.count == 1) load_one(next, one_n);
     }
     const int n = now.en.count;
     // 8 elements of this lane's block of half h, piece j, of plane p of token row i
@@ -529,11 +545,9 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
       return __builtin_bit_cast(bf16x8_t, v);
     };
     if (n == 1) {
-      // operand row 3 j + p: piece j of plane p; the sums of piece j are wanted
-      // in rows 3 j .. 3 j + 2
-      bf16x8_t f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) f[h] = act(r < 12, 0, r % 3, h, r / 3);
+      // the sums of piece j are wanted in rows 3 j .. 3 j + 2
+      if (!ROOMY) load_one(now, one);
+      const float weight = __int_as_float(load_uniform(reinterpret_cast<const int*>(now.weights)));
       float4_t acc[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.f, 0.f, 0.f, 0.f};
@@ -542,7 +556,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
         const float s = mx4_scale(mx4_own_scale(w, h, g) & 0xFFu);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], mx4_to_bf16(w.half[h][j], s), acc[j], 0, 0, 0);
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one[h], mx4_to_bf16(w.half[h][j], s), acc[j], 0, 0, 0);
       }
       // rows 4 g .. 4 g + 3 of this lane: smallest plane first
       float v = 0.f;
@@ -551,7 +565,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
       if (g == 2) v = acc[2][0] + ((acc[3][3] + acc[3][2]) + acc[3][1]);
       v += shfl_xor_f(v, 16);
       v += shfl_xor_f(v, 32);
-      if (g == 0) tiles[wave][now.en.token(0)][r] += now.weights[0] * v;
+      if (g == 0) tiles[wave][now.en.token(0)][r] += weight * v;
     } else {
       float4_t acc = {0.f, 0.f, 0.f, 0.f};
       const bool wide = n <= kMoeDownWide;  // operand row 3 i + p, else row i and one plane after the other
@@ -618,6 +632,8 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
     }
     now = next;
     w = wn;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) one[h] = one_n[h];
   }
   __syncthreads();
   const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
