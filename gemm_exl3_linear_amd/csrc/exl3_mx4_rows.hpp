@@ -47,11 +47,13 @@ __device__ __forceinline__ Mx4Row mx4_row(const uint8_t* codes, const uint8_t* s
 }
 
 // Unit u of a row of kb blocks; blocks past the row's end read as zeros with
-// scale 1.
+// scale 1.  WHOLE: the unit is known to lie inside (without the branch, the loads of
+// several rows and units are issued together).
+template <bool WHOLE = false>
 __device__ __forceinline__ void mx4_load_unit(const Mx4Row& row, int kb, int u, int g, Mx4Unit& t) {
   const uint32_t c = row.code_off + (uint32_t)(u * kMx4UnitBytes + 16 * g);
   const uint32_t s = row.scale_off + (uint32_t)(u * kMx4UnitBlocks);
-  if ((u + 1) * kMx4UnitBlocks <= kb) {
+  if (WHOLE || (u + 1) * kMx4UnitBlocks <= kb) {
     t.half[0] = load16(row.codes + c);
     t.half[1] = load16(row.codes + c + 64u);
     __builtin_memcpy(t.sc, row.scales + s, 8);
@@ -82,13 +84,14 @@ struct Mx4X {
 
 // Operand `q` of half h of unit u: lane (r, g) holds 8 elements of block 4 h + g,
 // piece q P + r / kRows, of row r % kRows; zeros past the row's end or where the
-// row is not there.  x: this lane's row.
-template <int P>
+// row is not there.  x: this lane's row.  WHOLE: the unit lies inside, and a row that
+// is not there may hold what it likes.
+template <int P, bool WHOLE = false>
 __device__ __forceinline__ f16x8_t mx4_load_x(const uint16_t* x, bool there, int kb, int u, int h, int g, int r,
                                               int q) {
   const int b = u * kMx4UnitBlocks + 4 * h + g;
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (there && b < kb) v = load16(x + (int64_t)b * kMx4Block + 8 * (q * P + r / Mx4X<P>::kRows));
+  if (WHOLE || (there && b < kb)) v = load16(x + (int64_t)b * kMx4Block + 8 * (q * P + r / Mx4X<P>::kRows));
   return __builtin_bit_cast(f16x8_t, v);
 }
 
