@@ -1,7 +1,7 @@
 // exl3_mx4_linear and exl3_mx4_matmul where few rows or small sizes leave the
 // weights' bytes, or the launch, as the bound: workgroups whose waves share k, and
-// the choice of the kernel by size.  Measured: one row 5120 -> 17408 (47 MB) 12.6 us
-// with fp16 rows, 10.8 with 4-bit rows; one row 2048 -> 512 3.7 us, of which a launch
+// the choice of the kernel by size.  Measured: one row 5120 -> 17408 (47 MB) 12.1 us
+// with fp16 rows, 11.3 with 4-bit rows; one row 2048 -> 512 3.6 us, of which a launch
 // is 1.6.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_linear.hpp"
