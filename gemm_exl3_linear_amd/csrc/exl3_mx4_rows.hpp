@@ -9,13 +9,15 @@
 //    loaded (the instruction applies both scales; no arithmetic of our own);
 //  - with fp16 rows: 16 conversions to fp16 (code times scale, exact for scale
 //    bytes 104 .. 140) and four 16x16x32 fp16 instructions, the j-th on the j-th
-//    dword (piece) of every lane's block.  A wave that holds a block with another
-//    scale byte multiplies the unscaled codes block by block and scales the sums.
+//    dword (piece) of every lane's block.  A wave that met a block with another
+//    scale byte takes its whole share again, block by block: the unscaled codes, then
+//    the sums by the block's scale (mx4_sum_blocks).
 //    Few rows: with at most 16 / P of them, one operand carries P pieces, piece p
 //    of row t in operand row p 16 / P + t, and piece p has sums of its own of which
 //    only those rows are wanted.  One load then brings P pieces; loads of one
 //    piece each, mostly masked, cost as much and bounded the time (5120 -> 17408,
-//    one row: 16 us against 12.8 with four pieces).
+//    one row: 16 us, 12.8 with four pieces; 12.1 with the loads of a whole unit
+//    issued without branches).
 // Output columns are the weight rows (matrix operand B), so a lane's sums all
 // belong to the column whose scales it loaded.
 #pragma once
