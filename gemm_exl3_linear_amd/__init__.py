@@ -624,6 +624,9 @@ class Exl3Mx4:
         object.__setattr__(self, "_record", record)
         object.__setattr__(self, "_ref", ctypes.byref(record))
 
+    def __reduce__(self):  # copies and pickles take the tensors, not the record's pointers
+        return Exl3Mx4, (self.codes, self.scales)
+
     @property
     def rows(self) -> int:
         return int(self.codes.shape[0])
@@ -714,6 +717,9 @@ class Exl3Mx4Moe:
                               sgu, sdn, _ptr(gate))
         object.__setattr__(self, "_record", record)
         object.__setattr__(self, "_ref", ctypes.byref(record))
+
+    def __reduce__(self):  # copies and pickles take the tensors, not the record's pointers
+        return Exl3Mx4Moe, (self.router, self.gate_up, self.down, self.shared)
 
 
 def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:

@@ -163,3 +163,19 @@ def test_binding_refuses_before_the_library():
             X.Exl3Mx4Moe(router, gu, dn)
     with pytest.raises(ValueError):
         X.exl3_mx4_moe(x, X.Exl3Mx4Moe(X.Exl3MoeRouter(r), gu, dn), 2)
+
+
+def test_copies_hold_their_own_tensors():
+    import copy
+    import pickle
+    torch = pytest.importorskip("torch")
+    a = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    w = X.Exl3Mx4(a(4, 64), a(4, 4))
+    l = X.Exl3Mx4Moe(X.Exl3MoeRouter(torch.zeros(3, 64, dtype=torch.float16)),
+                     X.Exl3Mx4Arena(a(3, 2, 32, 32), a(3, 2, 32, 2)), X.Exl3Mx4Arena(a(3, 1, 64, 16), a(3, 1, 64, 1)))
+    for twin in (copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))):
+        v, m = twin(w), twin(l)
+        assert v.codes.data_ptr() != w.codes.data_ptr() and v._record.codes == v.codes.data_ptr()
+        assert v._record.scales == v.scales.data_ptr() and (v._record.rows, v._record.k) == (4, 128)
+        assert m._record.router == m.router.weight.data_ptr() != l.router.weight.data_ptr()
+        assert m._record.gate_up.codes == m.gate_up.codes.data_ptr() and m._record.down.n == 64
