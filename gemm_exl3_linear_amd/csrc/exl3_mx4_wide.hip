@@ -148,7 +148,11 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
 #pragma unroll
   for (int j = 0; j < 4; ++j) read_x(j, lds0);
   uint32_t stage = lds0;  // of unit u
-  bool exact = true;      // every scale in fp16
+  // Every scale of these columns in fp16.  Those of rows past the last are what
+  // follows them in their dword, and have no say.
+  bool exact[kWideNI];
+#pragma unroll
+  for (int ni = 0; ni < kWideNI; ++ni) exact[ni] = true;
   for (int u = begin; u < end; ++u) {
     // this wave's copies of the next stage are in (those of kStages - 2 later
     // ones may not be) and its reads of stage u are done; then everybody's
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
     const Copy c = plan(u + kStages);
     float s[kWideNI];
 #pragma unroll
-    for (int ni = 0; ni < kWideNI; ++ni) exact = mx4_fp16_scale(w[ni], 0, g, s[ni]) && exact;
+    for (int ni = 0; ni < kWideNI; ++ni) exact[ni] = mx4_fp16_scale(w[ni], 0, g, s[ni]) && exact[ni];
     read_w(wn, next, u + 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -176,7 +180,10 @@ __global__ __launch_bounds__(kWideWaves * 64) void mx4_wide_kernel(Mx4RowsArgs q
     stage = next;
   }
 
-  if (__builtin_expect(!__all(exact), 0)) {
+  bool all_exact = true;
+#pragma unroll
+  for (int ni = 0; ni < kWideNI; ++ni) all_exact = (exact[ni] || cols + 16 * ni + r >= left) && all_exact;
+  if (__builtin_expect(!__all(all_exact), 0)) {
     const uint16_t* xr[MG];
     bool there[MG];
 #pragma unroll
