@@ -39,8 +39,9 @@ __device__ __forceinline__ f16x8_t mx4_to_f16(uint32_t codes, float scale = 1.0f
   return f16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// Eight codes times a scale to eight bf16 values (exact: two significand bits
-// and bf16's fp32 exponent range).
+// Eight codes times a scale to eight bf16 values: exact (two significand bits and
+// fp32's exponent range) but for magnitudes from 2^128, at scale bytes 253 and 254,
+// which become infinities.
 __device__ __forceinline__ bf16x8_t mx4_to_bf16(uint32_t codes, float scale) {
   const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
   const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);

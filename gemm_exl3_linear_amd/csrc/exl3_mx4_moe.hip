@@ -25,7 +25,8 @@
 //
 // a is kept as three bf16 pieces (8 + 8 + 8 significand bits, exact to fp32's
 // 24), so the down product runs on bf16 matrix instructions against weights
-// that are exact in bf16 at any scale byte.
+// that are exact in bf16 up to scale byte 252 (6 2^125); units with a block past
+// that are taken block by block (moe_down_far).
 #include "exl3_gemm.hpp"
 #include "exl3_internal.hpp"
 #include "exl3_mx4_rows.hpp"
@@ -477,6 +478,43 @@ struct MoeDownTask {
   int inter, kb, u;
 };
 
+// The sums of a unit with blocks at scale bytes 253 and 254, whose larger values
+// pass bf16's range: block by block, those blocks at 2^-4 of their scale and
+// their sums by 2^4.  The other blocks are taken out of both operands: an infinite
+// activation times their zeros would be NaN.  Operand row i is token i, one plane
+// after the other.
+__device__ __forceinline__ bool moe_down_is_far(uint32_t s) { return s - 253u <= 1u; }
+__device__ __forceinline__ bool moe_down_any_far(const Mx4Unit& w, int g) {
+  return __any(moe_down_is_far(mx4_own_scale(w, 0, g) & 0xFFu) || moe_down_is_far(mx4_own_scale(w, 1, g) & 0xFFu));
+}
+__device__ __forceinline__ float4_t moe_down_far(const MoeDownTask& t, const Mx4Unit& w, int g, int r) {
+  float4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int b = 0; b < kMx4UnitBlocks; ++b) {
+    const u32x4_t codes = b < 4 ? w.half[0] : w.half[1];
+    const uint32_t s = ((b < 4 ? w.sc[0] : w.sc[1]) >> (8 * (b & 3))) & 0xFFu;  // of this lane's column
+    const bool far = moe_down_is_far(s), own = g == (b & 3);
+    const float scale = mx4_scale(own ? (far ? s - 4u : s) : kMx4One), back = far ? 16.f : 1.f;
+    const int at = t.u * kMx4UnitBlocks + b;
+    const bool there = own && r < t.en.count && at < t.kb;
+    const uint16_t* a = t.a + (int64_t)(there ? r : 0) * t.inter + at * kMx4Block;
+    float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x8_t c = mx4_to_bf16(own ? codes[j] : 0u, scale);
+#pragma unroll
+      for (int p = 2; p >= 0; --p) {  // smallest plane first
+        u32x4_t f = {0u, 0u, 0u, 0u};
+        if (there) f = load16(a + p * t.plane + 8 * j);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f), c, v, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], back, acc[i]);
+  }
+  return acc;
+}
+
 // ROOMY: a workgroup a CU at most, whose waves may have twice the registers and
 // fetch the activations of several tokens together.
 template <bool ROOMY>
@@ -489,7 +527,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
   const int routed = load_uniform(q.count);
   const int units = (q.d.inter / kMx4Block + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   const int tasks = routed * units + (q.d.shared_inter / kMx4Block + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
-  auto task = [&](int id) {
+  auto task = [&](int id, int r) {
     MoeDownTask t;
     const bool shared = id >= routed * units;
     const int entry = shared ? q.most : id / units;
@@ -511,6 +549,13 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
   // in order, so one for this task would wait for the next one's weights.  (Its
   // routing weight comes by a scalar load for the same reason.  Two tasks in turn,
   // without the moves at the end, were slower for their longer code.)
+  // the sums of operand rows 4 g .. 4 g + 3, by their tokens' weights
+  auto add_rows = [&](const MoeDownTask& t, const float4_t& acc, int g, int r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * g + i < t.en.count) tiles[wave][t.en.token(4 * g + i)][r] += t.weights[4 * g + i] * acc[i];
+  };
+  bool met_far = false;  // a unit left for the second way
   MoeDownTask now, next;
   Mx4Unit w, wn;
   bf16x8_t one[2], one_n[2];
@@ -525,14 +570,14 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
   };
   const int first = (int)blockIdx.y * kMoeDownWaves + wave, stride = kMoeDownWaves * q.down_splits;
   if (first < tasks) {
-    now = task(first);
+    now = task(first, r);
     mx4_load_unit(now.row, now.kb, now.u, g, w);
     if (ROOMY && now.en.count == 1) load_one(now, one);
   }
   for (int id = first; id < tasks; id += stride) {
     const bool more = id + stride < tasks;
     if (more) {
-      next = task(id + stride);
+      next = task(id + stride, r);
       mx4_load_unit(next.row, next.kb, next.u, g, wn);
       if (ROOMY && next.en.count == 1) load_one(next, one_n);
     }
@@ -543,6 +588,12 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
       u32x4_t v = {0u, 0u, 0u, 0u};
       if (there && b < now.kb) v = load16(now.a + p * now.plane + (int64_t)i * now.inter + b * kMx4Block + 8 * j);
       return __builtin_bit_cast(bf16x8_t, v);
+    };
+    // asked after the products (and the loads before them), which then go nowhere
+    auto is_far = [&] {
+      const bool far = moe_down_any_far(w, g);
+      met_far = met_far || far;
+      return far;
     };
     if (n == 1) {
       // the sums of piece j are wanted in rows 3 j .. 3 j + 2
@@ -565,7 +616,7 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
       if (g == 2) v = acc[2][0] + ((acc[3][3] + acc[3][2]) + acc[3][1]);
       v += shfl_xor_f(v, 16);
       v += shfl_xor_f(v, 32);
-      if (g == 0) tiles[wave][now.en.token(0)][r] += weight * v;
+      if (!is_far() && g == 0) tiles[wave][now.en.token(0)][r] += weight * v;
     } else {
       float4_t acc = {0.f, 0.f, 0.f, 0.f};
       const bool wide = n <= kMoeDownWide;  // operand row 3 i + p, else row i and one plane after the other
@@ -615,7 +666,9 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
           }
         }
       }
-      if (wide) {
+      if (is_far()) {
+        // left for the second way
+      } else if (wide) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dump[wave][4 * g + i][r] = acc[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -625,15 +678,27 @@ __global__ __launch_bounds__(kMoeDownWaves * 64, ROOMY ? 4 : 8) void mx4_moe_dow
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * g + i < n) tiles[wave][now.en.token(4 * g + i)][r] += now.weights[4 * g + i] * acc[i];
+        add_rows(now, acc, g, r);
       }
     }
     now = next;
     w = wn;
 #pragma unroll
     for (int h = 0; h < 2; ++h) one[h] = one_n[h];
+  }
+  // in a loop of its own, with a lane that the compiler takes for another: inside the
+  // first loop, or sharing its addresses, it cost that one registers
+  if (__builtin_expect(met_far, 0)) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int fg = l >> 4, fr = l & 15;
+#pragma unroll 1
+    for (int id = first; id < tasks; id += stride) {
+      const MoeDownTask t = task(id, fr);
+      Mx4Unit v;
+      mx4_load_unit(t.row, t.kb, t.u, fg, v);
+      if (moe_down_any_far(v, fg)) add_rows(t, moe_down_far(t, v, fg, fr), fg, fr);
+    }
   }
   __syncthreads();
   const int t = threadIdx.x >> 4, c = threadIdx.x & 15;

@@ -36,3 +36,48 @@ def test_linear_whatever_follows_the_scales(m, n, k):
     ref, mag = M.product(x, M.decode(codes[cols], scales[cols]))
     B.assert_within(got[0].cpu().numpy()[:, cols], ref, B.bound(ref, mag, k, True))
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+# ---------------------------------------------------------------------------
+# the highest scale bytes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("hidden", [288, 4128])
+@pytest.mark.parametrize("t", [1, 5, 6, 16])
+def test_moe_down_at_the_highest_scale_bytes(t, hidden):
+    """Blocks of 2^126 and 2^127 whose values pass bf16's range, against small
+    activations, next to ordinary blocks and blocks at byte 0, in routed and shared
+    experts; a token of zeros gives zeros."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(47, t, 4, hidden, 288, si=96)
+    x = (x * np.float16(2.0 ** -3)).astype(np.float16)
+    if t > 1:
+        x[t - 1] = 0
+    l["gate_up"][1][:, 1] -= 60  # up: activations about 2^-64
+    l["shared"][0][1][:, 1] -= 60
+    for s in (l["down"][1], l["shared"][1][1]):
+        s[:, :, ::3, 1], s[:, :, 1::3, 2], s[:, :, ::5, 0] = 254, 253, 0
+    y = X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
+    ref, ids, w = M.moe(x, l, 2)
+    assert np.isfinite(ref).all() and np.abs(ref).max() > 2.0 ** 50
+    B.assert_within(y, ref, B.moe_limit(x, l, 2, ref, w, True))
+    if t > 1:
+        assert (y[t - 1] == 0).all()
+
+
+@pytest.mark.parametrize("t", [1, 5, 6, 16])
+def test_moe_infinite_activations_at_the_highest_scale_bytes(t):
+    # silu(g) u passes fp32's range for token 0 only, every code of down is 4.0:
+    # an infinity whatever the scales of its block and of the others
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(48, t, 3, 64, 288)
+    for k, s in (("gate_up", 190), ("down", 127)):
+        l[k][0][:] = 0x22
+        l[k][1][:] = s
+    l["down"][0][:] = 0x66  # 4.0
+    l["down"][1][:, :, ::2, 1], l["down"][1][:, :, ::3, 4] = 254, 253
+    x[:] = 0
+    x[0] = 1
+    y = X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
+    assert np.isposinf(y[0]).all() and (y[1:] == 0).all()
