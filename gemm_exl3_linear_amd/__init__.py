@@ -9,6 +9,7 @@ first call does, and a missing library raises instead of falling back.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 from dataclasses import dataclass
@@ -516,32 +517,33 @@ def _refuse(what: str):
 # look up each time is kept here, since an import inside a function costs 0.2 us.
 _dtype_codes = {}    # torch dtype -> EXL3_F16, EXL3_F32
 _cuda_queries = []   # current device, current stream of a device
+_shape = operator.attrgetter("shape")
 
 
-def _stream_for(t, what: str, stream) -> int:
-    """The stream's handle (the current one if None) for a call on t, which has
-    to be on the current device: the library launches there.  The raw query
-    costs 0.1 us of host time where torch.cuda.current_stream() costs 2.9."""
-    if not t.is_cuda:
+def _place(t, what: str, stream):
+    """Device index and stream handle (the current stream's if None) of a call on
+    t, which has to be on the current device: the library launches there.  The raw
+    query costs 0.1 us of host time where torch.cuda.current_stream() costs 2.9."""
+    i = t.get_device()
+    if i < 0:
         _refuse(f"{what} is not on a GPU")
     if not _cuda_queries:
         import torch
         _cuda_queries.extend((torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream))
-    i = t.get_device()
     if i != _cuda_queries[0]():
         _refuse(f"{what} is on GPU {i}, not on the current device")
     if stream is None:
-        return _cuda_queries[1](i)
+        return i, _cuda_queries[1](i)
     if stream.device_index != i:
         _refuse(f"the stream is of GPU {stream.device_index}, {what} is on GPU {i}")
-    return int(stream.cuda_stream)
+    return i, int(stream.cuda_stream)
 
 
 def _tensor(t, what: str, dtype, shape):
     """t, checked: dtype, shape (None entries are free), contiguous."""
     if t.dtype != dtype:
         _refuse(f"{what} is {t.dtype}, not {dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape)):
+    if t.shape != shape and (t.dim() != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape))):
         _refuse(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         _refuse(f"{what} is not contiguous")
@@ -558,16 +560,18 @@ def _f16_f32(t, what: str) -> int:
     return code
 
 
-def _f16_rows(x, cols: int) -> int:
-    """Row stride of the fp16 matrix x, checked."""
+def _f16_rows(x, cols: int):
+    """Rows and row stride of the fp16 matrix x, checked."""
     if _f16_f32(x, "x") != EXL3_F16:
         _refuse(f"x is {x.dtype}, not fp16")
-    return _row_stride(x, "x", None, cols)
+    m, _, ld = _matrix(x, "x", None, cols)
+    return m, ld
 
 
-def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
-    """Row stride of t, checked as a matrix of contiguous rows.  With fewer than
-    two rows the stride says nothing and the width, rounded up to 8, stands in."""
+def _matrix(t, what: str, rows: Optional[int], cols: Optional[int]):
+    """Rows, columns and row stride of t, checked as a matrix of contiguous rows.
+    With fewer than two rows the stride says nothing and the width, rounded up to
+    8, stands in."""
     stride = t.stride()
     if len(stride) != 2:
         _refuse(f"{what} is not a matrix")
@@ -576,7 +580,7 @@ def _row_stride(t, what: str, rows: Optional[int], cols: Optional[int]) -> int:
         _refuse(f"{what} has shape {(m, n)}, not {(rows, cols)}")
     if stride[1] != 1 and n > 1:
         _refuse(f"{what} does not have contiguous rows")
-    return stride[0] if m > 1 else -(-n // 8) * 8
+    return m, n, stride[0] if m > 1 else -(-n // 8) * 8
 
 
 def _new(make, shape, dtype, device, stream):
@@ -589,18 +593,18 @@ def _new(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
-def _scratch(workspace, zeroed: bool, need, args, like, stream):
+def _scratch(workspace, zeroed: bool, need, args, device: int, stream):
     """Address and bytes of the caller's workspace, or of a new one (need(*args)
-    bytes), and the tensor that holds it; on the device of `like`."""
+    bytes), and the tensor that holds it."""
     if workspace is None:
         n = need(*args)
         if not n:
             return 0, 0, None
         import torch
-        workspace = _new(torch.zeros if zeroed else torch.empty, n, torch.uint8, like.device, stream)
+        workspace = _new(torch.zeros if zeroed else torch.empty, n, torch.uint8, device, stream)
         return workspace.data_ptr(), n, workspace
     n = workspace.nbytes
-    if n and (workspace.get_device() != like.get_device() or not workspace.is_contiguous()):
+    if n and (workspace.get_device() != device or not workspace.is_contiguous()):
         _refuse("the workspace is on another device than the operands, or not contiguous")
     return workspace.data_ptr(), n, workspace
 
@@ -623,6 +627,17 @@ class Exl3Mx4:
         record = _Mx4(_ptr(self.codes), _ptr(self.scales), self.rows, self.k)
         object.__setattr__(self, "_record", record)
         object.__setattr__(self, "_ref", ctypes.byref(record))
+        object.__setattr__(self, "_seen", (_ptr(self.codes), _ptr(self.scales), self.codes.shape))
+        object.__setattr__(self, "_fields", (_ptr(self.codes), _ptr(self.scales), self.rows, self.k))
+
+    def _now(self):
+        """Addresses of codes and scales, rows and k, with the record of the same
+        at _ref: of the tensors as they are.  If their memory or shape was changed
+        under them (`.data =`, set_, resize_), they are checked and read again."""
+        c, s = self.codes, self.scales
+        if (c.data_ptr(), s.data_ptr(), c.shape) != self._seen:
+            self.__post_init__()
+        return self._fields
 
     def __reduce__(self):  # copies and pickles take the tensors, not the record's pointers
         return Exl3Mx4, (self.codes, self.scales)
@@ -660,6 +675,7 @@ class Exl3Mx4Arena:
             _refuse("codes and scales are on different devices")
 
     def _c(self) -> _Mx4Experts:
+        self.__post_init__()  # the tensors as they are now
         e, slots, n, half = self.codes.shape
         return _Mx4Experts(_ptr(self.codes), _ptr(self.scales), e, slots, n, 2 * half)
 
@@ -715,8 +731,21 @@ class Exl3Mx4Moe:
         scoring = ROUTE_SOFTMAX if r.scoring == "softmax" else ROUTE_SIGMOID
         record = _Mx4MoeLayer(_ptr(r.weight), _ptr(r.bias), scoring, int(r.renormalize), float(r.scale), gu, dn,
                               sgu, sdn, _ptr(gate))
+        arenas = [self.gate_up, self.down] + ([sh.gate_up, sh.down] if sh is not None else [])
+        parts = tuple(t for a in arenas for t in (a.codes, a.scales)) + tuple(
+            t for t in (r.weight, r.bias, gate) if t is not None)
+        widths = tuple(a.codes for a in arenas[::2])  # the others' shapes follow from these
         object.__setattr__(self, "_record", record)
         object.__setattr__(self, "_ref", ctypes.byref(record))
+        object.__setattr__(self, "_parts", (parts, widths, torch.Tensor.data_ptr))
+        object.__setattr__(self, "_seen", (list(map(_ptr, parts)), list(map(_shape, widths))))
+
+    def _now(self) -> _Mx4MoeLayer:
+        """The record of the tensors as they are (Exl3Mx4._now)."""
+        parts, widths, data_ptr = self._parts
+        if (list(map(data_ptr, parts)), list(map(_shape, widths))) != self._seen:
+            self.__post_init__()
+        return self._record
 
     def __reduce__(self):  # copies and pickles take the tensors, not the record's pointers
         return Exl3Mx4Moe, (self.router, self.gate_up, self.down, self.shared)
@@ -724,94 +753,95 @@ class Exl3Mx4Moe:
 
 def exl3_mx4_quantize(x, out: Optional[Exl3Mx4] = None, stream=None) -> Exl3Mx4:
     """MXFP4 of fp16 or fp32 rows x [rows, k], k a multiple of 32."""
-    ldx = _row_stride(x, "x", None, None)
+    rows, k, ldx = _matrix(x, "x", None, None)
     dtype = _f16_f32(x, "x")
-    on = _stream_for(x, "x", stream)
-    rows, k = x.shape
+    device, on = _place(x, "x", stream)
     if out is None:
         if k == 0 or k % MX4_BLOCK:
             _refuse(f"x has {k} columns, not a multiple of {MX4_BLOCK}")
         import torch
-        out = Exl3Mx4(_new(torch.empty, (rows, k // 2), torch.uint8, x.device, stream),
-                      _new(torch.empty, (rows, k // MX4_BLOCK), torch.uint8, x.device, stream))
-    r = out._record
-    if r.rows != rows or r.k != k or out.codes.get_device() != x.get_device():
+        out = Exl3Mx4(_new(torch.empty, (rows, k // 2), torch.uint8, device, stream),
+                      _new(torch.empty, (rows, k // MX4_BLOCK), torch.uint8, device, stream))
+    codes, scales, n, nk = out._now()
+    if n != rows or nk != k or out.codes.get_device() != device:
         _refuse("out does not match x")
-    _check(lib().exl3_mx4_quantize(x.data_ptr(), dtype, rows, k, ldx, r.codes, r.scales, on),
+    _check(lib().exl3_mx4_quantize(x.data_ptr(), dtype, rows, k, ldx, codes, scales, on),
            "exl3_mx4_quantize")
     return out
 
 
 def exl3_mx4_reconstruct(w: Exl3Mx4, dtype=None, out=None, stream=None):
     """The values w stands for, fp16 (the default) or fp32 [rows, k]."""
-    on = _stream_for(w.codes, "w", stream)
-    r = w._record
+    device, on = _place(w.codes, "w", stream)
+    _, _, n, k = w._now()
     if out is None:
         import torch
-        out = _new(torch.empty, (r.rows, r.k), dtype or torch.float16, w.codes.device, stream)
-    elif out.get_device() != w.codes.get_device():
+        out = _new(torch.empty, (n, k), dtype or torch.float16, device, stream)
+    elif out.get_device() != device:
         _refuse("out is on another device than w")
-    ldo = _row_stride(out, "out", r.rows, r.k)
+    ldo = _matrix(out, "out", n, k)[2]
     _check(lib().exl3_mx4_reconstruct(w._ref, out.data_ptr(), _f16_f32(out, "out"), ldo, on),
            "exl3_mx4_reconstruct")
     return out
 
 
-def _product_out(out, out_dtype, m: int, n: int, like, bias, stream):
+def _product_out(out, out_dtype, m: int, n: int, device: int, bias, stream):
     """The output of a product (a new one if none is given), its row stride and
-    type; on the device of `like`."""
+    type."""
     if out is None:
         import torch
-        out = _new(torch.empty, (m, n), out_dtype or torch.float16, like.device, stream)
-    elif out.get_device() != like.get_device():
+        out, ldy = _new(torch.empty, (m, n), out_dtype or torch.float16, device, stream), n
+    elif out.get_device() != device:
         _refuse("out is on another device than the operands")
-    ldy = _row_stride(out, "out", m, n)
+    else:
+        ldy = _matrix(out, "out", m, n)[2]
     if bias is not None:
         import torch
         _tensor(bias, "bias", torch.float16, (n,))
-        if bias.get_device() != like.get_device():
+        if bias.get_device() != device:
             _refuse("bias is on another device than the operands")
     return out, ldy, _f16_f32(out, "out")
 
 
 def exl3_mx4_matmul_workspace_size(a: Exl3Mx4, b: Exl3Mx4) -> int:
+    a._now(), b._now()
     return int(lib().exl3_mx4_matmul_workspace_size(a._ref, b._ref))
 
 
 def exl3_mx4_matmul(a: Exl3Mx4, b: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = a [m, k] b [n, k]^T (+ bias fp16 [n]), both MXFP4."""
-    like = a.codes
-    on = _stream_for(like, "a", stream)
-    if b.codes.get_device() != like.get_device():
+    device, on = _place(a.codes, "a", stream)
+    if b.codes.get_device() != device:
         _refuse("a and b are on different devices")
-    out, ldy, ydt = _product_out(out, out_dtype, a._record.rows, b._record.rows, like, bias, stream)
-    ws, nws, _keep = _scratch(workspace, False, exl3_mx4_matmul_workspace_size, (a, b), like, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, a._now()[2], b._now()[2], device, bias, stream)
+    ws, nws, _keep = _scratch(workspace, False, lib().exl3_mx4_matmul_workspace_size, (a._ref, b._ref), device, stream)
     _check(lib().exl3_mx4_matmul(a._ref, b._ref, _ptr(bias), out.data_ptr(), ldy, ydt, ws, nws, on),
            "exl3_mx4_matmul")
     return out
 
 
 def exl3_mx4_linear_workspace_size(w: Exl3Mx4, m: int) -> int:
+    w._now()
     return int(lib().exl3_mx4_linear_workspace_size(w._ref, int(m)))
 
 
 def exl3_mx4_linear(x, w: Exl3Mx4, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
     """y [m, n] = x w^T (+ bias fp16 [n]): fp16 rows x [m, k], m up to 64,
     against MXFP4 weights w [n, k]."""
-    r = w._record
-    ldx = _f16_rows(x, r.k)
-    on = _stream_for(x, "x", stream)
-    if w.codes.get_device() != x.get_device():
+    _, _, n, k = w._now()
+    m, ldx = _f16_rows(x, k)
+    device, on = _place(x, "x", stream)
+    if w.codes.get_device() != device:
         _refuse("x and w are on different devices")
-    m = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, m, r.rows, x, bias, stream)
-    ws, nws, _keep = _scratch(workspace, False, exl3_mx4_linear_workspace_size, (w, m), x, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, m, n, device, bias, stream)
+    ws, nws, _keep = _scratch(workspace, False, lib().exl3_mx4_linear_workspace_size, (w._ref, m), device, stream)
     _check(lib().exl3_mx4_linear(w._ref, _ptr(bias), x.data_ptr(), m, ldx, out.data_ptr(), ldy, ydt, ws, nws,
                                  on), "exl3_mx4_linear")
     return out
 
 
 def exl3_mx4_moe_workspace_size(layer: Exl3Mx4Moe, t: int, topk: int) -> int:
+    layer._now()
     return int(lib().exl3_mx4_moe_workspace_size(layer._ref, int(t), int(topk)))
 
 
@@ -823,17 +853,16 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
     passed in has to be zero-filled before its first use and is then left to
     this function."""
     import torch
-    hidden = layer._record.gate_up.k
-    ldx = _f16_rows(x, hidden)
-    on = _stream_for(x, "x", stream)
-    if layer.gate_up.codes.get_device() != x.get_device():
+    hidden = layer._now().gate_up.k
+    t, ldx = _f16_rows(x, hidden)
+    device, on = _place(x, "x", stream)
+    if layer.gate_up.codes.get_device() != device:
         _refuse("x and the layer are on different devices")
-    t = x.shape[0]
-    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, x, None, stream)
+    out, ldy, ydt = _product_out(out, out_dtype, t, hidden, device, None, stream)
     for v, what, dt in ((topk_ids, "topk_ids", torch.int32), (topk_weights, "topk_weights", torch.float32)):
-        if v is not None and _tensor(v, what, dt, (t, topk)).get_device() != x.get_device():
+        if v is not None and _tensor(v, what, dt, (t, topk)).get_device() != device:
             _refuse(f"{what} is on another device than x")
-    ws, nws, _keep = _scratch(workspace, True, exl3_mx4_moe_workspace_size, (layer, t, topk), x, stream)
+    ws, nws, _keep = _scratch(workspace, True, lib().exl3_mx4_moe_workspace_size, (layer._ref, t, topk), device, stream)
     _check(lib().exl3_mx4_moe(layer._ref, x.data_ptr(), t, ldx, topk, out.data_ptr(), ldy, ydt, _ptr(topk_ids),
                               _ptr(topk_weights), ws, nws, on), "exl3_mx4_moe")
     return out

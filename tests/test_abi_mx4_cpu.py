@@ -179,3 +179,45 @@ def test_copies_hold_their_own_tensors():
         assert v._record.scales == v.scales.data_ptr() and (v._record.rows, v._record.k) == (4, 128)
         assert m._record.router == m.router.weight.data_ptr() != l.router.weight.data_ptr()
         assert m._record.gate_up.codes == m.gate_up.codes.data_ptr() and m._record.down.n == 64
+
+
+def _swapped(t, new):
+    t.data = new
+    return t
+
+
+def test_tensors_swapped_after_construction_are_read_anew():
+    torch = pytest.importorskip("torch")
+    a = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    w, b = X.Exl3Mx4(a(4096, 2560), a(4096, 160)), X.Exl3Mx4(a(512, 2560), a(512, 160))
+    before = X.exl3_mx4_matmul_workspace_size(w, b)
+    _swapped(w.codes, a(1024, 2560)), _swapped(w.scales, a(1024, 160))
+    fresh = X.exl3_mx4_matmul_workspace_size(X.Exl3Mx4(w.codes, w.scales), b)
+    assert before != fresh == X.exl3_mx4_matmul_workspace_size(w, b)
+    assert X.exl3_mx4_linear_workspace_size(w, 40) == X.exl3_mx4_linear_workspace_size(X.Exl3Mx4(w.codes, w.scales), 40)
+    w.codes.set_(a(1024, 2560))  # the shape as it was, other memory
+    assert w._now() == (w.codes.data_ptr(), w.scales.data_ptr(), 1024, 5120)
+    assert w._record.codes == w.codes.data_ptr() and w._record.rows == 1024
+    _swapped(w.codes, a(1024, 24))
+    with pytest.raises(ValueError):
+        X.exl3_mx4_matmul_workspace_size(w, b)
+    with pytest.raises(ValueError):
+        X.exl3_mx4_linear_workspace_size(w, 1)
+
+    f = lambda *s: torch.zeros(s, dtype=torch.float16)
+    gu, dn = X.Exl3Mx4Arena(a(3, 2, 32, 32), a(3, 2, 32, 2)), X.Exl3Mx4Arena(a(3, 1, 64, 16), a(3, 1, 64, 1))
+    sh = X.Exl3Mx4Shared(X.Exl3Mx4Arena(a(1, 2, 96, 32), a(1, 2, 96, 2)), X.Exl3Mx4Arena(a(1, 1, 64, 48), a(1, 1, 64, 3)),
+                         gate=f(64))
+    l = X.Exl3Mx4Moe(X.Exl3MoeRouter(f(3, 64), bias=torch.zeros(3)), gu, dn, sh)
+    before = X.exl3_mx4_moe_workspace_size(l, 16, 2)
+    _swapped(gu.codes, a(3, 2, 320, 32)), _swapped(gu.scales, a(3, 2, 320, 2))
+    _swapped(dn.codes, a(3, 1, 64, 160)), _swapped(dn.scales, a(3, 1, 64, 10))
+    assert before < X.exl3_mx4_moe_workspace_size(l, 16, 2)
+    for t, at in ((l.router.weight, lambda r: r.router), (l.router.bias, lambda r: r.router_bias),
+                  (sh.gate, lambda r: r.shared_gate), (sh.down.scales, lambda r: r.shared_down.scales),
+                  (sh.gate_up.codes, lambda r: r.shared_gate_up.codes), (dn.codes, lambda r: r.down.codes)):
+        _swapped(t, t.clone())
+        assert at(l._now()) == t.data_ptr()
+    _swapped(gu.scales, a(3, 2, 320, 1))
+    with pytest.raises(ValueError):
+        X.exl3_mx4_moe_workspace_size(l, 16, 2)

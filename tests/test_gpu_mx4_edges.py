@@ -81,3 +81,45 @@ def test_moe_infinite_activations_at_the_highest_scale_bytes(t):
     x[0] = 1
     y = X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
     assert np.isposinf(y[0]).all() and (y[1:] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# tensors whose memory is swapped after their record was made
+# ---------------------------------------------------------------------------
+def test_weights_swapped_or_reloaded_between_calls():
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(5)
+    one, two = B.rand_mx(rng, 96, 512), B.rand_mx(rng, 160, 512)
+    x = G.to_dev(rng.standard_normal((3, 512)).astype(np.float16))
+    a = X.exl3_mx4_quantize(x)
+    calls = lambda w: (X.exl3_mx4_linear(x, w), X.exl3_mx4_matmul(a, w), X.exl3_mx4_reconstruct(w))
+    want = calls(B.mx(two))
+    w = B.mx(one)
+    calls(w)
+    w.codes.data, w.scales.data = G.to_dev(two[0]), G.to_dev(two[1])
+    for got in (calls(w), calls(w)):
+        assert all(torch.equal(g, r) for g, r in zip(got, want))
+    for t, host in ((w.codes, two[0]), (w.scales, two[1])):  # offloaded, its place taken, loaded again
+        t.untyped_storage().resize_(0)
+    taken = [torch.full((96, 256), 0x55, dtype=torch.uint8, device=G.dev()) for _ in range(8)]
+    for t, host in ((w.codes, two[0]), (w.scales, two[1])):
+        t.untyped_storage().resize_(host.size)
+        t.copy_(G.to_dev(host))
+    assert all(torch.equal(g, r) for g, r in zip(calls(w), want))
+    X.exl3_mx4_quantize(torch.zeros((160, 512), dtype=torch.float16, device=G.dev()), out=w)
+    assert not w.codes.any() and all((t == 0x55).all() for t in taken)
+
+    (xm, l), (_, m) = B.moe_case(71, 4, 6, 128, 64, si=32, gate=True, bias=True), B.moe_case(72, 4, 6, 128, 96, si=64,
+                                                                                          gate=True, bias=True)
+    xd, layer, other = G.to_dev(xm), B.moe_layer(l), B.moe_layer(m)
+    want = X.exl3_mx4_moe(xd, other, 3)
+    X.exl3_mx4_moe(xd, layer, 3)
+    pairs = [(layer.router.weight, other.router.weight), (layer.router.bias, other.router.bias),
+             (layer.shared.gate, other.shared.gate)]
+    for u, v in ((layer.gate_up, other.gate_up), (layer.down, other.down), (layer.shared.gate_up, other.shared.gate_up),
+                 (layer.shared.down, other.shared.down)):
+        pairs += [(u.codes, v.codes), (u.scales, v.scales)]
+    for u, v in pairs:
+        u.data = v.clone()
+    assert torch.equal(X.exl3_mx4_moe(xd, layer, 3), want)
