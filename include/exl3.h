@@ -461,7 +461,9 @@ typedef struct exl3_mx4_experts {
 /* How a router's logits become choices and weights (l = x W_r^T, b the bias,
  * 0 where there is none):
  *   EXL3_ROUTE_SOFTMAX  chosen by l + b, weight softmax(l + b) over all experts
- *   EXL3_ROUTE_SIGMOID  chosen by sigmoid(l) + b, weight sigmoid(l)          */
+ *   EXL3_ROUTE_SIGMOID  chosen by sigmoid(l) + b, weight sigmoid(l).  Without a
+ *                       bias chosen by l: the same order, where sigmoid(l)
+ *                       has not yet rounded to 1                             */
 typedef enum exl3_route {
     EXL3_ROUTE_SOFTMAX = 0,
     EXL3_ROUTE_SIGMOID = 1
@@ -521,7 +523,11 @@ size_t exl3_mx4_moe_workspace_size(const exl3_mx4_moe_layer* layer, int64_t t, i
  *                 other); calls that overlap on it race
  * 0 <= t <= EXL3_MX4_MOE_MAX_TOKENS, experts <= EXL3_MX4_MOE_MAX_EXPERTS;
  * t == 0 returns EXL3_OK.  A NaN score counts as the lowest, so the ids are
- * always valid; a token with NaN or infinite logits gets NaN weights.  For
+ * always valid; the weights are what the formulas give.  EXL3_ROUTE_SOFTMAX: all
+ * of a token's are NaN if an l + b is NaN or +infinity or every one -infinity; a
+ * -infinity next to finite ones has weight 0.  EXL3_ROUTE_SIGMOID: 1 for an l of
+ * +infinity, 0 for -infinity, NaN for a NaN that is chosen.  Divided by their sum,
+ * all are NaN if one is, or if the sum is 0.  For
  * more tokens: a router and exl3_grouped_experts, or quantized rows.        */
 exl3_status exl3_mx4_moe(const exl3_mx4_moe_layer* layer, const void* x, int64_t t, int64_t ldx,
                          int32_t topk, void* y, int64_t ldy, int32_t y_dtype, int32_t* topk_ids,

@@ -123,3 +123,54 @@ def test_weights_swapped_or_reloaded_between_calls():
     for u, v in pairs:
         u.data = v.clone()
     assert torch.equal(X.exl3_mx4_moe(xd, layer, 3), want)
+
+
+# ---------------------------------------------------------------------------
+# routing of tokens whose logits are not finite
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_moe_weights_of_tokens_without_finite_logits(scoring, renorm):
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(61, 7, 12, 96, 64, bias=True, scoring=scoring, renorm=renorm, scale=0.5)
+    r = l["router"]
+    r[:, 0] = np.where(np.arange(12) % 3 == 0, 1, -1)  # an infinite x[0]: +inf for every third expert
+    r[:, 1], r[:, 2] = -1, 1                           # x[1]: all -inf; x[2]: all +inf
+    r[:, 3] = 1
+    r[5, 3] = 0                                        # x[3]: +inf, but NaN for expert 5
+    l["bias"][[2, 8]] = -np.inf                        # -inf next to finite logits
+    for t in range(4):
+        x[t, t] = np.inf
+    x[4, 10] = np.nan
+    ids = torch.empty((7, 12), dtype=torch.int32, device=G.dev())
+    w = torch.empty((7, 12), dtype=torch.float32, device=G.dev())
+    for topk in (12, 5):
+        i, v = ids[:, :topk].contiguous(), w[:, :topk].contiguous()
+        X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), topk, topk_ids=i, topk_weights=v)
+        with np.errstate(invalid="ignore"):
+            logits = x.astype(np.float64) @ r.astype(np.float64).T
+            rid, rw = M.route(logits, topk, scoring, l["bias"], renorm, 0.5)
+        i, v = i.cpu().numpy(), v.cpu().numpy()
+        assert all(sorted(set(q)) == sorted(q) and min(q) >= 0 and max(q) < 12 for q in i.tolist())
+        np.testing.assert_array_equal(i[5:], rid[5:])
+        np.testing.assert_allclose(v, rw, rtol=2.0 ** -19 + 16 * 107 * 2.0 ** -24)
+        if scoring == "softmax":
+            assert np.isnan(v[:5]).all() and np.isfinite(v[5:]).all()
+        else:
+            assert np.isnan(v[4]).all() and (renorm or (v[2] == 0.5).all() and (v[1] == 0).all())
+
+
+def test_moe_sigmoid_without_a_bias_chooses_by_the_logit():
+    # sigmoids that round to 1 in fp32 keep the order of their logits
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(62, 2, 9, 64, 32, scoring="sigmoid")
+    l["router"][:], x[:] = 0, 0
+    l["router"][:, 0] = [20, 24, 40, 22, 18, -3, 30, 30, 1]
+    x[:, 0] = 1
+    ids = torch.empty((2, 6), dtype=torch.int32, device=G.dev())
+    w = torch.empty((2, 6), dtype=torch.float32, device=G.dev())
+    X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 6, topk_ids=ids, topk_weights=w)
+    assert ids.tolist() == [[2, 6, 7, 1, 3, 0]] * 2
+    np.testing.assert_allclose(w.cpu().numpy(), 1 / 6, rtol=2.0 ** -19)
