@@ -433,7 +433,8 @@ size_t exl3_mx4_linear_workspace_size(const exl3_mx4* w, int64_t m);
 /* exl3_mx4_linear - y = x W^T (+ bias) for decode and verify batches: fp16
  * activations, unrounded, against MXFP4 weights; products exact in fp32, sums
  * fp32.  For more than EXL3_MX4_LINEAR_MAX_ROWS rows the weights' bytes no
- * longer bound the product: quantize the rows and call exl3_mx4_matmul.
+ * longer bound the product: call it for so many at a time, or, where rows rounded
+ * to 4 bits will do, quantize them and call exl3_mx4_matmul.
  *   w      [n][k] (rows = n).  Blocks with scale bytes outside 104 .. 140, whose
  *          values fp16 cannot hold, are taken in a second, slower way
  *   x      fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
@@ -527,8 +528,10 @@ size_t exl3_mx4_moe_workspace_size(const exl3_mx4_moe_layer* layer, int64_t t, i
  * of a token's are NaN if an l + b is NaN or +infinity or every one -infinity; a
  * -infinity next to finite ones has weight 0.  EXL3_ROUTE_SIGMOID: 1 for an l of
  * +infinity, 0 for -infinity, NaN for a NaN that is chosen.  Divided by their sum,
- * all are NaN if one is, or if the sum is 0.  For
- * more tokens: a router and exl3_grouped_experts, or quantized rows.        */
+ * all are NaN if one is, or if the sum is 0.
+ * More tokens are taken EXL3_MX4_MOE_MAX_TOKENS a call (a token's result may depend
+ * on the others of its call, to rounding): no entry point takes MXFP4 experts for
+ * more at once, and exl3_grouped_experts takes trellis tensors.              */
 exl3_status exl3_mx4_moe(const exl3_mx4_moe_layer* layer, const void* x, int64_t t, int64_t ldx,
                          int32_t topk, void* y, int64_t ldy, int32_t y_dtype, int32_t* topk_ids,
                          float* topk_weights, void* ws, size_t ws_bytes, exl3_stream_t stream);

@@ -174,3 +174,28 @@ def test_moe_sigmoid_without_a_bias_chooses_by_the_logit():
     X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 6, topk_ids=ids, topk_weights=w)
     assert ids.tolist() == [[2, 6, 7, 1, 3, 0]] * 2
     np.testing.assert_allclose(w.cpu().numpy(), 1 / 6, rtol=2.0 ** -19)
+
+
+# ---------------------------------------------------------------------------
+# more rows than a call takes
+# ---------------------------------------------------------------------------
+def test_more_tokens_and_rows_than_a_call_takes():
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(63, 41, 12, 160, 96, si=32, gate=True)
+    layer, xd, n = B.moe_layer(l), G.to_dev(x), X.MX4_MOE_MAX_TOKENS
+    ws = torch.zeros(X.exl3_mx4_moe_workspace_size(layer, n, 3), dtype=torch.uint8, device=G.dev())
+    y = torch.empty((41, 160), dtype=torch.float32, device=G.dev())
+    for i in range(0, 41, n):
+        X.exl3_mx4_moe(xd[i:i + n], layer, 3, out=y[i:i + n], workspace=ws)
+    ref, _, w = M.moe(x, l, 3)
+    B.assert_within(y.cpu().numpy(), ref, B.moe_limit(x, l, 3, ref, w, True))
+
+    rng = np.random.default_rng(64)
+    q, rows = B.rand_mx(rng, 300, 2080, lo=112, hi=122), rng.standard_normal((150, 2080)).astype(np.float16)
+    w, xd, n = B.mx(q), G.to_dev(rows), X.MX4_LINEAR_MAX_ROWS
+    y = torch.empty((150, 300), dtype=torch.float32, device=G.dev())
+    for i in range(0, 150, n):
+        X.exl3_mx4_linear(xd[i:i + n], w, out=y[i:i + n])
+    ref, mag = M.product(rows, M.decode(*q))
+    B.assert_within(y.cpu().numpy(), ref, B.bound(ref, mag, 2080, True))
