@@ -18,18 +18,19 @@ __device__ __forceinline__ u32x2_t lds_read8(uint32_t at) {
 // The source needs dword alignment.
 // Written as assembly so that the compiler, which cannot tell the stages
 // apart, does not wait for it before every LDS read; the kernel waits itself
-// before the barrier that hands a stage over.  (M0 needs one wait state before
-// its use.)
+// before the barrier that hands a stage over.  The LDS address is an operand in M0,
+// so the compiler, which writes it there, knows what M0 holds; one wait state lies
+// between the two.
 __device__ __forceinline__ void lds_copy16(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
-               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
+               : "v"(lane_off), "s"(rsrc), "s"(off), "{m0}"(at)
                : "memory");
 }
 __device__ __forceinline__ void lds_copy4(u32x4_t rsrc, uint32_t at, uint32_t lane_off, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :
-               : "s"(at), "v"(lane_off), "s"(rsrc), "s"(off)
+               : "v"(lane_off), "s"(rsrc), "s"(off), "{m0}"(at)
                : "memory");
 }
 
