@@ -192,7 +192,8 @@ struct MoeRouteLds {
   int chunk_entries[EPL], chunk_rows[EPL];
 };
 
-// Routing of all tokens by one workgroup, from the partial logits.
+// Routing of all tokens by one workgroup of NW waves, at least as many as tokens,
+// from the partial logits.
 template <int EPL, int NW>
 __device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s) {
   constexpr int cols = MoeRouteLds<EPL>::kCols;
@@ -222,18 +223,15 @@ __device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s)
     s.gates[tid] = l;
   }
   __syncthreads();
-  constexpr int kTurns = kMoeTokens / NW;
-  int id[kTurns];
-  float weight[kTurns];
-#pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int t = wave + NW * i;
-    if (t >= q.t) break;
-    moe_route_token<EPL>(q, s.keys + t * cols, s.scores + t * cols, lane, id[i], weight[i]);
+  const int t = wave;  // a token a wave
+  int id = 0;
+  float weight = 0.f;
+  if (t < q.t) {
+    moe_route_token<EPL>(q, s.keys + t * cols, s.scores + t * cols, lane, id, weight);
     if (lane < q.topk) {
-      atomicOr(&s.masks[id[i]], 1u << t);
-      if (q.ids) q.ids[t * q.topk + lane] = id[i];
-      if (q.weights) q.weights[t * q.topk + lane] = weight[i];
+      atomicOr(&s.masks[id], 1u << t);
+      if (q.ids) q.ids[t * q.topk + lane] = id;
+      if (q.weights) q.weights[t * q.topk + lane] = weight;
     }
   }
   __syncthreads();
@@ -285,19 +283,15 @@ __device__ __forceinline__ void moe_route(const MoeArgs& q, MoeRouteLds<EPL>& s)
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int t = wave + NW * i;
-    if (t >= q.t) break;
-    if (lane < q.topk) {
-      const uint32_t earlier = s.masks[id[i]] & ((1u << t) - 1u);
-      q.wtab[s.place[id[i]] * kMoeTokens + __popc(earlier)] = weight[i];
-    }
-    if (lane == 0) {
-      float w = 1.f;
-      if (q.d.shared_gate) w = 1.f / (1.f + exp_f(-s.gates[t]));
-      q.wtab[q.most * kMoeTokens + t] = w;
-    }
+  if (t >= q.t) return;
+  if (lane < q.topk) {
+    const uint32_t earlier = s.masks[id] & ((1u << t) - 1u);
+    q.wtab[s.place[id] * kMoeTokens + __popc(earlier)] = weight;
+  }
+  if (lane == 0) {
+    float w = 1.f;
+    if (q.d.shared_gate) w = 1.f / (1.f + exp_f(-s.gates[t]));
+    q.wtab[q.most * kMoeTokens + t] = w;
   }
 }
 
