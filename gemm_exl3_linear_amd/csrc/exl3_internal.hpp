@@ -125,6 +125,7 @@ hipError_t launch_mx4_quantize(const void* x, bool f32, int64_t rows, int64_t k,
                                uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_mx4_reconstruct(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k,
                                   void* out, bool f32, int64_t ldo, hipStream_t s);
+bool mx4_matmul_fits(int64_t m, int64_t n, int64_t k);  // in one launch
 size_t mx4_matmul_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t m, const uint8_t* b,
                              const uint8_t* b_scales, int64_t n, int64_t k, const uint16_t* bias, void* y,

@@ -11,7 +11,10 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
-constexpr int64_t kMaxElements = (int64_t)1 << 35;  // eight a thread, 256 threads, 2^24 workgroups
+// Launch sizes: a grid holds less than 2^32 threads.  Quantizing, a thread takes
+// eight elements, of 256 a workgroup.
+constexpr int64_t kMaxElements = (int64_t)1 << 35;
+constexpr int64_t kMaxQuantized = kMaxElements - 2048;
 constexpr int64_t kMaxTiles = (int64_t)1 << 26;     // 16 x 16 output tiles
 constexpr int kMaxExpertDim = 65536;
 
@@ -123,7 +126,7 @@ extern "C" {
 
 exl3_status exl3_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int64_t ldx, uint8_t* codes,
                               uint8_t* scales, exl3_stream_t stream) {
-  if (!valid_dtype(dtype) || !valid_shape(rows, k) || rows * k >= kMaxElements) return EXL3_E_INVALID;
+  if (!valid_dtype(dtype) || !valid_shape(rows, k) || rows * k > kMaxQuantized) return EXL3_E_INVALID;
   if (ldx < k || ldx % 8) return EXL3_E_INVALID;
   if (rows == 0) return EXL3_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16))
@@ -148,6 +151,7 @@ exl3_status exl3_mx4_reconstruct(const exl3_mx4* w, void* out, int32_t dtype, in
 size_t exl3_mx4_matmul_workspace_size(const exl3_mx4* a, const exl3_mx4* b) {
   if (check_matrix(a) != EXL3_OK || check_matrix(b) != EXL3_OK || a->k != b->k) return 0;
   if (a->rows == 0 || b->rows == 0 || tiles16(a->rows, b->rows) >= kMaxTiles) return 0;
+  if (!exl3::mx4_matmul_fits(a->rows, b->rows, a->k)) return 0;
   return exl3::mx4_matmul_workspace(a->rows, b->rows, a->k);
 }
 
@@ -158,6 +162,7 @@ exl3_status exl3_mx4_matmul(const exl3_mx4* a, const exl3_mx4* b, const uint16_t
   if (a->k != b->k) return EXL3_E_INVALID;
   if ((st = check_product(bias, y, a->rows, b->rows, ldy, y_dtype)) != EXL3_OK) return st;
   if (a->rows == 0 || b->rows == 0) return EXL3_OK;
+  if (!exl3::mx4_matmul_fits(a->rows, b->rows, a->k)) return EXL3_E_INVALID;
   if (!have_workspace(ws, ws_bytes, exl3::mx4_matmul_workspace(a->rows, b->rows, a->k))) return EXL3_E_WORKSPACE;
   trace("mx4_matmul m k n", a->rows, a->k, b->rows, 0);
   return from_hip(exl3::launch_mx4_matmul(a->codes, a->scales, a->rows, b->codes, b->scales, b->rows, a->k, bias, y,

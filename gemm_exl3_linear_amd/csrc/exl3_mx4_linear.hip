@@ -50,7 +50,6 @@ __global__ __launch_bounds__(NW * 64) void mx4_rows_kernel(Mx4RowsArgs q) {
 #pragma unroll
       for (int p = 0; p < P; ++p) acc[ng][mg][p] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int units = (kb + kMx4UnitBlocks - 1) / kMx4UnitBlocks;
   bool exact = true;  // fp16 rows: every scale in fp16
   auto unit = [&](auto whole, int u) {
     constexpr bool W = decltype(whole)::value != 0;
@@ -265,6 +264,14 @@ static Mx4Cut matmul_cut(int64_t m, int64_t n, int64_t k) {
   for (int i = 0; i < 3; ++i)
     if (others[i] < least) least = others[i], best = cuts[i];
   return best;
+}
+// The tiles in LDS, and few rows or columns, always do.  The others' 512 threads a
+// tile pass a grid's 2^32 where the scales are too many for LDS tiles.
+bool mx4_matmul_fits(int64_t m, int64_t n, int64_t k) {
+  if (m <= 16 || n <= 16) return true;
+  const Mx4Cut cut = matmul_cut(m, n, k);
+  const int64_t rows = cut == Mx4Cut::k16 ? 16 : (cut == Mx4Cut::k32 ? 32 : 64), cols = cut == Mx4Cut::k16 ? 16 : 32;
+  return cut == Mx4Cut::kLds || ((m + rows - 1) / rows) * ((n + cols - 1) / cols) < ((int64_t)1 << 23);
 }
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
   return m > 16 && n > 16 && matmul_cut(m, n, k) == Mx4Cut::kLds;

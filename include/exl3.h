@@ -387,7 +387,7 @@ typedef struct exl3_mx4 {
  * A block of zeros gets scale byte 0.  A block that holds a NaN or an
  * infinity becomes a NaN block: scale byte 255, codes 0.  Every decision is
  * exact, so the output is bit-exact by definition.  rows == 0 returns
- * EXL3_OK.  rows * k must stay below 2^35 (launch size).                   */
+ * EXL3_OK.  rows * k at most 2^35 - 2048 (launch size).                    */
 exl3_status exl3_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int64_t ldx,
                               uint8_t* codes, uint8_t* scales, exl3_stream_t stream);
 
@@ -416,7 +416,8 @@ size_t exl3_mx4_matmul_workspace_size(const exl3_mx4* a, const exl3_mx4* b);
  *          that is 0), 16-byte aligned: scratch, whatever it holds before and
  *          after.  Calls that overlap in time on one workspace race.
  * m == 0 or n == 0 returns EXL3_OK.  Calls whose launch would not fit the
- * hardware's grid (ceil(m/16) * ceil(n/16) >= 2^26) return EXL3_E_INVALID.
+ * hardware's grid return EXL3_E_INVALID: ceil(m/16) * ceil(n/16) >= 2^26, or,
+ * from (m + n) ceil(k/256) >= 2^29 on, ceil(m/64) * ceil(n/32) >= 2^23.
  * Results are the same bits on every run of one shape; a row's result may
  * depend on m (the tile is chosen by size), to rounding.                   */
 exl3_status exl3_mx4_matmul(const exl3_mx4* a, const exl3_mx4* b, const uint16_t* bias, void* y,

@@ -221,3 +221,20 @@ def test_tensors_swapped_after_construction_are_read_anew():
     _swapped(gu.scales, a(3, 2, 320, 1))
     with pytest.raises(ValueError):
         X.exl3_mx4_moe_workspace_size(l, 16, 2)
+
+
+def test_sizes_past_a_grid_are_refused():
+    # a grid holds less than 2^32 threads: 2^32 - 4 chunks of eight elements round up
+    # to it, and so do 2^23 tiles of 512 threads
+    quantize = lambda rows, k: X.lib().exl3_mx4_quantize(16, F16, rows, k, k, 16, 16, 0)
+    k = 32 * 9 * 331
+    rows = ((1 << 35) - 32) // k
+    assert rows * k == (1 << 35) - 32 and quantize(rows, k) == INV
+    assert quantize(1 << 24, 2048) == INV and quantize((1 << 24) - 1, 2048 + 32) == INV
+    a, b = mx(1 << 24, 8192), mx(1000, 8192)
+    assert X.lib().exl3_mx4_matmul_workspace_size(ctypes.byref(a), ctypes.byref(b)) == 0
+    assert matmul(a, b, ldy=1000, ws=16, n=1 << 60) == INV
+    # as many tiles, with scales that go through LDS, are a call that wants its workspace
+    a, b = mx(1 << 24, 512), mx(1000, 512)
+    assert X.lib().exl3_mx4_matmul_workspace_size(ctypes.byref(a), ctypes.byref(b)) > 0
+    assert matmul(a, b, ldy=1000) == WS
