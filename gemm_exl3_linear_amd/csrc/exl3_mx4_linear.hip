@@ -268,10 +268,15 @@ static Mx4Cut matmul_cut(int64_t m, int64_t n, int64_t k) {
 // The tiles in LDS, and few rows or columns, always do.  The others' 512 threads a
 // tile pass a grid's 2^32 where the scales are too many for LDS tiles.
 bool mx4_matmul_fits(int64_t m, int64_t n, int64_t k) {
-  if (m <= 16 || n <= 16) return true;
-  const Mx4Cut cut = matmul_cut(m, n, k);
-  const int64_t rows = cut == Mx4Cut::k16 ? 16 : (cut == Mx4Cut::k32 ? 32 : 64), cols = cut == Mx4Cut::k16 ? 16 : 32;
-  return cut == Mx4Cut::kLds || ((m + rows - 1) / rows) * ((n + cols - 1) / cols) < ((int64_t)1 << 23);
+  constexpr int64_t kMost = (int64_t)1 << 23;
+  auto tiles = [&](int64_t rows, int64_t cols) { return ((m + rows - 1) / rows) * ((n + cols - 1) / cols); };
+  if (m <= 16 || n <= 16 || tiles(16, 16) < kMost) return true;
+  switch (matmul_cut(m, n, k)) {
+    case Mx4Cut::k16: return false;
+    case Mx4Cut::k32: return tiles(32, 32) < kMost;
+    case Mx4Cut::k64x32: return tiles(64, 32) < kMost;
+    default: return true;
+  }
 }
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
   return m > 16 && n > 16 && matmul_cut(m, n, k) == Mx4Cut::kLds;
