@@ -83,6 +83,56 @@ def test_moe_infinite_activations_at_the_highest_scale_bytes(t):
     assert np.isposinf(y[0]).all() and (y[1:] == 0).all()
 
 
+@pytest.mark.parametrize("m", [1, 4, 8, 16, 24, 64])
+def test_linear_at_the_highest_and_lowest_scale_bytes(m):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m)
+    n, k = 130, 544
+    codes, scales = B.rand_mx(rng, n, k)
+    scales[:] = rng.choice([0, 1, 2, 3], (n, k // 32))
+    scales[::2] = rng.choice([251, 252, 253, 254], (n // 2, k // 32))
+    x = (rng.standard_normal((m, k)) * 2.0 ** -12).astype(np.float16)
+    y = X.exl3_mx4_linear(G.to_dev(x), B.mx((codes, scales)), out_dtype=torch.float32).cpu().numpy()
+    ref, mag = M.product(x, M.decode(codes, scales))
+    B.assert_within(y, ref, B.bound(ref, mag, k, True) + k * 2.0 ** -149)  # products below the normals are rounded too
+
+
+# products of scales at both ends (as one factor they are ordinary), near fp32's
+# largest, below its normals, below its least
+ENDS = [("both", (0, 3), (251, 254)), ("large", (250, 251), (118, 119)), ("subnormal", (20, 21), (88, 89)),
+        ("least", (0, 1), (0, 1))]
+
+
+@pytest.mark.parametrize("name,la,lb", ENDS, ids=[e[0] for e in ENDS])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 544), (16, 5000, 288), (300, 290, 416), (64, 64, 256), (1100, 1300, 1056)])
+def test_matmul_at_the_ends_of_the_scales(m, n, k, name, la, lb):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + k)
+    a, b = B.rand_mx(rng, m, k, lo=la[0], hi=la[1]), B.rand_mx(rng, n, k, lo=lb[0], hi=lb[1])
+    y = X.exl3_mx4_matmul(B.mx(a), B.mx(b), out_dtype=torch.float32).cpu().numpy()
+    ref, mag = M.product(M.decode(*a), M.decode(*b))
+    assert np.abs(ref).max() < 2.0 ** 128
+    B.assert_within(y, ref, B.bound(ref, mag, k, True) + k * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("m,n", [(3, 40), (300, 290), (1100, 1300)])
+def test_matmul_zero_blocks_at_any_scale(m, n):
+    # blocks of zeros are zeros at 2^127 and 2^-127 alike, whatever they meet
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m)
+    a, b = B.rand_mx(rng, m, 416, lo=112, hi=122), B.rand_mx(rng, n, 416, lo=112, hi=122)
+    for q, at in ((a, 2), (b, 9)):
+        q[0][:, 16 * at:16 * at + 16] = 0x80
+        q[1][::2, at], q[1][1::2, at] = 254, 0
+    a[1][:, 9], b[1][:, 2] = 254, 254
+    y = X.exl3_mx4_matmul(B.mx(a), B.mx(b), out_dtype=torch.float32).cpu().numpy()
+    ref, mag = M.product(M.decode(*a), M.decode(*b))
+    B.assert_within(y, ref, B.bound(ref, mag, 416, True))
+
+
 # ---------------------------------------------------------------------------
 # tensors whose memory is swapped after their record was made
 # ---------------------------------------------------------------------------
@@ -199,3 +249,35 @@ def test_more_tokens_and_rows_than_a_call_takes():
         X.exl3_mx4_linear(xd[i:i + n], w, out=y[i:i + n])
     ref, mag = M.product(rows, M.decode(*q))
     B.assert_within(y.cpu().numpy(), ref, B.bound(ref, mag, 2080, True))
+
+
+# ---------------------------------------------------------------------------
+# expert layers of every kernel
+# ---------------------------------------------------------------------------
+# hidden past 4096 (more workgroups than CUs in down) with entries of one, of two to
+# five and of more tokens; 129 to 1024 experts for few and many tokens; gate and up by
+# one workgroup a CU, over lengths that end in a wave's first or second unit and inside
+# a unit
+LAYERS = [
+    dict(t=1, e=8, h=5120, i=64, topk=3),
+    dict(t=3, e=8, h=5120, i=96, topk=8, si=32),
+    dict(t=16, e=8, h=4608, i=320, topk=3, si=64, gate=True),
+    dict(t=16, e=32, h=4128, i=288, topk=2, bias=True),
+    dict(t=16, e=256, h=512, i=32, topk=8),
+    dict(t=9, e=128, h=256, i=64, topk=4, scoring="sigmoid"),
+    dict(t=2, e=300, h=256, i=32, topk=8),
+    dict(t=16, e=300, h=288, i=32, topk=4, renorm=False),
+    dict(t=2, e=512, h=256, i=32, topk=16, scoring="sigmoid", bias=True),
+    dict(t=16, e=512, h=256, i=32, topk=8, si=32, gate=True),
+    dict(t=16, e=600, h=288, i=32, topk=6),
+    dict(t=1, e=4, h=1440, i=32, topk=2, si=32),
+    dict(t=16, e=4, h=2080, i=32, topk=2, si=64, gate=True),
+    dict(t=5, e=2, h=2848, i=32, topk=1),
+    dict(t=16, e=4, h=1312, i=64, topk=4, si=32),
+]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_moe_layers(case, f32):
+    B.test_moe(case, f32)
