@@ -8,9 +8,11 @@
 // instruction applies the scales itself, so a wave only reads and multiplies:
 // 128 x 64 a wave of 256 x 256 is as large as its registers allow.
 //
-// What bounds it: 4096 rows 5120 -> 17408, 187 us, 3.9 PFLOP/s: about 160 for four
-// rounds of 256 x 256 tiles, with the matrix cores busy nearly half of the time, 20 for
-// the small tiles of the rest, 5 for the scales.  A loop of these instructions from
+// What bounds it: 4096 rows 5120 -> 17408, 181 to 198 us from card to card, 4.0 to 3.7
+// PFLOP/s.  Where it takes 184 (192 over 1.6 GB of tensors), a trace of the launches,
+// each by itself with its start and end, gives 175 for four rounds of 256 x 256 tiles,
+// with the matrix cores busy nearly half of the time, 19 for the small tiles of the rest
+// and 5 for the scales.  A loop of these instructions from
 // registers alone runs at 7.0 to 7.2 PFLOP/s with random codes and at 9.5 with zeros:
 // the clock falls with what the matrix cores switch, and this kernel, too, is a fifth
 // faster a step on zeros (1.49 against 1.83 us).

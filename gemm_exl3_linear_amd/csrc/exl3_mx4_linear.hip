@@ -1,8 +1,9 @@
 // exl3_mx4_linear and exl3_mx4_matmul where few rows or small sizes leave the
 // weights' bytes, or the launch, as the bound: workgroups whose waves share k, and
-// the choice of the kernel by size.  Measured: one row 5120 -> 17408 (47 MB) 12.1 us
-// with fp16 rows, 11.3 with 4-bit rows; one row 2048 -> 512 3.6 us, of which a launch
-// is 1.6.
+// the choice of the kernel by size.  Measured, as below, in graphs of such calls over
+// three sets of tensors in turn: one row 5120 -> 17408 (47 MB) 11.5 us with fp16 rows,
+// 11.0 with 4-bit rows; over 1 GB of sets, whose weights come from HBM, 12.5 (3.8 TB/s)
+// and 11.8 (4.0); one row 2048 -> 512 3.4 us, of which a launch is 1.6.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_linear.hpp"
 
@@ -178,17 +179,18 @@ static int wide_splits(int64_t n, int64_t k) {
 // and what further rounds of the CUs add; there, a start and steps that grow with
 // the rows, and a second launch for shares of k (up to 8 rows only where it is
 // clearly less).  As measured (us, 16 / 32 / LDS):
-//    8 rows  5120 ->  2048    6.6    8.0    -
-//    8 rows  5120 ->  5120   10.9    8.5   12.2
-//    8 rows 17408 ->   512   14.8   18.8   10.1
-//    6 rows 17408 ->  5120    -     18.2   19.4
-//   64 rows  2048 ->   512    5.2    5.9   11.0
-//   64 rows  5120 ->  2048   14.9   10.9   13.6
-//   20 rows   512 ->  8192    5.5    4.6    7.8
-//   40 rows 17408 ->    64   21.7   26.2   11.9
-//   32 rows  5120 ->  5120   21.0   17.8   14.2
-//   16 rows 17408 ->  5120    -     28.9   20.0
-//   16 rows  5120 ->  5120    -     11.1   12.7
+//    8 rows  5120 ->  2048    6.4    7.8    9.2
+//    8 rows  5120 ->  5120   10.2    8.3   12.4
+//    8 rows 17408 ->   512   14.4   18.8   10.0
+//    6 rows 17408 ->  5120   24.7   18.4   19.2
+//   64 rows  2048 ->   512    5.0    5.5   10.7
+//   64 rows  5120 ->  2048   14.5   10.1   14.9
+//   20 rows   512 ->  8192    4.7    4.3    7.5
+//   40 rows 17408 ->    64   21.3   25.7   11.1
+//   32 rows  5120 ->  5120   20.3   17.3   15.0
+//   16 rows 17408 ->  5120   41.2   27.5   20.2
+//   16 rows  5120 ->  5120   14.6   10.1   13.1
+// (over 1 GB of sets each is 0.1 to 5 us longer, in the same order)
 enum class Mx4RowsCut { k16, k32, kLds };
 static Mx4RowsCut rows_cut(int64_t m, int64_t n, int64_t k) {
   const int64_t units = (k + kMx4UnitK - 1) / kMx4UnitK, row_tiles = (m + 15) / 16;
@@ -220,9 +222,10 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
   const Mx4RowsArgs q{x, nullptr, ldx, codes, scales, bias, y, ldy, m, n, kb, y_f32, 0, 0, 1, nullptr};
   // up to 4 rows: four pieces (exl3_mx4_rows.hpp) where k is long enough for the fewer
   // loads to show, else two; 32 columns a workgroup where those fill half the chip and
-  // x has more than a row to fetch (us: one row 5120 -> 17408 four pieces 12.8, two
-  // 13.6, one 16; 2048 -> 2048 4.0 / 3.7; 16 / 32 columns: 4 rows 17408 -> 5120 21.3 /
-  // 16.7, 5120 -> 2048 5.9 / 7.3, one row 5120 -> 17408 12.8 / 14.7)
+  // x has more than a row to fetch (us: one row 5120 -> 17408 four pieces 11.4, two
+  // 12.3; 2048 -> 2048 3.6 / 3.5; 16 / 32 columns: 4 rows 17408 -> 5120 20.3 / 16.1,
+  // 5120 -> 2048 5.7 / 7.1, one row 5120 -> 17408 11.4 / 13.0, 17408 -> 5120, where the
+  // rule takes the slower, 14.6 / 13.0)
   if (m <= 4) {
     const bool cols32 = m > 1 && n >= 4096;
     if (k >= 4096) return cols32 ? launch_rows<false, 1, 4, 2, 8>(q, s) : launch_rows<false, 1, 4, 1, 8>(q, s);
@@ -241,14 +244,14 @@ hipError_t launch_mx4_linear(const uint8_t* codes, const uint8_t* scales, int64_
 // (exl3_mx4_gemm.hip).  Small tiles load more for a product and are more; the
 // estimates, in us, count the launch, a wave's turns over k and what further
 // rounds of the CUs add, which is less where k is too short for all waves.  As
-// measured (us, 16 / 32 / 64 x 32 / LDS, - not measured):
-//   100 rows 17408 ->   50   10.9   19.5   27.8    -
-//   333 rows  2080 -> 1111    8.7    7.6    7.5    -
-//   500 rows  5120 ->  500   13.3    8.4   11.0   14.7
-//   500 rows  2048 -> 1000   12.5    7.7    6.9   11.2
-//    32 rows 17408 -> 5120   28.5   20.3   25.6   19.8
-//  1000 rows  1024 -> 4000   35.9   21.8    -     10.1
-//  4000 rows    96 -> 5000  154.7  106.7    -     20.9
+// measured (us, 16 / 32 / 64 x 32 / LDS):
+//   100 rows 17408 ->   50   10.7   19.2   27.3   14.2
+//   333 rows  2080 -> 1111    8.5    7.8    6.7   15.1
+//   500 rows  5120 ->  500   13.0    8.5   11.3   14.6
+//   500 rows  2048 -> 1000   11.8    7.4    6.4   10.9
+//    32 rows 17408 -> 5120   27.9   21.0   23.9   20.1
+//  1000 rows  1024 -> 4000   34.2   21.8   19.0    9.8
+//  4000 rows    96 -> 5000  124     74.8   74.5   21.0
 enum class Mx4Cut { k16, k32, k64x32, kLds };
 static Mx4Cut matmul_cut(int64_t m, int64_t n, int64_t k) {
   const double units = (double)((k + kMx4UnitK - 1) / kMx4UnitK), eighth = units / 8;
@@ -303,9 +306,12 @@ hipError_t launch_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, int64_t 
   }
   // 16 rows or fewer in 32 columns a workgroup where the chip stays full, for
   // fewer loads of a; not for a row or two, whose a comes from cache, over very many
-  // columns (us, 16 / 32 columns: 16 rows 17408 -> 5120 20.0 / 16.0, 17408 -> 2048
-  // 11.4 / 15.7, 2048 -> 8192 5.1 / 4.6; one row 17408 -> 5120 15.0 / 12.8, 5120 ->
-  // 17408 11.5 / 12.2)
+  // columns, where the two are near each other and whole rounds of the CUs decide (us,
+  // 16 / 32 columns: 16 rows 17408 -> 5120 19.3 / 15.9, 17408 -> 2048 11.2 / 15.7, 2048 ->
+  // 8192 4.8 / 4.2; one row 17408 -> 5120 14.3 / 12.4, 5120 -> 15000 9.4 / 8.8, 5120 ->
+  // 17408 11.1 / 11.6, 5120 -> 20480 11.1 / 11.7, 4 rows 5120 -> 17408 12.2 / 12.5; the
+  // rule takes the slower for one row 5120 -> 12288, 7.8 / 8.7, and 2048 -> 32768, 8.6 /
+  // 8.3)
   return q.n >= 4096 && (q.m > 4 || q.n < 16384) ? launch_rows<true, 1, 1, 2, 8>(q, s)
                                                  : launch_rows<true, 1, 1, 1, 8>(q, s);
 }

@@ -15,13 +15,14 @@
 // matrix operand per expert and each expert's weights are read once, whatever
 // the routing.  The weights' bytes bound the two products.
 //
-// Measured (us, router / gate and up / down, of kernels; a call): 1 token, 8 of 256
-// experts 2048 x 512 7.4 / 6.2 / 4.9, 17.2; 16 tokens, about 101 experts of them and a
-// shared one 11 / 30 / 21, 62.0 (116 and 58 MB: 3.9 and 2.7 TB/s); 5 tokens, 4 of 60
-// experts 1440 x 352 6.4 / 7.2 / 8.5, 21.  Few tokens are bound by the three launches,
-// each with its loads, sums and routing one after the other; many experts by what
-// eight waves a SIMD have in flight: more loads a wave at the price of waves were
-// slower (two units at a time 67 us, six waves 74).
+// Measured (us, router / gate and up / down, of kernels; a call, and one over 1.4 GB
+// of weights in turn): 1 token, 8 of 256 experts 2048 x 512 7.4 / 6.5 / 4.9, 17.2, 19.7;
+// 16 tokens, about 101 experts of them and a shared one 11 / 30 / 22, 62, 63 (116 and 58
+// MB: 3.9 and 2.6 TB/s); 5 tokens, 4 of 60 experts 1440 x 352 6.6 / 7.6 / 7.9, 21, 24.5.
+// Few tokens are bound by the three launches, each with its loads, sums and routing
+// one after the other; many experts by what eight waves a SIMD have in flight: more
+// loads a wave at the price of waves were slower (two units at a time 67 us, six
+// waves 74).
 //
 // a is kept as three bf16 pieces (8 + 8 + 8 significand bits, exact to fp32's
 // 24), so the down product runs on bf16 matrix instructions against weights
@@ -128,8 +129,10 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
-// e^x to about an ulp in few instructions: x log2 e with the product's own
-// rounding error, and log2 e's, put back after the power.  (The routing runs once
+// e^x in few instructions: x log2 e with the product's own rounding error, and log2
+// e's, put back after the power.  To about an ulp for 2^-125 < e^x < 2^126; past that, where
+// a correction could meet an infinity or a subnormal, without it: off by up to 2^-17 of
+// the value.  (The routing runs once
 // a call, so its instructions come from memory: their number is its time.)
 __device__ __forceinline__ float exp_f(float x) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500e-8f, kLn2 = 0.693147180559945309f;

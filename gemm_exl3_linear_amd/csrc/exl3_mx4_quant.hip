@@ -11,9 +11,10 @@
 // Both kernels are bound by HBM.  Quantising, a thread takes eight elements, so a
 // wave's loads and its 4-byte code stores are contiguous; the four lanes of a block
 // meet in two quad permutations.  Back, a thread stores 16 bytes four times.
-// Measured: 4096 x 5120 fp16 12 us there and 9.5 back (53 MB each), 14000 x 5120 fp32
+// Measured: 4096 x 5120 fp16 12 us there and 10 back (53 MB each, some of it from
+// the last-level cache; 14 and 10 over 1.5 GB of tensors in turn), 14000 x 5120 fp32
 // 56 and 46 us (325 MB each, 5.8 and 7.0 TB/s; a 2 GiB copy reaches 4.9).  One row of
-// 5120: 1.6 us each, a launch.
+// 5120: 1.6 to 2 us each, a launch.
 #include "exl3_internal.hpp"
 #include "exl3_mx4.hpp"
 

@@ -20,9 +20,10 @@
 // reads, were 12 % slower; shares of k across the tiles' ends, to fill the chip for
 // any number of tiles, 10 %.)
 //
-// Measured: 37 rows 17408 -> 5120 (49 MB) 23.6 us: 11.3 steps of 1.25 us, 3.4 TB/s of
-// weights, then start, end and the second launch.  The copies bound a step: alone
-// they take 1.1 us with 16 rows and 1.5 with 48, the rest without them 0.95.
+// Measured: 37 rows 17408 -> 5120 (49 MB) 22.8 us over three sets of tensors in turn,
+// 24.1 over 1 GB of them: 11.3 steps of 1.25 us, 3.4 TB/s of weights, then start, end
+// and the second launch.  The copies bound a step: alone they take 1.1 us with 16
+// rows and 1.5 with 48, the rest without them 0.95.
 #include "exl3_internal.hpp"
 #include "exl3_mx4_lds.hpp"
 #include "exl3_mx4_linear.hpp"
