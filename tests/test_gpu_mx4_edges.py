@@ -281,3 +281,121 @@ LAYERS = [
 @pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
 def test_moe_layers(case, f32):
     B.test_moe(case, f32)
+
+
+# ---------------------------------------------------------------------------
+# NaN blocks as quantization makes them: scale byte 255, codes 0
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("m,n,k", [(1, 40, 544), (16, 5000, 288), (40, 3, 96), (64, 64, 256), (300, 290, 416),
+                                   (1100, 1300, 1056)])
+def test_quantized_nans_reach_the_products(m, n, k):
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(m + n)
+    x, v = rng.standard_normal((m, k)).astype(np.float16), rng.standard_normal((n, k)).astype(np.float16)
+    x[m // 2, k - 1], v[n - 1, 0], v[0, k // 2] = np.nan, np.inf, -np.inf
+    a, w = X.exl3_mx4_quantize(G.to_dev(x)), X.exl3_mx4_quantize(G.to_dev(v))
+    assert (w.scales == 255).sum() == 2 and (a.scales == 255).sum() == 1
+    y = X.exl3_mx4_matmul(a, w, out_dtype=torch.float32).cpu().numpy()
+    da, dw = M.decode(*M.quantize(x)), M.decode(*M.quantize(v))
+    ref, _ = M.product(da, dw)
+    B.assert_within(y, ref, B.bound(ref, M.product(np.nan_to_num(da), np.nan_to_num(dw))[1], k, True))
+    x[m // 2, k - 1] = 1
+    for rows in (x[:64], x[:7], x[:1]):
+        y = X.exl3_mx4_linear(G.to_dev(rows), w, out_dtype=torch.float32).cpu().numpy()
+        ref, _ = M.product(rows, dw)
+        B.assert_within(y, ref, B.bound(ref, M.product(rows, np.nan_to_num(dw))[1], k, True))
+
+
+@pytest.mark.parametrize("hidden", [288, 4128])
+@pytest.mark.parametrize("t", [1, 5, 6, 16])
+def test_moe_nan_blocks_of_zero_codes(t, hidden):
+    # in a unit of ordinary blocks, and next to a block at byte 254
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(49, t, 4, hidden, 288, si=96)
+    x = (x * np.float16(2.0 ** -3)).astype(np.float16)
+    l["gate_up"][1][:, 1] -= 60
+    l["shared"][0][1][:, 1] -= 60
+    for e, row, b in ((0, 3, 1), (1, 17, 8), (2, hidden - 1, 0), (3, 40, 5)):
+        l["down"][0][e, 0, row, 16 * b:16 * b + 16] = 0
+        l["down"][1][e, 0, row, b] = 255
+    l["down"][1][3, 0, 40, 2] = 254
+    l["shared"][1][0][0, 0, 60, 16:32], l["shared"][1][1][0, 0, 60, 1] = 0, 255
+    y = X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 4, out_dtype=torch.float32).cpu().numpy()
+    ref, ids, w = M.moe(x, l, 4)
+    assert np.isnan(ref).sum() == 5 * t
+    clean = {**l, "down": (l["down"][0], np.where(l["down"][1] == 255, 127, l["down"][1])),
+             "shared": (l["shared"][0], (l["shared"][1][0], np.where(l["shared"][1][1] == 255, 127, l["shared"][1][1])))}
+    B.assert_within(y, ref, B.moe_limit(x, clean, 4, ref, w, True))
+
+
+@pytest.mark.parametrize("t", [1, 5, 16])
+def test_moe_nan_blocks_of_zero_codes_in_gate_and_up(t):
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, l = B.moe_case(50, t, 4, 288, 96)
+    l["gate_up"][0][2, 1, 7, 64:80], l["gate_up"][1][2, 1, 7, 4] = 0, 255
+    y = X.exl3_mx4_moe(G.to_dev(x), B.moe_layer(l), 2, out_dtype=torch.float32).cpu().numpy()
+    _, ids, _ = M.moe(x, l, 2)
+    np.testing.assert_array_equal(np.isnan(y).all(1), (ids == 2).any(1))
+    np.testing.assert_array_equal(np.isnan(y).any(1), (ids == 2).any(1))
+
+
+# ---------------------------------------------------------------------------
+# captured calls that make their own outputs and workspaces, and graphs that share one
+# ---------------------------------------------------------------------------
+def test_captured_calls_with_their_own_memory():
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(81)
+    xm, l = B.moe_case(82, 16, 32, 512, 160, si=96, gate=True)
+    layer, xd = B.moe_layer(l), G.to_dev(xm)
+    w, rows = B.mx(B.rand_mx(rng, 640, 17408)), G.to_dev(rng.standard_normal((37, 17408)).astype(np.float16))
+    a, b = B.mx(B.rand_mx(rng, 700, 4128)), B.mx(B.rand_mx(rng, 1290, 4128))
+
+    def run():
+        q = X.exl3_mx4_quantize(xd)
+        return [X.exl3_mx4_moe(xd, layer, 4), X.exl3_mx4_linear(rows, w), X.exl3_mx4_matmul(a, b),
+                X.exl3_mx4_reconstruct(q), X.exl3_mx4_moe(X.exl3_mx4_reconstruct(q), layer, 4)]
+    want = run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for i in range(4):
+        for o in got:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(got, want)), f"replay {i}"
+        run()
+
+
+def test_graphs_of_layers_that_share_a_workspace():
+    # one after the other on one stream, with eager calls on the same workspace between
+    import torch
+    import gemm_exl3_linear_amd as X
+    cases = [(B.moe_case(83, 16, 32, 256, 96, si=64), 4), (B.moe_case(84, 2, 128, 512, 32), 8)]
+    built = [(G.to_dev(x), B.moe_layer(l), k) for (x, l), k in cases]
+    ws = torch.zeros(max(X.exl3_mx4_moe_workspace_size(l, x.shape[0], k) for x, l, k in built), dtype=torch.uint8,
+                     device=G.dev())
+    want = [X.exl3_mx4_moe(x, l, k) for x, l, k in built]
+    outs, graphs = [torch.empty_like(y) for y in want], []
+    for (x, l, k), y in zip(built, outs):
+        X.exl3_mx4_moe(x, l, k, out=y, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            X.exl3_mx4_moe(x, l, k, out=y, workspace=ws)
+        graphs.append(g)
+    for order in ([0, 1], [1, 0], [1, 1, 0, 0], [0, 1, 0, 1]):
+        for y in outs:
+            y.zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, r) for y, r in zip(outs, want))
+        x, l, k = built[order[0]]
+        X.exl3_mx4_moe(x[:1], l, k, workspace=ws)
