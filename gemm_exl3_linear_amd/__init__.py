@@ -37,6 +37,12 @@ MX4_MOE_MAX_TOKENS = 16
 MX4_MOE_MAX_EXPERTS = 1024
 ROUTE_SOFTMAX = 0
 ROUTE_SIGMOID = 1
+ROUTE_MAX_EXPERTS = 1024
+ROUTE_MAX_GROUPS = 64
+GROUP_MAX = 0
+GROUP_TOP2 = 1
+LORA_MAX_RANK = 256
+LORA_MAX_ADAPTERS = 4096
 
 
 class Exl3Error(RuntimeError):
@@ -76,6 +82,23 @@ class _Mx4MoeLayer(ctypes.Structure):
                 ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("gate_up", _Mx4Experts),
                 ("down", _Mx4Experts), ("shared_gate_up", _Mx4Experts), ("shared_down", _Mx4Experts),
                 ("shared_gate", ctypes.c_void_p)]
+
+
+class _RouteRule(ctypes.Structure):
+    _fields_ = [("balance", ctypes.c_void_p), ("experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("scoring", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _RouterWeight(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("experts", ctypes.c_int32),
+                ("hidden", ctypes.c_int32)]
+
+
+class _LoraStack(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("k", ctypes.c_int64), ("n", ctypes.c_int64)]
 
 
 _lib = None
@@ -151,6 +174,21 @@ def lib() -> ctypes.CDLL:
     L.exl3_mx4_moe_workspace_size.argtypes = [Lp, i64, i32]
     L.exl3_mx4_moe.restype = i32
     L.exl3_mx4_moe.argtypes = [Lp, vp, i64, i64, i32, vp, i64, i32, vp, vp, vp, sz, vp]
+    rule, router, lora = ctypes.POINTER(_RouteRule), ctypes.POINTER(_RouterWeight), ctypes.POINTER(_LoraStack)
+    L.exl3_route_topk.restype = i32
+    L.exl3_route_topk.argtypes = [rule, vp, i32, i64, i64, vp, vp, vp]
+    L.exl3_router_linear_workspace_size.restype = sz
+    L.exl3_router_linear_workspace_size.argtypes = [router, i64]
+    L.exl3_router_linear.restype = i32
+    L.exl3_router_linear.argtypes = [router, vp, i64, i64, vp, i64, vp, sz, vp]
+    L.exl3_router_workspace_size.restype = sz
+    L.exl3_router_workspace_size.argtypes = [router, i64, i32]
+    L.exl3_router.restype = i32
+    L.exl3_router.argtypes = [router, rule, vp, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+    L.exl3_lora_workspace_size.restype = sz
+    L.exl3_lora_workspace_size.argtypes = [lora, i64]
+    L.exl3_lora.restype = i32
+    L.exl3_lora.argtypes = [lora, vp, i64, i64, vp, vp, i64, vp, i64, i32, vp, sz, vp]
     _lib = L
     return L
 
@@ -578,7 +616,7 @@ def _matrix(t, what: str, rows: Optional[int], cols: Optional[int]):
     m, n = t.shape
     if (rows is not None and m != rows) or (cols is not None and n != cols):
         _refuse(f"{what} has shape {(m, n)}, not {(rows, cols)}")
-    if stride[1] != 1 and n > 1:
+    if stride[1] != 1 and n > 1 and m:  # of no elements strides say nothing
         _refuse(f"{what} does not have contiguous rows")
     return m, n, stride[0] if m > 1 else -(-n // 8) * 8
 
@@ -865,4 +903,261 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
     ws, nws, _keep = _scratch(workspace, True, lib().exl3_mx4_moe_workspace_size, (layer._ref, t, topk), device, stream)
     _check(lib().exl3_mx4_moe(layer._ref, x.data_ptr(), t, ldx, topk, out.data_ptr(), ldy, ydt, _ptr(topk_ids),
                               _ptr(topk_weights), ws, nws, on), "exl3_mx4_moe")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Routing to experts
+# ---------------------------------------------------------------------------
+class _Record:
+    """A record of tensors: subclasses give `_tensors()` (the checked tensors, None
+    left out) and `_make(...)`, the C record of them."""
+
+    def __post_init__(self):
+        import torch
+        parts = self._tensors()
+        if any(t.device != parts[0].device for t in parts):
+            _refuse("the tensors are on different devices")
+        record = self._make()
+        object.__setattr__(self, "_record", record)
+        object.__setattr__(self, "_ref", ctypes.byref(record))
+        object.__setattr__(self, "_parts", (parts, torch.Tensor.data_ptr))
+        object.__setattr__(self, "_seen", (list(map(_ptr, parts)), list(map(_shape, parts))))
+
+    def _now(self):
+        """The record of the tensors as they are: checked and read again if their
+        memory or shape was changed under them (`.data =`, set_, resize_)."""
+        parts, data_ptr = self._parts
+        if (list(map(data_ptr, parts)), list(map(_shape, parts))) != self._seen:
+            self.__post_init__()
+        return self._record
+
+    def __reduce__(self):  # copies and pickles take the tensors, not the record's pointers
+        return type(self), tuple(getattr(self, f) for f in self.__dataclass_fields__)
+
+
+@dataclass(frozen=True)
+class Exl3Router(_Record):
+    """A router's linear: weight fp16 [experts, hidden], bias fp32 [experts] or None."""
+    weight: "object"
+    bias: Optional["object"] = None
+
+    def _tensors(self):
+        import torch
+        parts = [_tensor(self.weight, "router weight", torch.float16, (None, None))]
+        if self.bias is not None:
+            parts.append(_tensor(self.bias, "router bias", torch.float32, (self.experts,)))
+        return parts
+
+    def _make(self):
+        return _RouterWeight(_ptr(self.weight), _ptr(self.bias), self.experts, self.hidden)
+
+    @property
+    def experts(self) -> int:
+        return int(self.weight.shape[0])
+
+    @property
+    def hidden(self) -> int:
+        return int(self.weight.shape[1])
+
+
+@dataclass(frozen=True)
+class Exl3RouteRule(_Record):
+    """How logits become choices and weights: scoring "softmax" or "sigmoid"; balance
+    fp32 [experts], added to the scores for the choice alone, or None; `groups` groups
+    of consecutive experts of which `topk_groups` (all if None) are kept, graded by
+    group_score "max" (their best) or "top2" (the sum of their two best); weights
+    divided by their sum if `renormalize`, then multiplied by `scale`."""
+    experts: int
+    topk: int
+    scoring: str = "softmax"
+    balance: Optional["object"] = None
+    groups: int = 1
+    topk_groups: Optional[int] = None
+    group_score: str = "max"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def _tensors(self):
+        if self.balance is None:
+            return []
+        import torch
+        return [_tensor(self.balance, "balance", torch.float32, (self.experts,))]
+
+    def _make(self):
+        if self.scoring not in ("softmax", "sigmoid"):
+            _refuse(f"scoring {self.scoring!r} is not softmax or sigmoid")
+        if self.group_score not in ("max", "top2"):
+            _refuse(f"group_score {self.group_score!r} is not max or top2")
+        return _RouteRule(_ptr(self.balance), self.experts, self.topk,
+                          ROUTE_SOFTMAX if self.scoring == "softmax" else ROUTE_SIGMOID, self.groups,
+                          self.groups if self.topk_groups is None else self.topk_groups,
+                          GROUP_MAX if self.group_score == "max" else GROUP_TOP2, int(self.renormalize),
+                          float(self.scale))
+
+
+def _choices(rule: Exl3RouteRule, t: int, topk_ids, topk_weights, device: int, stream):
+    """The tensors that take the choices (new ones where none are given), checked."""
+    import torch
+    if rule.balance is not None and rule.balance.get_device() != device:
+        _refuse("the balance is on another device than the operands")
+    shape = (t, rule.topk)
+    if topk_ids is None:
+        topk_ids = _new(torch.empty, shape, torch.int32, device, stream)
+    elif _tensor(topk_ids, "topk_ids", torch.int32, shape).get_device() != device:
+        _refuse("topk_ids is on another device than the operands")
+    if topk_weights is None:
+        topk_weights = _new(torch.empty, shape, torch.float32, device, stream)
+    elif _tensor(topk_weights, "topk_weights", torch.float32, shape).get_device() != device:
+        _refuse("topk_weights is on another device than the operands")
+    return topk_ids, topk_weights
+
+
+def exl3_route_topk(logits, rule: Exl3RouteRule, topk_ids=None, topk_weights=None, stream=None):
+    """Choices int32 [t, topk] and weights fp32 [t, topk] of tokens with the logits
+    fp16 or fp32 [t, experts]."""
+    rule._now()
+    t, _, ldl = _matrix(logits, "logits", None, rule.experts)
+    device, on = _place(logits, "logits", stream)
+    topk_ids, topk_weights = _choices(rule, t, topk_ids, topk_weights, device, stream)
+    _check(lib().exl3_route_topk(rule._ref, logits.data_ptr(), _f16_f32(logits, "logits"), t, ldl,
+                                 topk_ids.data_ptr(), topk_weights.data_ptr(), on), "exl3_route_topk")
+    return topk_ids, topk_weights
+
+
+def exl3_router_linear_workspace_size(router: Exl3Router, t: int) -> int:
+    router._now()
+    return int(lib().exl3_router_linear_workspace_size(router._ref, int(t)))
+
+
+def _logits(out, t: int, router: Exl3Router, device: int):
+    """Row stride of the logits' tensor, checked."""
+    if _f16_f32(out, "the logits' tensor") != EXL3_F32:
+        _refuse(f"the logits' tensor is {out.dtype}, not fp32")
+    if out.get_device() != device:
+        _refuse("the logits' tensor is on another device than x")
+    return _matrix(out, "the logits' tensor", t, router.experts)[2]
+
+
+def _router_rows(x, router: Exl3Router, stream):
+    hidden = router._now().hidden
+    t, ldx = _f16_rows(x, hidden)
+    device, on = _place(x, "x", stream)
+    if router.weight.get_device() != device:
+        _refuse("x and the router are on different devices")
+    return t, ldx, device, on
+
+
+def exl3_router_linear(x, router: Exl3Router, out=None, workspace=None, stream=None):
+    """Logits fp32 [t, experts] of fp16 rows x [t, hidden].  A workspace passed in has to
+    be zero-filled before its first use and is then left to the router's functions."""
+    t, ldx, device, on = _router_rows(x, router, stream)
+    if out is None:
+        import torch
+        out = _new(torch.empty, (t, router.experts), torch.float32, device, stream)
+    ldl = _logits(out, t, router, device)
+    ws, nws, _keep = _scratch(workspace, True, lib().exl3_router_linear_workspace_size, (router._ref, t), device,
+                              stream)
+    _check(lib().exl3_router_linear(router._ref, x.data_ptr(), t, ldx, out.data_ptr(), ldl, ws, nws, on),
+           "exl3_router_linear")
+    return out
+
+
+def exl3_router_workspace_size(router: Exl3Router, t: int, logits: bool = True) -> int:
+    """Bytes exl3_router needs; logits: whether the call gets a tensor for them."""
+    router._now()
+    return int(lib().exl3_router_workspace_size(router._ref, int(t), int(logits)))
+
+
+def exl3_router(x, router: Exl3Router, rule: Exl3RouteRule, logits=None, topk_ids=None, topk_weights=None,
+                workspace=None, stream=None):
+    """Choices int32 [t, topk] and weights fp32 [t, topk] of fp16 rows x [t, hidden]:
+    exl3_router_linear and exl3_route_topk in one call.  logits fp32 [t, experts]
+    receives the logits if given.  The workspace is exl3_router_linear's."""
+    rule._now()
+    t, ldx, device, on = _router_rows(x, router, stream)
+    ldl, ptr = (0, 0) if logits is None else (_logits(logits, t, router, device), logits.data_ptr())
+    topk_ids, topk_weights = _choices(rule, t, topk_ids, topk_weights, device, stream)
+    ws, nws, _keep = _scratch(workspace, True, lib().exl3_router_workspace_size,
+                              (router._ref, t, logits is not None), device, stream)
+    _check(lib().exl3_router(router._ref, rule._ref, x.data_ptr(), t, ldx, ptr, ldl, topk_ids.data_ptr(),
+                             topk_weights.data_ptr(), ws, nws, on), "exl3_router")
+    return topk_ids, topk_weights
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters
+# ---------------------------------------------------------------------------
+@dataclass(frozen=True)
+class Exl3Lora(_Record):
+    """Adapters of one projection: a fp16 [adapters, rank, k], b fp16 [adapters, n,
+    rank], scales fp32 [adapters] or None (1), ranks int32 [adapters] (each adapter's own
+    rank) or None."""
+    a: "object"
+    b: "object"
+    scales: Optional["object"] = None
+    ranks: Optional["object"] = None
+
+    def _tensors(self):
+        import torch
+        parts = [_tensor(self.a, "a", torch.float16, (None, None, None))]
+        count, rank, _ = self.a.shape
+        parts.append(_tensor(self.b, "b", torch.float16, (count, None, rank)))
+        if self.scales is not None:
+            parts.append(_tensor(self.scales, "scales", torch.float32, (count,)))
+        if self.ranks is not None:
+            parts.append(_tensor(self.ranks, "ranks", torch.int32, (count,)))
+        return parts
+
+    def _make(self):
+        return _LoraStack(_ptr(self.a), _ptr(self.b), _ptr(self.scales), _ptr(self.ranks), self.adapters, self.rank,
+                          self.k, self.n)
+
+    @property
+    def adapters(self) -> int:
+        return int(self.a.shape[0])
+
+    @property
+    def rank(self) -> int:
+        return int(self.a.shape[1])
+
+    @property
+    def k(self) -> int:
+        return int(self.a.shape[2])
+
+    @property
+    def n(self) -> int:
+        return int(self.b.shape[1])
+
+
+def exl3_lora_workspace_size(lora: Exl3Lora, m: int) -> int:
+    lora._now()
+    return int(lib().exl3_lora_workspace_size(lora._ref, int(m)))
+
+
+def exl3_lora(x, lora: Exl3Lora, rows, base=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """y [m, n] = base + scale_a B_a (A_a x) with a = rows[i] (int32 [m]) for row i;
+    rows whose value is no adapter (-1) get base, or zeros without one.  x fp16 [m, k],
+    base and y of one type, fp16 or fp32.  `out=base` adds in place."""
+    import torch
+    record = lora._now()
+    m, ldx = _f16_rows(x, record.k)
+    device, on = _place(x, "x", stream)
+    if lora.a.get_device() != device:
+        _refuse("x and the adapters are on different devices")
+    if _tensor(rows, "rows", torch.int32, (m,)).get_device() != device:
+        _refuse("rows is on another device than x")
+    if out_dtype is None and base is not None:
+        out_dtype = base.dtype
+    out, ldy, ydt = _product_out(out, out_dtype, m, record.n, device, None, stream)
+    ldb, ptr = 0, 0
+    if base is not None:
+        if base.dtype != out.dtype:
+            _refuse(f"base is {base.dtype}, the output {out.dtype}")
+        if base.get_device() != device:
+            _refuse("base is on another device than x")
+        ldb, ptr = _matrix(base, "base", m, record.n)[2], base.data_ptr()
+    ws, nws, _keep = _scratch(workspace, False, lib().exl3_lora_workspace_size, (lora._ref, m), device, stream)
+    _check(lib().exl3_lora(lora._ref, x.data_ptr(), m, ldx, rows.data_ptr(), ptr, ldb, out.data_ptr(), ldy, ydt, ws,
+                           nws, on), "exl3_lora")
     return out

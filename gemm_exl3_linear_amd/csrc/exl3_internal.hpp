@@ -157,4 +157,40 @@ size_t mx4_moe_workspace(const Mx4MoeDesc& d, int64_t t, int topk);
 hipError_t launch_mx4_moe(const Mx4MoeDesc& d, const uint16_t* x, int64_t t, int64_t ldx, int topk, void* y,
                           int64_t ldy, bool y_f32, int32_t* ids, float* weights, void* ws, hipStream_t s);
 
+// --- routing -----------------------------------------------------------------
+struct RouteRule {
+  const float* balance;  // [experts] or null
+  int experts, topk, scoring;
+  int groups, group_size, topk_groups, top2;
+  uint32_t group_inverse;  // e * group_inverse >> 20 == e / group_size
+  int renormalize;
+  float scale;
+};
+hipError_t launch_route_topk(const RouteRule& q, const void* logits, bool f32, int64_t t, int64_t ldl, int32_t* ids,
+                             float* weights, hipStream_t s);
+struct RouterDesc {
+  const uint16_t* weight;  // [experts][hidden]
+  const float* bias;       // [experts] or null
+  int experts, hidden;
+};
+size_t router_linear_workspace(const RouterDesc& d, int64_t t);
+hipError_t launch_router_linear(const RouterDesc& d, const uint16_t* x, int64_t t, int64_t ldx, float* logits,
+                                int64_t ldl, void* ws, hipStream_t s);
+size_t router_workspace(const RouterDesc& d, int64_t t, bool logits);  // logits: the caller's
+hipError_t launch_router(const RouterDesc& d, const RouteRule& rule, const uint16_t* x, int64_t t, int64_t ldx,
+                         float* logits, int64_t ldl, int32_t* ids, float* weights, void* ws, hipStream_t s);
+
+// --- low-rank adapters -------------------------------------------------------
+struct LoraDesc {
+  const uint16_t* a;     // [adapters][rank][k]
+  const uint16_t* b;     // [adapters][n][rank]
+  const float* scales;   // [adapters] or null
+  const int32_t* ranks;  // [adapters] or null
+  int adapters, rank;
+  int64_t k, n;
+};
+size_t lora_workspace(const LoraDesc& d, int64_t m);
+hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t ldx, const int32_t* rows,
+                       const void* base, int64_t ldb, void* y, int64_t ldy, bool f32, void* ws, hipStream_t s);
+
 }  // namespace exl3

@@ -537,6 +537,163 @@ exl3_status exl3_mx4_moe(const exl3_mx4_moe_layer* layer, const void* x, int64_t
                          int32_t topk, void* y, int64_t ldy, int32_t y_dtype, int32_t* topk_ids,
                          float* topk_weights, void* ws, size_t ws_bytes, exl3_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Routing to experts: from hidden rows or logits to the topk_ids and
+ * topk_weights that exl3_grouped_experts takes.
+ * ------------------------------------------------------------------------ */
+#define EXL3_ROUTE_MAX_EXPERTS 1024
+#define EXL3_ROUTE_MAX_GROUPS 64
+
+/* What grades a group of experts. */
+typedef enum exl3_group_score {
+    EXL3_GROUP_MAX = 0, /* its best choice value */
+    EXL3_GROUP_TOP2 = 1 /* the sum of its two best choice values (of its two best
+                           scores where there is no balance) */
+} exl3_group_score;
+
+/* How logits l become choices and weights:
+ *   scores         s = softmax(l) over all experts (EXL3_ROUTE_SOFTMAX) or
+ *                  sigmoid(l) (EXL3_ROUTE_SIGMOID)
+ *   choice values  v = s + balance, or l itself without a balance (the same order)
+ *   groups         experts / groups consecutive experts each, 1 for none; the
+ *                  topk_groups best graded ones are kept, equal grades going to the
+ *                  lower group
+ *   choices        the topk best of the kept groups, best first, equal values going
+ *                  to the lower expert
+ *   weights        s of the chosen, divided by their sum if renormalize is not 0,
+ *                  times scale
+ * Here a balance shifts choices only, for softmax scores too; a bias of the router's
+ * linear, which shifts logits, is exl3_router_weight's.
+ *   balance      fp32 [experts] device pointer, 4-byte aligned, or NULL
+ *   experts      1..EXL3_ROUTE_MAX_EXPERTS, a multiple of groups
+ *   topk         1..EXL3_MAX_TOPK, at most topk_groups * (experts / groups)
+ *   groups       1..EXL3_ROUTE_MAX_GROUPS; EXL3_GROUP_TOP2 needs groups of two
+ *   topk_groups  1..groups
+ * Without a balance logits are compared as they are.  With one, and for
+ * EXL3_GROUP_TOP2, values are computed in 64 bits and compared to 42 significant
+ * bits, so that choices do not depend on how 32 bits would have rounded.
+ * A NaN value counts as the lowest, so the ids are always valid and a token's are
+ * distinct.  Weights are what the formulas give: softmax of a token with a NaN or
+ * +infinite logit, or with -infinite ones only, is NaN throughout; a -infinite logit
+ * next to finite ones has the score 0, for sigmoid too. */
+typedef struct exl3_route_rule {
+    const float* balance;
+    int32_t experts;
+    int32_t topk;
+    int32_t scoring;
+    int32_t groups;
+    int32_t topk_groups;
+    int32_t group_score;
+    int32_t renormalize;
+    float scale;
+} exl3_route_rule;
+
+/* exl3_route_topk - choices and weights of t tokens from their logits.
+ *   logits        [t][ldl] of `dtype` (EXL3_F16 or EXL3_F32), ldl >= experts; rows
+ *                 need no alignment beyond the element's own
+ *   topk_ids      int32 [t][topk]
+ *   topk_weights  fp32 [t][topk]
+ * 0 <= t <= 2^24; t == 0 returns EXL3_OK.  The same bits on every run; a token's
+ * result does not depend on the others of its call.                          */
+exl3_status exl3_route_topk(const exl3_route_rule* rule, const void* logits, int32_t dtype, int64_t t, int64_t ldl,
+                            int32_t* topk_ids, float* topk_weights, exl3_stream_t stream);
+
+/* A router's linear: l = x W^T (+ bias).
+ *   weight   fp16 [experts][hidden], row-major, 16-byte aligned
+ *   bias     fp32 [experts] device pointer, 4-byte aligned, or NULL
+ *   experts  1..EXL3_ROUTE_MAX_EXPERTS
+ *   hidden   a multiple of 8, at most 65536                                  */
+typedef struct exl3_router_weight {
+    const uint16_t* weight;
+    const float* bias;
+    int32_t experts;
+    int32_t hidden;
+} exl3_router_weight;
+
+/* Bytes of device workspace exl3_router_linear needs (0 if none is needed, or the
+ * arguments are invalid). */
+size_t exl3_router_linear_workspace_size(const exl3_router_weight* w, int64_t t);
+
+/* exl3_router_linear - the logits of t tokens: fp16 rows and weights, products exact
+ * in fp32, sums fp32, not rounded.
+ *   x       fp16 [t][ldx], ldx >= hidden, multiple of 8, 16-byte aligned
+ *   logits  fp32 [t][ldl], ldl >= experts, 4-byte aligned; it may not overlap x
+ *   ws      device workspace of at least the queried size (may be NULL when that is
+ *           0), 16-byte aligned, zero-filled before its first use and then left to
+ *           the router's entry points, which leave its arrival counts at zero (calls
+ *           of any router and size may share it, one after the other); calls that
+ *           overlap on it race
+ * 0 <= t <= 2^24; t == 0 returns EXL3_OK.  The same bits on every run of one shape; a
+ * row's result may depend on t, to rounding.                                */
+exl3_status exl3_router_linear(const exl3_router_weight* w, const void* x, int64_t t, int64_t ldx, float* logits,
+                               int64_t ldl, void* ws, size_t ws_bytes, exl3_stream_t stream);
+
+/* Bytes of device workspace exl3_router needs (0 if the arguments are invalid);
+ * logits: not 0 if the call is given memory for them. */
+size_t exl3_router_workspace_size(const exl3_router_weight* w, int64_t t, int32_t logits);
+
+/* exl3_router - exl3_router_linear and exl3_route_topk of its logits in one call (one
+ * launch for a few tokens).  Arguments, limits and results are those of the two.
+ *   logits  fp32 [t][ldl], or NULL where the caller has no use for them
+ *   ws      as for exl3_router_linear, and it may be the same one             */
+exl3_status exl3_router(const exl3_router_weight* w, const exl3_route_rule* rule, const void* x, int64_t t,
+                        int64_t ldx, float* logits, int64_t ldl, int32_t* topk_ids, float* topk_weights, void* ws,
+                        size_t ws_bytes, exl3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.
+ * ------------------------------------------------------------------------ */
+#define EXL3_LORA_MAX_RANK 256
+#define EXL3_LORA_MAX_ADAPTERS 4096
+
+/* A stack of adapters of one projection [k] -> [n]:
+ *   a       fp16 [adapters][rank][k], row-major, 16-byte aligned
+ *   b       fp16 [adapters][n][rank], row-major, 16-byte aligned
+ *   scales  fp32 [adapters] device pointer, 4-byte aligned, or NULL (1)
+ *   ranks   int32 [adapters] device pointer, 4-byte aligned, or NULL: the rank of each
+ *           adapter, taken between 0 and `rank`; what a and b hold past it has no say
+ *   adapters  0..EXL3_LORA_MAX_ADAPTERS (a and b may be NULL when 0)
+ *   rank      a multiple of 8, at most EXL3_LORA_MAX_RANK
+ *   k, n      at most 2^20, k a multiple of 8                               */
+typedef struct exl3_lora_stack {
+    const uint16_t* a;
+    const uint16_t* b;
+    const float* scales;
+    const int32_t* ranks;
+    int32_t adapters;
+    int32_t rank;
+    int64_t k;
+    int64_t n;
+} exl3_lora_stack;
+
+/* Bytes of device workspace exl3_lora needs for m rows (0 if none is needed, or the
+ * arguments are invalid). */
+size_t exl3_lora_workspace_size(const exl3_lora_stack* l, int64_t m);
+
+/* exl3_lora - y_i = base_i + scale_a B_a (A_a x_i), a = rows[i]: what the adapter of
+ * each row's request adds to a projection's output (exl3_linear, exl3_mx4_linear, ...).
+ * Products of A are exact in fp32, sums fp32; A x is kept to 24 bits (below 2^-25 of
+ * the row's largest fewer, 2^-40 of that is lost) between the products; one rounding to
+ * an fp16 output.
+ *   x     fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
+ *   rows  int32 [m] device pointer, 4-byte aligned: each row's adapter; a value outside
+ *         0 .. adapters-1 (-1, say) stands for none, and y_i is base_i
+ *   base  [m][ldb] of y's type, ldb >= n, or NULL (zeros)
+ *   y     [m][ldy] of y_dtype (EXL3_F16 or EXL3_F32), ldy >= n; y may be base itself
+ *         (ldb == ldy: added in place, rows without an adapter left alone), but may not
+ *         overlap it, x or the adapters otherwise.  Rows of base and y need no alignment
+ *         beyond the element's own
+ *   ws    device workspace of at least the queried size (may be NULL when that is 0),
+ *         16-byte aligned: scratch, whatever it holds before and after.  Calls that
+ *         overlap in time on one workspace race.
+ * 0 <= m <= 2^24; m == 0 returns EXL3_OK.  A row whose x, base or adapter holds NaN or
+ * an infinity gets what the formula gives; other rows are not touched by it.  The same
+ * bits on every run of one shape and assignment of rows; a row's result may depend on
+ * the others', to rounding.                                                  */
+exl3_status exl3_lora(const exl3_lora_stack* l, const void* x, int64_t m, int64_t ldx, const int32_t* rows,
+                      const void* base, int64_t ldb, void* y, int64_t ldy, int32_t y_dtype, void* ws, size_t ws_bytes,
+                      exl3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
