@@ -1,6 +1,6 @@
 // exl3_router_linear and exl3_router: a router's logits l = x W^T (+ c), fp16 matrix
 // instructions with fp32 sums, and for few tokens their routing in the same launch.
-#include "exl3_mx4.hpp"
+#include "exl3_mx4_lds.hpp"
 #include "exl3_route.hpp"
 
 namespace exl3 {
@@ -8,7 +8,6 @@ namespace exl3 {
 constexpr int kRouterRows = 16;           // of an operand
 constexpr int kRouterCounts = 128;        // arrival counts at the head of a workspace: one a group of 16 experts,
                                           // and the routing's
-constexpr int kRouterWaves = 8;
 
 struct RouterArgs {
   RouterDesc d;
@@ -16,7 +15,7 @@ struct RouterArgs {
   int64_t t, ldx;
   float* logits;  // may be null where the routing takes the sums
   int64_t ldl;
-  int splits;
+  int splits;         // shares of hidden
   uint32_t* arrived;  // 0 between calls
   float* part;        // [splits][t][estride], with several splits or the routing
   int estride;
@@ -28,12 +27,12 @@ struct RouterArgs {
 // Sums of 16 experts (blockIdx.x / splits) for 16 tokens (from blockIdx.y on) over a
 // share of hidden.  VPL > 0: the last workgroup to arrive routes every token, expert 64 i +
 // lane at a lane's i-th place.
-template <int VPL, int K>
-__global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterArgs q) {
+template <int VPL, int K, int NW>
+__global__ __launch_bounds__(NW * 64) void router_rows_kernel(RouterArgs q) {
   constexpr bool kRoutes = VPL > 0;
   constexpr int kV = kRoutes ? VPL : 1;
-  __shared__ float4_t sums[kRouterWaves * 64];
-  __shared__ RouteLds<64, kV> lds[kRoutes ? kRouterWaves : 1];
+  __shared__ float4_t sums[NW * 64];
+  __shared__ RouteLds<64, kV> lds[kRoutes ? NW : 1];
   __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
@@ -44,8 +43,8 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
     const uint16_t* x = q.x + (row_there ? (row0 + r) * q.ldx : 0);
     const uint16_t* w = q.d.weight + (e_there ? (int64_t)e * q.d.hidden : 0);
     float4_t acc = {0.f, 0.f, 0.f, 0.f};
-    const int stride = kRouterWaves * q.splits;
-    for (int st = split * kRouterWaves + wave; 32 * st < q.d.hidden; st += 4 * stride) {
+    const int stride = NW * q.splits;
+    for (int st = split * NW + wave; 32 * st < q.d.hidden; st += 4 * stride) {
       u32x4_t a[4], b[4];  // four steps' loads at a time
   #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -63,7 +62,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
     __syncthreads();
     if (wave == 0) {
   #pragma unroll
-      for (int o = 1; o < kRouterWaves; ++o) acc += sums[o * 64 + lane];
+      for (int o = 1; o < NW; ++o) acc += sums[o * 64 + lane];
       const bool whole = q.splits == 1 && !kRoutes;
       const float c = whole && q.d.bias && e_there ? q.d.bias[e] : 0.f;
   #pragma unroll
@@ -92,10 +91,10 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
     return q.d.bias ? l + q.d.bias[expert] : l;
   };
   if constexpr (!kRoutes) {
-    for (int i = threadIdx.x; i < (int)q.t * 16; i += kRouterWaves * 64)
+    for (int i = threadIdx.x; i < (int)q.t * 16; i += NW * 64)
       if (const int o = group * 16 + (i & 15); o < q.d.experts) q.logits[(i >> 4) * q.ldl + o] = sum(i >> 4, o);
   } else {
-    for (int row = wave; row < (int)q.t; row += kRouterWaves) {
+    for (int row = wave; row < (int)q.t; row += NW) {
       float l[kV];
 #pragma unroll
       for (int i = 0; i < kV; ++i) l[i] = 64 * i + lane < q.d.experts ? sum(row, 64 * i + lane) : 0.f;
@@ -114,20 +113,199 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
   }
 }
 
+// ---------------------------------------------------------------------------
+// many tokens
+// ---------------------------------------------------------------------------
+// 64 tokens x 64 experts by eight waves over a share of k (blockIdx.y), in stages of 128
+// that go from memory straight to LDS, three of them in flight.  A wave takes 16 of a
+// stage's 128 k for the whole tile, so that LDS is read once (a quarter of the tile each
+// would read it twice), and reads the next stage while it multiplies this one; the waves'
+// sums meet in LDS at the end.
+//
+// LDS: a stage holds rows of 256 bytes, 64 of x and then 64 of W; 16-byte piece c of row
+// r lies at place c ^ (r % 16), so that sixteen rows' pieces c cover all 64 banks.
+constexpr int kGemmTile = 64;
+constexpr int kGemmWaves = 8;
+constexpr int kGemmK = 16 * kGemmWaves;                // of a stage
+constexpr int kGemmRing = 4;                           // stages of LDS
+constexpr int kGemmStage = 2 * kGemmTile * kGemmK * 2;  // bytes
+constexpr int kGemmCopies = kGemmStage / 1024 / kGemmWaves;  // a wave's 1 KB copies of a stage, half of x
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+// A wave's operands of a stage: 64 rows of 16 k of x and of W.
+struct RouterOperands {
+  f16x8_t x[2], w[2];
+};
+
+__global__ __launch_bounds__(kGemmWaves * 64) void router_gemm_kernel(RouterArgs q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kGemmRing * kGemmStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // a row tile's workgroups run on one XCD (workgroup i on XCD i % 8), one behind the
+  // other, so that x comes from memory once
+  const int across = (q.d.experts + kGemmTile - 1) / kGemmTile;
+  const int64_t j = blockIdx.x >> 3;
+  const int64_t row0 = ((j / across) * 8 + (blockIdx.x & 7)) * kGemmTile;
+  const int e0 = (int)(j % across) * kGemmTile;
+  if (row0 >= q.t) return;
+  const int64_t ldx = q.ldx;
+  const int rows = (int)(q.t - row0 < kGemmTile ? q.t - row0 : kGemmTile);
+  const int cols = q.d.experts - e0 < kGemmTile ? q.d.experts - e0 : kGemmTile;
+  const uint32_t hidden = (uint32_t)q.d.hidden;
+  const u32x4_t xs = buffer_words(reinterpret_cast<const uint8_t*>(q.x + row0 * ldx),
+                                  ((uint64_t)(rows - 1) * ldx + hidden) * 2);
+  const u32x4_t ws = buffer_words(reinterpret_cast<const uint8_t*>(q.d.weight + (int64_t)e0 * hidden),
+                                  (uint64_t)cols * hidden * 2);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)ring;
+  // copies 2 wave, 2 wave + 1 of x and of W: four rows each, a piece a lane
+  uint32_t off[kGemmCopies], piece[kGemmCopies];
+#pragma unroll
+  for (int i = 0; i < kGemmCopies; ++i) {
+    const uint32_t row = 4 * (2 * wave + (i & 1)) + (lane >> 4);
+    piece[i] = 8 * ((lane & 15) ^ (row & 15));
+    off[i] = (row * (i < 2 ? (uint32_t)ldx : hidden) + piece[i]) * 2;
+  }
+  const int stages = (int)((hidden + kGemmK - 1) / kGemmK);
+  const int first = (int)((int64_t)stages * blockIdx.y / q.splits);
+  const int end = (int)((int64_t)stages * (blockIdx.y + 1) / q.splits);
+  const auto fetch = [&](int st) {
+    const uint32_t at = base + (uint32_t)(st % kGemmRing) * kGemmStage;
+#pragma unroll
+    for (int i = 0; i < kGemmCopies; ++i) {
+      const bool there = (uint32_t)st * kGemmK + piece[i] < hidden;  // past the end: zeros
+      lds_copy16(i < 2 ? xs : ws, at + (uint32_t)((i < 2 ? 0 : 2 * kGemmWaves) + 2 * wave + (i & 1)) * 1024,
+                 there ? off[i] : kPastEnd, (uint32_t)st * kGemmK * 2);
+    }
+  };
+  const uint32_t r = lane & 31, c = 2 * wave + (lane >> 5);
+  const uint32_t in_tile = r * 256 + 16 * (c ^ (r & 15));
+  const auto read = [&](int st, RouterOperands& o) {
+    const uint32_t at = base + (uint32_t)(st % kGemmRing) * kGemmStage + in_tile;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      o.x[a] = __builtin_bit_cast(f16x8_t, lds_read16(at + a * 8192));
+      o.w[a] = __builtin_bit_cast(f16x8_t, lds_read16(at + kGemmStage / 2 + a * 8192));
+    }
+  };
+  float16_t acc[2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+  const auto multiply = [&](const RouterOperands& o) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.x[a], o.w[b], acc[a][b], 0, 0, 0);
+  };
+  // Waits until at most the two stages after the next are open here: the next has landed
+  // here, and behind the barrier everywhere, and this one's place is read and free.
+  static_assert(kGemmRing == 4 && kGemmCopies == 4, "8 copies of two stages");
+  const auto step = [&](int st, const RouterOperands& now, RouterOperands& next) {
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    fetch(st + kGemmRing);
+    read(st + 1, next);
+    multiply(now);
+  };
+  for (int st = first; st < first + kGemmRing; ++st) fetch(st);
+  asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+  RouterOperands even, odd;
+  read(first, even);
+  int st = first;  // what is read past the end is never multiplied
+  for (; st + 1 < end; st += 2) {
+    step(st, even, odd);
+    step(st + 1, odd, even);
+  }
+  if (st < end) multiply(even);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  float* sums = reinterpret_cast<float*>(ring);  // [wave][row][expert]
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        sums[(wave * 64 + 32 * a + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)) * 64 + 32 * b + r] = acc[a][b][i];
+  __syncthreads();
+  if (lane >= cols) return;
+  const bool whole = q.splits == 1;
+  const float bias = whole && q.d.bias ? q.d.bias[e0 + lane] : 0.f;
+  float* out = whole ? q.logits + row0 * q.ldl : q.part + ((int64_t)blockIdx.y * q.t + row0) * q.estride;
+  const int64_t ld = whole ? q.ldl : q.estride;
+#pragma unroll 4
+  for (int row = wave; row < rows; row += kGemmWaves) {
+    float v = sums[row * 64 + lane];
+#pragma unroll
+    for (int o = 1; o < kGemmWaves; ++o) v += sums[(o * 64 + row) * 64 + lane];
+    out[row * ld + e0 + lane] = v + bias;
+  }
+}
+
+// The logits of shares of k: a thread takes four experts of a token.
+__global__ __launch_bounds__(256) void router_sum_kernel(RouterArgs q) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int across = q.estride / 4;
+  const int64_t row = i / across;
+  const int e = (int)(i - row * across) * 4;
+  if (row >= q.t) return;
+  const float* p = q.part + row * q.estride + e;
+  float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = 0; k < q.splits; ++k) v += *reinterpret_cast<const float4_t*>(p + (int64_t)k * q.t * q.estride);
+#pragma unroll
+  for (int o = 0; o < 4; ++o)
+    if (e + o < q.d.experts) q.logits[row * q.ldl + e + o] = v[o] + (q.d.bias ? q.d.bias[e + o] : 0.f);
+}
+
 namespace {
 
 constexpr int kFewTokens = 16;  // of which one launch makes the logits and routes them
 
-int router_splits(const RouterDesc& d, int64_t t) {
-  if (t > kFewTokens) return 1;
-  const int groups = (d.experts + 15) / 16;
-  const int most = (d.hidden + 32 * kRouterWaves * 4 - 1) / (32 * kRouterWaves * 4);
-  const int want = (256 + groups - 1) / groups;
-  return want < most ? want : most;
+// How a router's product is cut: shares of k, 16 x 16 by router_rows_kernel or 64 x 64
+// by router_gemm_kernel.
+struct RouterCut {
+  bool tiled;
+  int splits;
+};
+
+// The cut by estimates in us, fitted to kernels alone, and measured where they meet
+// (tokens x hidden x experts, by rows / tiled): 64 x 5120 x 256 11.0 / 9.5 (of 8), 512
+// 20.6 / 11.4, 4096 142 / 20.5; 1024 x 2048 x 64 6.8 / 8.4, 2048 9.8 / 8.4; 333 x 1440 x
+// 60 4.3 / 7.4.
+RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx) {
+  const int64_t groups = (d.experts + 15) / 16, rows = (t + kRouterRows - 1) / kRouterRows;
+  if (t <= kFewTokens) {
+    const int most = (d.hidden + 32 * 8 * 4 - 1) / (32 * 8 * 4);
+    const int want = (int)((256 + groups - 1) / groups);
+    return {false, want < most ? want : most};
+  }
+  // by rows: 16 bytes a clock and CU of operands that are loaded as they are multiplied,
+  // 9.6 TB/s of all
+  const double lone = 1.7 / 1024 * d.hidden, all = groups * rows * 64.0 * d.hidden / 9.6e6;
+  RouterCut best{false, 1};
+  double cost = 2.5 + (lone > all ? lone : all);
+  if (ldx >= (1 << 24)) return best;  // offsets into 64 rows have 32 bits
+  // tiled: 0.36 a stage and round of a workgroup a CU; sums of shares 4.5 and their bytes
+  const int64_t tiles = (t + kGemmTile - 1) / kGemmTile * ((d.experts + kGemmTile - 1) / kGemmTile);
+  const int stages = (d.hidden + kGemmK - 1) / kGemmK;
+  for (int splits = 1; splits <= 8 && splits <= stages; splits *= 2) {
+    const double rounds = (double)((tiles * splits + 255) / 256);
+    double c = 3.0 + 0.36 * ((stages + splits - 1) / splits) * rounds;
+    if (splits > 1) c += 4.5 + splits * (double)t * d.experts * 8 / 4.5e6;
+    if (c < cost) {
+      cost = c;
+      best = {true, splits};
+    }
+  }
+  return best;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int router_estride(const RouterDesc& d) { return (d.experts + 15) / 16 * 16; }
+// Of any ldx: far rows are not cut.
+int router_splits(const RouterDesc& d, int64_t t) { return router_cut(d, t, 0).splits; }
 size_t router_parts(const RouterDesc& d, int64_t t, int splits) {
   return align256((size_t)splits * t * router_estride(d) * 4);
 }
@@ -141,7 +319,7 @@ RouterArgs router_args(const RouterDesc& d, const uint16_t* x, int64_t t, int64_
   q.ldx = ldx;
   q.logits = logits;
   q.ldl = ldl;
-  q.splits = router_splits(d, t);
+  q.splits = router_cut(d, t, ldx).splits;
   q.arrived = static_cast<uint32_t*>(ws);
   q.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kRouterCounts * 4);
   q.estride = router_estride(d);
@@ -155,10 +333,10 @@ dim3 router_grid(const RouterArgs& q) {
 
 template <int VPL>
 void launch_fused(const RouterArgs& q, hipStream_t s) {
-  const dim3 grid = router_grid(q), block(kRouterWaves * 64);
-  if (q.rule.topk <= 4) hipLaunchKernelGGL((router_rows_kernel<VPL, 4>), grid, block, 0, s, q);
-  else if (q.rule.topk <= 8) hipLaunchKernelGGL((router_rows_kernel<VPL, 8>), grid, block, 0, s, q);
-  else hipLaunchKernelGGL((router_rows_kernel<VPL, 16>), grid, block, 0, s, q);
+  const dim3 grid = router_grid(q), block(512);
+  if (q.rule.topk <= 4) hipLaunchKernelGGL((router_rows_kernel<VPL, 4, 8>), grid, block, 0, s, q);
+  else if (q.rule.topk <= 8) hipLaunchKernelGGL((router_rows_kernel<VPL, 8, 8>), grid, block, 0, s, q);
+  else hipLaunchKernelGGL((router_rows_kernel<VPL, 16, 8>), grid, block, 0, s, q);
 }
 
 }  // namespace
@@ -177,7 +355,15 @@ static size_t router_head(const RouterDesc& d, int64_t t) {
 hipError_t launch_router_linear(const RouterDesc& d, const uint16_t* x, int64_t t, int64_t ldx, float* logits,
                                 int64_t ldl, void* ws, hipStream_t s) {
   const RouterArgs q = router_args(d, x, t, ldx, logits, ldl, ws);
-  hipLaunchKernelGGL((router_rows_kernel<0, 1>), router_grid(q), dim3(kRouterWaves * 64), 0, s, q);
+  if (router_cut(d, t, ldx).tiled) {
+    const int64_t down = (t + kGemmTile - 1) / kGemmTile, across = (d.experts + kGemmTile - 1) / kGemmTile;
+    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits), block(kGemmWaves * 64);
+    hipLaunchKernelGGL(router_gemm_kernel, grid, block, 0, s, q);
+    if (q.splits > 1)
+      hipLaunchKernelGGL(router_sum_kernel, dim3((uint32_t)((t * (q.estride / 4) + 255) / 256)), dim3(256), 0, s, q);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((router_rows_kernel<0, 1, 8>), router_grid(q), dim3(512), 0, s, q);
   return hipGetLastError();
 }
 
