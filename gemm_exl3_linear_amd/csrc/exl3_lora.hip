@@ -14,7 +14,7 @@
 // into fp16 pieces hi + lo (hi holds 11 bits, lo the next 11 and, down to 2^-40 of the
 // row's largest, at least 13 bits of what is left); both meet one load of B.
 #include "exl3_internal.hpp"
-#include "exl3_mx4.hpp"
+#include "exl3_tile64.hpp"
 
 namespace exl3 {
 
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q) {
 }
 
 // Segment z as the workgroup's task; false past the last.  lds: [adapters + 1].
-template <int S>
+template <int S, int W>
 __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, LoraTask& task) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (q.count) {
@@ -179,25 +179,25 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
     __syncthreads();
     return true;
   }
-  constexpr int kEach = kLoraPlanRows / kLoraThreads;
-  __shared__ int waves[4], found[2], chunk[kEach * 4];
+  constexpr int kThreads = 64 * W, kEach = kLoraPlanRows / kThreads;
+  __shared__ int waves[W], found[2], chunk[kEach * W];
   const int buckets = q.d.adapters + 1;
   int bucket[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int row = i * kLoraThreads + tid;
+    const int row = i * kThreads + tid;
     bucket[i] = row < q.m ? lora_bucket(q, row) : -1;
   }
-  for (int b = tid; b < buckets; b += kLoraThreads) lds[b] = 0;
+  for (int b = tid; b < buckets; b += kThreads) lds[b] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
     if (bucket[i] >= 0) lora_count(lds, bucket[i]);
   __syncthreads();
-  const int per = (buckets + kLoraThreads - 1) / kLoraThreads;
+  const int per = (buckets + kThreads - 1) / kThreads;
   int mine = 0, total;
   for (int b = tid * per; b < buckets && b < (tid + 1) * per; ++b) mine += lora_segments<S>(q, b, lds[b]);
-  int at = block_sum<4>(mine, waves, total) - mine;
+  int at = block_sum<W>(mine, waves, total) - mine;
   if (z >= total) return false;
   if (z >= at && z < at + mine) {
     int b = tid * per;
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     same[i] = __ballot(bucket[i] == b);
-    if (lane == 0) chunk[i * 4 + wave] = (int)__popcll(same[i]);
+    if (lane == 0) chunk[i * W + wave] = (int)__popcll(same[i]);
   }
   __syncthreads();
   const int left = lds[b] - first, count = left < S ? left : S;
@@ -225,10 +225,10 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
   for (int i = 0; i < kEach; ++i) {
     if (bucket[i] != b) continue;
     int place = (int)__popcll(same[i] & ((1ull << lane) - 1)) - first;
-    for (int c = 0; c < i * 4 + wave; ++c) place += chunk[c];
-    if (place >= 0 && place < S) task.row[place] = i * kLoraThreads + tid;
+    for (int c = 0; c < i * W + wave; ++c) place += chunk[c];
+    if (place >= 0 && place < S) task.row[place] = i * kThreads + tid;
     if (place == 0)
-      for (int p = count; p < S; ++p) task.row[p] = i * kLoraThreads + tid;
+      for (int p = count; p < S; ++p) task.row[p] = i * kThreads + tid;
   }
   if (tid == 0) {
     task.adapter = b == q.d.adapters ? -1 : b;
@@ -247,11 +247,12 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& q, int adapter) {
 // ---------------------------------------------------------------------------
 // shrink
 // ---------------------------------------------------------------------------
-// 16 MT rows against 16 RT ranks (from 64 blockIdx.z on); a wave takes whole lines of 64
+// 16 rows against 16 RT ranks (from 64 blockIdx.z on); a wave takes whole lines of 64
 // k one after the other, lane (row or rank r, g) their places 16 g .. 16 g + 15.
-template <int MT, int RT>
+template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
-  constexpr int U = MT + RT <= 2 ? 4 : MT + RT <= 3 ? 2 : 1;  // lines whose loads go out together
+  constexpr int MT = 1;
+  constexpr int U = 4 / RT;  // lines whose loads go out together
   extern __shared__ int lds[];
   __shared__ float4_t part[4][MT * RT][64];
   __shared__ LoraTask task;
@@ -259,85 +260,114 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
   const int g = lane >> 4, r = lane & 15;
   const int split = blockIdx.y, r0 = 64 * blockIdx.z;
   const int64_t k = q.d.k;
-  for (int z = blockIdx.x; lora_task<16 * MT>(q, z, lds, task); z += gridDim.x) {
-    const int rank = task.adapter < 0 ? 0 : lora_rank(q, task.adapter);
-    if (rank > r0) {
-      const uint16_t* x[MT];
-      const uint16_t* a[RT];
+  if (!lora_task<16, 4>(q, blockIdx.x, lds, task)) return;
+  const int rank = task.adapter < 0 ? 0 : lora_rank(q, task.adapter);
+  if (rank > r0) {
+    const uint16_t* x[MT];
+    const uint16_t* a[RT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) x[i] = q.x + (int64_t)task.row[16 * i + r] * q.ldx;
+    for (int i = 0; i < MT; ++i) x[i] = q.x + (int64_t)task.row[16 * i + r] * q.ldx;
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {  // past the rank: the last rank's, whose sums are not used
-        const int of = r0 + 16 * j + r;
-        a[j] = q.d.a + ((int64_t)task.adapter * q.d.rank + (of < rank ? of : rank - 1)) * k;
-      }
-      float4_t acc[MT][RT];
+    for (int j = 0; j < RT; ++j) {  // past the rank: the last rank's, whose sums are not used
+      const int of = r0 + 16 * j + r;
+      a[j] = q.d.a + ((int64_t)task.adapter * q.d.rank + (of < rank ? of : rank - 1)) * k;
+    }
+    float4_t acc[MT][RT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-      const int lines = (int)((k + 63) / 64);
-      const int first = (int)((int64_t)lines * split / q.splits), end = (int)((int64_t)lines * (split + 1) / q.splits);
-      for (int u0 = first + wave; u0 < end; u0 += 4 * U) {
-        u32x4_t xv[U][2][MT], av[U][2][RT];
+      for (int j = 0; j < RT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+    const int lines = (int)((k + 63) / 64);
+    const int first = (int)((int64_t)lines * split / q.splits), end = (int)((int64_t)lines * (split + 1) / q.splits);
+    for (int u0 = first + wave; u0 < end; u0 += 4 * U) {
+      u32x4_t xv[U][2][MT], av[U][2][RT];
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int u = u0 + 4 * v;
+          const int64_t at = 64 * (int64_t)u + 16 * g + 8 * s;
+          const int64_t from = u < end && at < k ? at : 0;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) xv[v][s][i] = load16(x[i] + from);
+#pragma unroll
+          for (int j = 0; j < RT; ++j) av[v][s][j] = load16(a[j] + from);
+        }
+      if (64 * (int64_t)(u0 + 4 * (U - 1) + 1) > k || u0 + 4 * (U - 1) >= end) {  // what is not there is 0
 #pragma unroll
         for (int v = 0; v < U; ++v)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const int u = u0 + 4 * v;
-            const int64_t at = 64 * (int64_t)u + 16 * g + 8 * s;
-            const int64_t from = u < end && at < k ? at : 0;
+            const bool there = u < end && 64 * (int64_t)u + 16 * g + 8 * s < k;
+            const u32x4_t zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < MT; ++i) xv[v][s][i] = load16(x[i] + from);
+            for (int i = 0; i < MT; ++i) xv[v][s][i] = there ? xv[v][s][i] : zero;
 #pragma unroll
-            for (int j = 0; j < RT; ++j) av[v][s][j] = load16(a[j] + from);
+            for (int j = 0; j < RT; ++j) av[v][s][j] = there ? av[v][s][j] : zero;
           }
-        if (64 * (int64_t)(u0 + 4 * (U - 1) + 1) > k || u0 + 4 * (U - 1) >= end) {  // what is not there is 0
-#pragma unroll
-          for (int v = 0; v < U; ++v)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const int u = u0 + 4 * v;
-              const bool there = u < end && 64 * (int64_t)u + 16 * g + 8 * s < k;
-              const u32x4_t zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-              for (int i = 0; i < MT; ++i) xv[v][s][i] = there ? xv[v][s][i] : zero;
-#pragma unroll
-              for (int j = 0; j < RT; ++j) av[v][s][j] = there ? av[v][s][j] : zero;
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < U; ++v)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int j = 0; j < RT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xv[v][s][i]),
-                                                                   __builtin_bit_cast(f16x8_t, av[v][s][j]), acc[i][j],
-                                                                   0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int v = 0; v < U; ++v)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) part[wave][i * RT + j][lane] = acc[i][j];
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xv[v][s][i]),
+                                                                 __builtin_bit_cast(f16x8_t, av[v][s][j]), acc[i][j],
+                                                                 0, 0, 0);
     }
-    __syncthreads();
-    if (rank > r0) {
-      for (int t = wave; t < MT * RT; t += 4) {
-        const int col = r0 + 16 * (t % RT) + r;
-        float4_t sum = part[0][t][lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) sum += part[w][t][lane];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 16 * (t / RT) + 4 * g + j;
-          if (i < task.count && col < q.rpad) q.h[((int64_t)split * q.m + task.row[i]) * q.rpad + col] = sum[j];
-        }
+      for (int j = 0; j < RT; ++j) part[wave][i * RT + j][lane] = acc[i][j];
+  }
+  __syncthreads();
+  if (rank > r0) {
+    for (int t = wave; t < MT * RT; t += 4) {
+      const int col = r0 + 16 * (t % RT) + r;
+      float4_t sum = part[0][t][lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) sum += part[w][t][lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 16 * (t / RT) + 4 * g + j;
+        if (i < task.count && col < q.rpad) q.h[((int64_t)split * q.m + task.row[i]) * q.rpad + col] = sum[j];
       }
     }
-    __syncthreads();
+  }
+}
+
+// 64 rows against 64 ranks (from 64 blockIdx.z on), for rows that 32-bit offsets reach.
+__global__ __launch_bounds__(kTile64Waves * 64) void lora_shrink_tiled(LoraArgs q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
+  __shared__ LoraTask task;
+  const int split = blockIdx.y, r0 = 64 * blockIdx.z;
+  const uint32_t k = (uint32_t)q.d.k;
+  if (!lora_task<64, kTile64Waves>(q, blockIdx.x, reinterpret_cast<int*>(lds), task)) return;
+  const int rank = task.adapter < 0 ? 0 : lora_rank(q, task.adapter);
+  if (rank > r0) {
+    const int ranks = rank - r0 < 64 ? rank - r0 : 64;
+    const uint16_t* a = q.d.a + ((int64_t)task.adapter * q.d.rank + r0) * q.d.k;
+    const u32x4_t rsrc[2] = {buffer_words(reinterpret_cast<const uint8_t*>(q.x), ((q.m - 1) * q.ldx + k) * 2),
+                             buffer_words(reinterpret_cast<const uint8_t*>(a), (uint64_t)ranks * k * 2)};
+    uint32_t row[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t of = tile64_row(i);
+      row[0][i] = (int)of < task.count ? (uint32_t)task.row[of] * (uint32_t)q.ldx * 2 : kPastEnd;
+      row[1][i] = of * k * 2;  // past the ranks: past the buffer's end
+    }
+    const int stages = (int)((k + kTile64K - 1) / kTile64K);
+    __syncthreads();  // the segment's search is done with lds
+    const float* sums = tile64_sums(rsrc, row, k, (int)((int64_t)stages * split / q.splits),
+                                    (int)((int64_t)stages * (split + 1) / q.splits), lds);
+    const int col = threadIdx.x & 63;
+    if (col < ranks)
+      for (int i = threadIdx.x >> 6; i < task.count; i += kTile64Waves)
+        q.h[((int64_t)split * q.m + task.row[i]) * q.rpad + r0 + col] = tile64_sum(sums, i, col);
   }
 }
 
@@ -357,13 +387,16 @@ constexpr int kLoraOutStride = 68;  // floats of a row of a wave's 64 columns in
 __device__ __forceinline__ void lora_mend(const LoraArgs& q, const LoraTask& task, int row0, int64_t n0, int rank,
                                        float scale, const uint16_t* b, float* out) {
   const int64_t n = n0 + (threadIdx.x & 63);
+#pragma clang loop unroll(disable)
   for (int i = 0; i < 16 && row0 + i < task.count; ++i) {
     float* at = out + i * kLoraOutStride + (threadIdx.x & 63);
     if (n >= q.d.n || __builtin_isfinite(*at)) continue;
     const float* h = q.h + (int64_t)task.row[row0 + i] * q.rpad;
     float sum = 0.f;
+#pragma clang loop unroll(disable)
     for (int j = 0; j < rank; ++j) {
       float v = 0.f;
+#pragma clang loop unroll(disable)
       for (int s = 0; s < q.splits; ++s) v += h[(int64_t)s * q.m * q.rpad + j];
       sum = __builtin_fmaf(v, (float)__builtin_bit_cast(_Float16, b[n * q.d.rank + j]), sum);
     }
@@ -379,21 +412,17 @@ __device__ __forceinline__ f16x8_t lora_keep(f16x8_t w, int left) {
   return w;
 }
 
-template <int MT>
-struct LoraExpandLds {
-  // pieces: [hi, lo][row][32 chunks ranks], rows 16 bytes apart beyond that: the 16 rows
-  // of an operand lie in different banks
-  static __host__ __device__ int row_bytes(int chunks) { return 64 * chunks + 16; }
-  static __host__ __device__ int pieces(int chunks) { return 2 * 16 * MT * row_bytes(chunks); }
-  static __host__ __device__ int out() { return 4 * 16 * kLoraOutStride * 4; }  // 16 rows a wave
-};
+// Pieces in LDS: [hi, lo][row][32 chunks ranks], a row 16 bytes longer than that, so that
+// the 16 rows of an operand lie in different banks.
+__host__ __device__ constexpr int lora_piece_row(int chunks) { return 64 * chunks + 16; }
 
-// The task's h as pieces in LDS, and each row's exponent.
-template <int MT>
-__device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& task, int rank, int chunks, uint8_t* lds,
-                                            int* exponent) {
-  constexpr int kEach = kLoraThreads / (16 * MT);  // threads of a row
-  constexpr int kMost = 256 / 4 / kEach;
+// The task's h as pieces in LDS, and each row's factors of the sums.
+template <int S, int CHUNKS>
+__device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& task, int rank, float scale,
+                                            uint8_t* lds, float* factor) {
+  constexpr int kEach = kLoraThreads / S;  // threads of a row
+  constexpr int kMost = (8 * CHUNKS + kEach - 1) / kEach;
+  constexpr int stride = lora_piece_row(CHUNKS);
   const int row = threadIdx.x / kEach, part = threadIdx.x % kEach;
   float4_t h[kMost];
   float top = 0.f;
@@ -403,7 +432,15 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
     h[i] = float4_t{0.f, 0.f, 0.f, 0.f};
     if (row < task.count && at < rank) {
       const float* p = q.h + (int64_t)task.row[row] * q.rpad + at;
-      for (int s = 0; s < q.splits; ++s) h[i] += *reinterpret_cast<const float4_t*>(p + (int64_t)s * q.m * q.rpad);
+      for (int s = 0; s < q.splits; s += 4) {  // four shares' loads at a time
+        float4_t v[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+          v[o] = *reinterpret_cast<const float4_t*>(p + (int64_t)(s + o < q.splits ? s + o : s) * q.m * q.rpad);
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+          if (s + o < q.splits) h[i] += v[o];
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -415,12 +452,14 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
 #pragma unroll
   for (int d = 1; d < kEach; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
   const int e = top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
-  if (part == 0) exponent[row] = -e;
-  const int stride = LoraExpandLds<MT>::row_bytes(chunks);
+  if (part == 0) {  // scale 2^-e in two factors, neither of which leaves fp32 by itself
+    factor[row] = __builtin_ldexpf(1.f, -e / 2);
+    factor[S + row] = __builtin_ldexpf(scale, -e - -e / 2);
+  }
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int at = 4 * (part + i * kEach);
-    if (at >= 32 * chunks) continue;
+    if (at >= 32 * CHUNKS) continue;
     half4_t hi, lo;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -429,16 +468,17 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
       lo[j] = (_Float16)(__builtin_isfinite(v) ? v - (float)hi[j] : 0.f);
     }
     *reinterpret_cast<half4_t*>(lds + row * stride + 2 * at) = hi;
-    *reinterpret_cast<half4_t*>(lds + (16 * MT + row) * stride + 2 * at) = lo;
+    *reinterpret_cast<half4_t*>(lds + (S + row) * stride + 2 * at) = lo;
   }
 }
 
-// Bits of V bytes a lane, of base and of y.
+// How a wave's lanes take 16 rows of 64 columns of base and of y: 16 bytes a lane, or an
+// element where rows are not whole 16 bytes.
 template <class T, bool VEC>
 struct LoraIo {
-  static constexpr int kElems = VEC ? 16 / (int)sizeof(T) : 1;  // of a lane
-  static constexpr int kLanes = 64 / kElems;                    // of a row of 64 columns
-  static constexpr int kRows = 64 / kLanes;                     // of an instruction
+  static constexpr int kElems = 16 / (int)sizeof(T);  // of a lane
+  static constexpr int kLanes = 64 / kElems;          // of a row
+  static constexpr int kRows = 64 / kLanes;           // of an instruction
   typedef T vec __attribute__((ext_vector_type(kElems)));
 };
 template <class T>
@@ -450,187 +490,204 @@ struct LoraIo<T, false> {
   };
 };
 
-// 16 MT rows; a wave takes tiles of 64 columns: matrix row i of tile t is column 16 t + i,
-// a matrix column is a row of the task.  PAIR (ranks up to 16): an operand's upper half of
-// k holds another 16 columns, met by pieces that are zero in the other half.
+// Up to S rows; a wave takes tiles of 64 columns, of which B's rows stay in registers
+// while 16 of the task's rows after the other pass: matrix row i of tile t is column
+// 16 t + i, matrix columns are rows of the task.  The next 16 rows' base, and the next
+// tile's B, are under way meanwhile.
+// CH: chunks of 32 ranks; 0: up to 16 ranks, where an operand's upper half of k holds
+// another 16 columns, met by pieces that are zero in the other half.
 // VEC: base and y have rows of whole 16 bytes.
-template <int MT, bool PAIR, class T, bool VEC>
-__global__ __launch_bounds__(kLoraThreads, MT == 4 ? 2 : 4) void lora_expand(LoraArgs q) {
-  using L = LoraExpandLds<MT>;
+template <int S, int CH, class T, bool VEC>
+__global__ __launch_bounds__(kLoraThreads, CH <= 1 ? 4 : CH == 2 ? 3 : 2) void lora_expand(LoraArgs q) {
+  constexpr bool PAIR = CH == 0;
+  constexpr int kChunks = PAIR ? 1 : CH;   // of the pieces
+  constexpr int kB = PAIR ? 2 : 4 * CH;    // registers' worth of B
+  constexpr bool kAhead = CH <= 2;         // room for the next tile's
   using Io = LoraIo<T, VEC>;
+  constexpr int kIo = 16 / Io::kRows;      // instructions of 16 rows
+  constexpr int kRow = lora_piece_row(kChunks);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ LoraTask task;
-  __shared__ int exponent[16 * MT];
+  __shared__ float factor[2 * S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
-  const int64_t N = q.d.n;
-  const int64_t tile0 = (int64_t)blockIdx.y * 4 * q.tiles;
-  for (int z = blockIdx.x; lora_task<16 * MT>(q, z, reinterpret_cast<int*>(smem), task); z += gridDim.x) {
-    const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
-    const int count = __builtin_amdgcn_readfirstlane(task.count);
-    const int rank = adapter < 0 ? 0 : lora_rank(q, adapter);
-    const int chunks = (rank + 31) / 32;
-    const float scale = adapter >= 0 && q.d.scales ? q.d.scales[adapter] : 1.f;
-    lora_pieces<MT>(q, task, rank, chunks, smem, exponent);
-    __syncthreads();
-    const int stride = L::row_bytes(chunks);
-    float* out = reinterpret_cast<float*>(smem + L::pieces(chunks)) + wave * (16 * kLoraOutStride);
-    const uint16_t* b = q.d.b + (int64_t)(adapter < 0 ? 0 : adapter) * N * q.d.rank;
-    for (int it = 0; it < q.tiles; ++it) {
-      const int64_t n0 = 64 * (tile0 + wave + 4 * it);
-      if (n0 >= N) break;
-      // base ahead of the products; of rows past count another row's, of columns past n
-      // the first's
-      const int col = lane % Io::kLanes * Io::kElems, sub = lane / Io::kLanes;
-      const bool col_there = n0 + col < N;
-      constexpr int kIo = 16 / Io::kRows;  // instructions of 16 rows
-      typename Io::vec from[MT][kIo];
-      if (q.base) {
-        const T* at = static_cast<const T*>(q.base) + (col_there ? n0 + col : 0);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int o = 0; o < kIo; ++o)
-            from[i][o] = *reinterpret_cast<const typename Io::vec*>(at + task.row[16 * i + Io::kRows * o + sub] * q.ldb);
-      }
-      float4_t acc[MT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[i][t] = float4_t{0.f, 0.f, 0.f, 0.f};
-      if constexpr (PAIR) {
-        if (rank > 0) {
-          f16x8_t w[2];
-          const int at = 8 * (g & 1);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int64_t n = n0 + 32 * p + 16 * (g >> 1) + r;
-            w[p] = __builtin_bit_cast(f16x8_t, load16(b + (n < N ? n : N - 1) * q.d.rank + (at < rank ? at : 0)));
-          }
-          if (rank < 16)
-            for (int p = 0; p < 2; ++p) w[p] = lora_keep(w[p], rank - at);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const f16x8_t h = *reinterpret_cast<const f16x8_t*>(smem + (p * 16 * MT + 16 * i + r) * stride + 2 * at);
-#pragma unroll
-              for (int o = 0; o < 2; ++o) {
-                const f16x8_t part = lora_keep(h, (g >> 1) == o ? 8 : 0);
-#pragma unroll
-                for (int v = 0; v < 2; ++v)
-                  acc[i][2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[v], part, acc[i][2 * v + o], 0, 0, 0);
-              }
-            }
+  const int col = lane % Io::kLanes * Io::kElems, sub = lane / Io::kLanes;
+  const int N = (int)q.d.n, R = q.d.rank;
+  const int first_tile = blockIdx.y * 4 * q.tiles + wave;
+  const T* base = static_cast<const T*>(q.base);
+  T* y = static_cast<T*>(q.y);
+  if (!lora_task<S, 4>(q, blockIdx.x, reinterpret_cast<int*>(smem), task)) return;
+  const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
+  const int count = __builtin_amdgcn_readfirstlane(task.count);
+  const int tiles = (N + 63) / 64;
+  const int end_tile = first_tile + 4 * q.tiles < tiles ? first_tile + 4 * q.tiles : tiles;
+  if (adapter < 0) {  // only where y is not base
+    for (int tile = first_tile; tile < end_tile; tile += 4)
+#pragma clang loop unroll(disable)
+      for (int row = sub; row < count; row += Io::kRows)
+        if (64 * tile + col < N) {
+          const int64_t i = task.row[row];
+          typename Io::vec v{};
+          if (q.base) v = *reinterpret_cast<const typename Io::vec*>(base + i * q.ldb + 64 * tile + col);
+          *reinterpret_cast<typename Io::vec*>(y + i * q.ldy + 64 * tile + col) = v;
         }
-      } else {
-        const uint16_t* of[4];
+    return;
+  }
+  const int rank = lora_rank(q, adapter);
+  const float scale = q.d.scales ? q.d.scales[adapter] : 1.f;
+  const uint16_t* b = q.d.b + (int64_t)adapter * N * R;
+  // Of columns past n and ranks past the adapter's, others': neither has a say.  So it is
+  // with tiles past the last, so that every load is made and none waited for early.
+  const auto load_b = [&](int tile, f16x8_t* w) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int64_t n = n0 + 16 * t + r;
-          of[t] = b + (n < N ? n : N - 1) * q.d.rank;
-        }
-        for (int c = 0; c < chunks; ++c) {
-          const int at = 32 * c + 8 * g;
-          f16x8_t w[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) w[t] = __builtin_bit_cast(f16x8_t, load16(of[t] + (at < rank ? at : 0)));
-          if (32 * c + 32 > rank) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) w[t] = lora_keep(w[t], rank - at);
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const f16x8_t h = *reinterpret_cast<const f16x8_t*>(smem + (p * 16 * MT + 16 * i + r) * stride + 2 * at);
-#pragma unroll
-              for (int t = 0; t < 4; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h, acc[i][t], 0, 0, 0);
-            }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (16 * i >= count) break;
-        const int e = exponent[16 * i + r];
-        bool odd = false;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float4_t v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            odd = odd || !__builtin_isfinite(acc[i][t][j]);
-            v[j] = scale * __builtin_ldexpf(acc[i][t][j], e);
-          }
-          *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = v;
-        }
-        wave_lds_sync();
-        if (__builtin_expect(__any(odd), 0)) lora_mend(q, task, 16 * i, n0, rank, scale, b, out);
-#pragma unroll
-        for (int o = 0; o < kIo; ++o) {
-          const int row = 16 * i + Io::kRows * o + sub;
-          const float* p = out + (Io::kRows * o + sub) * kLoraOutStride + col;
-          typename Io::vec to;
-#pragma unroll
-          for (int j = 0; j < Io::kElems; ++j)
-            to[j] = !q.base ? (T)(adapter < 0 ? 0.f : p[j])
-                            : adapter < 0 ? from[i][o][j] : (T)((float)from[i][o][j] + p[j]);
-          if (row < count && col_there)
-            *reinterpret_cast<typename Io::vec*>(static_cast<T*>(q.y) + task.row[row] * q.ldy + n0 + col) = to;
-        }
-        wave_lds_sync();
-      }
+    for (int i = 0; i < kB; ++i) {
+      const int n = 64 * tile + (PAIR ? 32 * i + 16 * (g >> 1) + r : 16 * (i & 3) + r);
+      const int at = PAIR ? 8 * (g & 1) : 32 * (i >> 2) + 8 * g;
+      w[i] = __builtin_bit_cast(f16x8_t, load16(b + (int64_t)(n < N ? n : N - 1) * R + (at < rank ? at : 0)));
     }
-    __syncthreads();
+  };
+  const T* from_where = q.base ? base : y;  // without a base what is loaded is dropped
+  const int64_t from_ld = q.base ? q.ldb : q.ldy;
+  const auto load_base = [&](int tile, int i0, typename Io::vec (&v)[kIo]) {
+    const T* at = from_where + (64 * tile + col < N ? 64 * tile + col : 0);
+#pragma unroll
+    for (int o = 0; o < kIo; ++o)
+      v[o] = *reinterpret_cast<const typename Io::vec*>(at + task.row[i0 + Io::kRows * o + sub] * from_ld);
+  };
+  f16x8_t w[kB];
+  typename Io::vec from[kIo];
+  load_b(first_tile, w);
+  load_base(first_tile, 0, from);
+  __syncthreads();  // the segment's search is done with smem
+  lora_pieces<S, kChunks>(q, task, rank, scale, smem, factor);
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem + 2 * S * kRow) + wave * (16 * kLoraOutStride);
+  for (int tile = first_tile; tile < end_tile; tile += 4) {
+    f16x8_t w_next[kB];
+    if constexpr (kAhead) load_b(tile + 4, w_next);
+    if (rank < (PAIR ? 16 : 32 * CH)) {
+#pragma unroll
+      for (int i = 0; i < kB; ++i) w[i] = lora_keep(w[i], rank - (PAIR ? 8 * (g & 1) : 32 * (i >> 2) + 8 * g));
+    }
+#pragma clang loop unroll(disable)
+    for (int i0 = 0; i0 < count; i0 += 16) {
+      typename Io::vec from_next[kIo];
+      const bool last_rows = i0 + 16 >= count;
+      load_base(last_rows ? tile + 4 : tile, last_rows ? 0 : i0 + 16, from_next);
+      float4_t acc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const f16x8_t h =
+              *reinterpret_cast<const f16x8_t*>(smem + (p * S + i0 + r) * kRow + 64 * c + 16 * (PAIR ? g & 1 : g));
+          if constexpr (PAIR) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const f16x8_t part = lora_keep(h, (g >> 1) == o ? 8 : 0);
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                acc[2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[v], part, acc[2 * v + o], 0, 0, 0);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[4 * c + t], h, acc[t], 0, 0, 0);
+          }
+        }
+      const float f0 = factor[i0 + r], f1 = factor[S + i0 + r];
+      float odd = 0.f;  // NaN if a sum is not finite
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
+        *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+      }
+      wave_lds_sync();
+      if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, i0, 64 * tile, rank, scale, b, out);
+#pragma unroll
+      for (int o = 0; o < kIo; ++o) {
+        const int row = i0 + Io::kRows * o + sub;
+        const float* p = out + (Io::kRows * o + sub) * kLoraOutStride + col;
+        typename Io::vec to;
+#pragma unroll
+        for (int j = 0; j < Io::kElems; ++j) to[j] = (T)((q.base ? (float)from[o][j] : 0.f) + p[j]);
+        if (row < count && 64 * tile + col < N)
+          *reinterpret_cast<typename Io::vec*>(y + task.row[row] * q.ldy + 64 * tile + col) = to;
+      }
+      wave_lds_sync();
+#pragma unroll
+      for (int o = 0; o < kIo; ++o) from[o] = from_next[o];
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kB; ++i) w[i] = w_next[i];
+    } else {
+      load_b(tile + 4, w);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-// A workgroup takes a row (blockIdx.y) and 4096 / RJ columns: it makes the row's whole h
+// A workgroup takes a row (blockIdx.y) and 8192 / RJ columns: it makes the row's whole h
 // itself (A from L2, which costs less than a launch) and then its columns, RJ / 8 threads
-// a column.  RJ: a power of two >= rank.
-constexpr int kLoraFewThreads = 512;
+// a column.  RJ: a power of two >= rank.  A wave takes 8 ranks of every 512 k from its
+// place on.
+constexpr int kLoraFewThreads = 1024;
 
 template <int RJ, class T>
 __global__ __launch_bounds__(kLoraFewThreads) void lora_few(LoraArgs q) {
-  constexpr int NW = kLoraFewThreads / 64, kEach = RJ / 8, kCols = kLoraFewThreads / kEach;
-  __shared__ float part[NW][RJ];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  constexpr int NW = kLoraFewThreads / 64, G = RJ / 8, kCols = kLoraFewThreads / G;
+  __shared__ float part[NW][8];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t row = blockIdx.y, k = q.d.k;
-  const int bucket = lora_bucket(q, row);
+  const int bucket = __builtin_amdgcn_readfirstlane(lora_bucket(q, row));
   const bool none = bucket == q.d.adapters;
   if (none && !q.copy) return;
-  const int64_t n = (int64_t)blockIdx.x * kCols + threadIdx.x / kEach;
-  const int j0 = 8 * (threadIdx.x % kEach);
+  const int64_t n = (int64_t)blockIdx.x * kCols + threadIdx.x / G;
+  const int j0 = 8 * (threadIdx.x % G);
+  const bool writes = j0 == 0 && n < q.d.n;
+  T from = (T)0;
+  if (writes && q.base) from = static_cast<const T*>(q.base)[row * q.ldb + n];
   const int rank = none ? 0 : lora_rank(q, bucket);
+  const float scale = none ? 0.f : q.d.scales ? q.d.scales[bucket] : 1.f;
   f16x8_t w = {0, 0, 0, 0, 0, 0, 0, 0};
   if (n < q.d.n && j0 < rank)
     w = __builtin_bit_cast(f16x8_t, load16(q.d.b + ((int64_t)bucket * q.d.n + n) * q.d.rank + j0));
-  float acc[RJ];
+  float acc[8];
 #pragma unroll
-  for (int j = 0; j < RJ; ++j) acc[j] = 0.f;
-  if (rank > 0) {
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  const int a0 = 8 * (wave % G);  // this wave's ranks
+  if (a0 < rank) {
     const uint16_t* x = q.x + row * q.ldx;
-    const uint16_t* a = q.d.a + (int64_t)bucket * q.d.rank * k;
-    for (int64_t at = 512 * wave + 8 * lane; at < k; at += 512 * NW) {
+    const uint16_t* a = q.d.a + ((int64_t)bucket * q.d.rank + a0) * k;
+    for (int64_t at = 512 * (wave / G) + 8 * lane; at < k; at += 512 * (NW / G)) {
       const f16x8_t xv = __builtin_bit_cast(f16x8_t, load16(x + at));
+      f16x8_t av[8];
 #pragma unroll
-      for (int j = 0; j < RJ; ++j) {
-        const f16x8_t av = __builtin_bit_cast(f16x8_t, load16(a + (j < rank ? j : 0) * k + at));
+      for (int j = 0; j < 8; ++j) av[j] = __builtin_bit_cast(f16x8_t, load16(a + (a0 + j < rank ? j : 0) * k + at));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j] = __builtin_fmaf((float)av[i], (float)xv[i], acc[j]);
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j] = __builtin_fmaf((float)av[j][i], (float)xv[i], acc[j]);
+    }
+    // over the lanes: halves exchange what the other half sums up, so that eight sums take
+    // 4 + 2 + 1 + 3 exchanges; lane 8 j ends with sum j
+#pragma unroll
+    for (int d = 4; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = 0; j < d; ++j) {
+        const bool upper = lane & (8 * d);
+        const float mine = upper ? acc[j + d] : acc[j], other = upper ? acc[j] : acc[j + d];
+        acc[j] = mine + __shfl_xor(other, 8 * d);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-      float v = acc[j];
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-      if (lane == 0) part[wave][j] = v;
-    }
+    for (int d = 4; d >= 1; d /= 2) acc[0] += __shfl_xor(acc[0], d);
   }
+  if ((lane & 7) == 0) part[wave][lane >> 3] = acc[0];
   __syncthreads();
   float sum = 0.f;
 #pragma unroll
@@ -638,25 +695,19 @@ __global__ __launch_bounds__(kLoraFewThreads) void lora_few(LoraArgs q) {
     if (j0 + i < rank) {
       float h = 0.f;
 #pragma unroll
-      for (int o = 0; o < NW; ++o) h += part[o][j0 + i];
+      for (int o = 0; o < NW / G; ++o) h += part[o * G + threadIdx.x % G][i];
       sum = __builtin_fmaf(h, (float)w[i], sum);
     }
   }
 #pragma unroll
-  for (int d = 1; d < kEach; d *= 2) sum += __shfl_xor(sum, d);
-  if (j0 || n >= q.d.n) return;
-  const float delta = none ? 0.f : (q.d.scales ? q.d.scales[bucket] : 1.f) * sum;
+  for (int d = 1; d < G; d *= 2) sum += __shfl_xor(sum, d);
+  if (!writes) return;
   T* to = static_cast<T*>(q.y) + row * q.ldy + n;
-  if (!q.base) *to = (T)delta;
-  else {
-    const T from = static_cast<const T*>(q.base)[row * q.ldb + n];
-    *to = none ? from : (T)((float)from + delta);
-  }
+  *to = !q.base ? (T)(none ? 0.f : scale * sum) : none ? from : (T)((float)from + scale * sum);
 }
 
 namespace {
 
-constexpr int kLoraGrid = 8192;  // segments' workgroups at most: each takes every gridDim.x-th
 constexpr int kLoraFewRows = 4, kLoraFewRank = 64;
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -665,35 +716,38 @@ bool lora_is_few(const LoraDesc& d, int64_t m) {
   return m <= kLoraFewRows && d.rank <= kLoraFewRank && d.rank * d.k <= (int64_t)1 << 17;
 }
 
-// 64 rows a segment where adapters have more than 16 each on average.
-bool lora_long(const LoraDesc& d, int64_t m) { return m > 16 * (int64_t)(d.adapters > 1 ? d.adapters : 1); }
+// 64 rows a segment where adapters have more than 16 each on average, enough of them for
+// the chip and 32-bit offsets for the copies to LDS.
+bool lora_long(const LoraDesc& d, int64_t m, int64_t ldx) {
+  return m >= 512 && m > 16 * (int64_t)d.adapters && m * ldx < (int64_t)1 << 31;
+}
 
-int64_t lora_most_segs(const LoraDesc& d, int64_t m) {
-  const int s = lora_long(d, m) ? 64 : 16;
+int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
+  const int s = longer ? 64 : 16;
   const int64_t most = m / s + d.adapters + 1;  // a bucket's last may be short, that of none too
   return most < m ? most : m;
 }
 
-int lora_splits(const LoraDesc& d, int64_t m) {
-  const int64_t lines = (d.k + 63) / 64;
-  const int64_t groups = lora_most_segs(d, m) * ((d.rank + 63) / 64);
-  const int64_t want = 512 / groups, most = lines / 8;  // two lines a wave
-  const int64_t s = want < most ? want : most;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+int lora_splits(const LoraDesc& d, int64_t m, bool longer) {
+  const int64_t groups = lora_most_segs(d, m, longer) * ((d.rank + 63) / 64);
+  // a workgroup of 64 rows fills a CU, and every share is read again by all that expand
+  const int64_t want = (longer ? 256 : 512) / groups, most = longer ? (d.k + 511) / 512 : (d.k + 511) / 512;
+  const int64_t s = want < most ? want : most, cap = longer ? 4 : 16;
+  return (int)(s < 1 ? 1 : s > cap ? cap : s);
 }
 
 struct LoraLayout {
   size_t segs, order, h, total;
 };
-LoraLayout lora_layout(const LoraDesc& d, int64_t m) {
+LoraLayout lora_layout(const LoraDesc& d, int64_t m, bool longer) {
   LoraLayout L;
   size_t off = 256;
   L.segs = off;
-  if (m > kLoraPlanRows) off += align256((size_t)lora_most_segs(d, m) * sizeof(LoraSeg));
+  if (m > kLoraPlanRows) off += align256((size_t)lora_most_segs(d, m, longer) * sizeof(LoraSeg));
   L.order = off;
   if (m > kLoraPlanRows) off += align256((size_t)m * 4);
   L.h = off;
-  off += align256((size_t)lora_splits(d, m) * m * ((d.rank + 15) / 16 * 16) * 4);
+  off += align256((size_t)lora_splits(d, m, longer) * m * ((d.rank + 15) / 16 * 16) * 4);
   L.total = off;
   return L;
 }
@@ -709,41 +763,51 @@ void launch_few(const LoraArgs& q, hipStream_t s) {
   else hipLaunchKernelGGL((lora_few<64, T>), grid, block, 0, s, q);
 }
 
-template <int MT, class T, bool VEC>
-void launch_expand(const LoraArgs& q, dim3 grid, size_t lds, hipStream_t s) {
-  if (q.d.rank <= 16) hipLaunchKernelGGL((lora_expand<MT, true, T, VEC>), grid, dim3(kLoraThreads), lds, s, q);
-  else hipLaunchKernelGGL((lora_expand<MT, false, T, VEC>), grid, dim3(kLoraThreads), lds, s, q);
+template <int S, int CH>
+void launch_expand(const LoraArgs& q, bool f32, bool vec, dim3 grid, size_t plan, hipStream_t s) {
+  const size_t need = 2 * S * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
+  const size_t lds = need > plan ? need : plan;
+  const dim3 block(kLoraThreads);
+  if (f32 && vec) hipLaunchKernelGGL((lora_expand<S, CH, float, true>), grid, block, lds, s, q);
+  else if (f32) hipLaunchKernelGGL((lora_expand<S, CH, float, false>), grid, block, lds, s, q);
+  else if (vec) hipLaunchKernelGGL((lora_expand<S, CH, _Float16, true>), grid, block, lds, s, q);
+  else hipLaunchKernelGGL((lora_expand<S, CH, _Float16, false>), grid, block, lds, s, q);
 }
 
-template <int MT>
-void launch_mt(LoraArgs q, bool f32, hipStream_t s) {
-  const int64_t segs = lora_most_segs(q.d, q.m);
-  const uint32_t gx = (uint32_t)(segs < kLoraGrid ? segs : kLoraGrid);
+template <int S>
+void launch_segments(LoraArgs q, bool f32, hipStream_t s) {
+  const int64_t segs = lora_most_segs(q.d, q.m, S == 64);
+  const uint32_t gx = (uint32_t)segs;
   const size_t plan = (size_t)(q.d.adapters + 1) * 4;
   const dim3 shrink(gx, (uint32_t)q.splits, (uint32_t)((q.d.rank + 63) / 64)), block(kLoraThreads);
-  if (q.d.rank <= 16) hipLaunchKernelGGL((lora_shrink<MT, 1>), shrink, block, plan, s, q);
-  else if (q.d.rank <= 32) hipLaunchKernelGGL((lora_shrink<MT, 2>), shrink, block, plan, s, q);
-  else hipLaunchKernelGGL((lora_shrink<MT, 4>), shrink, block, plan, s, q);
+  if (S == 64) hipLaunchKernelGGL(lora_shrink_tiled, shrink, dim3(kTile64Waves * 64), 0, s, q);
+  else if (q.d.rank <= 16) hipLaunchKernelGGL((lora_shrink<1>), shrink, block, plan, s, q);
+  else if (q.d.rank <= 32) hipLaunchKernelGGL((lora_shrink<2>), shrink, block, plan, s, q);
+  else hipLaunchKernelGGL((lora_shrink<4>), shrink, block, plan, s, q);
   const int64_t tiles = (q.d.n + 63) / 64;
   // more tiles a workgroup where there are workgroups enough
   int each = 4;
   while (each > 1 && (int64_t)gx * ((tiles + 4 * each - 1) / (4 * each)) < 1024) each /= 2;
   q.tiles = each;
   const dim3 grid(gx, (uint32_t)((tiles + 4 * each - 1) / (4 * each)));
-  const size_t need = LoraExpandLds<MT>::pieces((q.d.rank + 31) / 32) + LoraExpandLds<MT>::out();
-  const size_t lds = need > plan ? need : plan;
   const uintptr_t at = reinterpret_cast<uintptr_t>(q.base) | reinterpret_cast<uintptr_t>(q.y);
   const int64_t elems = f32 ? 4 : 8;
   const bool vec = at % 16 == 0 && q.d.n % elems == 0 && q.ldy % elems == 0 && (!q.base || q.ldb % elems == 0);
-  if (f32 && vec) launch_expand<MT, float, true>(q, grid, lds, s);
-  else if (f32) launch_expand<MT, float, false>(q, grid, lds, s);
-  else if (vec) launch_expand<MT, _Float16, true>(q, grid, lds, s);
-  else launch_expand<MT, _Float16, false>(q, grid, lds, s);
+  if (q.d.rank <= 16) launch_expand<S, 0>(q, f32, vec, grid, plan, s);
+  else if (q.d.rank <= 32) launch_expand<S, 1>(q, f32, vec, grid, plan, s);
+  else if (q.d.rank <= 64) launch_expand<S, 2>(q, f32, vec, grid, plan, s);
+  else if (q.d.rank <= 128) launch_expand<S, 4>(q, f32, vec, grid, plan, s);
+  else launch_expand<S, 8>(q, f32, vec, grid, plan, s);
 }
 
 }  // namespace
 
-size_t lora_workspace(const LoraDesc& d, int64_t m) { return lora_is_few(d, m) ? 0 : lora_layout(d, m).total; }
+// Of any ldx.
+size_t lora_workspace(const LoraDesc& d, int64_t m) {
+  if (lora_is_few(d, m)) return 0;
+  const size_t a = lora_layout(d, m, false).total, b = lora_layout(d, m, lora_long(d, m, d.k)).total;
+  return a > b ? a : b;
+}
 
 hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t ldx, const int32_t* rows,
                        const void* base, int64_t ldb, void* y, int64_t ldy, bool f32, void* ws, hipStream_t s) {
@@ -763,12 +827,12 @@ hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t 
     else launch_few<_Float16>(q, s);
     return hipGetLastError();
   }
-  const LoraLayout L = lora_layout(d, m);
+  const bool longer = lora_long(d, m, ldx);
+  const LoraLayout L = lora_layout(d, m, longer);
   unsigned char* w = static_cast<unsigned char*>(ws);
-  q.splits = lora_splits(d, m);
+  q.splits = lora_splits(d, m, longer);
   q.rpad = (d.rank + 15) / 16 * 16;
   q.h = reinterpret_cast<float*>(w + L.h);
-  const bool longer = lora_long(d, m);
   if (m > kLoraPlanRows) {
     q.count = reinterpret_cast<int*>(w);
     q.segs = reinterpret_cast<LoraSeg*>(w + L.segs);
@@ -777,8 +841,8 @@ hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t 
     if (longer) hipLaunchKernelGGL((lora_plan<64>), dim3(1), dim3(kLoraPlanThreads), lds, s, q);
     else hipLaunchKernelGGL((lora_plan<16>), dim3(1), dim3(kLoraPlanThreads), lds, s, q);
   }
-  if (longer) launch_mt<4>(q, f32, s);
-  else launch_mt<1>(q, f32, s);
+  if (longer) launch_segments<64>(q, f32, s);
+  else launch_segments<16>(q, f32, s);
   return hipGetLastError();
 }
 

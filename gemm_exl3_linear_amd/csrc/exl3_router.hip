@@ -1,7 +1,7 @@
 // exl3_router_linear and exl3_router: a router's logits l = x W^T (+ c), fp16 matrix
 // instructions with fp32 sums, and for few tokens their routing in the same launch.
-#include "exl3_mx4_lds.hpp"
 #include "exl3_route.hpp"
+#include "exl3_tile64.hpp"
 
 namespace exl3 {
 
@@ -116,131 +116,40 @@ __global__ __launch_bounds__(NW * 64) void router_rows_kernel(RouterArgs q) {
 // ---------------------------------------------------------------------------
 // many tokens
 // ---------------------------------------------------------------------------
-// 64 tokens x 64 experts by eight waves over a share of k (blockIdx.y), in stages of 128
-// that go from memory straight to LDS, three of them in flight.  A wave takes 16 of a
-// stage's 128 k for the whole tile, so that LDS is read once (a quarter of the tile each
-// would read it twice), and reads the next stage while it multiplies this one; the waves'
-// sums meet in LDS at the end.
-//
-// LDS: a stage holds rows of 256 bytes, 64 of x and then 64 of W; 16-byte piece c of row
-// r lies at place c ^ (r % 16), so that sixteen rows' pieces c cover all 64 banks.
-constexpr int kGemmTile = 64;
-constexpr int kGemmWaves = 8;
-constexpr int kGemmK = 16 * kGemmWaves;                // of a stage
-constexpr int kGemmRing = 4;                           // stages of LDS
-constexpr int kGemmStage = 2 * kGemmTile * kGemmK * 2;  // bytes
-constexpr int kGemmCopies = kGemmStage / 1024 / kGemmWaves;  // a wave's 1 KB copies of a stage, half of x
-typedef float float16_t __attribute__((ext_vector_type(16)));
-
-// A wave's operands of a stage: 64 rows of 16 k of x and of W.
-struct RouterOperands {
-  f16x8_t x[2], w[2];
-};
-
-__global__ __launch_bounds__(kGemmWaves * 64) void router_gemm_kernel(RouterArgs q) {
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[kGemmRing * kGemmStage];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+// 64 tokens x 64 experts over a share of k (blockIdx.y): exl3_tile64.hpp.
+__global__ __launch_bounds__(kTile64Waves * 64) void router_gemm_kernel(RouterArgs q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
   // a row tile's workgroups run on one XCD (workgroup i on XCD i % 8), one behind the
   // other, so that x comes from memory once
-  const int across = (q.d.experts + kGemmTile - 1) / kGemmTile;
+  const int across = (q.d.experts + kTile64 - 1) / kTile64;
   const int64_t j = blockIdx.x >> 3;
-  const int64_t row0 = ((j / across) * 8 + (blockIdx.x & 7)) * kGemmTile;
-  const int e0 = (int)(j % across) * kGemmTile;
+  const int64_t row0 = ((j / across) * 8 + (blockIdx.x & 7)) * kTile64;
+  const int e0 = (int)(j % across) * kTile64;
   if (row0 >= q.t) return;
-  const int64_t ldx = q.ldx;
-  const int rows = (int)(q.t - row0 < kGemmTile ? q.t - row0 : kGemmTile);
-  const int cols = q.d.experts - e0 < kGemmTile ? q.d.experts - e0 : kGemmTile;
+  const int rows = (int)(q.t - row0 < kTile64 ? q.t - row0 : kTile64);
+  const int cols = q.d.experts - e0 < kTile64 ? q.d.experts - e0 : kTile64;
   const uint32_t hidden = (uint32_t)q.d.hidden;
-  const u32x4_t xs = buffer_words(reinterpret_cast<const uint8_t*>(q.x + row0 * ldx),
-                                  ((uint64_t)(rows - 1) * ldx + hidden) * 2);
-  const u32x4_t ws = buffer_words(reinterpret_cast<const uint8_t*>(q.d.weight + (int64_t)e0 * hidden),
-                                  (uint64_t)cols * hidden * 2);
-  const uint32_t base = (uint32_t)(uintptr_t)(lds_u8*)ring;
-  // copies 2 wave, 2 wave + 1 of x and of W: four rows each, a piece a lane
-  uint32_t off[kGemmCopies], piece[kGemmCopies];
+  const u32x4_t rsrc[2] = {buffer_words(reinterpret_cast<const uint8_t*>(q.x + row0 * q.ldx),
+                                        ((uint64_t)(rows - 1) * q.ldx + hidden) * 2),
+                           buffer_words(reinterpret_cast<const uint8_t*>(q.d.weight + (int64_t)e0 * hidden),
+                                        (uint64_t)cols * hidden * 2)};
+  uint32_t row[2][2];  // past the last: past the buffer's end
 #pragma unroll
-  for (int i = 0; i < kGemmCopies; ++i) {
-    const uint32_t row = 4 * (2 * wave + (i & 1)) + (lane >> 4);
-    piece[i] = 8 * ((lane & 15) ^ (row & 15));
-    off[i] = (row * (i < 2 ? (uint32_t)ldx : hidden) + piece[i]) * 2;
+  for (int i = 0; i < 2; ++i) {
+    row[0][i] = tile64_row(i) * (uint32_t)q.ldx * 2;
+    row[1][i] = tile64_row(i) * hidden * 2;
   }
-  const int stages = (int)((hidden + kGemmK - 1) / kGemmK);
-  const int first = (int)((int64_t)stages * blockIdx.y / q.splits);
-  const int end = (int)((int64_t)stages * (blockIdx.y + 1) / q.splits);
-  const auto fetch = [&](int st) {
-    const uint32_t at = base + (uint32_t)(st % kGemmRing) * kGemmStage;
-#pragma unroll
-    for (int i = 0; i < kGemmCopies; ++i) {
-      const bool there = (uint32_t)st * kGemmK + piece[i] < hidden;  // past the end: zeros
-      lds_copy16(i < 2 ? xs : ws, at + (uint32_t)((i < 2 ? 0 : 2 * kGemmWaves) + 2 * wave + (i & 1)) * 1024,
-                 there ? off[i] : kPastEnd, (uint32_t)st * kGemmK * 2);
-    }
-  };
-  const uint32_t r = lane & 31, c = 2 * wave + (lane >> 5);
-  const uint32_t in_tile = r * 256 + 16 * (c ^ (r & 15));
-  const auto read = [&](int st, RouterOperands& o) {
-    const uint32_t at = base + (uint32_t)(st % kGemmRing) * kGemmStage + in_tile;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      o.x[a] = __builtin_bit_cast(f16x8_t, lds_read16(at + a * 8192));
-      o.w[a] = __builtin_bit_cast(f16x8_t, lds_read16(at + kGemmStage / 2 + a * 8192));
-    }
-  };
-  float16_t acc[2][2];
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
-  const auto multiply = [&](const RouterOperands& o) {
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.x[a], o.w[b], acc[a][b], 0, 0, 0);
-  };
-  // Waits until at most the two stages after the next are open here: the next has landed
-  // here, and behind the barrier everywhere, and this one's place is read and free.
-  static_assert(kGemmRing == 4 && kGemmCopies == 4, "8 copies of two stages");
-  const auto step = [&](int st, const RouterOperands& now, RouterOperands& next) {
-    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    fetch(st + kGemmRing);
-    read(st + 1, next);
-    multiply(now);
-  };
-  for (int st = first; st < first + kGemmRing; ++st) fetch(st);
-  asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
-  RouterOperands even, odd;
-  read(first, even);
-  int st = first;  // what is read past the end is never multiplied
-  for (; st + 1 < end; st += 2) {
-    step(st, even, odd);
-    step(st + 1, odd, even);
-  }
-  if (st < end) multiply(even);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  float* sums = reinterpret_cast<float*>(ring);  // [wave][row][expert]
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        sums[(wave * 64 + 32 * a + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)) * 64 + 32 * b + r] = acc[a][b][i];
-  __syncthreads();
+  const int stages = (int)((hidden + kTile64K - 1) / kTile64K);
+  const float* sums = tile64_sums(rsrc, row, hidden, (int)((int64_t)stages * blockIdx.y / q.splits),
+                                  (int)((int64_t)stages * (blockIdx.y + 1) / q.splits), lds);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (lane >= cols) return;
   const bool whole = q.splits == 1;
   const float bias = whole && q.d.bias ? q.d.bias[e0 + lane] : 0.f;
   float* out = whole ? q.logits + row0 * q.ldl : q.part + ((int64_t)blockIdx.y * q.t + row0) * q.estride;
   const int64_t ld = whole ? q.ldl : q.estride;
 #pragma unroll 4
-  for (int row = wave; row < rows; row += kGemmWaves) {
-    float v = sums[row * 64 + lane];
-#pragma unroll
-    for (int o = 1; o < kGemmWaves; ++o) v += sums[(o * 64 + row) * 64 + lane];
-    out[row * ld + e0 + lane] = v + bias;
-  }
+  for (int i = wave; i < rows; i += kTile64Waves) out[i * ld + e0 + lane] = tile64_sum(sums, i, lane) + bias;
 }
 
 // The logits of shares of k: a thread takes four experts of a token.
@@ -288,8 +197,8 @@ RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx) {
   double cost = 2.5 + (lone > all ? lone : all);
   if (ldx >= (1 << 24)) return best;  // offsets into 64 rows have 32 bits
   // tiled: 0.36 a stage and round of a workgroup a CU; sums of shares 4.5 and their bytes
-  const int64_t tiles = (t + kGemmTile - 1) / kGemmTile * ((d.experts + kGemmTile - 1) / kGemmTile);
-  const int stages = (d.hidden + kGemmK - 1) / kGemmK;
+  const int64_t tiles = (t + kTile64 - 1) / kTile64 * ((d.experts + kTile64 - 1) / kTile64);
+  const int stages = (d.hidden + kTile64K - 1) / kTile64K;
   for (int splits = 1; splits <= 8 && splits <= stages; splits *= 2) {
     const double rounds = (double)((tiles * splits + 255) / 256);
     double c = 3.0 + 0.36 * ((stages + splits - 1) / splits) * rounds;
@@ -356,8 +265,8 @@ hipError_t launch_router_linear(const RouterDesc& d, const uint16_t* x, int64_t 
                                 int64_t ldl, void* ws, hipStream_t s) {
   const RouterArgs q = router_args(d, x, t, ldx, logits, ldl, ws);
   if (router_cut(d, t, ldx).tiled) {
-    const int64_t down = (t + kGemmTile - 1) / kGemmTile, across = (d.experts + kGemmTile - 1) / kGemmTile;
-    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits), block(kGemmWaves * 64);
+    const int64_t down = (t + kTile64 - 1) / kTile64, across = (d.experts + kTile64 - 1) / kTile64;
+    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits), block(kTile64Waves * 64);
     hipLaunchKernelGGL(router_gemm_kernel, grid, block, 0, s, q);
     if (q.splits > 1)
       hipLaunchKernelGGL(router_sum_kernel, dim3((uint32_t)((t * (q.estride / 4) + 255) / 256)), dim3(256), 0, s, q);
