@@ -25,9 +25,7 @@ constexpr int kLoraMaxSeg = 64;
 
 struct LoraSeg {
   int adapter;  // -1: none, y is base
-  int first;    // of its rows in the order of adapters
-  int count;
-  int pad;
+  int count;    // of its rows; 0: no such segment
 };
 
 struct LoraArgs {
@@ -44,9 +42,9 @@ struct LoraArgs {
   int rpad;    // floats of a row of h
   int tiles;   // 64-column tiles of a workgroup of lora_expand
   // workspace
-  int* count;     // segments; null where workgroups find their own
-  LoraSeg* segs;
-  int* order;     // [m] rows in the order of adapters
+  LoraSeg* segs;  // [segments at most]; null where workgroups find their own
+  int* order;     // [segments at most][rows of a segment]
+  int* place;     // [m] a row's place among its adapter's, where registers do not hold it
   float* h;       // [splits][m][rpad]
 };
 
@@ -62,16 +60,15 @@ __device__ __forceinline__ int lora_bucket(const LoraArgs& q, int64_t i) {
   return (unsigned)a < (unsigned)q.d.adapters ? a : q.d.adapters;
 }
 
-// Counts a row in its bucket; the rows of a wave are mostly of one request, and 64
-// additions to one place would take their turns.
-__device__ __forceinline__ void lora_count(int* rows, int bucket) {
-  const int first = __builtin_amdgcn_readfirstlane(bucket);
-  if (__all(bucket == first)) {
-    const uint64_t here = __ballot(true);
-    if (__ffsll((unsigned long long)here) - 1 == (int)(threadIdx.x & 63)) atomicAdd(&rows[bucket], (int)__popcll(here));
-  } else {
-    atomicAdd(&rows[bucket], 1);
-  }
+// Counts a row in its bucket and gives its place there.  The rows of a wave are mostly of
+// one request, and 64 additions to one place would take their turns.
+__device__ __forceinline__ int lora_count(int* rows, int bucket) {
+  const int first = __builtin_amdgcn_readfirstlane(bucket), lane = threadIdx.x & 63;
+  if (!__all(bucket == first)) return atomicAdd(&rows[bucket], 1);
+  const uint64_t here = __ballot(true);
+  int start = 0;
+  if (__ffsll((unsigned long long)here) - 1 == lane) start = atomicAdd(&rows[bucket], (int)__popcll(here));
+  return __builtin_amdgcn_readfirstlane(start) + (int)__popcll(here & ((1ull << lane) - 1));
 }
 
 template <int S>
@@ -102,65 +99,57 @@ __device__ __forceinline__ int block_sum(int v, int* waves, int& total) {
 // ---------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------
+// One workgroup.  Rows of an adapter get places in the order of their counting, which is
+// not the same in every run; a row's result does not depend on its place.
 template <int S>
-__global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q) {
-  extern __shared__ int lds[];  // [buckets + 1] rows, then first row; [buckets + 1] first segment
-  __shared__ int waves[16];
+__global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q, int most) {
+  extern __shared__ int lds[];  // [buckets] rows; [buckets] first segment
+  __shared__ int waves[kLoraPlanThreads / 64];
+  constexpr int kHeld = 8;  // rows a thread whose buckets and places stay in registers
   const int buckets = q.d.adapters + 1, tid = threadIdx.x;
+  const bool held = q.m <= kHeld * kLoraPlanThreads;
   int* rows = lds;
-  int* segs = lds + buckets + 1;
+  int* segs = lds + buckets;
+  int bucket[kHeld], place[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int64_t row = (int64_t)i * kLoraPlanThreads + tid;
+    bucket[i] = held && row < q.m ? lora_bucket(q, row) : -1;
+  }
   for (int b = tid; b < buckets; b += kLoraPlanThreads) rows[b] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < q.m; i += kLoraPlanThreads) lora_count(rows, lora_bucket(q, i));
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (bucket[i] >= 0) place[i] = lora_count(rows, bucket[i]);
+  } else {
+    for (int64_t i = tid; i < q.m; i += kLoraPlanThreads) q.place[i] = lora_count(rows, lora_bucket(q, i));
+  }
   __syncthreads();
-  // exclusive sums over the buckets, consecutive ones a thread
+  // first segments: exclusive sums over the buckets, consecutive ones a thread
   const int per = (buckets + kLoraPlanThreads - 1) / kLoraPlanThreads;
-  int my_rows = 0, my_segs = 0, total, all;
+  int mine = 0, all;
+  for (int b = tid * per; b < buckets && b < (tid + 1) * per; ++b) mine += lora_segments<S>(q, b, rows[b]);
+  int at = block_sum<kLoraPlanThreads / 64>(mine, waves, all) - mine;
   for (int b = tid * per; b < buckets && b < (tid + 1) * per; ++b) {
-    my_rows += rows[b];
-    my_segs += lora_segments<S>(q, b, rows[b]);
+    segs[b] = at;
+    at += lora_segments<S>(q, b, rows[b]);
   }
-  int at_row = block_sum<16>(my_rows, waves, total) - my_rows;
-  int at_seg = block_sum<16>(my_segs, waves, all) - my_segs;
-  for (int b = tid * per; b < buckets && b < (tid + 1) * per; ++b) {
-    const int n = rows[b];
-    rows[b] = at_row;
-    segs[b] = at_seg;
-    at_row += n;
-    at_seg += lora_segments<S>(q, b, n);
-  }
-  if (tid == 0) {
-    rows[buckets] = (int)q.m;
-    segs[buckets] = all;
-    q.count[0] = all;
-  }
+  for (int z = all + tid; z < most; z += kLoraPlanThreads) q.segs[z] = LoraSeg{0, 0};
   __syncthreads();
-  for (int z = tid; z < all; z += kLoraPlanThreads) {
-    int lo = 0, hi = buckets;  // the last bucket whose first segment is not past z
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (segs[mid] <= z) lo = mid;
-      else hi = mid;
-    }
-    const int first = rows[lo] + (z - segs[lo]) * S;
-    const int left = rows[lo + 1] - first;
-    q.segs[z] = LoraSeg{lo == q.d.adapters ? -1 : lo, first, left < S ? left : S, 0};
-  }
-  __syncthreads();
-  // places in a bucket by its count; their order has no say in any row's result
-  for (int64_t i = tid; i < q.m; i += kLoraPlanThreads) {
-    const int b = lora_bucket(q, i), lane = tid & 63;
-    const int first = __builtin_amdgcn_readfirstlane(b);
-    int at;
-    if (__all(b == first)) {
-      const uint64_t here = __ballot(true);
-      int start = 0;
-      if (__ffsll((unsigned long long)here) - 1 == lane) start = atomicAdd(&rows[b], (int)__popcll(here));
-      at = __builtin_amdgcn_readfirstlane(start) + __popcll(here & ((1ull << lane) - 1));
-    } else {
-      at = atomicAdd(&rows[b], 1);
-    }
-    q.order[at] = (int)i;
+  const auto put = [&](int64_t row, int b, int p) {
+    const bool none = b == q.d.adapters;
+    if (none && !q.copy) return;
+    const int z = segs[b] + p / S, left = rows[b] - p;
+    q.order[(int64_t)z * S + p % S] = (int)row;
+    if (p % S == 0) q.segs[z] = LoraSeg{none ? -1 : b, left < S ? left : S};
+  };
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (bucket[i] >= 0) put((int64_t)i * kLoraPlanThreads + tid, bucket[i], place[i]);
+  } else {
+    for (int64_t i = tid; i < q.m; i += kLoraPlanThreads) put(i, lora_bucket(q, i), q.place[i]);
   }
 }
 
@@ -168,13 +157,44 @@ __global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q) {
 template <int S, int W>
 __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, LoraTask& task) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (q.count) {
-    if (z >= q.count[0]) return false;
+  if (q.segs) {
+    const int row = tid < S ? q.order[(int64_t)z * S + tid] : 0;
     const LoraSeg sg = q.segs[z];
-    if (tid < S) task.row[tid] = q.order[sg.first + (tid < sg.count ? tid : 0)];
+    if (sg.count == 0) return false;
+    if (tid < S) {  // one wave: past count its first row
+      const int first = __builtin_amdgcn_readfirstlane(row);
+      task.row[tid] = tid < sg.count ? row : first;
+    }
     if (tid == 0) {
       task.adapter = sg.adapter;
       task.count = sg.count;
+    }
+    __syncthreads();
+    return true;
+  }
+  if (q.m <= 64) {  // every wave by itself, a row a lane
+    const int bucket = lane < q.m ? lora_bucket(q, lane) : 0;
+    uint64_t same = lane < q.m ? ~0ull : 0ull;  // lanes of this lane's adapter
+    for (int bit = 0; (q.d.adapters >> bit) != 0; ++bit) {
+      const uint64_t set = __ballot(bucket >> bit & 1);
+      same &= bucket >> bit & 1 ? set : ~set;
+    }
+    same &= q.m == 64 ? ~0ull : (1ull << q.m) - 1;
+    const uint64_t before = (1ull << lane) - 1;
+    const int place = (int)__popcll(same & before);
+    const bool leads = lane < q.m && place % S == 0 && (bucket != q.d.adapters || q.copy);
+    const uint64_t leaders = __ballot(leads);
+    const uint64_t mine = __ballot(leads && (int)__popcll(leaders & before) == z);
+    if (mine == 0) return false;
+    const int lead = __ffsll((unsigned long long)mine) - 1;
+    const int b = __builtin_amdgcn_readlane(bucket, lead), first = __builtin_amdgcn_readlane(place, lead);
+    const uint64_t members = __ballot(lane < q.m && bucket == b);
+    const int left = (int)__popcll(members) - first, count = left < S ? left : S;
+    if ((members >> lane & 1) && place >= first && place < first + S) task.row[place - first] = lane;
+    if (lane >= count && lane < S) task.row[lane] = lead;
+    if (lane == 0) {
+      task.adapter = b == q.d.adapters ? -1 : b;
+      task.count = count;
     }
     __syncthreads();
     return true;
@@ -209,8 +229,8 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
     found[0] = b;
     found[1] = z - at;
   }
-  // a row's place among its adapter's: those of the chunks of 64 rows before, and of the
-  // lanes before
+  // a row's place among its adapter's, the same in every workgroup: those of the chunks of
+  // 64 rows before, and of the lanes before
   __syncthreads();
   const int b = found[0], first = found[1] * S;
   uint64_t same[kEach];
@@ -430,7 +450,7 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
   for (int i = 0; i < kMost; ++i) {
     const int at = 4 * (part + i * kEach);
     h[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-    if (row < task.count && at < rank) {
+    if (row < task.count && at < q.rpad) {
       const float* p = q.h + (int64_t)task.row[row] * q.rpad + at;
       for (int s = 0; s < q.splits; s += 4) {  // four shares' loads at a time
         float4_t v[4];
@@ -708,12 +728,17 @@ __global__ __launch_bounds__(kLoraFewThreads) void lora_few(LoraArgs q) {
 
 namespace {
 
-constexpr int kLoraFewRows = 4, kLoraFewRank = 64;
+constexpr int kLoraFewRank = 64;
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+int lora_few_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : 64; }
+
 bool lora_is_few(const LoraDesc& d, int64_t m) {
-  return m <= kLoraFewRows && d.rank <= kLoraFewRank && d.rank * d.k <= (int64_t)1 << 17;
+  if (d.rank > kLoraFewRank || m > 256) return false;
+  const int64_t cols = kLoraFewThreads * 8 / lora_few_rank(d.rank);
+  const int64_t groups = m * ((d.n + cols - 1) / cols), each = d.rank * d.k * 2;
+  return groups <= 256 && each <= 384 << 10 && groups * each <= 64 << 20;
 }
 
 // 64 rows a segment where adapters have more than 16 each on average, enough of them for
@@ -729,23 +754,28 @@ int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
 }
 
 int lora_splits(const LoraDesc& d, int64_t m, bool longer) {
-  const int64_t groups = lora_most_segs(d, m, longer) * ((d.rank + 63) / 64);
-  // a workgroup of 64 rows fills a CU, and every share is read again by all that expand
-  const int64_t want = (longer ? 256 : 512) / groups, most = longer ? (d.k + 511) / 512 : (d.k + 511) / 512;
+  // of 64 rows, a workgroup fills a CU; every share is read again by all that expand
+  const int64_t segs = longer ? (m + 63) / 64 : lora_most_segs(d, m, false);
+  const int64_t groups = segs * ((d.rank + 63) / 64);
+  const int64_t want = (longer ? 256 : 512) / groups, most = (d.k + 511) / 512;
   const int64_t s = want < most ? want : most, cap = longer ? 4 : 16;
   return (int)(s < 1 ? 1 : s > cap ? cap : s);
 }
 
 struct LoraLayout {
-  size_t segs, order, h, total;
+  size_t segs, order, place, h, total;
 };
 LoraLayout lora_layout(const LoraDesc& d, int64_t m, bool longer) {
   LoraLayout L;
-  size_t off = 256;
+  size_t off = 0;
+  const bool planned = m > kLoraPlanRows;
+  const size_t most = planned ? (size_t)lora_most_segs(d, m, longer) : 0;
   L.segs = off;
-  if (m > kLoraPlanRows) off += align256((size_t)lora_most_segs(d, m, longer) * sizeof(LoraSeg));
+  off += align256(most * sizeof(LoraSeg));
   L.order = off;
-  if (m > kLoraPlanRows) off += align256((size_t)m * 4);
+  off += align256(most * (longer ? 64 : 16) * 4);
+  L.place = off;
+  off += align256(planned ? (size_t)m * 4 : 0);
   L.h = off;
   off += align256((size_t)lora_splits(d, m, longer) * m * ((d.rank + 15) / 16 * 16) * 4);
   L.total = off;
@@ -754,7 +784,7 @@ LoraLayout lora_layout(const LoraDesc& d, int64_t m, bool longer) {
 
 template <class T>
 void launch_few(const LoraArgs& q, hipStream_t s) {
-  const int rj = q.d.rank <= 8 ? 8 : q.d.rank <= 16 ? 16 : q.d.rank <= 32 ? 32 : 64;
+  const int rj = lora_few_rank(q.d.rank);
   const int cols = kLoraFewThreads * 8 / rj;
   const dim3 grid((uint32_t)((q.d.n + cols - 1) / cols), (uint32_t)q.m), block(kLoraFewThreads);
   if (rj == 8) hipLaunchKernelGGL((lora_few<8, T>), grid, block, 0, s, q);
@@ -834,12 +864,13 @@ hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t 
   q.rpad = (d.rank + 15) / 16 * 16;
   q.h = reinterpret_cast<float*>(w + L.h);
   if (m > kLoraPlanRows) {
-    q.count = reinterpret_cast<int*>(w);
     q.segs = reinterpret_cast<LoraSeg*>(w + L.segs);
     q.order = reinterpret_cast<int*>(w + L.order);
-    const size_t lds = 2 * (size_t)(d.adapters + 2) * 4;
-    if (longer) hipLaunchKernelGGL((lora_plan<64>), dim3(1), dim3(kLoraPlanThreads), lds, s, q);
-    else hipLaunchKernelGGL((lora_plan<16>), dim3(1), dim3(kLoraPlanThreads), lds, s, q);
+    q.place = reinterpret_cast<int*>(w + L.place);
+    const size_t lds = 2 * (size_t)(d.adapters + 1) * 4;
+    const int most = (int)lora_most_segs(d, m, longer);
+    if (longer) hipLaunchKernelGGL((lora_plan<64>), dim3(1), dim3(kLoraPlanThreads), lds, s, q, most);
+    else hipLaunchKernelGGL((lora_plan<16>), dim3(1), dim3(kLoraPlanThreads), lds, s, q, most);
   }
   if (longer) launch_segments<64>(q, f32, s);
   else launch_segments<16>(q, f32, s);
