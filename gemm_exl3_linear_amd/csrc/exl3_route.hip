@@ -1,55 +1,91 @@
 // exl3_route_topk: choices and weights of every token from its logits.
+//
+// Many tokens of up to 256 experts take 16 lanes each: a wave's instructions are what
+// they cost (a merge of two lists of eight is 56 of them), and four tokens share them.
+// Few tokens wait for one wave's instructions, and for their way from memory: they take
+// a wave each, whose lanes hold a quarter of the values.
+// Measured (us of the kernel, a wave / 16 lanes a token, 8 of 256 experts): softmax, 1
+// token 3.2 / 4.3, 2048 4.5 / 4.7, 4096 6.5 / 4.8, 16384 19.0 / 10.0; balanced sigmoids
+// in 8 groups 4.9 / 7.2, 6.1 / 7.7, 8.8 / 7.9, 25.6 / 16.5; 4 of 60 experts, 2048 tokens
+// 3.2 / 2.9, 16384 10.3 / 4.0.
+#include "exl3_mx4.hpp"
 #include "exl3_route.hpp"
 
 namespace exl3 {
 
 constexpr int kRouteWaves = 4;
+constexpr int64_t kRouteFew = 2048;  // tokens that take a wave each
 
-template <int VPL, int K>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_topk_kernel(RouteRule q, const void* logits, int f32,
-                                                                      int64_t t, int64_t ldl, int32_t* ids,
-                                                                      float* weights) {
-  __shared__ RouteLds<64, VPL> lds[kRouteWaves];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (row >= t) return;
+template <int LANES, int VPL, int K, class T>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_topk_kernel(RouteRule q, const T* logits, int vec, int64_t t,
+                                                                      int64_t ldl, int32_t* ids, float* weights) {
+  constexpr int kTokens = kRouteWaves * 64 / LANES;  // of a workgroup
+  constexpr int V = VPL < 4 ? VPL : 4;
+  typedef T four __attribute__((ext_vector_type(V)));
+  __shared__ RouteLds<LANES, VPL> lds[kTokens];
+  const int token = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * kTokens + token;
+  const T* p = logits + (row < t ? row : t - 1) * ldl;  // past the last: it again, and nothing is stored
   float l[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = 64 * i + lane;
-    l[i] = 0.f;
-    if (e < q.experts)
-      l[i] = f32 ? static_cast<const float*>(logits)[row * ldl + e]
-                 : (float)static_cast<const _Float16*>(logits)[row * ldl + e];
+  for (int i = 0; i < VPL; i += V) {
+    const int e = route_expert<LANES, VPL>(i, lane);
+    if (vec) {  // experts and rows are whole fours, so that one holds all or none
+      const four f = *reinterpret_cast<const four*>(p + (e < q.experts ? e : 0));
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[i + j] = (float)f[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[i + j] = (float)p[e + j < q.experts ? e + j : 0];
+    }
   }
   int id;
   float weight;
-  route_token<64, VPL, K>(q, l, lane, lds + wave, id, weight);
-  if (lane < q.topk) {
+  route_token<LANES, VPL, K>(q, l, lane, lds + token, [&](int e) { return (float)p[e]; }, id, weight);
+  if (lane < q.topk && row < t) {
     ids[row * q.topk + lane] = id;
     weights[row * q.topk + lane] = weight;
   }
 }
 
-template <int VPL>
-static void launch_vpl(const RouteRule& q, const void* logits, bool f32, int64_t t, int64_t ldl, int32_t* ids,
-                       float* weights, hipStream_t s) {
-  const dim3 grid((uint32_t)((t + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * 64);
+namespace {
+
+template <int LANES, int VPL, class T>
+void launch_vpl(const RouteRule& q, const T* logits, int64_t t, int64_t ldl, int32_t* ids, float* weights,
+                hipStream_t s) {
+  constexpr int kTokens = kRouteWaves * 64 / LANES, V = VPL < 4 ? VPL : 4;
+  const dim3 grid((uint32_t)((t + kTokens - 1) / kTokens)), block(kRouteWaves * 64);
+  const int vec = q.experts % V == 0 && ldl % V == 0 && reinterpret_cast<uintptr_t>(logits) % (V * sizeof(T)) == 0;
   if (q.topk <= 4)
-    hipLaunchKernelGGL((route_topk_kernel<VPL, 4>), grid, block, 0, s, q, logits, (int)f32, t, ldl, ids, weights);
+    hipLaunchKernelGGL((route_topk_kernel<LANES, VPL, 4, T>), grid, block, 0, s, q, logits, vec, t, ldl, ids, weights);
   else if (q.topk <= 8)
-    hipLaunchKernelGGL((route_topk_kernel<VPL, 8>), grid, block, 0, s, q, logits, (int)f32, t, ldl, ids, weights);
+    hipLaunchKernelGGL((route_topk_kernel<LANES, VPL, 8, T>), grid, block, 0, s, q, logits, vec, t, ldl, ids, weights);
   else
-    hipLaunchKernelGGL((route_topk_kernel<VPL, 16>), grid, block, 0, s, q, logits, (int)f32, t, ldl, ids, weights);
+    hipLaunchKernelGGL((route_topk_kernel<LANES, VPL, 16, T>), grid, block, 0, s, q, logits, vec, t, ldl, ids, weights);
 }
+
+template <class T>
+void launch_type(const RouteRule& q, const T* logits, int64_t t, int64_t ldl, int32_t* ids, float* weights,
+                 hipStream_t s) {
+  if (q.experts > 256 || t <= kRouteFew) {
+    if (q.experts <= 64) launch_vpl<64, 1>(q, logits, t, ldl, ids, weights, s);
+    else if (q.experts <= 128) launch_vpl<64, 2>(q, logits, t, ldl, ids, weights, s);
+    else if (q.experts <= 256) launch_vpl<64, 4>(q, logits, t, ldl, ids, weights, s);
+    else if (q.experts <= 512) launch_vpl<64, 8>(q, logits, t, ldl, ids, weights, s);
+    else launch_vpl<64, 16>(q, logits, t, ldl, ids, weights, s);
+  } else {
+    if (q.experts <= 64) launch_vpl<16, 4>(q, logits, t, ldl, ids, weights, s);
+    else if (q.experts <= 128) launch_vpl<16, 8>(q, logits, t, ldl, ids, weights, s);
+    else launch_vpl<16, 16>(q, logits, t, ldl, ids, weights, s);
+  }
+}
+
+}  // namespace
 
 hipError_t launch_route_topk(const RouteRule& q, const void* logits, bool f32, int64_t t, int64_t ldl, int32_t* ids,
                              float* weights, hipStream_t s) {
-  if (q.experts <= 64) launch_vpl<1>(q, logits, f32, t, ldl, ids, weights, s);
-  else if (q.experts <= 128) launch_vpl<2>(q, logits, f32, t, ldl, ids, weights, s);
-  else if (q.experts <= 256) launch_vpl<4>(q, logits, f32, t, ldl, ids, weights, s);
-  else if (q.experts <= 512) launch_vpl<8>(q, logits, f32, t, ldl, ids, weights, s);
-  else launch_vpl<16>(q, logits, f32, t, ldl, ids, weights, s);
+  if (f32) launch_type(q, static_cast<const float*>(logits), t, ldl, ids, weights, s);
+  else launch_type(q, static_cast<const _Float16*>(logits), t, ldl, ids, weights, s);
   return hipGetLastError();
 }
 

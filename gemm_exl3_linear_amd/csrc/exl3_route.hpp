@@ -26,14 +26,16 @@ constexpr int kRouteMaxTopk = 16;
 constexpr double kKeyInf = 1e300, kKeyNan = -1.2e300, kKeyNone = -1.7e308;
 constexpr uint32_t kKeyPlace = 1023;
 
-// The key of value v at place e: larger for larger v, then for lower e.
+// The key of a finite value v at place e: larger for larger v, then for lower e.
+__device__ __forceinline__ double route_key_finite(double v, uint32_t e) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);  // -0 is 0
+  const uint32_t sign = (uint32_t)((int32_t)(b >> 32) >> 31);
+  return __longlong_as_double((long long)((b & ~(uint64_t)kKeyPlace) | ((kKeyPlace - e) ^ (sign & kKeyPlace))));
+}
+// The same of any value.
 __device__ __forceinline__ double route_key(double v, uint32_t e) {
-  v = v > kKeyInf ? kKeyInf : v;
-  v = v < -kKeyInf ? -kKeyInf : v;
-  v = (v != v ? kKeyNan : v) + 0.0;  // -0 is 0
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint32_t place = (int64_t)b < 0 ? e : kKeyPlace - e;
-  return __longlong_as_double((long long)((b & ~(uint64_t)kKeyPlace) | place));
+  const double held = __builtin_fmax(__builtin_fmin(v, kKeyInf), -kKeyInf);
+  return route_key_finite(v != v ? kKeyNan : held, e);
 }
 __device__ __forceinline__ uint32_t route_place(double key) {
   const uint64_t b = (uint64_t)__double_as_longlong(key);
@@ -55,7 +57,7 @@ typedef uint32_t u32pair_t __attribute__((ext_vector_type(2)));
 // The value of the lane N places on in its row of 16.
 template <int N>
 __device__ __forceinline__ uint32_t row_turn(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, true);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, true);
 }
 template <int N>
 __device__ __forceinline__ float row_turn(float v) {
@@ -119,18 +121,18 @@ __device__ __forceinline__ void key_order(double& a, double& b) {
   b = lo;
 }
 
+// Batcher's odd-even merge sort, highest first (19 pairs for eight).
 template <int N>
 __device__ __forceinline__ void keys_sort(double* v) {
 #pragma unroll
-  for (int k = 2; k <= N; k *= 2)
+  for (int p = 1; p < N; p *= 2)
 #pragma unroll
-    for (int j = k / 2; j > 0; j /= 2)
+    for (int k = p; k >= 1; k /= 2)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (!(i & j)) {
-          if (!(i & k)) key_order(v[i], v[i | j]);
-          else key_order(v[i | j], v[i]);
-        }
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (j + i + k < N && (j + i) / (2 * p) == (j + i + k) / (2 * p)) key_order(v[j + i], v[j + i + k]);
 }
 
 // a: the highest K of two lists of K.
@@ -161,6 +163,41 @@ __device__ __forceinline__ void keys_both(double (&a)[K]) {
 }
 
 // ---------------------------------------------------------------------------
+// scores in 64 bits
+// ---------------------------------------------------------------------------
+// e^x for x that is not NaN, to about 2^-50 of itself: 2^n 2^f with |f| <= 1/2 and the
+// Taylor series of 2^f, whose 12th term is below 2^-47 (values are compared to 2^-42).
+// From e^708 on that, below 2^-1074 zero.
+__device__ __forceinline__ double exp_d(double x) {
+  constexpr double kLog2e = 1.4426950408889634, kLog2eRest = 2.0355273740931033e-17, kLn2 = 0.6931471805599453;
+  x = __builtin_fmax(__builtin_fmin(x, 708.0), -760.0);
+  const double n = __builtin_rint(x * kLog2e);
+  const double f = __builtin_fma(x, kLog2eRest, __builtin_fma(x, kLog2e, -n));
+  constexpr double c2 = kLn2 * kLn2 / 2, c3 = c2 * kLn2 / 3, c4 = c3 * kLn2 / 4, c5 = c4 * kLn2 / 5,
+                   c6 = c5 * kLn2 / 6, c7 = c6 * kLn2 / 7, c8 = c7 * kLn2 / 8, c9 = c8 * kLn2 / 9,
+                   c10 = c9 * kLn2 / 10, c11 = c10 * kLn2 / 11;
+  double p = __builtin_fma(f, c11, c10);
+  p = __builtin_fma(f, p, c9);
+  p = __builtin_fma(f, p, c8);
+  p = __builtin_fma(f, p, c7);
+  p = __builtin_fma(f, p, c6);
+  p = __builtin_fma(f, p, c5);
+  p = __builtin_fma(f, p, c4);
+  p = __builtin_fma(f, p, c3);
+  p = __builtin_fma(f, p, c2);
+  p = __builtin_fma(f, p, kLn2);
+  p = __builtin_fma(f, p, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / y for 1 <= y < 2^1023: the instruction's estimate and two Newton steps.
+__device__ __forceinline__ double recip_d(double y) {
+  double r = __builtin_amdgcn_rcp(y);
+  r = __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+  return __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+}
+
+// ---------------------------------------------------------------------------
 // one token
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void wave_sync() {  // LDS of other lanes of this wave
@@ -170,95 +207,163 @@ __device__ __forceinline__ void wave_sync() {  // LDS of other lanes of this wav
 
 __device__ __forceinline__ float sigmoid_f(float l) { return 1.f / (1.f + exp_f(-l)); }
 
-// What a token of grouped routing needs of LDS.
+// A lane's i-th expert: four (or all, if fewer) neighbours a lane.
+template <int LANES, int VPL>
+__device__ __forceinline__ int route_expert(int i, int lane) {
+  constexpr int V = VPL < 4 ? VPL : 4;
+  return i / V * (LANES * V) + lane * V + i % V;
+}
+
+// What a token of grouped routing needs of LDS: values, or the two best of four.
 template <int LANES, int VPL>
 struct RouteLds {
   double value[LANES * VPL];
   double grade[kRouteMaxGroups];
 };
 
-// l[i] is the logit of expert LANES i + lane (any value past the experts).  Lane s
-// ends with choice s and its weight.
-template <int LANES, int VPL, int K>
-__device__ __forceinline__ void route_token(const RouteRule& q, const float (&l)[VPL], int lane,
-                                            RouteLds<LANES, VPL>* lds, int& id, float& weight) {
+// The keys of a lane's values.  (What is not finite is rare, and its instructions, which
+// a call of few tokens waits for, stay out of the way.)
+template <int LANES, int VPL>
+__device__ __forceinline__ void route_keys(double (&v)[VPL], bool finite, int lane) {
+  if (__builtin_expect(finite, 1)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = route_key_finite(v[i], route_expert<LANES, VPL>(i, lane));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = route_key(v[i], route_expert<LANES, VPL>(i, lane));
+  }
+}
+
+// The groups that are kept, a bit each: fewer than topk_groups are graded higher, or as
+// high and before it.  key: a lane's keys.
+template <int LANES, int VPL>
+__device__ __forceinline__ uint64_t route_groups(const RouteRule& q, const double (&key)[VPL], int lane,
+                                                 RouteLds<LANES, VPL>* lds) {
+  const bool fours = VPL >= 4 && q.group_size % 4 == 0;  // four neighbours are of one group
+  if (fours) {
+#pragma unroll
+    for (int i = 0; i + 3 < VPL; i += 4) {
+      double k[4] = {key[i], key[i + 1], key[i + 2], key[i + 3]};
+      key_order(k[0], k[1]);
+      key_order(k[2], k[3]);
+      double* at = lds->value + route_expert<LANES, VPL>(i, lane) / 2;
+      at[0] = __builtin_fmax(k[0], k[2]);
+      at[1] = __builtin_fmax(__builtin_fmin(k[0], k[2]), __builtin_fmax(k[1], k[3]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) lds->value[route_expert<LANES, VPL>(i, lane)] = key[i];
+  }
+  wave_sync();
+  for (int g = lane; g < q.groups; g += LANES) {
+    double best = kKeyNone, second = kKeyNone;
+    const int n = q.group_size / (fours ? 2 : 1);
+    const double* at = lds->value + g * n;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      second = __builtin_fmax(second, __builtin_fmin(best, at[j]));
+      best = __builtin_fmax(best, at[j]);
+    }
+    lds->grade[g] = route_key(route_value(best) + (q.top2 ? route_value(second) : 0.0), g);
+  }
+  wave_sync();
+  uint64_t kept = 0;
+  for (int g0 = 0; g0 < q.groups; g0 += LANES) {
+    const int g = g0 + lane;
+    const double mine = g < q.groups ? lds->grade[g] : kKeyNone;
+    int ahead = 0;
+#pragma unroll 4
+    for (int o = 0; o < q.groups; ++o) ahead += lds->grade[o] > mine;
+    const uint64_t all = __ballot(g < q.groups && ahead < q.topk_groups);
+    if constexpr (LANES == 64) kept = all;
+    else kept |= ((all >> (threadIdx.x & 48)) & 0xFFFFull) << g0;
+  }
+  wave_sync();
+  return kept;
+}
+
+// l[i] is the logit of the lane's i-th expert (any value past the experts); logit(e) gives
+// expert e's again.  Lane s ends with choice s and its weight.
+template <int LANES, int VPL, int K, class Logit>
+__device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL], int lane,
+                                            RouteLds<LANES, VPL>* lds, const Logit& logit, int& id, float& weight) {
   const auto max_f = [](float a, float b) { return __builtin_fmaxf(a, b); };
   const auto sum_f = [](float a, float b) { return a + b; };
-  const bool softmax = q.scoring == 0;
-  const bool sums = q.groups > 1 && q.top2;
-  float high = -__builtin_huge_valf();  // of the logits, NaN aside
+  const bool softmax = q.scoring == 0, ragged = q.experts < LANES * VPL;
+  float worst = 0.f;  // NaN if a logit is not finite
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) worst = __builtin_fmaf(l[i], 0.f, worst);
+  const bool finite = !__any(worst != 0.f);
+  if (ragged) {  // past the experts: nothing to the highest and to the softmax's sum
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = route_expert<LANES, VPL>(i, lane) < q.experts ? l[i] : -__builtin_huge_valf();
+  }
+  float high = -__builtin_huge_valf(), total = 0.f;  // of the logits (NaN aside) and of the softmax
   if (softmax) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (LANES * i + lane < q.experts) high = max_f(high, l[i]);
+    for (int i = 0; i < VPL; ++i) high = max_f(high, l[i]);
     high = route_all<LANES>(high, max_f);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) total += exp_f(l[i] - high);
+    total = route_all<LANES>(total, sum_f);
   }
   double v[VPL];
-  if (q.balance || sums) {  // scores in 64 bits
-    double total = 1.0;
+  uint64_t kept = ~0ull;
+  const auto none_past = [&] {
+    if (ragged) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] = route_expert<LANES, VPL>(i, lane) < q.experts ? v[i] : kKeyNone;
+    }
+  };
+  const bool scores = q.balance || (q.groups > 1 && q.top2);
+  if (scores) {  // in 64 bits
+    double all = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = exp_d(softmax ? (double)l[i] - (double)high : -(double)l[i]);
+      all += v[i];
+    }
     if (softmax) {
-      total = 0.0;
+      const double sum = route_all<LANES>(all, [](double a, double b) { return a + b; });
+      const double scale = total != total ? __builtin_nan("") : recip_d(sum);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] *= scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] = recip_d(1.0 + v[i]);
+      if (!finite) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = l[i] != l[i] ? (double)l[i] : v[i];
+      }
+    }
+    if (q.balance) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        v[i] = exp((double)l[i] - (double)high);
-        if (LANES * i + lane < q.experts) total += v[i];
+        const int e = route_expert<LANES, VPL>(i, lane);
+        v[i] += (double)q.balance[e < q.experts ? e : 0];
       }
-      total = route_all<LANES>(total, [](double a, double b) { return a + b; });
     }
+    double odd = 0.0;  // NaN if a value is not finite
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = LANES * i + lane;
-      const double s = softmax ? v[i] / total : 1.0 / (1.0 + exp(-(double)l[i]));
-      v[i] = q.balance && e < q.experts ? s + (double)q.balance[e] : s;
-    }
-  } else {
+    for (int i = 0; i < VPL; ++i) odd = __builtin_fma(v[i], 0.0, odd);
+    route_keys<LANES, VPL>(v, !__any(odd != 0.0), lane);
+    none_past();
+    if (q.groups > 1) kept = route_groups<LANES, VPL>(q, v, lane, lds);
+  }
+  if (!q.balance) {  // in the order of the logits
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = (double)l[i];
+    route_keys<LANES, VPL>(v, finite, lane);
+    none_past();
+    if (q.groups > 1 && !scores) kept = route_groups<LANES, VPL>(q, v, lane, lds);
   }
   if (q.groups > 1) {
-    // a group a lane; a group is kept if fewer than topk_groups are graded higher, or as
-    // high and before it
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) lds->value[LANES * i + lane] = route_key(v[i], LANES * i + lane);
-    wave_sync();
-    for (int g = lane; g < q.groups; g += LANES) {
-      double best = kKeyNone, second = kKeyNone;
-      for (int j = 0; j < q.group_size; ++j) {
-        const double key = lds->value[g * q.group_size + j];
-        second = __builtin_fmax(second, __builtin_fmin(best, key));
-        best = __builtin_fmax(best, key);
-      }
-      const double grade = q.top2 ? route_value(best) + route_value(second) : route_value(best);
-      lds->grade[g] = route_key(grade, g);
-    }
-    wave_sync();
-    uint64_t kept = 0;
-    for (int g0 = 0; g0 < q.groups; g0 += LANES) {
-      const int g = g0 + lane;
-      bool keep = false;
-      if (g < q.groups) {
-        const double mine = lds->grade[g];
-        int ahead = 0;
-        for (int o = 0; o < q.groups; ++o) ahead += lds->grade[o] > mine;
-        keep = ahead < q.topk_groups;
-      }
-      const uint64_t all = __ballot(keep);
-      if constexpr (LANES == 64) kept = all;
-      else kept |= ((all >> (threadIdx.x & 48)) & 0xFFFFull) << g0;
-    }
-    wave_sync();
+    const bool fours = VPL >= 4 && q.group_size % 4 == 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const uint32_t e = LANES * i + lane;
-      const bool in = e < (uint32_t)q.experts && (kept >> ((e * q.group_inverse) >> 20) & 1);
-      const double key = route_key(!q.balance ? (double)l[i] : v[i], e);
-      v[i] = in ? key : kKeyNone;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = LANES * i + lane;
-      v[i] = e < q.experts ? route_key(v[i], e) : kKeyNone;
+      // four neighbours are of the first one's group
+      const uint32_t e = route_expert<LANES, VPL>(fours ? i & ~3 : i, lane);
+      v[i] = (kept >> ((e * q.group_inverse) >> 20) & 1) ? v[i] : kKeyNone;
     }
   }
   double top[K];
@@ -291,21 +396,8 @@ __device__ __forceinline__ void route_token(const RouteRule& q, const float (&l)
 #pragma unroll
   for (int s = 1; s < K; ++s) mine = lane == s ? top[s] : mine;
   id = (int)route_place(mine);
-  // its logit, from the lane that holds it
-  float chosen = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const float o = __shfl(l[i], id % LANES, LANES);
-    chosen = id / LANES == i ? o : chosen;
-  }
-  if (softmax) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += LANES * i + lane < q.experts ? exp_f(l[i] - high) : 0.f;
-    weight = exp_f(chosen - high) / route_all<LANES>(sum, sum_f);
-  } else {
-    weight = sigmoid_f(chosen);
-  }
+  const float chosen = q.balance ? logit(id) : (float)route_value(mine);
+  weight = softmax ? exp_f(chosen - high) / total : sigmoid_f(chosen);
   if (q.renormalize) weight = weight / route_all<LANES>(lane < q.topk ? weight : 0.f, sum_f);
   weight *= q.scale;
 }

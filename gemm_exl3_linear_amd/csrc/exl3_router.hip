@@ -1,5 +1,6 @@
 // exl3_router_linear and exl3_router: a router's logits l = x W^T (+ c), fp16 matrix
 // instructions with fp32 sums, and for few tokens their routing in the same launch.
+#include <stdlib.h>
 #include "exl3_route.hpp"
 #include "exl3_tile64.hpp"
 
@@ -97,14 +98,27 @@ __global__ __launch_bounds__(NW * 64) void router_rows_kernel(RouterArgs q) {
     for (int row = wave; row < (int)q.t; row += NW) {
       float l[kV];
 #pragma unroll
-      for (int i = 0; i < kV; ++i) l[i] = 64 * i + lane < q.d.experts ? sum(row, 64 * i + lane) : 0.f;
+      for (int i = 0; i < kV; ++i) {
+        const int e = route_expert<64, kV>(i, lane);
+        l[i] = e < q.d.experts ? sum(row, e) : 0.f;
+      }
       if (q.logits)
 #pragma unroll
         for (int i = 0; i < kV; ++i)
-          if (64 * i + lane < q.d.experts) q.logits[row * q.ldl + 64 * i + lane] = l[i];
+          if (const int e = route_expert<64, kV>(i, lane); e < q.d.experts) q.logits[row * q.ldl + e] = l[i];
       int id;
       float weight;
-      route_token<64, kV, K>(q.rule, l, lane, lds + wave, id, weight);
+      const auto logit = [&](int e) {  // from the lane that holds it
+        constexpr int V = kV < 4 ? kV : 4;
+        float at = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const float o = __shfl(l[i], e / V % 64);
+          at = route_expert<64, kV>(i, e / V % 64) == e ? o : at;
+        }
+        return at;
+      };
+      route_token<64, kV, K>(q.rule, l, lane, lds + wave, logit, id, weight);
       if (lane < q.rule.topk) {
         q.ids[(int64_t)row * q.rule.topk + lane] = id;
         q.weights[(int64_t)row * q.rule.topk + lane] = weight;
@@ -170,7 +184,8 @@ __global__ __launch_bounds__(256) void router_sum_kernel(RouterArgs q) {
 
 namespace {
 
-constexpr int kFewTokens = 16;  // of which one launch makes the logits and routes them
+constexpr int kFewTokens = 16;  // of one tile, whose k is shared by workgroups
+static int kFusedTokens = getenv("XFUSE") ? atoi(getenv("XFUSE")) : 16;  // of which the same launch routes them
 
 // How a router's product is cut: shares of k, 16 x 16 by router_rows_kernel or 64 x 64
 // by router_gemm_kernel.
@@ -277,13 +292,13 @@ hipError_t launch_router_linear(const RouterDesc& d, const uint16_t* x, int64_t 
 }
 
 size_t router_workspace(const RouterDesc& d, int64_t t, bool logits) {
-  if (t <= kFewTokens) return kRouterCounts * 4 + router_parts(d, t, router_splits(d, t));
+  if (t <= kFusedTokens) return kRouterCounts * 4 + router_parts(d, t, router_splits(d, t));
   return logits ? router_linear_workspace(d, t) : router_head(d, t) + router_parts(d, t, 1);
 }
 
 hipError_t launch_router(const RouterDesc& d, const RouteRule& rule, const uint16_t* x, int64_t t, int64_t ldx,
                          float* logits, int64_t ldl, int32_t* ids, float* weights, void* ws, hipStream_t s) {
-  if (t > kFewTokens) {
+  if (t > kFusedTokens) {
     if (!logits) {
       logits = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + router_head(d, t));
       ldl = router_estride(d);
