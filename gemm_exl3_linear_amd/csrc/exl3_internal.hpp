@@ -168,6 +168,19 @@ struct RouteRule {
 };
 hipError_t launch_route_topk(const RouteRule& q, const void* logits, bool f32, int64_t t, int64_t ldl, int32_t* ids,
                              float* weights, hipStream_t s);
+// The logits as sums of shares of k, [splits][t][stride] (rows of whole 64 bytes), and the
+// bias; they are stored where `logits` is not null.
+struct RouteParts {
+  const float* part;
+  int splits, stride;
+  const float* bias;
+  float* logits;
+  int64_t ldl;
+};
+constexpr int64_t kRouteFew = 2048;  // tokens that are routed by a wave each
+// t <= kRouteFew
+hipError_t launch_route_parts(const RouteRule& q, const RouteParts& parts, int64_t t, int32_t* ids, float* weights,
+                              hipStream_t s);
 struct RouterDesc {
   const uint16_t* weight;  // [experts][hidden]
   const float* bias;       // [experts] or null

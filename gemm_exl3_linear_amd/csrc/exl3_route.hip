@@ -14,7 +14,6 @@
 namespace exl3 {
 
 constexpr int kRouteWaves = 4;
-constexpr int64_t kRouteFew = 2048;  // tokens that take a wave each
 
 template <int LANES, int VPL, int K, class T>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_topk_kernel(RouteRule q, const T* logits, int vec, int64_t t,
@@ -48,7 +47,59 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_topk_kernel(RouteRule 
   }
 }
 
+// The same from sums of shares of k, a wave a token.
+template <int VPL, int K>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_parts_kernel(RouteRule q, RouteParts parts, int64_t t,
+                                                                       int32_t* ids, float* weights) {
+  constexpr int V = VPL < 4 ? VPL : 4;
+  typedef float four __attribute__((ext_vector_type(V)));
+  __shared__ RouteLds<64, VPL> lds[kRouteWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (row >= t) return;
+  const float* p = parts.part + row * parts.stride;
+  const int64_t step = t * parts.stride;
+  float l[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; i += V) {
+    const int e = route_expert<64, VPL>(i, lane);
+    four sum = {};
+    if (e < q.experts) {
+#pragma unroll 4
+      for (int k = 0; k < parts.splits; ++k) sum += *reinterpret_cast<const four*>(p + k * step + e);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const bool there = e + j < q.experts;
+      l[i + j] = there ? parts.bias ? sum[j] + parts.bias[e + j] : sum[j] : 0.f;
+      if (there && parts.logits) parts.logits[row * parts.ldl + e + j] = l[i + j];
+    }
+  }
+  const auto logit = [&](int e) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts.splits; ++k) sum += p[k * step + e];
+    return parts.bias ? sum + parts.bias[e] : sum;
+  };
+  int id;
+  float weight;
+  route_token<64, VPL, K>(q, l, lane, lds + wave, logit, id, weight);
+  if (lane < q.topk) {
+    ids[row * q.topk + lane] = id;
+    weights[row * q.topk + lane] = weight;
+  }
+}
+
 namespace {
+
+template <int VPL>
+void launch_parts(const RouteRule& q, const RouteParts& parts, int64_t t, int32_t* ids, float* weights,
+                  hipStream_t s) {
+  const dim3 grid((uint32_t)((t + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * 64);
+  if (q.topk <= 4) hipLaunchKernelGGL((route_parts_kernel<VPL, 4>), grid, block, 0, s, q, parts, t, ids, weights);
+  else if (q.topk <= 8) hipLaunchKernelGGL((route_parts_kernel<VPL, 8>), grid, block, 0, s, q, parts, t, ids, weights);
+  else hipLaunchKernelGGL((route_parts_kernel<VPL, 16>), grid, block, 0, s, q, parts, t, ids, weights);
+}
 
 template <int LANES, int VPL, class T>
 void launch_vpl(const RouteRule& q, const T* logits, int64_t t, int64_t ldl, int32_t* ids, float* weights,
@@ -86,6 +137,16 @@ hipError_t launch_route_topk(const RouteRule& q, const void* logits, bool f32, i
                              float* weights, hipStream_t s) {
   if (f32) launch_type(q, static_cast<const float*>(logits), t, ldl, ids, weights, s);
   else launch_type(q, static_cast<const _Float16*>(logits), t, ldl, ids, weights, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_parts(const RouteRule& q, const RouteParts& parts, int64_t t, int32_t* ids, float* weights,
+                              hipStream_t s) {
+  if (q.experts <= 64) launch_parts<1>(q, parts, t, ids, weights, s);
+  else if (q.experts <= 128) launch_parts<2>(q, parts, t, ids, weights, s);
+  else if (q.experts <= 256) launch_parts<4>(q, parts, t, ids, weights, s);
+  else if (q.experts <= 512) launch_parts<8>(q, parts, t, ids, weights, s);
+  else launch_parts<16>(q, parts, t, ids, weights, s);
   return hipGetLastError();
 }
 

@@ -1,14 +1,15 @@
 // exl3_router_linear and exl3_router: a router's logits l = x W^T (+ c), fp16 matrix
-// instructions with fp32 sums, and for few tokens their routing in the same launch.
-#include <stdlib.h>
+// instructions with fp32 sums, and their routing: in the same launch for a token or a few,
+// else in a second one, which also adds the shares of k.
 #include "exl3_route.hpp"
 #include "exl3_tile64.hpp"
 
 namespace exl3 {
 
-constexpr int kRouterRows = 16;           // of an operand
-constexpr int kRouterCounts = 128;        // arrival counts at the head of a workspace: one a group of 16 experts,
-                                          // and the routing's
+constexpr int kRouterRows = 16;     // of an operand
+constexpr int kRouterCounts = 128;  // arrival counts at the head of a workspace: one a group of 16 experts, and the
+                                    // routing's
+constexpr int kRouterWaves = 8;
 
 struct RouterArgs {
   RouterDesc d;
@@ -25,65 +26,68 @@ struct RouterArgs {
   float* weights;
 };
 
+// What becomes of the sums: logits, or shares of k in `part` for another launch; shares
+// that the last workgroup of their experts adds (one tile of tokens); shares that the last
+// workgroup of all adds and routes.
+enum class RouterEnd { kStore, kAdd, kRoute };
+
 // Sums of 16 experts (blockIdx.x / splits) for 16 tokens (from blockIdx.y on) over a
-// share of hidden.  VPL > 0: the last workgroup to arrive routes every token, expert 64 i +
-// lane at a lane's i-th place.
-template <int VPL, int K, int NW>
-__global__ __launch_bounds__(NW * 64) void router_rows_kernel(RouterArgs q) {
-  constexpr bool kRoutes = VPL > 0;
-  constexpr int kV = kRoutes ? VPL : 1;
-  __shared__ float4_t sums[NW * 64];
-  __shared__ RouteLds<64, kV> lds[kRoutes ? NW : 1];
+// share of hidden.  END == kRoute: at most 64 VPL experts, topk <= K.
+template <RouterEnd END, int VPL, int K>
+__global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterArgs q) {
+  constexpr bool kRoutes = END == RouterEnd::kRoute;
+  __shared__ float4_t sums[kRouterWaves * 64];
+  __shared__ RouteLds<64, VPL> lds[kRoutes ? kRouterWaves : 1];
   __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int group = blockIdx.x / q.splits, split = blockIdx.x - group * q.splits;
   const int e = group * 16 + r;
+  const bool e_there = e < q.d.experts;
+  const uint16_t* w = q.d.weight + (e_there ? (int64_t)e * q.d.hidden : 0);
+  const int stride = kRouterWaves * q.splits;
   for (int64_t row0 = (int64_t)blockIdx.y * kRouterRows; row0 < q.t; row0 += (int64_t)gridDim.y * kRouterRows) {
-    const bool row_there = row0 + r < q.t, e_there = e < q.d.experts;
+    const bool row_there = row0 + r < q.t;
     const uint16_t* x = q.x + (row_there ? (row0 + r) * q.ldx : 0);
-    const uint16_t* w = q.d.weight + (e_there ? (int64_t)e * q.d.hidden : 0);
     float4_t acc = {0.f, 0.f, 0.f, 0.f};
-    const int stride = NW * q.splits;
-    for (int st = split * NW + wave; 32 * st < q.d.hidden; st += 4 * stride) {
+    for (int st = split * kRouterWaves + wave; 32 * st < q.d.hidden; st += 4 * stride) {
       u32x4_t a[4], b[4];  // four steps' loads at a time
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int at = 32 * (st + i * stride) + 8 * g;
         a[i] = b[i] = u32x4_t{0u, 0u, 0u, 0u};
         if (row_there && at < q.d.hidden) a[i] = load16(x + at);
         if (e_there && at < q.d.hidden) b[i] = load16(w + at);
       }
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < 4; ++i)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a[i]), __builtin_bit_cast(f16x8_t, b[i]),
-                                                     acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a[i]),
+                                                     __builtin_bit_cast(f16x8_t, b[i]), acc, 0, 0, 0);
     }
     sums[wave * 64 + lane] = acc;
     __syncthreads();
     if (wave == 0) {
-  #pragma unroll
-      for (int o = 1; o < NW; ++o) acc += sums[o * 64 + lane];
-      const bool whole = q.splits == 1 && !kRoutes;
+#pragma unroll
+      for (int o = 1; o < kRouterWaves; ++o) acc += sums[o * 64 + lane];
+      const bool whole = END == RouterEnd::kStore && q.splits == 1;
       const float c = whole && q.d.bias && e_there ? q.d.bias[e] : 0.f;
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t row = row0 + 4 * g + i;
         if (!e_there || row >= q.t) continue;
+        float* part = q.part + ((int64_t)split * q.t + row) * q.estride + e;
         if (whole) q.logits[row * q.ldl + e] = acc[i] + c;
-        else store_shared(q.part + ((int64_t)split * q.t + row) * q.estride + e, acc[i]);
+        else if (END == RouterEnd::kStore) *part = acc[i];
+        else store_shared(part, acc[i]);
       }
-      if (!whole) {
+      if (END != RouterEnd::kStore) {
         wait_stores();
         if (lane == 0) last = kRoutes ? last_in(q.arrived, gridDim.x) : last_in(q.arrived + 1 + group, q.splits);
       }
     }
-    if (kRoutes || q.splits > 1) break;  // all tokens are in one tile
     __syncthreads();
   }
-  if (q.splits == 1 && !kRoutes) return;
-  __syncthreads();
-  if (!last) return;
+  if (END == RouterEnd::kStore || !last) return;
   const auto sum = [&](int64_t row, int expert) {
     const float* p = q.part + row * q.estride + expert;
     float l = 0.f;
@@ -92,33 +96,33 @@ __global__ __launch_bounds__(NW * 64) void router_rows_kernel(RouterArgs q) {
     return q.d.bias ? l + q.d.bias[expert] : l;
   };
   if constexpr (!kRoutes) {
-    for (int i = threadIdx.x; i < (int)q.t * 16; i += NW * 64)
+    for (int i = threadIdx.x; i < (int)q.t * 16; i += kRouterWaves * 64)
       if (const int o = group * 16 + (i & 15); o < q.d.experts) q.logits[(i >> 4) * q.ldl + o] = sum(i >> 4, o);
   } else {
-    for (int row = wave; row < (int)q.t; row += NW) {
-      float l[kV];
+    for (int row = wave; row < (int)q.t; row += kRouterWaves) {
+      float l[VPL];
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int e = route_expert<64, kV>(i, lane);
-        l[i] = e < q.d.experts ? sum(row, e) : 0.f;
+      for (int i = 0; i < VPL; ++i) {
+        const int o = route_expert<64, VPL>(i, lane);
+        l[i] = o < q.d.experts ? sum(row, o) : 0.f;
       }
       if (q.logits)
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-          if (const int e = route_expert<64, kV>(i, lane); e < q.d.experts) q.logits[row * q.ldl + e] = l[i];
-      int id;
-      float weight;
-      const auto logit = [&](int e) {  // from the lane that holds it
-        constexpr int V = kV < 4 ? kV : 4;
+        for (int i = 0; i < VPL; ++i)
+          if (const int o = route_expert<64, VPL>(i, lane); o < q.d.experts) q.logits[row * q.ldl + o] = l[i];
+      const auto logit = [&](int chosen) {  // from the lane that holds it
+        constexpr int V = VPL < 4 ? VPL : 4;
         float at = 0.f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const float o = __shfl(l[i], e / V % 64);
-          at = route_expert<64, kV>(i, e / V % 64) == e ? o : at;
+        for (int i = 0; i < VPL; ++i) {
+          const float o = __shfl(l[i], chosen / V % 64);
+          at = route_expert<64, VPL>(i, chosen / V % 64) == chosen ? o : at;
         }
         return at;
       };
-      route_token<64, kV, K>(q.rule, l, lane, lds + wave, logit, id, weight);
+      int id;
+      float weight;
+      route_token<64, VPL, K>(q.rule, l, lane, lds + wave, logit, id, weight);
       if (lane < q.rule.topk) {
         q.ids[(int64_t)row * q.rule.topk + lane] = id;
         q.weights[(int64_t)row * q.rule.topk + lane] = weight;
@@ -184,40 +188,58 @@ __global__ __launch_bounds__(256) void router_sum_kernel(RouterArgs q) {
 
 namespace {
 
-constexpr int kFewTokens = 16;  // of one tile, whose k is shared by workgroups
-static int kFusedTokens = getenv("XFUSE") ? atoi(getenv("XFUSE")) : 16;  // of which the same launch routes them
+// Who adds shares of k: a launch of its own, or, for a tile of tokens, their last workgroup
+// (exl3_router_linear); the routing's launch (exl3_router); the routing in the same launch.
+enum class RouterJoin { kLinear, kRouted, kFused };
 
-// How a router's product is cut: shares of k, 16 x 16 by router_rows_kernel or 64 x 64
-// by router_gemm_kernel.
+// A product's cut: shares of k, 16 x 16 by router_rows_kernel or 64 x 64 by
+// router_gemm_kernel.
 struct RouterCut {
   bool tiled;
   int splits;
 };
 
+// Routed by the launch that makes the logits: the last workgroup's waves route a token
+// after the other (us, fused / in two launches, of which the host bounds the latter at
+// 10.5: 256 experts, 4 tokens 8.5 / 10.4, 8 9.7 / 10.6, 16 14.1 / 10.5; 64 experts, 16
+// tokens 8.6 / 10.6; 1024 experts, 1 token 22 / 10.9).
+bool router_fused(const RouterDesc& d, int64_t t) { return d.experts <= 256 && t * d.experts <= 1024; }
+
 // The cut by estimates in us, fitted to kernels alone, and measured where they meet
 // (tokens x hidden x experts, by rows / tiled): 64 x 5120 x 256 11.0 / 9.5 (of 8), 512
 // 20.6 / 11.4, 4096 142 / 20.5; 1024 x 2048 x 64 6.8 / 8.4, 2048 9.8 / 8.4; 333 x 1440 x
 // 60 4.3 / 7.4.
-RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx) {
+RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx, RouterJoin join) {
   const int64_t groups = (d.experts + 15) / 16, rows = (t + kRouterRows - 1) / kRouterRows;
-  if (t <= kFewTokens) {
-    const int most = (d.hidden + 32 * 8 * 4 - 1) / (32 * 8 * 4);
-    const int want = (int)((256 + groups - 1) / groups);
-    return {false, want < most ? want : most};
-  }
-  // by rows: 16 bytes a clock and CU of operands that are loaded as they are multiplied,
-  // 9.6 TB/s of all
-  const double lone = 1.7 / 1024 * d.hidden, all = groups * rows * 64.0 * d.hidden / 9.6e6;
+  const auto joined = [&](int splits) {
+    if (splits == 1) return 0.0;
+    if (join == RouterJoin::kFused) return 0.3 * splits;
+    if (join == RouterJoin::kRouted) return 0.3 + splits * (double)t * d.experts * 8 / 4.5e6;
+    return t <= kRouterRows ? 1.0 + 0.1 * splits : 4.5 + splits * (double)t * d.experts * 8 / 4.5e6;
+  };
+  // many tokens are routed from whole logits
+  const int most = join == RouterJoin::kRouted && t > kRouteFew ? 1 : 16;
   RouterCut best{false, 1};
-  double cost = 2.5 + (lone > all ? lone : all);
-  if (ldx >= (1 << 24)) return best;  // offsets into 64 rows have 32 bits
-  // tiled: 0.36 a stage and round of a workgroup a CU; sums of shares 4.5 and their bytes
+  double cost = 1e30;
+  // by rows: 16 bytes a clock and CU of operands that are loaded as they are multiplied,
+  // 9.6 TB/s of all; shares of 256 k at least, a load a wave
+  const double all = groups * rows * 64.0 * d.hidden / 9.6e6;
+  for (int splits = 1; splits <= most && (splits == 1 || splits * 256 <= d.hidden); splits *= 2) {
+    const double lone = 1.7 / 1024 * d.hidden / splits;
+    const double c = 2.5 + (lone > all ? lone : all) + joined(splits);
+    if (c < cost) {
+      cost = c;
+      best = {false, splits};
+    }
+  }
+  if (ldx >= (1 << 24) || t <= kRouterRows) return best;  // offsets into 64 rows have 32 bits
+  // tiled: 0.36 a stage and round of a workgroup a CU; of fewer stages than the ring's a
+  // share is all latency
   const int64_t tiles = (t + kTile64 - 1) / kTile64 * ((d.experts + kTile64 - 1) / kTile64);
   const int stages = (d.hidden + kTile64K - 1) / kTile64K;
-  for (int splits = 1; splits <= 8 && splits <= stages; splits *= 2) {
+  for (int splits = 1; splits <= most && (splits == 1 || splits * kTile64Ring <= stages); splits *= 2) {
     const double rounds = (double)((tiles * splits + 255) / 256);
-    double c = 3.0 + 0.36 * ((stages + splits - 1) / splits) * rounds;
-    if (splits > 1) c += 4.5 + splits * (double)t * d.experts * 8 / 4.5e6;
+    const double c = 3.0 + 0.36 * ((stages + splits - 1) / splits) * rounds + joined(splits);
     if (c < cost) {
       cost = c;
       best = {true, splits};
@@ -228,12 +250,18 @@ RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int router_estride(const RouterDesc& d) { return (d.experts + 15) / 16 * 16; }
-// Of any ldx: far rows are not cut.
-int router_splits(const RouterDesc& d, int64_t t) { return router_cut(d, t, 0).splits; }
 size_t router_parts(const RouterDesc& d, int64_t t, int splits) {
   return align256((size_t)splits * t * router_estride(d) * 4);
 }
 
+// Bytes of a call of any ldx: far rows are cut by rows, in as many shares or fewer.
+size_t router_bytes(const RouterDesc& d, int64_t t, RouterJoin join) {
+  const int near = router_cut(d, t, 0, join).splits, far = router_cut(d, t, 1 << 24, join).splits;
+  const int splits = near > far ? near : far;
+  return splits == 1 && join != RouterJoin::kFused ? 0 : kRouterCounts * 4 + router_parts(d, t, splits);
+}
+
+// The counts at a workspace's head are never written over.
 RouterArgs router_args(const RouterDesc& d, const uint16_t* x, int64_t t, int64_t ldx, float* logits, int64_t ldl,
                        void* ws) {
   RouterArgs q{};
@@ -243,7 +271,6 @@ RouterArgs router_args(const RouterDesc& d, const uint16_t* x, int64_t t, int64_
   q.ldx = ldx;
   q.logits = logits;
   q.ldl = ldl;
-  q.splits = router_cut(d, t, ldx).splits;
   q.arrived = static_cast<uint32_t*>(ws);
   q.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kRouterCounts * 4);
   q.estride = router_estride(d);
@@ -255,67 +282,75 @@ dim3 router_grid(const RouterArgs& q) {
   return dim3((uint32_t)((q.d.experts + 15) / 16 * q.splits), (uint32_t)(tiles < 65535 ? tiles : 65535));
 }
 
+// The logits, or shares of them in q.part; true if those are left to be added.
+bool launch_product(RouterArgs& q, RouterJoin join, hipStream_t s) {
+  const RouterCut cut = router_cut(q.d, q.t, q.ldx, join);
+  q.splits = cut.splits;
+  if (cut.tiled) {
+    const int64_t down = (q.t + kTile64 - 1) / kTile64, across = (q.d.experts + kTile64 - 1) / kTile64;
+    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits);
+    hipLaunchKernelGGL(router_gemm_kernel, grid, dim3(kTile64Waves * 64), 0, s, q);
+    return q.splits > 1;
+  }
+  const dim3 block(kRouterWaves * 64);
+  if (q.splits > 1 && join == RouterJoin::kLinear && q.t <= kRouterRows) {
+    hipLaunchKernelGGL((router_rows_kernel<RouterEnd::kAdd, 1, 1>), router_grid(q), block, 0, s, q);
+    return false;
+  }
+  hipLaunchKernelGGL((router_rows_kernel<RouterEnd::kStore, 1, 1>), router_grid(q), block, 0, s, q);
+  return q.splits > 1;
+}
+
 template <int VPL>
-void launch_fused(const RouterArgs& q, hipStream_t s) {
-  const dim3 grid = router_grid(q), block(512);
-  if (q.rule.topk <= 4) hipLaunchKernelGGL((router_rows_kernel<VPL, 4, 8>), grid, block, 0, s, q);
-  else if (q.rule.topk <= 8) hipLaunchKernelGGL((router_rows_kernel<VPL, 8, 8>), grid, block, 0, s, q);
-  else hipLaunchKernelGGL((router_rows_kernel<VPL, 16, 8>), grid, block, 0, s, q);
+void launch_fused(RouterArgs& q, hipStream_t s) {
+  q.splits = router_cut(q.d, q.t, q.ldx, RouterJoin::kFused).splits;
+  const dim3 grid = router_grid(q), block(kRouterWaves * 64);
+  if (q.rule.topk <= 4) hipLaunchKernelGGL((router_rows_kernel<RouterEnd::kRoute, VPL, 4>), grid, block, 0, s, q);
+  else if (q.rule.topk <= 8) hipLaunchKernelGGL((router_rows_kernel<RouterEnd::kRoute, VPL, 8>), grid, block, 0, s, q);
+  else hipLaunchKernelGGL((router_rows_kernel<RouterEnd::kRoute, VPL, 16>), grid, block, 0, s, q);
 }
 
 }  // namespace
 
-size_t router_linear_workspace(const RouterDesc& d, int64_t t) {
-  const int splits = router_splits(d, t);
-  return splits > 1 ? kRouterCounts * 4 + router_parts(d, t, splits) : 0;
-}
-
-// Bytes ahead of what else a workspace holds: the counts are never written over.
-static size_t router_head(const RouterDesc& d, int64_t t) {
-  const size_t linear = router_linear_workspace(d, t);
-  return linear ? linear : kRouterCounts * 4;
-}
+size_t router_linear_workspace(const RouterDesc& d, int64_t t) { return router_bytes(d, t, RouterJoin::kLinear); }
 
 hipError_t launch_router_linear(const RouterDesc& d, const uint16_t* x, int64_t t, int64_t ldx, float* logits,
                                 int64_t ldl, void* ws, hipStream_t s) {
-  const RouterArgs q = router_args(d, x, t, ldx, logits, ldl, ws);
-  if (router_cut(d, t, ldx).tiled) {
-    const int64_t down = (t + kTile64 - 1) / kTile64, across = (d.experts + kTile64 - 1) / kTile64;
-    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits), block(kTile64Waves * 64);
-    hipLaunchKernelGGL(router_gemm_kernel, grid, block, 0, s, q);
-    if (q.splits > 1)
-      hipLaunchKernelGGL(router_sum_kernel, dim3((uint32_t)((t * (q.estride / 4) + 255) / 256)), dim3(256), 0, s, q);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL((router_rows_kernel<0, 1, 8>), router_grid(q), dim3(512), 0, s, q);
+  RouterArgs q = router_args(d, x, t, ldx, logits, ldl, ws);
+  if (launch_product(q, RouterJoin::kLinear, s))
+    hipLaunchKernelGGL(router_sum_kernel, dim3((uint32_t)((t * (q.estride / 4) + 255) / 256)), dim3(256), 0, s, q);
   return hipGetLastError();
 }
 
 size_t router_workspace(const RouterDesc& d, int64_t t, bool logits) {
-  if (t <= kFusedTokens) return kRouterCounts * 4 + router_parts(d, t, router_splits(d, t));
-  return logits ? router_linear_workspace(d, t) : router_head(d, t) + router_parts(d, t, 1);
+  if (router_fused(d, t)) return router_bytes(d, t, RouterJoin::kFused);
+  const size_t shares = router_bytes(d, t, RouterJoin::kRouted);
+  const size_t whole = logits ? 0 : kRouterCounts * 4 + router_parts(d, t, 1);  // logits of its own
+  return shares > whole ? shares : whole;
 }
 
 hipError_t launch_router(const RouterDesc& d, const RouteRule& rule, const uint16_t* x, int64_t t, int64_t ldx,
                          float* logits, int64_t ldl, int32_t* ids, float* weights, void* ws, hipStream_t s) {
-  if (t > kFusedTokens) {
-    if (!logits) {
-      logits = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + router_head(d, t));
-      ldl = router_estride(d);
-    }
-    const hipError_t e = launch_router_linear(d, x, t, ldx, logits, ldl, ws, s);
-    return e != hipSuccess ? e : launch_route_topk(rule, logits, true, t, ldl, ids, weights, s);
-  }
   RouterArgs q = router_args(d, x, t, ldx, logits, ldl, ws);
-  q.rule = rule;
-  q.ids = ids;
-  q.weights = weights;
-  if (d.experts <= 64) launch_fused<1>(q, s);
-  else if (d.experts <= 128) launch_fused<2>(q, s);
-  else if (d.experts <= 256) launch_fused<4>(q, s);
-  else if (d.experts <= 512) launch_fused<8>(q, s);
-  else launch_fused<16>(q, s);
-  return hipGetLastError();
+  if (router_fused(d, t)) {
+    q.rule = rule;
+    q.ids = ids;
+    q.weights = weights;
+    if (d.experts <= 64) launch_fused<1>(q, s);
+    else if (d.experts <= 128) launch_fused<2>(q, s);
+    else launch_fused<4>(q, s);
+    return hipGetLastError();
+  }
+  if (!logits) {  // where they are not left as shares
+    q.logits = q.part;
+    q.ldl = q.estride;
+  }
+  if (launch_product(q, RouterJoin::kRouted, s)) {
+    const RouteParts parts{q.part, q.splits, q.estride, d.bias, logits, ldl};
+    return launch_route_parts(rule, parts, t, ids, weights, s);
+  }
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_route_topk(rule, q.logits, true, t, q.ldl, ids, weights, s);
 }
 
 }  // namespace exl3
