@@ -40,7 +40,7 @@ struct LoraArgs {
   int copy;    // rows without an adapter are copied (base is not y)
   int splits;  // shares of k
   int rpad;    // floats of a row of h
-  int tiles;   // 64-column tiles of a workgroup of lora_expand
+  int tiles;   // 64-column tiles of a wave (lora_expand) or a workgroup (lora_expand_long)
   // workspace
   LoraSeg* segs;  // [segments at most]; null where workgroups find their own
   int* order;     // [segments at most][rows of a segment]
@@ -492,46 +492,87 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
   }
 }
 
-// How a wave's lanes take 16 rows of 64 columns of base and of y: 16 bytes a lane, or an
-// element where rows are not whole 16 bytes.
-template <class T, bool VEC>
+// How a wave's lanes take 16 rows of 64 columns of base and of y: 16 bytes a lane, of any
+// alignment.  Where a tile has fewer than 64 columns, the last lanes' pieces end with it and
+// overlap their neighbours', or begin in the tile before, and what lies there is not stored.
+// TINY: rows of less than 16 bytes, by elements.
+template <class T, bool TINY>
 struct LoraIo {
   static constexpr int kElems = 16 / (int)sizeof(T);  // of a lane
   static constexpr int kLanes = 64 / kElems;          // of a row
   static constexpr int kRows = 64 / kLanes;           // of an instruction
+  static constexpr int kInstr = 16 / kRows;           // of 16 rows
   typedef T vec __attribute__((ext_vector_type(kElems)));
-};
-template <class T>
-struct LoraIo<T, false> {
-  static constexpr int kElems = 1, kLanes = 64, kRows = 1;
-  struct vec {
-    T v;
-    __device__ T& operator[](int) { return v; }
-  };
+  typedef vec any __attribute__((aligned(sizeof(T))));
+
+  // A lane's first column in a tile with `left` columns, maybe negative; whether the lane
+  // has any.
+  static __device__ __forceinline__ int column(int lane, int left) {
+    const int col = lane % kLanes * kElems;
+    return TINY || col < left - kElems ? col : left - kElems;
+  }
+  static __device__ __forceinline__ bool takes(int lane, int left) { return lane % kLanes * kElems < left; }
+
+  static __device__ __forceinline__ vec load(const T* p, int col, int left) {
+    if constexpr (!TINY) return *reinterpret_cast<const any*>(p + col);
+    vec v{};
+#pragma unroll
+    for (int j = 0; j < kElems; ++j)
+      if (col + j < left) v[j] = p[col + j];
+    return v;
+  }
+  // once: without a place in the caches.
+  static __device__ __forceinline__ void store(T* p, int col, int left, vec v, bool once = false) {
+    if (!TINY && __builtin_expect(col >= 0, 1)) {
+      if (once) __builtin_nontemporal_store(v, reinterpret_cast<any*>(p + col));
+      else *reinterpret_cast<any*>(p + col) = v;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kElems; ++j)
+      if (col + j >= 0 && col + j < left) p[col + j] = v[j];
+  }
+  // base and the sums of a lane's columns, which a wave holds in LDS.
+  static __device__ __forceinline__ vec add(const vec& from, bool with, const float* sums, int col, int left) {
+    vec to;
+    if (left >= 64) {
+      const float* p = static_cast<const float*>(__builtin_assume_aligned(sums + col, 16));
+#pragma unroll
+      for (int j = 0; j < kElems; ++j) to[j] = (T)((with ? (float)from[j] : 0.f) + p[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kElems; ++j) {
+        const int at = col + j < 0 ? 0 : col + j < 64 ? col + j : 63;
+        to[j] = (T)((with ? (float)from[j] : 0.f) + sums[at]);
+      }
+    }
+    return to;
+  }
 };
 
-// Up to S rows; a wave takes tiles of 64 columns, of which B's rows stay in registers
-// while 16 of the task's rows after the other pass: matrix row i of tile t is column
-// 16 t + i, matrix columns are rows of the task.  The next 16 rows' base, and the next
-// tile's B, are under way meanwhile.
+// Up to 16 rows; a wave takes every fourth tile of 64 columns from its first on: matrix row
+// i of a tile's product t is column 16 t + i, matrix columns are rows of the task.  The
+// loads of a wave's next tile go out before it waits for this one's.
 // CH: chunks of 32 ranks; 0: up to 16 ranks, where an operand's upper half of k holds
 // another 16 columns, met by pieces that are zero in the other half.
-// VEC: base and y have rows of whole 16 bytes.
-template <int S, int CH, class T, bool VEC>
-__global__ __launch_bounds__(kLoraThreads, CH <= 1 ? 4 : CH == 2 ? 3 : 2) void lora_expand(LoraArgs q) {
+// Workgroups a CU.
+__host__ __device__ constexpr int lora_expand_groups(int ch) { return ch == 0 ? 5 : ch == 1 ? 4 : ch == 2 ? 3 : 2; }
+
+template <int CH, class T, bool TINY>
+__global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_expand(LoraArgs q) {
+  constexpr int S = 16;
   constexpr bool PAIR = CH == 0;
   constexpr int kChunks = PAIR ? 1 : CH;   // of the pieces
   constexpr int kB = PAIR ? 2 : 4 * CH;    // registers' worth of B
-  constexpr bool kAhead = CH <= 2;         // room for the next tile's
-  using Io = LoraIo<T, VEC>;
-  constexpr int kIo = 16 / Io::kRows;      // instructions of 16 rows
+  using Io = LoraIo<T, TINY>;
+  constexpr int kIo = Io::kInstr;
   constexpr int kRow = lora_piece_row(kChunks);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ LoraTask task;
   __shared__ float factor[2 * S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
-  const int col = lane % Io::kLanes * Io::kElems, sub = lane / Io::kLanes;
+  const int sub = lane / Io::kLanes;  // a lane's row of an instruction's
   const int N = (int)q.d.n, R = q.d.rank;
   const int first_tile = blockIdx.y * 4 * q.tiles + wave;
   const T* base = static_cast<const T*>(q.base);
@@ -540,17 +581,18 @@ __global__ __launch_bounds__(kLoraThreads, CH <= 1 ? 4 : CH == 2 ? 3 : 2) void l
   const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
   const int count = __builtin_amdgcn_readfirstlane(task.count);
   const int tiles = (N + 63) / 64;
-  const int end_tile = first_tile + 4 * q.tiles < tiles ? first_tile + 4 * q.tiles : tiles;
   if (adapter < 0) {  // only where y is not base
-    for (int tile = first_tile; tile < end_tile; tile += 4)
+    for (int tile = first_tile; tile < tiles && tile < first_tile + 4 * q.tiles; tile += 4) {
+      const int n0 = 64 * tile, left = N - n0, col = Io::column(lane, left);
 #pragma clang loop unroll(disable)
       for (int row = sub; row < count; row += Io::kRows)
-        if (64 * tile + col < N) {
+        if (Io::takes(lane, left)) {
           const int64_t i = task.row[row];
           typename Io::vec v{};
-          if (q.base) v = *reinterpret_cast<const typename Io::vec*>(base + i * q.ldb + 64 * tile + col);
-          *reinterpret_cast<typename Io::vec*>(y + i * q.ldy + 64 * tile + col) = v;
+          if (q.base) v = Io::load(base + i * q.ldb + n0, col, left);
+          Io::store(y + i * q.ldy + n0, col, left, v);
         }
+    }
     return;
   }
   const int rank = lora_rank(q, adapter);
@@ -568,85 +610,253 @@ __global__ __launch_bounds__(kLoraThreads, CH <= 1 ? 4 : CH == 2 ? 3 : 2) void l
   };
   const T* from_where = q.base ? base : y;  // without a base what is loaded is dropped
   const int64_t from_ld = q.base ? q.ldb : q.ldy;
-  const auto load_base = [&](int tile, int i0, typename Io::vec (&v)[kIo]) {
-    const T* at = from_where + (64 * tile + col < N ? 64 * tile + col : 0);
+  const auto load_base = [&](int tile, typename Io::vec (&v)[kIo]) {
+    const int n0 = 64 * (tile < tiles ? tile : tiles - 1), left = N - n0, col = Io::column(lane, left);
 #pragma unroll
     for (int o = 0; o < kIo; ++o)
-      v[o] = *reinterpret_cast<const typename Io::vec*>(at + task.row[i0 + Io::kRows * o + sub] * from_ld);
+      v[o] = Io::load(from_where + task.row[Io::kRows * o + sub] * from_ld + n0, col, left);
   };
-  f16x8_t w[kB];
-  typename Io::vec from[kIo];
-  load_b(first_tile, w);
-  load_base(first_tile, 0, from);
+  struct Tile {
+    f16x8_t w[kB];
+    typename Io::vec from[kIo];
+  } even, odd;
+  const auto load = [&](int tile, Tile& to) {
+    load_b(tile, to.w);
+    load_base(tile, to.from);
+  };
+  load(first_tile, even);
   __syncthreads();  // the segment's search is done with smem
   lora_pieces<S, kChunks>(q, task, rank, scale, smem, factor);
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem + 2 * S * kRow) + wave * (16 * kLoraOutStride);
-  for (int tile = first_tile; tile < end_tile; tile += 4) {
-    f16x8_t w_next[kB];
-    if constexpr (kAhead) load_b(tile + 4, w_next);
+  const auto take = [&](int tile, Tile& now) {
     if (rank < (PAIR ? 16 : 32 * CH)) {
 #pragma unroll
-      for (int i = 0; i < kB; ++i) w[i] = lora_keep(w[i], rank - (PAIR ? 8 * (g & 1) : 32 * (i >> 2) + 8 * g));
+      for (int i = 0; i < kB; ++i)
+        now.w[i] = lora_keep(now.w[i], rank - (PAIR ? 8 * (g & 1) : 32 * (i >> 2) + 8 * g));
     }
-#pragma clang loop unroll(disable)
-    for (int i0 = 0; i0 < count; i0 += 16) {
-      typename Io::vec from_next[kIo];
-      const bool last_rows = i0 + 16 >= count;
-      load_base(last_rows ? tile + 4 : tile, last_rows ? 0 : i0 + 16, from_next);
-      float4_t acc[4];
+    float4_t acc[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const f16x8_t h =
-              *reinterpret_cast<const f16x8_t*>(smem + (p * S + i0 + r) * kRow + 64 * c + 16 * (PAIR ? g & 1 : g));
-          if constexpr (PAIR) {
+      for (int p = 0; p < 2; ++p) {
+        const f16x8_t h =
+            *reinterpret_cast<const f16x8_t*>(smem + (p * S + r) * kRow + 64 * c + 16 * (PAIR ? g & 1 : g));
+        if constexpr (PAIR) {
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const f16x8_t part = lora_keep(h, (g >> 1) == o ? 8 : 0);
+          for (int o = 0; o < 2; ++o) {
+            const f16x8_t part = lora_keep(h, (g >> 1) == o ? 8 : 0);
 #pragma unroll
-              for (int v = 0; v < 2; ++v)
-                acc[2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[v], part, acc[2 * v + o], 0, 0, 0);
-            }
-          } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[4 * c + t], h, acc[t], 0, 0, 0);
+            for (int v = 0; v < 2; ++v)
+              acc[2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[v], part, acc[2 * v + o], 0, 0, 0);
           }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[4 * c + t], h, acc[t], 0, 0, 0);
         }
-      const float f0 = factor[i0 + r], f1 = factor[S + i0 + r];
-      float odd = 0.f;  // NaN if a sum is not finite
+      }
+    const float f0 = factor[r], f1 = factor[S + r];
+    float odd = 0.f;  // NaN if a sum is not finite
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
+      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+    }
+    wave_lds_sync();
+    if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, 0, 64 * tile, rank, scale, b, out);
+    const int left = N - 64 * tile, col = Io::column(lane, left);
+#pragma unroll
+    for (int o = 0; o < kIo; ++o) {
+      const int row = Io::kRows * o + sub;
+      const typename Io::vec to = Io::add(now.from[o], q.base != nullptr, out + row * kLoraOutStride, col, left);
+      if (row < count && Io::takes(lane, left)) Io::store(y + task.row[row] * q.ldy + 64 * tile, col, left, to);
+    }
+    wave_lds_sync();
+  };
+  const int end_tile = first_tile + 4 * q.tiles < tiles ? first_tile + 4 * q.tiles : tiles;
+  int tile = first_tile;
+  if (tile >= end_tile) return;
+  if constexpr (CH <= 2) {
+    for (; tile + 8 < end_tile; tile += 8) {
+      load(tile + 4, odd);
+      take(tile, even);
+      load(tile + 8, even);
+      take(tile + 4, odd);
+    }
+    if (tile + 4 < end_tile) {
+      load(tile + 4, odd);
+      take(tile, even);
+      take(tile + 4, odd);
+    } else {
+      take(tile, even);
+    }
+  } else {  // no room for another tile's
+    for (; tile + 4 < end_tile; tile += 4) {
+      take(tile, even);
+      load(tile + 4, even);
+    }
+    take(tile, even);
+  }
+}
+
+// Up to 64 rows, 16 a wave, whose pieces stay in registers while tiles of 64 columns pass:
+// a tile's B goes from memory straight to LDS, two tiles ahead, and serves the four waves.
+// (Loaded by the lanes that multiply it, 16 rows an instruction, it comes at 16 bytes a
+// clock and CU, which for 64 ranks is as long as base and y take.)
+//
+// LDS: a tile holds a row of 4 CH 16-byte pieces for each column; piece c of row n lies at
+// place c ^ turn(n), so that sixteen rows' pieces c cover all 64 banks.
+constexpr int kLoraRing = 3;
+
+template <int CH>
+__device__ __forceinline__ uint32_t lora_turn(uint32_t n) {
+  return CH == 1 ? n >> 2 & 3 : CH == 2 ? n >> 1 & 7 : n & 15;
+}
+
+template <int CH, class T>
+__global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
+  using Io = LoraIo<T, false>;
+  constexpr int S = 64, kIo = Io::kInstr;
+  constexpr int kRow = lora_piece_row(CH);
+  constexpr int kPieces = 4 * CH, kTile = 64 * 16 * kPieces;  // of a row; bytes of a tile
+  constexpr int kCopies = kTile / 1024 / 4;                   // a wave's
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ LoraTask task;
+  __shared__ float factor[2 * S];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int g = lane >> 4, r = lane & 15;
+  const int sub = lane / Io::kLanes;  // a lane's row of an instruction's
+  const int N = (int)q.d.n, R = q.d.rank;
+  const int first_tile = blockIdx.y * q.tiles, tiles = (N + 63) / 64;
+  const int end_tile = first_tile + q.tiles < tiles ? first_tile + q.tiles : tiles;
+  const T* base = static_cast<const T*>(q.base);
+  T* y = static_cast<T*>(q.y);
+  if (!lora_task<S, 4>(q, blockIdx.x, reinterpret_cast<int*>(smem), task)) return;
+  const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
+  const int count = __builtin_amdgcn_readfirstlane(task.count);
+  const int i0 = 16 * wave;
+  if (adapter < 0) {  // only where y is not base
+    for (int tile = first_tile; tile < end_tile; ++tile) {
+      const int n0 = 64 * tile, left = N - n0, col = Io::column(lane, left);
+#pragma clang loop unroll(disable)
+      for (int row = i0 + sub; row < count && row < i0 + 16; row += Io::kRows)
+        if (Io::takes(lane, left)) {
+          const int64_t i = task.row[row];
+          typename Io::vec v{};
+          if (q.base) v = Io::load(base + i * q.ldb + n0, col, left);
+          Io::store(y + i * q.ldy + n0, col, left, v);
+        }
+    }
+    return;
+  }
+  const int rank = lora_rank(q, adapter);
+  const float scale = q.d.scales ? q.d.scales[adapter] : 1.f;
+  const uint16_t* b = q.d.b + (int64_t)adapter * N * R;
+  __syncthreads();  // the segment's search is done with smem
+  lora_pieces<S, CH>(q, task, rank, scale, smem, factor);
+  __syncthreads();
+  f16x8_t h[CH][2];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      h[c][p] = *reinterpret_cast<const f16x8_t*>(smem + (p * S + i0 + r) * kRow + 64 * c + 16 * g);
+  __syncthreads();
+  const float f0 = factor[i0 + r], f1 = factor[S + i0 + r];
+  float* out = reinterpret_cast<float*>(smem + kLoraRing * kTile) + wave * (16 * kLoraOutStride);
+  const uint32_t ring = (uint32_t)(uintptr_t)(lds_u8*)smem;
+  const u32x4_t rsrc = buffer_words(reinterpret_cast<const uint8_t*>(b), (uint64_t)N * R * 2);
+  uint32_t off[kCopies];  // a lane's piece of a copy: ranks past the adapter's are zeros
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const uint32_t at = 64 * (kCopies * wave + i) + lane, n = at / kPieces;
+    const uint32_t piece = (at % kPieces) ^ lora_turn<CH>(n);
+    off[i] = 8 * piece < (uint32_t)rank ? n * R * 2 + 16 * piece : kPastEnd;
+  }
+  const auto fetch = [&](int tile, int place) {  // past the last tile: zeros
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      lds_copy16(rsrc, ring + (uint32_t)place * kTile + (uint32_t)(kCopies * wave + i) * 1024,
+                 tile < end_tile ? off[i] : kPastEnd, (uint32_t)(tile < end_tile ? tile : 0) * (128u * R));
+  };
+  // Without a base what is loaded is dropped.  Of rows past count and columns past n,
+  // others'.
+  const T* from_row[kIo];
+  T* to_row[kIo];
+#pragma unroll
+  for (int o = 0; o < kIo; ++o) {
+    const int64_t i = task.row[i0 + Io::kRows * o + sub];
+    to_row[o] = y + i * q.ldy;
+    from_row[o] = q.base ? base + i * q.ldb : to_row[o];
+  }
+  const auto load_base = [&](int tile, typename Io::vec (&v)[kIo]) {
+    const int n0 = 64 * (tile < end_tile ? tile : end_tile - 1), left = N - n0, col = Io::column(lane, left);
+#pragma unroll
+    for (int o = 0; o < kIo; ++o) v[o] = Io::load(from_row[o] + n0, col, left);
+  };
+  int place = 0;  // of the ring
+  const auto step = [&](int tile, typename Io::vec (&from)[kIo], typename Io::vec (&next)[kIo]) {
+    // The tile's copies, made two steps ago, have landed here when at most those of the
+    // next tile, and the base loaded with either, are open; behind the barrier they have
+    // everywhere, and the tile before has been read.
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kCopies + 2 * kIo) : "memory");
+    fetch(tile + 2, (place + 2) % kLoraRing);
+    load_base(tile + 1, next);
+    float4_t acc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    const uint32_t at = ring + (uint32_t)place * kTile;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      f16x8_t w[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
-        *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+        const uint32_t n = 16 * t + r;
+        w[t] = __builtin_bit_cast(f16x8_t, lds_read16(at + 16 * (n * kPieces + ((4 * c + g) ^ lora_turn<CH>(n)))));
       }
-      wave_lds_sync();
-      if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, i0, 64 * tile, rank, scale, b, out);
+      if (rank % 8) {
 #pragma unroll
-      for (int o = 0; o < kIo; ++o) {
-        const int row = i0 + Io::kRows * o + sub;
-        const float* p = out + (Io::kRows * o + sub) * kLoraOutStride + col;
-        typename Io::vec to;
-#pragma unroll
-        for (int j = 0; j < Io::kElems; ++j) to[j] = (T)((q.base ? (float)from[o][j] : 0.f) + p[j]);
-        if (row < count && 64 * tile + col < N)
-          *reinterpret_cast<typename Io::vec*>(y + task.row[row] * q.ldy + 64 * tile + col) = to;
+        for (int t = 0; t < 4; ++t) w[t] = lora_keep(w[t], rank - 32 * c - 8 * g);
       }
-      wave_lds_sync();
 #pragma unroll
-      for (int o = 0; o < kIo; ++o) from[o] = from_next[o];
-    }
-    if constexpr (kAhead) {
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int i = 0; i < kB; ++i) w[i] = w_next[i];
-    } else {
-      load_b(tile + 4, w);
+        for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][p], acc[t], 0, 0, 0);
     }
+    place = place == kLoraRing - 1 ? 0 : place + 1;
+    if (i0 >= count) return;
+    float odd = 0.f;  // NaN if a sum is not finite
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
+      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+    }
+    wave_lds_sync();
+    if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, i0, 64 * tile, rank, scale, b, out);
+    const int left = N - 64 * tile, col = Io::column(lane, left);
+#pragma unroll
+    for (int o = 0; o < kIo; ++o) {
+      const int row = Io::kRows * o + sub;
+      const typename Io::vec to = Io::add(from[o], q.base != nullptr, out + row * kLoraOutStride, col, left);
+      if (i0 + row < count && Io::takes(lane, left)) Io::store(to_row[o] + 64 * tile, col, left, to, true);
+    }
+    wave_lds_sync();
+  };
+  typename Io::vec even[kIo], odd[kIo];
+  fetch(first_tile, 0);
+  fetch(first_tile + 1, 1);
+  load_base(first_tile, even);
+  // the first tile's copies have nothing else behind them
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies + kIo) : "memory");
+  for (int tile = first_tile; tile < end_tile; tile += 2) {
+    step(tile, even, odd);
+    if (tile + 1 < end_tile) step(tile + 1, odd, even);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // copies to LDS
 }
 
 // ---------------------------------------------------------------------------
@@ -744,7 +954,7 @@ bool lora_is_few(const LoraDesc& d, int64_t m) {
 // 64 rows a segment where adapters have more than 16 each on average, enough of them for
 // the chip and 32-bit offsets for the copies to LDS.
 bool lora_long(const LoraDesc& d, int64_t m, int64_t ldx) {
-  return m >= 512 && m > 16 * (int64_t)d.adapters && m * ldx < (int64_t)1 << 31;
+  return m >= 512 && d.n >= 8 && m > 16 * (int64_t)d.adapters && m * ldx < (int64_t)1 << 31;
 }
 
 int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
@@ -793,41 +1003,57 @@ void launch_few(const LoraArgs& q, hipStream_t s) {
   else hipLaunchKernelGGL((lora_few<64, T>), grid, block, 0, s, q);
 }
 
-template <int S, int CH>
-void launch_expand(const LoraArgs& q, bool f32, bool vec, dim3 grid, size_t plan, hipStream_t s) {
-  const size_t need = 2 * S * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
+template <int CH, bool TINY = false>
+void launch_expand(LoraArgs q, bool f32, hipStream_t s) {
+  const size_t plan = (size_t)(q.d.adapters + 1) * 4;
+  const size_t need = 2 * 16 * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
   const size_t lds = need > plan ? need : plan;
-  const dim3 block(kLoraThreads);
-  if (f32 && vec) hipLaunchKernelGGL((lora_expand<S, CH, float, true>), grid, block, lds, s, q);
-  else if (f32) hipLaunchKernelGGL((lora_expand<S, CH, float, false>), grid, block, lds, s, q);
-  else if (vec) hipLaunchKernelGGL((lora_expand<S, CH, _Float16, true>), grid, block, lds, s, q);
-  else hipLaunchKernelGGL((lora_expand<S, CH, _Float16, false>), grid, block, lds, s, q);
+  const int64_t segs = lora_most_segs(q.d, q.m, false), tiles = (q.d.n + 63) / 64;
+  // one round of workgroups: each begins with the segment's search and its h, 4 us
+  const int64_t slots = 256 * lora_expand_groups(CH);
+  q.tiles = 1;
+  while (segs * ((tiles + 4 * q.tiles - 1) / (4 * q.tiles)) > slots && 4 * q.tiles < tiles && q.tiles < 16) ++q.tiles;
+  const dim3 grid((uint32_t)segs, (uint32_t)((tiles + 4 * q.tiles - 1) / (4 * q.tiles)));
+  if (f32) hipLaunchKernelGGL((lora_expand<CH, float, TINY>), grid, dim3(kLoraThreads), lds, s, q);
+  else hipLaunchKernelGGL((lora_expand<CH, _Float16, TINY>), grid, dim3(kLoraThreads), lds, s, q);
 }
 
-template <int S>
-void launch_segments(LoraArgs q, bool f32, hipStream_t s) {
-  const int64_t segs = lora_most_segs(q.d, q.m, S == 64);
-  const uint32_t gx = (uint32_t)segs;
+template <int CH>
+void launch_expand_long(const LoraArgs& q, bool f32, dim3 grid, size_t plan, hipStream_t s) {
+  size_t lds = kLoraRing * 4096 * CH + 4 * 16 * kLoraOutStride * 4;
+  if (const size_t pieces = 2 * 64 * lora_piece_row(CH); lds < pieces) lds = pieces;
+  if (lds < plan) lds = plan;
+  if (f32) hipLaunchKernelGGL((lora_expand_long<CH, float>), grid, dim3(kLoraThreads), lds, s, q);
+  else hipLaunchKernelGGL((lora_expand_long<CH, _Float16>), grid, dim3(kLoraThreads), lds, s, q);
+}
+
+void launch_segments(LoraArgs q, bool longer, bool f32, hipStream_t s) {
+  const uint32_t gx = (uint32_t)lora_most_segs(q.d, q.m, longer);
   const size_t plan = (size_t)(q.d.adapters + 1) * 4;
   const dim3 shrink(gx, (uint32_t)q.splits, (uint32_t)((q.d.rank + 63) / 64)), block(kLoraThreads);
-  if (S == 64) hipLaunchKernelGGL(lora_shrink_tiled, shrink, dim3(kTile64Waves * 64), 0, s, q);
+  if (longer) hipLaunchKernelGGL(lora_shrink_tiled, shrink, dim3(kTile64Waves * 64), 0, s, q);
   else if (q.d.rank <= 16) hipLaunchKernelGGL((lora_shrink<1>), shrink, block, plan, s, q);
   else if (q.d.rank <= 32) hipLaunchKernelGGL((lora_shrink<2>), shrink, block, plan, s, q);
   else hipLaunchKernelGGL((lora_shrink<4>), shrink, block, plan, s, q);
   const int64_t tiles = (q.d.n + 63) / 64;
-  // more tiles a workgroup where there are workgroups enough
-  int each = 4;
-  while (each > 1 && (int64_t)gx * ((tiles + 4 * each - 1) / (4 * each)) < 1024) each /= 2;
-  q.tiles = each;
-  const dim3 grid(gx, (uint32_t)((tiles + 4 * each - 1) / (4 * each)));
-  const uintptr_t at = reinterpret_cast<uintptr_t>(q.base) | reinterpret_cast<uintptr_t>(q.y);
-  const int64_t elems = f32 ? 4 : 8;
-  const bool vec = at % 16 == 0 && q.d.n % elems == 0 && q.ldy % elems == 0 && (!q.base || q.ldb % elems == 0);
-  if (q.d.rank <= 16) launch_expand<S, 0>(q, f32, vec, grid, plan, s);
-  else if (q.d.rank <= 32) launch_expand<S, 1>(q, f32, vec, grid, plan, s);
-  else if (q.d.rank <= 64) launch_expand<S, 2>(q, f32, vec, grid, plan, s);
-  else if (q.d.rank <= 128) launch_expand<S, 4>(q, f32, vec, grid, plan, s);
-  else launch_expand<S, 8>(q, f32, vec, grid, plan, s);
+  if (longer) {
+    // a round of workgroups, as many as LDS holds
+    const int64_t slots = 256 * (q.d.rank <= 64 ? 3 : q.d.rank <= 128 ? 2 : 1);
+    const int64_t each = (q.m / 64 * tiles + slots - 1) / slots;
+    q.tiles = (int)(each < 4 ? 4 : each);
+    const dim3 grid(gx, (uint32_t)((tiles + q.tiles - 1) / q.tiles));
+    if (q.d.rank <= 32) launch_expand_long<1>(q, f32, grid, plan, s);
+    else if (q.d.rank <= 64) launch_expand_long<2>(q, f32, grid, plan, s);
+    else if (q.d.rank <= 128) launch_expand_long<4>(q, f32, grid, plan, s);
+    else launch_expand_long<8>(q, f32, grid, plan, s);
+    return;
+  }
+  if (q.d.n < (f32 ? 4 : 8)) launch_expand<8, true>(q, f32, s);
+  else if (q.d.rank <= 16) launch_expand<0>(q, f32, s);
+  else if (q.d.rank <= 32) launch_expand<1>(q, f32, s);
+  else if (q.d.rank <= 64) launch_expand<2>(q, f32, s);
+  else if (q.d.rank <= 128) launch_expand<4>(q, f32, s);
+  else launch_expand<8>(q, f32, s);
 }
 
 }  // namespace
@@ -872,8 +1098,7 @@ hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t 
     if (longer) hipLaunchKernelGGL((lora_plan<64>), dim3(1), dim3(kLoraPlanThreads), lds, s, q, most);
     else hipLaunchKernelGGL((lora_plan<16>), dim3(1), dim3(kLoraPlanThreads), lds, s, q, most);
   }
-  if (longer) launch_segments<64>(q, f32, s);
-  else launch_segments<16>(q, f32, s);
+  launch_segments(q, longer, f32, s);
   return hipGetLastError();
 }
 

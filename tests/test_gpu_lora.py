@@ -158,6 +158,37 @@ def test_lora_of_whole_numbers_is_exact(m):
         np.testing.assert_array_equal(call(d, True).cpu().numpy(), reference(d)[0])
 
 
+@pytest.mark.parametrize("n", [8, 63, 200, 1111, 4096, 4101])
+@pytest.mark.parametrize("rank", [8, 16, 24, 64, 72, 136, 256])
+def test_lora_many_rows_of_whole_numbers_are_exact(rank, n):
+    """Long segments, several tiles a workgroup, every column: each sum is a whole number
+    below 2^22 in magnitude (100 * 2 * 2 by rank * 3), which fp32 and both pieces hold."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    g = torch.Generator(device=G.dev()).manual_seed(rank * 7 + n)
+    whole = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=G.dev())
+    k = 104
+    for m, L in ((600, 3), (2100, 1), (5000, 7)):
+        x, a = whole(-2, 3, m, k).half(), whole(-2, 3, L, rank, k).half()
+        b, rows = whole(-3, 4, L, n, rank).half(), whole(-1, L, m).int()
+        lora = X.Exl3Lora(a, b)
+        base = whole(-99, 100, m, n).float()
+        ref = base.double()
+        for i in range(L):
+            mine = rows == i
+            ref[mine] += (x[mine].double() @ a[i].double().T) @ b[i].double().T
+        for _ in range(3):
+            y = X.exl3_lora(x, lora, rows, base)
+            assert torch.equal(y.double(), ref), (m, L)
+        y = base.clone()
+        X.exl3_lora(x, lora, rows, y, out=y)
+        assert torch.equal(y.double(), ref), (m, L)
+        small = whole(-9, 10, m, n).half()
+        y = X.exl3_lora(x, lora, rows, small)
+        ref += small.double() - base.double()
+        assert torch.equal(y, ref.to(torch.float16)), (m, L)
+
+
 @pytest.mark.parametrize("m", [1, 4, 40, 300])
 @pytest.mark.parametrize("rank", [8, 16, 40, 256])
 def test_lora_what_lies_past_a_rank_has_no_say(m, rank):
