@@ -32,7 +32,8 @@ struct RouterArgs {
 enum class RouterEnd { kStore, kAdd, kRoute };
 
 // Sums of 16 experts (blockIdx.x / splits) for 16 tokens (from blockIdx.y on) over a
-// share of hidden.  END == kRoute: at most 64 VPL experts, topk <= K.
+// share of hidden.  END == kRoute: at most 64 VPL experts, topk <= K.  kAdd and kRoute: one
+// tile of tokens (gridDim.y is 1).
 template <RouterEnd END, int VPL, int K>
 __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterArgs q) {
   constexpr bool kRoutes = END == RouterEnd::kRoute;
@@ -202,8 +203,11 @@ struct RouterCut {
 // Routed by the launch that makes the logits: the last workgroup's waves route a token
 // after the other (us, fused / in two launches, of which the host bounds the latter at
 // 10.5: 256 experts, 4 tokens 8.5 / 10.4, 8 9.7 / 10.6, 16 14.1 / 10.5; 64 experts, 16
-// tokens 8.6 / 10.6; 1024 experts, 1 token 22 / 10.9).
-bool router_fused(const RouterDesc& d, int64_t t) { return d.experts <= 256 && t * d.experts <= 1024; }
+// tokens 8.6 / 10.6; 1024 experts, 1 token 22 / 10.9).  One tile of tokens: the arrivals
+// that make a workgroup the last are counted over the experts and shares of one.
+bool router_fused(const RouterDesc& d, int64_t t) {
+  return t <= kRouterRows && d.experts <= 256 && t * d.experts <= 1024;
+}
 
 // The cut by estimates in us, fitted to kernels alone, and measured where they meet
 // (tokens x hidden x experts, by rows / tiled): 64 x 5120 x 256 11.0 / 9.5 (of 8), 512

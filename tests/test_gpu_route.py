@@ -357,6 +357,26 @@ def oracle_logits(x, r, ws):
     return l.cpu().numpy().astype(np.float64)
 
 
+@pytest.mark.parametrize("t,hidden,experts,topk", [(17, 2048, 60, 4), (24, 1000, 33, 2), (40, 264, 20, 3),
+                                                   (100, 5120, 8, 2), (300, 72, 3, 1), (1024, 520, 1, 1)])
+def test_router_more_tokens_than_a_tile_and_few_experts(t, hidden, experts, topk):
+    """Tokens times experts as few as one tile's: the sums of every tile are whole when
+    they are routed, and the workspace's counts end at zero."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, w, c = router_case(t, hidden, experts, True, seed=5)
+    r, rule, xd = handle(w, c), rule_of(experts, topk), G.to_dev(x)
+    ref, mag = S.logits(x, w, c)
+    ws = torch.zeros(X.exl3_router_workspace_size(r, t), dtype=torch.uint8, device=G.dev())
+    for _ in range(3):
+        logits = torch.full((t, experts), float("nan"), device=G.dev())
+        ids, wt = X.exl3_router(xd, r, rule, logits=logits, workspace=ws)
+        got = logits.cpu().numpy()
+        assert (np.abs(got - ref) <= logit_bound(mag, hidden)).all()
+        check(ids, wt, got.astype(np.float64), rule)
+        assert not ws[:512].any()
+
+
 def test_router_refuses_a_mismatch():
     import torch
     import gemm_exl3_linear_amd as X
