@@ -289,3 +289,61 @@ def test_lora_past_32_bits(m):
     got = X.exl3_lora(put(last["x"]), X.Exl3Lora(a, b, scales=scales),
                       torch.full((m,), L - 1, dtype=torch.int32, device=G.dev()), put(last["base"]))
     check(got, last, True)
+
+
+# ---------------------------------------------------------------------------
+# many rows an adapter, and more rows than registers hold
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m", [512, 1100, 9000])
+def test_lora_many_rows_strides_and_what_lies_between(m, f32):
+    test_lora_strides_and_what_lies_between(m, f32)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m,k,n,rank,adapters", [(512, 136, 129, 64, 5), (1100, 72, 65, 8, 2), (700, 264, 8, 136, 1),
+                                                 (9000, 64, 70, 16, 3), (9000, 64, 30, 24, 700),
+                                                 (1300, 64, 1000, 256, 90), (513, 8, 9, 8, 4096)])
+def test_lora_many_rows_without_base_and_in_place(m, k, n, rank, adapters, f32):
+    test_lora_without_base_and_in_place(m, k, n, rank, adapters, f32)
+
+
+@pytest.mark.parametrize("order", list(ORDERS))
+@pytest.mark.parametrize("m", [512, 1023, 1025, 8192, 8193])
+def test_lora_many_rows_orders(m, order):
+    test_lora_orders_of_rows(m, order)
+
+
+@pytest.mark.parametrize("m", [512, 1100])
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 136, 256])
+def test_lora_many_rows_what_lies_past_a_rank_has_no_say(m, rank):
+    test_lora_what_lies_past_a_rank_has_no_say(m, rank)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("m", [512, 1100])
+def test_lora_many_rows_bad_rows_stay_alone(m, f32):
+    test_lora_bad_rows_stay_alone(m, f32)
+
+
+@pytest.mark.parametrize("m", [600, 1100])
+def test_lora_many_rows_large_and_small(m):
+    test_lora_large_and_small(m)
+
+
+@pytest.mark.parametrize("past", [False, True])
+def test_lora_many_rows_past_32_bits(past):
+    """x whose last row ends just below 2^32 bytes, and past them; base and y past."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    m, k, n, rank, L = 600, 72, 70, 40, 3
+    d = case(m, k, n, rank, L, f32=True)
+    put = G.to_dev
+    pitch = ((1 << 31) - 1) // m // 8 * 8 + (8 if past else 0)
+    xb = torch.zeros(m * pitch, dtype=torch.float16, device=G.dev()).view(m, pitch)
+    xb[:, pitch - k:] = put(d["x"])
+    wide = torch.zeros((2, m, pitch + 3), device=G.dev())
+    base, y = wide[0, :, 1:n + 1], wide[1, :, 2:n + 2]
+    base.copy_(put(d["base"]))
+    X.exl3_lora(xb[:, pitch - k:], handle(d), put(d["rows"]), base, out=y)
+    check(y, d, True)
