@@ -6,9 +6,9 @@
 //   2. lora_expand  workgroup (segment, columns): h as two fp16 pieces against B, added
 //      to base.
 // A segment is up to 16 or 64 rows of one adapter, so that an adapter is read once for
-// as many rows.  Up to kLoraPlanRows rows every workgroup finds its own segment (two
-// passes over the rows' adapters in LDS, about a microsecond: less than a launch); more
-// are sorted into segments by a launch of one workgroup before (lora_plan).
+// as many rows.  Up to kLoraPlanRows rows lora_shrink's workgroups find their own segments
+// (two passes over the rows' adapters in LDS, about a microsecond) and leave them to
+// lora_expand; more are sorted by a launch of one workgroup before (lora_plan, 6 us).
 //
 // h is kept to 24 bits: a row's h is scaled by a power of two to below 2^15 and split
 // into fp16 pieces hi + lo (hi holds 11 bits, lo the next 11 and, down to 2^-40 of the
@@ -18,6 +18,8 @@
 
 namespace exl3 {
 
+// By workgroups / by lora_plan, us of a call 5120 -> 5120: 1024 rows 20.6 / 26, 2048 rows
+// 33.5 / 34.7 of 8 adapters and 38 to 46 / 40.5 of 256, 4096 rows 58.5 / 57.
 constexpr int kLoraPlanRows = 1024;
 constexpr int kLoraPlanThreads = 1024;
 constexpr int kLoraThreads = 256;
@@ -42,7 +44,8 @@ struct LoraArgs {
   int rpad;    // floats of a row of h
   int tiles;   // 64-column tiles of a wave (lora_expand) or a workgroup (lora_expand_long)
   // workspace
-  LoraSeg* segs;  // [segments at most]; null where workgroups find their own
+  int planned;    // segments are in the workspace before lora_shrink, not from it
+  LoraSeg* segs;  // [segments at most]
   int* order;     // [segments at most][rows of a segment]
   int* place;     // [m] a row's place among its adapter's, where registers do not hold it
   float* h;       // [splits][m][rpad]
@@ -153,54 +156,64 @@ __global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q, int mo
   }
 }
 
-// Segment z as the workgroup's task; false past the last.  lds: [adapters + 1].
+// Segment z from the workspace; false past the last.
+template <int S>
+__device__ __forceinline__ bool lora_read(const LoraArgs& q, int z, LoraTask& task) {
+  const int tid = threadIdx.x;
+  const int row = tid < S ? q.order[(int64_t)z * S + tid] : 0;
+  const LoraSeg sg = q.segs[z];
+  if (sg.count == 0) return false;
+  if (tid < S) {  // one wave: past count its first row
+    const int first = __builtin_amdgcn_readfirstlane(row);
+    task.row[tid] = tid < sg.count ? row : first;
+  }
+  if (tid == 0) {
+    task.adapter = sg.adapter;
+    task.count = sg.count;
+  }
+  __syncthreads();
+  return true;
+}
+
+// Segment z of up to 64 rows, found by every wave by itself, a row a lane.
+template <int S>
+__device__ __forceinline__ bool lora_ballots(const LoraArgs& q, int z, LoraTask& task) {
+  const int lane = threadIdx.x & 63;
+  const int bucket = lane < q.m ? lora_bucket(q, lane) : 0;
+  uint64_t same = lane < q.m ? ~0ull : 0ull;  // lanes of this lane's adapter
+  for (int bit = 0; (q.d.adapters >> bit) != 0; ++bit) {
+    const uint64_t set = __ballot(bucket >> bit & 1);
+    same &= bucket >> bit & 1 ? set : ~set;
+  }
+  same &= q.m == 64 ? ~0ull : (1ull << q.m) - 1;
+  const uint64_t before = (1ull << lane) - 1;
+  const int place = (int)__popcll(same & before);
+  const bool leads = lane < q.m && place % S == 0 && (bucket != q.d.adapters || q.copy);
+  const uint64_t leaders = __ballot(leads);
+  const uint64_t mine = __ballot(leads && (int)__popcll(leaders & before) == z);
+  if (mine == 0) return false;
+  const int lead = __ffsll((unsigned long long)mine) - 1;
+  const int b = __builtin_amdgcn_readlane(bucket, lead), first = __builtin_amdgcn_readlane(place, lead);
+  const uint64_t members = __ballot(lane < q.m && bucket == b);
+  const int left = (int)__popcll(members) - first, count = left < S ? left : S;
+  if ((members >> lane & 1) && place >= first && place < first + S) task.row[place - first] = lane;
+  if (lane >= count && lane < S) task.row[lane] = lead;
+  if (lane == 0) {
+    task.adapter = b == q.d.adapters ? -1 : b;
+    task.count = count;
+  }
+  __syncthreads();
+  return true;
+}
+
+// Segment z of up to kLoraPlanRows rows, found by the workgroup's W waves.  lds:
+// [adapters + 1].
 template <int S, int W>
-__device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, LoraTask& task) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (q.segs) {
-    const int row = tid < S ? q.order[(int64_t)z * S + tid] : 0;
-    const LoraSeg sg = q.segs[z];
-    if (sg.count == 0) return false;
-    if (tid < S) {  // one wave: past count its first row
-      const int first = __builtin_amdgcn_readfirstlane(row);
-      task.row[tid] = tid < sg.count ? row : first;
-    }
-    if (tid == 0) {
-      task.adapter = sg.adapter;
-      task.count = sg.count;
-    }
-    __syncthreads();
-    return true;
-  }
-  if (q.m <= 64) {  // every wave by itself, a row a lane
-    const int bucket = lane < q.m ? lora_bucket(q, lane) : 0;
-    uint64_t same = lane < q.m ? ~0ull : 0ull;  // lanes of this lane's adapter
-    for (int bit = 0; (q.d.adapters >> bit) != 0; ++bit) {
-      const uint64_t set = __ballot(bucket >> bit & 1);
-      same &= bucket >> bit & 1 ? set : ~set;
-    }
-    same &= q.m == 64 ? ~0ull : (1ull << q.m) - 1;
-    const uint64_t before = (1ull << lane) - 1;
-    const int place = (int)__popcll(same & before);
-    const bool leads = lane < q.m && place % S == 0 && (bucket != q.d.adapters || q.copy);
-    const uint64_t leaders = __ballot(leads);
-    const uint64_t mine = __ballot(leads && (int)__popcll(leaders & before) == z);
-    if (mine == 0) return false;
-    const int lead = __ffsll((unsigned long long)mine) - 1;
-    const int b = __builtin_amdgcn_readlane(bucket, lead), first = __builtin_amdgcn_readlane(place, lead);
-    const uint64_t members = __ballot(lane < q.m && bucket == b);
-    const int left = (int)__popcll(members) - first, count = left < S ? left : S;
-    if ((members >> lane & 1) && place >= first && place < first + S) task.row[place - first] = lane;
-    if (lane >= count && lane < S) task.row[lane] = lead;
-    if (lane == 0) {
-      task.adapter = b == q.d.adapters ? -1 : b;
-      task.count = count;
-    }
-    __syncthreads();
-    return true;
-  }
-  constexpr int kThreads = 64 * W, kEach = kLoraPlanRows / kThreads;
-  __shared__ int waves[W], found[2], chunk[kEach * W];
+__device__ __forceinline__ bool lora_search(const LoraArgs& q, int z, int* lds, LoraTask& task) {
+  constexpr int kThreads = 64 * W, kEach = kLoraPlanRows / kThreads, kChunks = kLoraPlanRows / 64;
+  static_assert(kChunks <= 64, "a chunk of rows a lane");
+  __shared__ int waves[W], found[2], chunk[kChunks];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int buckets = q.d.adapters + 1;
   int bucket[kEach];
 #pragma unroll
@@ -240,12 +253,19 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
     if (lane == 0) chunk[i * W + wave] = (int)__popcll(same[i]);
   }
   __syncthreads();
+  const int here = lane < kChunks ? chunk[lane] : 0;
+  int before = here;
+  for (int d = 1; d < kChunks; d *= 2) {
+    const int o = __shfl_up(before, d);
+    before += lane >= d ? o : 0;
+  }
+  before -= here;
   const int left = lds[b] - first, count = left < S ? left : S;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
+    const int place =
+        __builtin_amdgcn_readlane(before, i * W + wave) + (int)__popcll(same[i] & ((1ull << lane) - 1)) - first;
     if (bucket[i] != b) continue;
-    int place = (int)__popcll(same[i] & ((1ull << lane) - 1)) - first;
-    for (int c = 0; c < i * W + wave; ++c) place += chunk[c];
     if (place >= 0 && place < S) task.row[place] = i * kThreads + tid;
     if (place == 0)
       for (int p = count; p < S; ++p) task.row[p] = i * kThreads + tid;
@@ -258,6 +278,19 @@ __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, Lo
   return true;
 }
 
+// Segment z as the workgroup's task; false past the last.  Found here, it is left in the
+// workspace for lora_expand by one of the segment's workgroups.  lds: [adapters + 1].
+template <int S, int W>
+__device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, LoraTask& task) {
+  if (q.planned) return lora_read<S>(q, z, task);
+  const bool there = q.m <= 64 ? lora_ballots<S>(q, z, task) : lora_search<S, W>(q, z, lds, task);
+  if (blockIdx.y == 0 && blockIdx.z == 0) {
+    if (there && threadIdx.x < S) q.order[(int64_t)z * S + threadIdx.x] = task.row[threadIdx.x];
+    if (threadIdx.x == 0) q.segs[z] = there ? LoraSeg{task.adapter, task.count} : LoraSeg{0, 0};
+  }
+  return there;
+}
+
 __device__ __forceinline__ int lora_rank(const LoraArgs& q, int adapter) {
   if (!q.d.ranks) return q.d.rank;
   const int r = q.d.ranks[adapter];
@@ -268,7 +301,8 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& q, int adapter) {
 // shrink
 // ---------------------------------------------------------------------------
 // 16 rows against 16 RT ranks (from 64 blockIdx.z on); a wave takes whole lines of 64
-// k one after the other, lane (row or rank r, g) their places 16 g .. 16 g + 15.
+// k one after the other, lane (row or rank r, g) their places 16 g .. 16 g + 15.  64 rows
+// of 5120 and 64 adapters of rank 16, 11 MB, in 5.6 us: start, loads' latency and end.
 template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
   constexpr int MT = 1;
@@ -361,6 +395,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
 }
 
 // 64 rows against 64 ranks (from 64 blockIdx.z on), for rows that 32-bit offsets reach.
+// 4096 x 5120 of rank 64 in 18 us: 84 MB to LDS, 42 of them from memory, behind 4 us of
+// start and end.
 __global__ __launch_bounds__(kTile64Waves * 64) void lora_shrink_tiled(LoraArgs q) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
   __shared__ LoraTask task;
@@ -555,7 +591,10 @@ struct LoraIo {
 // loads of a wave's next tile go out before it waits for this one's.
 // CH: chunks of 32 ranks; 0: up to 16 ranks, where an operand's upper half of k holds
 // another 16 columns, met by pieces that are zero in the other half.
-// Workgroups a CU.
+// What bounds it is base, y and B: 64 rows 5120 -> 17408 of 64 adapters of rank 16, 40 MB
+// in 12.7 us (3.2 TB/s) where a workgroup's start, 4 us, counts.
+//
+// Workgroups a CU:
 __host__ __device__ constexpr int lora_expand_groups(int ch) { return ch == 0 ? 5 : ch == 1 ? 4 : ch == 2 ? 3 : 2; }
 
 template <int CH, class T, bool TINY>
@@ -577,7 +616,7 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
   const int first_tile = blockIdx.y * 4 * q.tiles + wave;
   const T* base = static_cast<const T*>(q.base);
   T* y = static_cast<T*>(q.y);
-  if (!lora_task<S, 4>(q, blockIdx.x, reinterpret_cast<int*>(smem), task)) return;
+  if (!lora_read<S>(q, blockIdx.x, task)) return;
   const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
   const int count = __builtin_amdgcn_readfirstlane(task.count);
   const int tiles = (N + 63) / 64;
@@ -625,7 +664,6 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
     load_base(tile, to.from);
   };
   load(first_tile, even);
-  __syncthreads();  // the segment's search is done with smem
   lora_pieces<S, kChunks>(q, task, rank, scale, smem, factor);
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem + 2 * S * kRow) + wave * (16 * kLoraOutStride);
@@ -705,7 +743,8 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
 // Up to 64 rows, 16 a wave, whose pieces stay in registers while tiles of 64 columns pass:
 // a tile's B goes from memory straight to LDS, two tiles ahead, and serves the four waves.
 // (Loaded by the lanes that multiply it, 16 rows an instruction, it comes at 16 bytes a
-// clock and CU, which for 64 ranks is as long as base and y take.)
+// clock and CU, which for 64 ranks is as long as base and y take.)  Bound by base and y:
+// 4096 rows, n 17408, rank 64, four adapters, 294 MB in 66 us (4.4 TB/s).
 //
 // LDS: a tile holds a row of 4 CH 16-byte pieces for each column; piece c of row n lies at
 // place c ^ turn(n), so that sixteen rows' pieces c cover all 64 banks.
@@ -734,7 +773,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
   const int end_tile = first_tile + q.tiles < tiles ? first_tile + q.tiles : tiles;
   const T* base = static_cast<const T*>(q.base);
   T* y = static_cast<T*>(q.y);
-  if (!lora_task<S, 4>(q, blockIdx.x, reinterpret_cast<int*>(smem), task)) return;
+  if (!lora_read<S>(q, blockIdx.x, task)) return;
   const int adapter = __builtin_amdgcn_readfirstlane(task.adapter);
   const int count = __builtin_amdgcn_readfirstlane(task.count);
   const int i0 = 16 * wave;
@@ -755,7 +794,6 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
   const int rank = lora_rank(q, adapter);
   const float scale = q.d.scales ? q.d.scales[adapter] : 1.f;
   const uint16_t* b = q.d.b + (int64_t)adapter * N * R;
-  __syncthreads();  // the segment's search is done with smem
   lora_pieces<S, CH>(q, task, rank, scale, smem, factor);
   __syncthreads();
   f16x8_t h[CH][2];
@@ -865,7 +903,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
 // A workgroup takes a row (blockIdx.y) and 8192 / RJ columns: it makes the row's whole h
 // itself (A from L2, which costs less than a launch) and then its columns, RJ / 8 threads
 // a column.  RJ: a power of two >= rank.  A wave takes 8 ranks of every 512 k from its
-// place on.
+// place on.  One row 5120 -> 17408 of rank 16, 0.8 MB, in 6.2 us: latency, first of A and
+// x, then of the sums' way through LDS.
 constexpr int kLoraFewThreads = 1024;
 
 template <int RJ, class T>
@@ -944,6 +983,10 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 int lora_few_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : 64; }
 
+// One launch while a round of workgroups holds it and the A that each reads is short (us,
+// one launch / two, 16 adapters): 5120 -> 17408 of rank 16, 1 row 6.2 / 8.9, 4 6.4 / 9.5, 8
+// (272 workgroups) 11.2 / 9.9; of rank 32, 1 row 7.0 / 8.5; of rank 64 (655 KB) 9.9 / 9.9;
+// 17408 -> 5120 of rank 16 (557 KB), 8 rows 12.0 / 10.6; 2048 -> 512, 64 rows 5.2 / 8.9.
 bool lora_is_few(const LoraDesc& d, int64_t m) {
   if (d.rank > kLoraFewRank || m > 256) return false;
   const int64_t cols = kLoraFewThreads * 8 / lora_few_rank(d.rank);
@@ -952,7 +995,10 @@ bool lora_is_few(const LoraDesc& d, int64_t m) {
 }
 
 // 64 rows a segment where adapters have more than 16 each on average, enough of them for
-// the chip and 32-bit offsets for the copies to LDS.
+// the chip and 32-bit offsets for the copies to LDS.  Segments of 64 / of 16 rows, us,
+// 5120 -> 17408 of rank 64: 256 rows of one adapter 23.6 / 20.4, 512 27.2 / 28.6, 1024 rows
+// of 16 adapters 44 / 57, of 63 83 / 87, of 128 133 / 131, 4096 rows of 64 128 / 211, of 200
+// 269 / 252; 5120 -> 5120 of rank 16: 512 rows of 8 19.4 / 18.4, 4096 of 64 47 / 58.
 bool lora_long(const LoraDesc& d, int64_t m, int64_t ldx) {
   return m >= 512 && d.n >= 8 && m > 16 * (int64_t)d.adapters && m * ldx < (int64_t)1 << 31;
 }
@@ -963,9 +1009,14 @@ int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
   return most < m ? most : m;
 }
 
+// Segments of 64 rows that may be expected: of each adapter the last is half full.
+int64_t lora_long_segs(const LoraDesc& d, int64_t m) { return (m + 63) / 64 + d.adapters / 2; }
+
 int lora_splits(const LoraDesc& d, int64_t m, bool longer) {
-  // of 64 rows, a workgroup fills a CU; every share is read again by all that expand
-  const int64_t segs = longer ? (m + 63) / 64 : lora_most_segs(d, m, false);
+  // of 64 rows, a workgroup fills a CU (a second round costs more than longer shares: 4096
+  // rows of four adapters in 3 shares 19 us, in 2 22, in 7 23); every share is read again by
+  // all that expand
+  const int64_t segs = longer ? lora_long_segs(d, m) : lora_most_segs(d, m, false);
   const int64_t groups = segs * ((d.rank + 63) / 64);
   const int64_t want = (longer ? 256 : 512) / groups, most = (d.k + 511) / 512;
   const int64_t s = want < most ? want : most, cap = longer ? 4 : 16;
@@ -979,7 +1030,7 @@ LoraLayout lora_layout(const LoraDesc& d, int64_t m, bool longer) {
   LoraLayout L;
   size_t off = 0;
   const bool planned = m > kLoraPlanRows;
-  const size_t most = planned ? (size_t)lora_most_segs(d, m, longer) : 0;
+  const size_t most = (size_t)lora_most_segs(d, m, longer);
   L.segs = off;
   off += align256(most * sizeof(LoraSeg));
   L.order = off;
@@ -1005,9 +1056,7 @@ void launch_few(const LoraArgs& q, hipStream_t s) {
 
 template <int CH, bool TINY = false>
 void launch_expand(LoraArgs q, bool f32, hipStream_t s) {
-  const size_t plan = (size_t)(q.d.adapters + 1) * 4;
-  const size_t need = 2 * 16 * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
-  const size_t lds = need > plan ? need : plan;
+  const size_t lds = 2 * 16 * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
   const int64_t segs = lora_most_segs(q.d, q.m, false), tiles = (q.d.n + 63) / 64;
   // one round of workgroups: each begins with the segment's search and its h, 4 us
   const int64_t slots = 256 * lora_expand_groups(CH);
@@ -1019,10 +1068,9 @@ void launch_expand(LoraArgs q, bool f32, hipStream_t s) {
 }
 
 template <int CH>
-void launch_expand_long(const LoraArgs& q, bool f32, dim3 grid, size_t plan, hipStream_t s) {
+void launch_expand_long(const LoraArgs& q, bool f32, dim3 grid, hipStream_t s) {
   size_t lds = kLoraRing * 4096 * CH + 4 * 16 * kLoraOutStride * 4;
   if (const size_t pieces = 2 * 64 * lora_piece_row(CH); lds < pieces) lds = pieces;
-  if (lds < plan) lds = plan;
   if (f32) hipLaunchKernelGGL((lora_expand_long<CH, float>), grid, dim3(kLoraThreads), lds, s, q);
   else hipLaunchKernelGGL((lora_expand_long<CH, _Float16>), grid, dim3(kLoraThreads), lds, s, q);
 }
@@ -1037,15 +1085,18 @@ void launch_segments(LoraArgs q, bool longer, bool f32, hipStream_t s) {
   else hipLaunchKernelGGL((lora_shrink<4>), shrink, block, plan, s, q);
   const int64_t tiles = (q.d.n + 63) / 64;
   if (longer) {
-    // a round of workgroups, as many as LDS holds
-    const int64_t slots = 256 * (q.d.rank <= 64 ? 3 : q.d.rank <= 128 ? 2 : 1);
-    const int64_t each = (q.m / 64 * tiles + slots - 1) / slots;
+    // a round of workgroups, as many as LDS holds: shorter ones begin, with their h, too
+    // often (4096 rows 5120 -> 17408 of rank 64 of four adapters 93 us, of half as many
+    // tiles a workgroup 97, of a quarter 108)
+    const int64_t slots = 256 * (q.d.rank <= 32 ? 5 : q.d.rank <= 64 ? 3 : q.d.rank <= 128 ? 2 : 1);
+    const int64_t segs = lora_long_segs(q.d, q.m), groups = slots > segs ? slots / segs : 1;
+    const int64_t each = (tiles + groups - 1) / groups;
     q.tiles = (int)(each < 4 ? 4 : each);
     const dim3 grid(gx, (uint32_t)((tiles + q.tiles - 1) / q.tiles));
-    if (q.d.rank <= 32) launch_expand_long<1>(q, f32, grid, plan, s);
-    else if (q.d.rank <= 64) launch_expand_long<2>(q, f32, grid, plan, s);
-    else if (q.d.rank <= 128) launch_expand_long<4>(q, f32, grid, plan, s);
-    else launch_expand_long<8>(q, f32, grid, plan, s);
+    if (q.d.rank <= 32) launch_expand_long<1>(q, f32, grid, s);
+    else if (q.d.rank <= 64) launch_expand_long<2>(q, f32, grid, s);
+    else if (q.d.rank <= 128) launch_expand_long<4>(q, f32, grid, s);
+    else launch_expand_long<8>(q, f32, grid, s);
     return;
   }
   if (q.d.n < (f32 ? 4 : 8)) launch_expand<8, true>(q, f32, s);
@@ -1089,10 +1140,11 @@ hipError_t launch_lora(const LoraDesc& d, const uint16_t* x, int64_t m, int64_t 
   q.splits = lora_splits(d, m, longer);
   q.rpad = (d.rank + 15) / 16 * 16;
   q.h = reinterpret_cast<float*>(w + L.h);
-  if (m > kLoraPlanRows) {
-    q.segs = reinterpret_cast<LoraSeg*>(w + L.segs);
-    q.order = reinterpret_cast<int*>(w + L.order);
-    q.place = reinterpret_cast<int*>(w + L.place);
+  q.segs = reinterpret_cast<LoraSeg*>(w + L.segs);
+  q.order = reinterpret_cast<int*>(w + L.order);
+  q.place = reinterpret_cast<int*>(w + L.place);
+  q.planned = m > kLoraPlanRows;
+  if (q.planned) {
     const size_t lds = 2 * (size_t)(d.adapters + 1) * 4;
     const int most = (int)lora_most_segs(d, m, longer);
     if (longer) hipLaunchKernelGGL((lora_plan<64>), dim3(1), dim3(kLoraPlanThreads), lds, s, q, most);

@@ -571,7 +571,8 @@ typedef enum exl3_group_score {
  *   topk_groups  1..groups
  * Without a balance logits are compared as they are.  With one, and for
  * EXL3_GROUP_TOP2, values are computed in 64 bits and compared to 42 significant
- * bits, so that choices do not depend on how 32 bits would have rounded.
+ * bits (scores below 10^-300 to fewer), so that choices do not depend on how 32 bits
+ * would have rounded.
  * A NaN value counts as the lowest, so the ids are always valid and a token's are
  * distinct.  Weights are what the formulas give: softmax of a token with a NaN or
  * +infinite logit, or with -infinite ones only, is NaN throughout; a -infinite logit
@@ -628,8 +629,8 @@ size_t exl3_router_linear_workspace_size(const exl3_router_weight* w, int64_t t)
 exl3_status exl3_router_linear(const exl3_router_weight* w, const void* x, int64_t t, int64_t ldx, float* logits,
                                int64_t ldl, void* ws, size_t ws_bytes, exl3_stream_t stream);
 
-/* Bytes of device workspace exl3_router needs (0 if the arguments are invalid);
- * logits: not 0 if the call is given memory for them. */
+/* Bytes of device workspace exl3_router needs (0 if none is needed, or the arguments
+ * are invalid); logits: not 0 if the call is given memory for them. */
 size_t exl3_router_workspace_size(const exl3_router_weight* w, int64_t t, int32_t logits);
 
 /* exl3_router - exl3_router_linear and exl3_route_topk of its logits in one call (one
