@@ -555,6 +555,7 @@ def _refuse(what: str):
 # look up each time is kept here, since an import inside a function costs 0.2 us.
 _dtype_codes = {}    # torch dtype -> EXL3_F16, EXL3_F32
 _cuda_queries = []   # current device, current stream of a device
+_number_types = []   # torch.int32, torch.float32 (from the first _place on)
 _shape = operator.attrgetter("shape")
 
 
@@ -567,6 +568,7 @@ def _place(t, what: str, stream):
         _refuse(f"{what} is not on a GPU")
     if not _cuda_queries:
         import torch
+        _number_types[:] = (torch.int32, torch.float32)
         _cuda_queries.extend((torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream))
     if i != _cuda_queries[0]():
         _refuse(f"{what} is on GPU {i}, not on the current device")
@@ -998,17 +1000,19 @@ class Exl3RouteRule(_Record):
 
 def _choices(rule: Exl3RouteRule, t: int, topk_ids, topk_weights, device: int, stream):
     """The tensors that take the choices (new ones where none are given), checked."""
-    import torch
+    int32, float32 = _number_types
     if rule.balance is not None and rule.balance.get_device() != device:
         _refuse("the balance is on another device than the operands")
     shape = (t, rule.topk)
+    if topk_ids is None or topk_weights is None:
+        import torch
     if topk_ids is None:
-        topk_ids = _new(torch.empty, shape, torch.int32, device, stream)
-    elif _tensor(topk_ids, "topk_ids", torch.int32, shape).get_device() != device:
+        topk_ids = _new(torch.empty, shape, int32, device, stream)
+    elif _tensor(topk_ids, "topk_ids", int32, shape).get_device() != device:
         _refuse("topk_ids is on another device than the operands")
     if topk_weights is None:
-        topk_weights = _new(torch.empty, shape, torch.float32, device, stream)
-    elif _tensor(topk_weights, "topk_weights", torch.float32, shape).get_device() != device:
+        topk_weights = _new(torch.empty, shape, float32, device, stream)
+    elif _tensor(topk_weights, "topk_weights", float32, shape).get_device() != device:
         _refuse("topk_weights is on another device than the operands")
     return topk_ids, topk_weights
 
@@ -1139,13 +1143,12 @@ def exl3_lora(x, lora: Exl3Lora, rows, base=None, out_dtype=None, out=None, work
     """y [m, n] = base + scale_a B_a (A_a x) with a = rows[i] (int32 [m]) for row i;
     rows whose value is no adapter (-1) get base, or zeros without one.  x fp16 [m, k],
     base and y of one type, fp16 or fp32.  `out=base` adds in place."""
-    import torch
     record = lora._now()
     m, ldx = _f16_rows(x, record.k)
     device, on = _place(x, "x", stream)
     if lora.a.get_device() != device:
         _refuse("x and the adapters are on different devices")
-    if _tensor(rows, "rows", torch.int32, (m,)).get_device() != device:
+    if _tensor(rows, "rows", _number_types[0], (m,)).get_device() != device:
         _refuse("rows is on another device than x")
     if out_dtype is None and base is not None:
         out_dtype = base.dtype
