@@ -347,3 +347,45 @@ def test_lora_many_rows_past_32_bits(past):
     base.copy_(put(d["base"]))
     X.exl3_lora(xb[:, pitch - k:], handle(d), put(d["rows"]), base, out=y)
     check(y, d, True)
+
+
+@pytest.mark.parametrize("m", [300, 700, 1100])
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128, 256])
+def test_lora_bad_weights_stay_in_their_columns(m, rank):
+    """NaN and infinities in single elements of B, next to and 16 columns away from sound
+    ones, and in single ranks of A."""
+    d = case(m, 136, 150, rank, 5, f32=True, rows=np.arange(m) % 5, none=0)
+    d["b"][0, 17, 0], d["b"][0, 40, rank - 1], d["b"][0, 149, 3] = np.inf, np.nan, -np.inf
+    d["b"][1, 0, :], d["b"][1, 64, 5] = np.nan, np.inf
+    d["b"][2, ::7, rank // 2] = np.inf
+    d["a"][3, rank - 1, 135] = -np.inf
+    d["a"][4, 0, 0], d["b"][4, 33, 0] = np.inf, 0
+    check(call(d, True), d, True)
+
+
+@pytest.mark.parametrize("m", [70, 600, 1500])
+def test_lora_graphs_take_rows_as_they_are(m):
+    """A captured call finds its segments anew at every replay: same bits as eager calls."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    d = case(m, 264, 200, 24, 9, f32=True)
+    lora, x, rows, base = handle(d), G.to_dev(d["x"]), G.to_dev(d["rows"]), G.to_dev(d["base"])
+    ws = [torch.full((X.exl3_lora_workspace_size(lora, m),), 255, dtype=torch.uint8, device=G.dev()) for _ in range(2)]
+    y, z = torch.empty_like(base), torch.empty_like(base)
+    X.exl3_lora(x, lora, rows, base, out=y, workspace=ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        X.exl3_lora(x, lora, rows, base, out=y, workspace=ws[0])
+    rng = np.random.default_rng(m)
+    for order in ("one", "turns", "none", "runs", "few", "lonely"):
+        d["rows"] = ORDERS[order](m, 9).astype(np.int32)
+        d["x"] = rng.standard_normal(d["x"].shape).astype(np.float16)
+        rows.copy_(G.to_dev(d["rows"]))
+        x.copy_(G.to_dev(d["x"]))
+        y.fill_(-3)
+        graph.replay()
+        X.exl3_lora(x, lora, rows, base, out=z, workspace=ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(y, z), order
+        check(y, d, True, order)
