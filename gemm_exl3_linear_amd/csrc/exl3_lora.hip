@@ -478,6 +478,7 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
                                             uint8_t* lds, float* factor) {
   constexpr int kEach = kLoraThreads / S;  // threads of a row
   constexpr int kMost = (8 * CHUNKS + kEach - 1) / kEach;
+  constexpr int kAtOnce = kMost == 1 ? 8 : 4;  // shares whose loads go out together
   constexpr int stride = lora_piece_row(CHUNKS);
   const int row = threadIdx.x / kEach, part = threadIdx.x % kEach;
   float4_t h[kMost];
@@ -488,13 +489,13 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
     h[i] = float4_t{0.f, 0.f, 0.f, 0.f};
     if (row < task.count && at < q.rpad) {
       const float* p = q.h + (int64_t)task.row[row] * q.rpad + at;
-      for (int s = 0; s < q.splits; s += 4) {  // four shares' loads at a time
-        float4_t v[4];
+      for (int s = 0; s < q.splits; s += kAtOnce) {
+        float4_t v[kAtOnce];
 #pragma unroll
-        for (int o = 0; o < 4; ++o)
+        for (int o = 0; o < kAtOnce; ++o)
           v[o] = *reinterpret_cast<const float4_t*>(p + (int64_t)(s + o < q.splits ? s + o : s) * q.m * q.rpad);
 #pragma unroll
-        for (int o = 0; o < 4; ++o)
+        for (int o = 0; o < kAtOnce; ++o)
           if (s + o < q.splits) h[i] += v[o];
       }
     }
