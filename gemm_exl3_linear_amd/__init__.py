@@ -581,6 +581,8 @@ def _place(t, what: str, stream):
 
 def _tensor(t, what: str, dtype, shape):
     """t, checked: dtype, shape (None entries are free), contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     if t.dtype != dtype:
         _refuse(f"{what} is {t.dtype}, not {dtype}")
     if t.shape != shape and (t.dim() != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape))):
@@ -930,7 +932,7 @@ class _Record:
         """The record of the tensors as they are: checked and read again if their
         memory or shape was changed under them (`.data =`, set_, resize_)."""
         parts, data_ptr = self._parts
-        if (list(map(data_ptr, parts)), list(map(_shape, parts))) != self._seen:
+        if parts and (list(map(data_ptr, parts)), list(map(_shape, parts))) != self._seen:
             self.__post_init__()
         return self._record
 
