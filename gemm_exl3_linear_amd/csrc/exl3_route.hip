@@ -75,15 +75,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_parts_kernel(RouteRule
       if (there && parts.logits) parts.logits[row * parts.ldl + e + j] = l[i + j];
     }
   }
-  const auto logit = [&](int e) {
-    float sum = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < parts.splits; ++k) sum += p[k * step + e];
-    return parts.bias ? sum + parts.bias[e] : sum;
-  };
   int id;
   float weight;
-  route_token<64, VPL, K>(q, l, lane, lds + wave, logit, id, weight);
+  route_token<64, VPL, K>(q, l, lane, lds + wave, [&](int e) { return route_held<VPL>(l, e); }, id, weight);
   if (lane < q.topk) {
     ids[row * q.topk + lane] = id;
     weights[row * q.topk + lane] = weight;

