@@ -576,7 +576,9 @@ typedef enum exl3_group_score {
  * A NaN value counts as the lowest, so the ids are always valid and a token's are
  * distinct.  Weights are what the formulas give: softmax of a token with a NaN or
  * +infinite logit, or with -infinite ones only, is NaN throughout; a -infinite logit
- * next to finite ones has the score 0, for sigmoid too. */
+ * next to finite ones has the score 0, for sigmoid too.  They are fp32: a score below
+ * 2^-125 is held to 2^-17 of itself, one below 2^-128 is 0 for sigmoid, and weights
+ * divided by a sum of 0 are NaN. */
 typedef struct exl3_route_rule {
     const float* balance;
     int32_t experts;
