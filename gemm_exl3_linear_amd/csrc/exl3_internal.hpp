@@ -178,7 +178,6 @@ struct RouteParts {
   int64_t ldl;
 };
 constexpr int64_t kRouteFew = 2048;  // tokens that are routed by a wave each
-// t <= kRouteFew
 hipError_t launch_route_parts(const RouteRule& q, const RouteParts& parts, int64_t t, int32_t* ids, float* weights,
                               hipStream_t s);
 struct RouterDesc {

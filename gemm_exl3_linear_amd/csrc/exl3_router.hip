@@ -10,6 +10,7 @@ constexpr int kRouterRows = 16;     // of an operand
 constexpr int kRouterCounts = 128;  // arrival counts at the head of a workspace: one a group of 16 experts, and the
                                     // routing's
 constexpr int kRouterWaves = 8;
+constexpr int kRouterShares = 16;  // of k at most
 
 struct RouterArgs {
   RouterDesc d;
@@ -134,12 +135,14 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
 __global__ __launch_bounds__(kTile64Waves * 64) void router_gemm_kernel(RouterArgs q) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
   // a row tile's workgroups run on one XCD (workgroup i on XCD i % 8), one behind the
-  // other, so that x comes from memory once
-  const int across = (q.d.experts + kTile64 - 1) / kTile64;
-  const int64_t j = blockIdx.x >> 3;
-  const int64_t row0 = ((j / across) * 8 + (blockIdx.x & 7)) * kTile64;
-  const int e0 = (int)(j % across) * kTile64;
-  if (row0 >= q.t) return;
+  // other, so that x comes from memory once; those of the last down % 8 row tiles as they
+  // come, with no empty one between (which would hold a CU's LDS for a microsecond)
+  const uint32_t across = (q.d.experts + kTile64 - 1) / kTile64, down = gridDim.x / across, whole8 = down / 8 * 8;
+  const uint32_t rest = blockIdx.x - whole8 * across;  // wraps before them
+  const bool last = blockIdx.x >= whole8 * across;
+  const uint32_t j = blockIdx.x >> 3;
+  const int64_t row0 = (int64_t)(last ? whole8 + rest % (down - whole8) : j / across * 8 + (blockIdx.x & 7)) * kTile64;
+  const int e0 = (int)(last ? rest / (down - whole8) : j % across) * kTile64;
   const int rows = (int)(q.t - row0 < kTile64 ? q.t - row0 : kTile64);
   const int cols = q.d.experts - e0 < kTile64 ? q.d.experts - e0 : kTile64;
   const uint32_t hidden = (uint32_t)q.d.hidden;
@@ -205,25 +208,25 @@ bool router_fused(const RouterDesc& d, int64_t t) {
 }
 
 // The cut by estimates in us, fitted to kernels alone, and measured where they meet
-// (tokens x hidden x experts, by rows / tiled): 64 x 5120 x 256 11.0 / 9.5 (of 8), 512
-// 20.6 / 11.4, 4096 142 / 20.5; 1024 x 2048 x 64 6.8 / 8.4, 2048 9.8 / 8.4; 333 x 1440 x
-// 60 4.3 / 7.4.
+// (tokens x hidden x experts, by rows / tiled, shares in brackets): 64 x 5120 x 256 8.0
+// (8) / 8.8 (8), 256 13.1 (1) / 9.6 (8), 1000 38 (1) / 13.9 (4); 17 x 5120 x 1000 9.4 (4) /
+// 8.4 (8), 512 74 (1) / 21 (2); 1000 x 2048 x 60 7.2 (1) / 9.0 (8), 2000 10.6 (1) / 9.2 (1).
 RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx, RouterJoin join) {
   const int64_t groups = (d.experts + 15) / 16, rows = (t + kRouterRows - 1) / kRouterRows;
   const auto joined = [&](int splits) {
     if (splits == 1) return 0.0;
     if (join == RouterJoin::kFused) return 0.3 * splits;
-    if (join == RouterJoin::kRouted) return 0.3 + splits * (double)t * d.experts * 8 / 4.5e6;
-    return t <= kRouterRows ? 1.0 + 0.1 * splits : 4.5 + splits * (double)t * d.experts * 8 / 4.5e6;
+    const double moved = splits * (double)t * d.experts * 8 / 4.5e6;
+    if (join == RouterJoin::kRouted)  // many tokens are else routed by 16 lanes each
+      return 0.3 + 0.15 * splits + 0.002 * d.experts + moved + (t > kRouteFew ? 1e-3 * t : 0.0);
+    return t <= kRouterRows ? 1.0 + 0.1 * splits : 4.5 + moved;
   };
-  // many tokens are routed from whole logits
-  const int most = join == RouterJoin::kRouted && t > kRouteFew ? 1 : 16;
   RouterCut best{false, 1};
   double cost = 1e30;
   // by rows: 16 bytes a clock and CU of operands that are loaded as they are multiplied,
   // 9.6 TB/s of all; shares of 256 k at least, a load a wave
   const double all = groups * rows * 64.0 * d.hidden / 9.6e6;
-  for (int splits = 1; splits <= most && (splits == 1 || splits * 256 <= d.hidden); splits *= 2) {
+  for (int splits = 1; splits <= kRouterShares && (splits == 1 || splits * 256 <= d.hidden); splits *= 2) {
     const double lone = 1.7 / 1024 * d.hidden / splits;
     const double c = 2.5 + (lone > all ? lone : all) + joined(splits);
     if (c < cost) {
@@ -236,7 +239,7 @@ RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx, RouterJoin joi
   // share is all latency
   const int64_t tiles = (t + kTile64 - 1) / kTile64 * ((d.experts + kTile64 - 1) / kTile64);
   const int stages = (d.hidden + kTile64K - 1) / kTile64K;
-  for (int splits = 1; splits <= most && (splits == 1 || splits * kTile64Ring <= stages); splits *= 2) {
+  for (int splits = 1; splits <= kRouterShares && (splits == 1 || splits * kTile64Ring <= stages); splits *= 2) {
     const double rounds = (double)((tiles * splits + 255) / 256);
     const double c = 3.0 + 0.36 * ((stages + splits - 1) / splits) * rounds + joined(splits);
     if (c < cost) {
@@ -287,7 +290,7 @@ bool launch_product(RouterArgs& q, RouterJoin join, hipStream_t s) {
   q.splits = cut.splits;
   if (cut.tiled) {
     const int64_t down = (q.t + kTile64 - 1) / kTile64, across = (q.d.experts + kTile64 - 1) / kTile64;
-    const dim3 grid((uint32_t)((down + 7) / 8 * 8 * across), (uint32_t)q.splits);
+    const dim3 grid((uint32_t)(down * across), (uint32_t)q.splits);
     hipLaunchKernelGGL(router_gemm_kernel, grid, dim3(kTile64Waves * 64), 0, s, q);
     return q.splits > 1;
   }

@@ -413,3 +413,37 @@ def test_router_of_rows_past_32_bits():
         check(ids, wt, got.astype(np.float64), rule)
         ids2, _ = X.exl3_route_topk(logits[:n], rule)
         assert torch.equal(ids, ids2)
+
+
+@pytest.mark.parametrize("t,hidden,experts", [(17, 8192, 1000), (33, 5120, 512), (70, 5120, 1000), (130, 8192, 256),
+                                              (450, 5120, 300), (577, 5120, 1000), (1025, 4104, 130)])
+def test_router_shares_of_a_few_tiles(t, hidden, experts):
+    """Row tiles that are no multiple of eight, in several shares: logits, and routed."""
+    import gemm_exl3_linear_amd as X
+    x, w, c = router_case(t, hidden, experts, True, seed=3)
+    r, rule, xd = handle(w, c), rule_of(experts, 5), G.to_dev(x)
+    ref, mag = S.logits(x, w, c)
+    got = X.exl3_router_linear(xd, r).cpu().numpy()
+    assert (np.abs(got - ref) <= logit_bound(mag, hidden)).all()
+    logits = G.to_dev(np.full((t, experts), np.nan, dtype=np.float32))
+    ids, wt = X.exl3_router(xd, r, rule, logits=logits)
+    got = logits.cpu().numpy()
+    assert (np.abs(got - ref) <= logit_bound(mag, hidden)).all()
+    check(ids, wt, got.astype(np.float64), rule)
+    ids2, wt2 = X.exl3_router(xd, r, rule)
+    assert (ids == ids2).all() and (wt == wt2).all()
+
+
+def test_router_many_tokens_in_shares():
+    """More tokens than are else routed by a wave each, from shares of k."""
+    import gemm_exl3_linear_amd as X
+    x, w, c = router_case(4000, 5120, 60, True, seed=3)
+    r, xd = handle(w, c), G.to_dev(x)
+    rule = rule_of(60, 4, np.random.default_rng(4).standard_normal(60) * 0.1, scoring="sigmoid", groups=4,
+                   topk_groups=2, group_score="top2")
+    logits = G.to_dev(np.full((4000, 60), np.nan, dtype=np.float32))
+    ids, wt = X.exl3_router(xd, r, rule, logits=logits)
+    ref, mag = S.logits(x, w, c)
+    got = logits.cpu().numpy()
+    assert (np.abs(got - ref) <= logit_bound(mag, 5120)).all()
+    check(ids, wt, got.astype(np.float64), rule)
