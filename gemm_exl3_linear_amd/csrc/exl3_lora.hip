@@ -143,6 +143,7 @@ __global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q, int mo
   const auto put = [&](int64_t row, int b, int p) {
     const bool none = b == q.d.adapters;
     if (none && !q.copy) return;
+    if ((uint32_t)p >= (uint32_t)rows[b]) return;  // as in lora_read
     const int z = segs[b] + p / S, left = rows[b] - p;
     q.order[(int64_t)z * S + p % S] = (int)row;
     if (p % S == 0) q.segs[z] = LoraSeg{none ? -1 : b, left < S ? left : S};
@@ -156,23 +157,26 @@ __global__ __launch_bounds__(kLoraPlanThreads) void lora_plan(LoraArgs q, int mo
   }
 }
 
-// Segment z from the workspace; false past the last.
+// Segment z from the workspace; false past the last.  What is read there is held to the
+// rows and adapters that exist: a workspace that another stream writes meanwhile gives
+// wrong results, but leads nowhere else.
 template <int S>
 __device__ __forceinline__ bool lora_read(const LoraArgs& q, int z, LoraTask& task) {
   const int tid = threadIdx.x;
-  const int row = tid < S ? q.order[(int64_t)z * S + tid] : 0;
-  const LoraSeg sg = q.segs[z];
-  if (sg.count == 0) return false;
   if (tid < S) {  // one wave: past count its first row
+    const uint32_t at = (uint32_t)q.order[(int64_t)z * S + tid];
+    const LoraSeg sg = q.segs[z];
+    const int row = at < (uint32_t)q.m ? (int)at : 0;
+    const int count = (uint32_t)sg.count <= (uint32_t)S ? sg.count : S;
     const int first = __builtin_amdgcn_readfirstlane(row);
-    task.row[tid] = tid < sg.count ? row : first;
-  }
-  if (tid == 0) {
-    task.adapter = sg.adapter;
-    task.count = sg.count;
+    task.row[tid] = tid < count ? row : first;
+    if (tid == 0) {
+      task.adapter = (uint32_t)sg.adapter < (uint32_t)q.d.adapters ? sg.adapter : -1;
+      task.count = count;
+    }
   }
   __syncthreads();
-  return true;
+  return task.count != 0;
 }
 
 // Segment z of up to 64 rows, found by every wave by itself, a row a lane.
