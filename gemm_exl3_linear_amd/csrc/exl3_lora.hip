@@ -1017,15 +1017,28 @@ int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
 // Segments of 64 rows that may be expected: of each adapter the last is half full.
 int64_t lora_long_segs(const LoraDesc& d, int64_t m) { return (m + 63) / 64 + d.adapters / 2; }
 
+// Shares of k: workgroups for the chip against what each share costs lora_expand, which
+// adds them, the more the longer h is.  Fitted to 744 shapes of 8 to 2048 rows, rank 8 to
+// 256, k 2048 to 17408 and 1 to 64 adapters, at most 18 % from their best (us, shares in
+// brackets, 5120 -> 5120: 333 rows of 8 adapters of rank 16 15.4 (4), 13.7 (8), 16.6 (16); 64
+// rows of rank 256 27 (2), 22 (4), 28 (16); 17408 -> 5120, 600 rows of rank 8 26 (4), 21 (8),
+// 600 of rank 256 45 (4), 56 (8)).
 int lora_splits(const LoraDesc& d, int64_t m, bool longer) {
-  // of 64 rows, a workgroup fills a CU (a second round costs more than longer shares: 4096
-  // rows of four adapters in 3 shares 19 us, in 2 22, in 7 23); every share is read again by
-  // all that expand
-  const int64_t segs = longer ? lora_long_segs(d, m) : lora_most_segs(d, m, false);
-  const int64_t groups = segs * ((d.rank + 63) / 64);
-  const int64_t want = (longer ? 256 : 512) / groups, most = (d.k + 511) / 512;
-  const int64_t s = want < most ? want : most, cap = longer ? 4 : 16;
-  return (int)(s < 1 ? 1 : s > cap ? cap : s);
+  const int64_t ranks = (d.rank + 63) / 64;
+  int64_t s, most, cap;
+  if (longer) {
+    // a workgroup fills a CU, and a second round costs more than longer shares (4096 x 5120
+    // of four adapters of rank 64: 19 us in 3 shares, 22 in 2, 23 in 7)
+    s = 256 / (lora_long_segs(d, m) * ranks);
+    most = ranks == 1 ? (d.k < 8192 ? 4 : d.k / 2048) : (d.k < 8192 ? 2 : d.k / 4096);
+    cap = ranks == 1 ? 8 : 4;
+  } else {
+    s = (ranks == 1 ? 1024 : 2048) / (lora_most_segs(d, m, false) * ranks);
+    most = ranks == 1 ? (d.k + 639) / 640 : (d.k + 511) / 512;
+    cap = ranks == 1 ? 16 : 8;
+  }
+  most = most < cap ? most : cap;
+  return (int)(s < 1 ? 1 : s < most ? s : most);
 }
 
 struct LoraLayout {
