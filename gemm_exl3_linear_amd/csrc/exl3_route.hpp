@@ -298,7 +298,8 @@ __device__ __forceinline__ uint64_t route_groups(const RouteRule& q, const doubl
 }
 
 // l[i] is the logit of the lane's i-th expert (any value past the experts); logit(e) gives
-// expert e's again.  Lane s ends with choice s and its weight.
+// expert e's again, and is asked for experts alone.  Lane s < topk ends with choice s and
+// its weight.
 template <int LANES, int VPL, int K, class Logit>
 __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL], int lane,
                                             RouteLds<LANES, VPL>* lds, const Logit& logit, int& id, float& weight) {
@@ -411,7 +412,8 @@ __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL],
 #pragma unroll
   for (int s = 1; s < K; ++s) mine = lane == s ? top[s] : mine;
   id = (int)route_place(mine);
-  const float chosen = q.balance ? logit(id) : (float)route_value(mine);
+  // (a lane past the choices may hold no expert's key, whose place is any)
+  const float chosen = q.balance ? logit(lane < q.topk ? id : 0) : (float)route_value(mine);
   weight = softmax ? exp_f(chosen - high) / total : sigmoid_f(chosen);
   if (q.renormalize) weight = weight / route_all<LANES>(lane < q.topk ? weight : 0.f, sum_f);
   weight *= q.scale;
