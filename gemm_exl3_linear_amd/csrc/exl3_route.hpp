@@ -54,20 +54,34 @@ __device__ __forceinline__ double route_value(double key) {
 // ---------------------------------------------------------------------------
 typedef uint32_t u32pair_t __attribute__((ext_vector_type(2)));
 
-// The value of the lane N places on in its row of 16.
-template <int N>
-__device__ __forceinline__ uint32_t row_turn(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, true);
+// The value of another lane of the same row of 16.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
-template <int N>
-__device__ __forceinline__ float row_turn(float v) {
-  return __uint_as_float(row_turn<N>(__float_as_uint(v)));
+template <int CTRL>
+__device__ __forceinline__ float row_move(float v) {
+  return __uint_as_float(row_move<CTRL>(__float_as_uint(v)));
 }
-template <int N>
-__device__ __forceinline__ double row_turn(double v) {
+template <int CTRL>
+__device__ __forceinline__ double row_move(double v) {
   const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint64_t lo = row_turn<N>((uint32_t)b), hi = row_turn<N>((uint32_t)(b >> 32));
+  const uint64_t lo = row_move<CTRL>((uint32_t)b), hi = row_move<CTRL>((uint32_t)(b >> 32));
   return __longlong_as_double((long long)(hi << 32 | lo));
+}
+// Of the lane N places on in the row.
+template <int N, class T>
+__device__ __forceinline__ T row_turn(T v) {
+  return row_move<0x120 + N>(v);
+}
+// Of the lane ^ 1 and of the lane ^ 2.
+template <class T>
+__device__ __forceinline__ T row_pair(T v) {
+  return row_move<0xB1>(v);
+}
+template <class T>
+__device__ __forceinline__ T row_other_pair(T v) {
+  return row_move<0x4E>(v);
 }
 
 // v of both halves of the wave (HALF), or of both rows of a pair of rows.
@@ -110,6 +124,51 @@ __device__ __forceinline__ T route_all(T v, Op op) {
     v = op(a, b);
   }
   return v;
+}
+
+// v + that of the other half of the wave (HALF), or of the other row of a pair of rows.
+template <bool HALF, class T>
+__device__ __forceinline__ T add_both(T v) {
+  T a, b;
+  both<HALF>(v, a, b);
+  return a + b;
+}
+
+// The sum of a token's values; every lane ends with it.  Up to 256 experts one tree for
+// 16 lanes and for 64, so that a token's bits do not depend on the number of tokens: fours
+// of neighbours in two pairs, then the fours that lie 16 apart, then 8, 4, 2 and 1 apart.
+// Zeros past the experts change no sum.
+template <int LANES, int VPL, class T>
+__device__ __forceinline__ T route_sum(const T (&v)[VPL]) {
+  static_assert(LANES == 64 || (VPL >= 4 && VPL <= 16), "16 lanes hold fours of up to 256 experts");
+  if constexpr (VPL == 1) {
+    T s = v[0] + row_pair(v[0]);
+    s += row_other_pair(s);
+    s = add_both<false>(add_both<true>(s));
+    s += row_turn<8>(s);
+    return s + row_turn<4>(s);
+  } else if constexpr (VPL == 2) {
+    T s = v[0] + v[1];
+    s += row_pair(s);
+    s = add_both<false>(add_both<true>(s));
+    s += row_turn<8>(s);
+    s += row_turn<4>(s);
+    return s + row_turn<2>(s);
+  } else {
+    T four[VPL / 4];
+#pragma unroll
+    for (int c = 0; c < VPL / 4; ++c) four[c] = (v[4 * c] + v[4 * c + 1]) + (v[4 * c + 2] + v[4 * c + 3]);
+#pragma unroll
+    for (int d = 1; d < VPL / 4; d *= 2)
+#pragma unroll
+      for (int c = 0; c < VPL / 4; c += 2 * d) four[c] += four[c + d];
+    T s = four[0];
+    if constexpr (LANES == 64) s = add_both<true>(add_both<false>(s));
+    s += row_turn<8>(s);
+    s += row_turn<4>(s);
+    s += row_turn<2>(s);
+    return s + row_turn<1>(s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -303,6 +362,7 @@ __device__ __forceinline__ uint64_t route_groups(const RouteRule& q, const doubl
 template <int LANES, int VPL, int K, class Logit>
 __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL], int lane,
                                             RouteLds<LANES, VPL>* lds, const Logit& logit, int& id, float& weight) {
+#pragma clang fp contract(off)  // the same roundings in every instance
   const auto max_f = [](float a, float b) { return __builtin_fmaxf(a, b); };
   const auto sum_f = [](float a, float b) { return a + b; };
   const bool softmax = q.scoring == 0, ragged = q.experts < LANES * VPL;
@@ -319,9 +379,10 @@ __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL],
 #pragma unroll
     for (int i = 0; i < VPL; ++i) high = max_f(high, l[i]);
     high = route_all<LANES>(high, max_f);
+    float part[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) total += exp_f(l[i] - high);
-    total = route_all<LANES>(total, sum_f);
+    for (int i = 0; i < VPL; ++i) part[i] = exp_f(l[i] - high);
+    total = route_sum<LANES>(part);
   }
   double v[VPL];
   uint64_t kept = ~0ull;
@@ -333,15 +394,10 @@ __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL],
   };
   const bool scores = q.balance || (q.groups > 1 && q.top2);
   if (scores) {  // in 64 bits
-    double all = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      v[i] = exp_d(softmax ? (double)l[i] - (double)high : -(double)l[i]);
-      all += v[i];
-    }
+    for (int i = 0; i < VPL; ++i) v[i] = exp_d(softmax ? (double)l[i] - (double)high : -(double)l[i]);
     if (softmax) {
-      const double sum = route_all<LANES>(all, [](double a, double b) { return a + b; });
-      const double scale = total != total ? __builtin_nan("") : recip_d(sum);
+      const double scale = total != total ? __builtin_nan("") : recip_d(route_sum<LANES>(v));
 #pragma unroll
       for (int i = 0; i < VPL; ++i) v[i] *= scale;
     } else {

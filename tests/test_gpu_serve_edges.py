@@ -33,3 +33,47 @@ def test_route_logits_that_end_with_their_memory(t, experts, topk, groups, topk_
     buf[-400:] = G.to_dev(l)
     ids, w = X.exl3_route_topk(buf, rule)
     R.check(ids[-400:], w[-400:], l, rule)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("scoring,balanced,group_score", [("softmax", False, "max"), ("softmax", True, "max"),
+                                                          ("softmax", True, "top2"), ("softmax", False, "top2"),
+                                                          ("sigmoid", True, "top2"), ("sigmoid", False, "max")])
+@pytest.mark.parametrize("experts,topk,groups,topk_groups", [(256, 8, 8, 4), (256, 16, 1, 1), (250, 3, 1, 1),
+                                                             (160, 6, 8, 3), (128, 8, 4, 2), (96, 4, 2, 1),
+                                                             (65, 8, 1, 1), (64, 6, 1, 1), (60, 4, 4, 2), (33, 2, 1, 1),
+                                                             (8, 8, 1, 1), (5, 1, 1, 1), (300, 5, 1, 1)])
+def test_a_tokens_route_does_not_depend_on_the_others(experts, topk, groups, topk_groups, scoring, balanced,
+                                                      group_score, f32):
+    """The same bits among thousands of tokens, among a few and alone."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(experts + topk)
+    b = rng.standard_normal(experts) * (0.1 if scoring == "sigmoid" else 0.5 / experts) if balanced else None
+    rule = R.rule_of(experts, topk, b, scoring=scoring, groups=groups, topk_groups=topk_groups,
+                     group_score=group_score, renormalize=topk % 2 == 0)
+    l = G.to_dev((rng.standard_normal((4500, experts)) * 1.5).astype(np.float32 if f32 else np.float16))
+    ids, w = X.exl3_route_topk(l, rule)
+    for rows in (slice(0, 2049), slice(0, 2048), slice(2048, 4096), slice(4096, 4500), slice(7, 8), slice(4499, 4500)):
+        i, v = X.exl3_route_topk(l[rows], rule)
+        assert torch.equal(i, ids[rows]), rows
+        assert torch.equal(v, w[rows]), rows
+
+
+def test_a_tokens_route_beside_bad_tokens():
+    """Tokens of the same wave with NaN and infinite logits leave a token's bits alone."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(2)
+    for experts in (60, 256):
+        for scoring in ("softmax", "sigmoid"):
+            rule = R.rule_of(experts, 6, rng.standard_normal(experts) * 0.1, scoring=scoring, groups=4, topk_groups=2,
+                             group_score="top2")
+            l = (rng.standard_normal((4096, experts)) * 1.5).astype(np.float32)
+            want = X.exl3_route_topk(G.to_dev(l), rule)
+            bad = l.copy()
+            bad[1::4, 3], bad[2::4, ::5], bad[3::8, 7] = np.nan, -np.inf, np.inf
+            for t in (4096, 2000):
+                got = X.exl3_route_topk(G.to_dev(bad[:t]), rule)
+                for a, b in zip(got, want):
+                    assert torch.equal(a[::4], b[:t:4])
