@@ -1078,8 +1078,9 @@ def exl3_router_workspace_size(router: Exl3Router, t: int, logits: bool = True) 
 def exl3_router(x, router: Exl3Router, rule: Exl3RouteRule, logits=None, topk_ids=None, topk_weights=None,
                 workspace=None, stream=None):
     """Choices int32 [t, topk] and weights fp32 [t, topk] of fp16 rows x [t, hidden]:
-    exl3_router_linear and exl3_route_topk in one call.  logits fp32 [t, experts]
-    receives the logits if given.  The workspace is exl3_router_linear's."""
+    a router's linear and exl3_route_topk of its logits in one call.  logits fp32
+    [t, experts] receives the logits if given; they are exl3_router_linear's to rounding.
+    The workspace is exl3_router_linear's."""
     rule._now()
     t, ldx, device, on = _router_rows(x, router, stream)
     ldl, ptr = (0, 0) if logits is None else (_logits(logits, t, router, device), logits.data_ptr())

@@ -595,7 +595,7 @@ typedef struct exl3_route_rule {
  *   logits        [t][ldl] of `dtype` (EXL3_F16 or EXL3_F32), ldl >= experts; rows
  *                 need no alignment beyond the element's own
  *   topk_ids      int32 [t][topk]
- *   topk_weights  fp32 [t][topk]
+ *   topk_weights  fp32 [t][topk]; neither may overlap the logits
  * 0 <= t <= 2^24; t == 0 returns EXL3_OK.  The same bits on every run; a token's
  * result does not depend on the others of its call.                          */
 exl3_status exl3_route_topk(const exl3_route_rule* rule, const void* logits, int32_t dtype, int64_t t, int64_t ldl,
@@ -635,8 +635,12 @@ exl3_status exl3_router_linear(const exl3_router_weight* w, const void* x, int64
  * are invalid); logits: not 0 if the call is given memory for them. */
 size_t exl3_router_workspace_size(const exl3_router_weight* w, int64_t t, int32_t logits);
 
-/* exl3_router - exl3_router_linear and exl3_route_topk of its logits in one call (one
- * launch for a few tokens).  Arguments, limits and results are those of the two.
+/* exl3_router - a router's linear and the routing of its logits in one call (one
+ * launch for a few tokens).  Arguments and limits are those of exl3_router_linear and
+ * exl3_route_topk.  The logits are summed in shares of k of their own: they are
+ * exl3_router_linear's to rounding, and choices of values that near may differ from
+ * those of the two calls.  The choices and weights are, bit for bit, exl3_route_topk's of
+ * the logits that this call gives, whether it stores them or not.
  *   logits  fp32 [t][ldl], or NULL where the caller has no use for them
  *   ws      as for exl3_router_linear, and it may be the same one             */
 exl3_status exl3_router(const exl3_router_weight* w, const exl3_route_rule* rule, const void* x, int64_t t,

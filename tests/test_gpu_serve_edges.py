@@ -4,6 +4,7 @@ tests/test_gpu_route.py and tests/test_gpu_lora.py, or derived at the test."""
 import numpy as np
 import pytest
 
+from oracle import serve_oracle as S
 from tests import _gpu as G
 from tests import test_gpu_route as R
 
@@ -77,3 +78,33 @@ def test_a_tokens_route_beside_bad_tokens():
                 got = X.exl3_route_topk(G.to_dev(bad[:t]), rule)
                 for a, b in zip(got, want):
                     assert torch.equal(a[::4], b[:t:4])
+
+
+# both in a call: tokens in one launch, in rows, in tiles, in shares of either, past 2048
+@pytest.mark.parametrize("scoring,balanced,group_score", [("softmax", False, "max"), ("softmax", True, "top2"),
+                                                          ("sigmoid", True, "max")])
+@pytest.mark.parametrize("t,hidden,experts", [(1, 2048, 256), (4, 2048, 256), (3, 520, 40), (16, 5120, 256),
+                                              (16, 1024, 60), (9, 4096, 1000), (33, 2048, 256), (64, 5120, 256),
+                                              (333, 1440, 60), (700, 4104, 130), (2049, 5120, 60), (4000, 5120, 60),
+                                              (2500, 264, 256)])
+def test_router_routes_its_own_logits(t, hidden, experts, scoring, balanced, group_score):
+    """The choices and weights of exl3_router are the bits of exl3_route_topk of its
+    logits, the same without memory for them, and the logits exl3_router_linear's to
+    rounding: the bound of either, twice."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    x, w, c = R.router_case(t, hidden, experts, True, seed=21)
+    rng = np.random.default_rng(t)
+    b = rng.standard_normal(experts) * (0.1 if scoring == "sigmoid" else 0.5 / experts) if balanced else None
+    groups = 4 if experts % 4 == 0 else 1
+    rule = R.rule_of(experts, 5, b, scoring=scoring, groups=groups, topk_groups=max(1, groups // 2),
+                     group_score=group_score, scale=2.5)
+    r, xd = R.handle(w, c), G.to_dev(x)
+    logits = torch.full((t, experts + 3), 7.0, device=G.dev())
+    ids, wt = X.exl3_router(xd, r, rule, logits=logits[:, :experts])
+    for got in (X.exl3_route_topk(logits[:, :experts], rule), X.exl3_route_topk(logits[:, :experts].contiguous(), rule),
+                X.exl3_router(xd, r, rule)):
+        assert torch.equal(ids, got[0]) and torch.equal(wt, got[1])
+    apart = X.exl3_router_linear(xd, r)
+    _, mag = S.logits(x, w, c)
+    assert (np.abs((apart.double() - logits[:, :experts].double()).cpu().numpy()) <= 2 * R.logit_bound(mag, hidden)).all()
