@@ -10,9 +10,12 @@
 // (two passes over the rows' adapters in LDS, about a microsecond) and leave them to
 // lora_expand; more are sorted by a launch of one workgroup before (lora_plan, 6 us).
 //
-// h is kept to 24 bits: a row's h is scaled by a power of two to below 2^15 and split
-// into fp16 pieces hi + lo (hi holds 11 bits, lo the next 11 and, down to 2^-40 of the
-// row's largest, at least 13 bits of what is left); both meet one load of B.
+// h is kept to 23 bits: a row's h is scaled by a power of two to below 2^15 and split
+// into fp16 pieces hi + 2^-12 lo, both of which meet one load of B.  hi is off by at most
+// 2^-12 of the value, and lo, of the same size, by as much of that: hi + 2^-12 lo is off
+// by at most 2^-23 of the value down to 2^-29 of the row's largest, where hi leaves fp16's
+// normals, and by at most 2^-51 of the largest below.  (fp32 sums of a thousand products
+// are off by more.)  lo's sums are made first and scaled, or apart.
 #include "exl3_internal.hpp"
 #include "exl3_tile64.hpp"
 
@@ -476,6 +479,8 @@ __device__ __forceinline__ f16x8_t lora_keep(f16x8_t w, int left) {
 // the 16 rows of an operand lie in different banks.
 __host__ __device__ constexpr int lora_piece_row(int chunks) { return 64 * chunks + 16; }
 
+constexpr float kLoraLow = 1.f / 4096;  // of lo
+
 // The task's h as pieces in LDS, and each row's factors of the sums.
 template <int S, int CHUNKS>
 __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& task, int rank, float scale,
@@ -526,7 +531,7 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
     for (int j = 0; j < 4; ++j) {
       const float v = __builtin_ldexpf(h[i][j], e);
       hi[j] = (_Float16)v;
-      lo[j] = (_Float16)(__builtin_isfinite(v) ? v - (float)hi[j] : 0.f);
+      lo[j] = (_Float16)(__builtin_isfinite(v) ? (v - (float)hi[j]) * (1 / kLoraLow) : 0.f);
     }
     *reinterpret_cast<half4_t*>(lds + row * stride + 2 * at) = hi;
     *reinterpret_cast<half4_t*>(lds + (S + row) * stride + 2 * at) = lo;
@@ -682,9 +687,9 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int p = 1; p >= 0; --p) {  // lo, then hi
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int c = 0; c < kChunks; ++c) {
         const f16x8_t h =
             *reinterpret_cast<const f16x8_t*>(smem + (p * S + r) * kRow + 64 * c + 16 * (PAIR ? g & 1 : g));
         if constexpr (PAIR) {
@@ -700,6 +705,10 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
           for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[4 * c + t], h, acc[t], 0, 0, 0);
         }
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (p) acc[t] *= kLoraLow;
+    }
     const float f0 = factor[r], f1 = factor[S + r];
     float odd = 0.f;  // NaN if a sum is not finite
 #pragma unroll
@@ -848,9 +857,9 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kCopies + 2 * kIo) : "memory");
     fetch(tile + 2, (place + 2) % kLoraRing);
     load_base(tile + 1, next);
-    float4_t acc[4];
+    float4_t acc[4], low[4];  // hi's sums and lo's; of one chunk lo's go first, which takes fewer registers
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) acc[t] = low[t] = float4_t{0.f, 0.f, 0.f, 0.f};
     const uint32_t at = ring + (uint32_t)place * kTile;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -865,9 +874,19 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
         for (int t = 0; t < 4; ++t) w[t] = lora_keep(w[t], rank - 32 * c - 8 * g);
       }
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int t = 0; t < 4; ++t) low[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][1], low[t], 0, 0, 0);
+      if constexpr (CH == 1) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][p], acc[t], 0, 0, 0);
+        for (int t = 0; t < 4; ++t) acc[t] = low[t] * kLoraLow;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][0], acc[t], 0, 0, 0);
+    }
+    if constexpr (CH > 1) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = __builtin_fmaf(low[t][j], kLoraLow, acc[t][j]);
     }
     place = place == kLoraRing - 1 ? 0 : place + 1;
     if (i0 >= count) return;

@@ -679,9 +679,9 @@ size_t exl3_lora_workspace_size(const exl3_lora_stack* l, int64_t m);
 
 /* exl3_lora - y_i = base_i + scale_a B_a (A_a x_i), a = rows[i]: what the adapter of
  * each row's request adds to a projection's output (exl3_linear, exl3_mx4_linear, ...).
- * Products of A are exact in fp32, sums fp32; A x is kept to 24 bits (below 2^-25 of
- * the row's largest fewer, 2^-40 of that is lost) between the products; one rounding to
- * an fp16 output.
+ * Products of A are exact in fp32, sums fp32; between the products A x is kept to 23 bits
+ * at least (each element within 2^-23 of itself; below 2^-29 of the row's largest, within
+ * 2^-51 of that); one rounding to an fp16 output.
  *   x     fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
  *   rows  int32 [m] device pointer, 4-byte aligned: each row's adapter; a value outside
  *         0 .. adapters-1 (-1, say) stands for none, and y_i is base_i

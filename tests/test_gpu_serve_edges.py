@@ -6,6 +6,7 @@ import pytest
 
 from oracle import serve_oracle as S
 from tests import _gpu as G
+from tests import test_gpu_lora as L
 from tests import test_gpu_route as R
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +109,75 @@ def test_router_routes_its_own_logits(t, hidden, experts, scoring, balanced, gro
     apart = X.exl3_router_linear(xd, r)
     _, mag = S.logits(x, w, c)
     assert (np.abs((apart.double() - logits[:, :experts].double()).cpu().numpy()) <= 2 * R.logit_bound(mag, hidden)).all()
+
+
+# ---------------------------------------------------------------------------
+# adapters: what is kept of A x between the two products
+# ---------------------------------------------------------------------------
+# rows and adapters by the kernels they take: segments of 16 found by ballots, by search
+# and by the plan, of 64 by search and by the plan
+SEGMENTS = [(20, 3), (333, 40), (1100, 300), (600, 3), (2100, 2)]
+
+
+@pytest.mark.parametrize("m,adapters", SEGMENTS)
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 104, 128, 256])
+def test_lora_keeps_the_low_bits_of_the_inner_sums(rank, m, adapters):
+    """Whole numbers again, with inner sums that need more than the 11 bits of one fp16:
+    sums below 2^24 are exact in two pieces, and in fp32 in any order.  One piece would
+    give other sums (checked here)."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    g = torch.Generator(device=G.dev()).manual_seed(rank * 7 + m)
+    whole = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=G.dev())
+    k = 104
+    for n in (8, 70, 521):
+        x, a = whole(-40, 41, m, k).half(), whole(-40, 41, adapters, rank, k).half()
+        b, rows = whole(-1, 2, adapters, n, rank).half(), whole(-1, adapters, m).int()
+        base = whole(-99, 100, m, n).float()
+        ref, one = base.double(), base.double()
+        most = 0.0
+        for i in range(adapters):
+            mine = rows == i
+            h = x[mine].double() @ a[i].double().T
+            most = max(most, float(h.abs().sum(-1).max()) if h.numel() else 0.0)
+            ref[mine] += h @ b[i].double().T
+            step = torch.exp2(torch.floor(torch.log2(h.abs().clamp(min=1))) - 10)
+            one[mine] += (torch.round(h / step) * step) @ b[i].double().T
+        assert most + 99 < 2 ** 24 and not torch.equal(one, ref)
+        y = X.exl3_lora(x, X.Exl3Lora(a, b), rows, base)
+        assert torch.equal(y.double(), ref), n
+
+
+@pytest.mark.parametrize("m,adapters", SEGMENTS)
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 64, 128, 256])
+def test_lora_keeps_small_inner_sums_beside_large_ones(rank, m, adapters):
+    """B is the unit matrix, so that y_c is the kept value of (A x)_c, whose sums of two
+    products are exact in fp32.  Kept: each within 2^-23 of itself down to 2^-29 of the
+    row's largest, below that within 2^-51 of the largest; and a rounding of the sum of
+    the pieces, 2^-24."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(rank + m)
+    k, n = 72, rank
+    x = np.zeros((m, k))
+    x[:, 3], x[:, 70] = 1.0, 2.0 ** -12
+    a = np.zeros((adapters, rank, k))
+    size = np.exp2(rng.integers(-22, 5, (adapters, rank)))  # the least fp16 that holds 11 bits: 2^-24 * 1024
+    size[:, rng.integers(rank)] = 2.0 ** 5
+    sign = rng.choice([-1.0, 1.0], (adapters, rank))
+    a[:, :, 3] = sign * rng.integers(1024, 2048, (adapters, rank)) * size
+    a[:, :, 70] = rng.integers(-2047, 2048, (adapters, rank)) * size
+    b = np.broadcast_to(np.eye(rank), (adapters, n, rank))
+    a16, x16 = a.astype(np.float16), x.astype(np.float16)
+    assert (a16 == a).all() and (x16 == x).all()
+    rows = rng.integers(0, adapters, m).astype(np.int32)
+    h = np.einsum("mk,mrk->mr", x[:, [3, 70]], a[rows][:, :, [3, 70]])
+    assert (h == h.astype(np.float32)).all()
+    lora = X.Exl3Lora(G.to_dev(a16), G.to_dev(b.astype(np.float16).copy()))
+    y = X.exl3_lora(G.to_dev(x16), lora, G.to_dev(rows), out_dtype=torch.float32).cpu().numpy().astype(np.float64)
+    top = np.abs(h).max(-1, keepdims=True)
+    assert (np.abs(h) < top * 2.0 ** -22).any() and (np.abs(h) > 0).all()
+    limit = np.where(np.abs(h) >= top * 2.0 ** -29, 2.0 ** -23 * np.abs(h), 2.0 ** -51 * top) + 2.0 ** -24 * np.abs(h)
+    bad = np.abs(y - h) > limit
+    assert not bad.any(), (f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {h[bad][0]!r}, "
+                           f"row's largest {np.broadcast_to(top, h.shape)[bad][0]!r}")
