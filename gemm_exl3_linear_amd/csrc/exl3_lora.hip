@@ -15,7 +15,7 @@
 // 2^-12 of the value, and lo, of the same size, by as much of that: hi + 2^-12 lo is off
 // by at most 2^-23 of the value down to 2^-29 of the row's largest, where hi leaves fp16's
 // normals, and by at most 2^-51 of the largest below.  (fp32 sums of a thousand products
-// are off by more.)  lo's sums are made first and scaled, or apart.
+// are off by more.)
 #include "exl3_internal.hpp"
 #include "exl3_tile64.hpp"
 
@@ -538,6 +538,17 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
   }
 }
 
+// The sums of h from those of hi and of lo, made apart: a matrix instruction adds its
+// products and its operand C as if no factor were subnormal, to about 24 bits below such a
+// product's exponent, so that lo's sums, brought in by C, would be cut where weights are
+// subnormal (at 2^-16 of the result for weights of 2^-22).
+__device__ __forceinline__ void lora_join(float4_t (&hi)[4], const float4_t (&low)[4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hi[t][j] = __builtin_fmaf(low[t][j], kLoraLow, hi[t][j]);
+}
+
 // How a wave's lanes take 16 rows of 64 columns of base and of y: 16 bytes a lane, of any
 // alignment.  Where a tile has fewer than 64 columns, the last lanes' pieces end with it and
 // overlap their neighbours', or begin in the tile before, and what lies there is not stored.
@@ -683,13 +694,14 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
       for (int i = 0; i < kB; ++i)
         now.w[i] = lora_keep(now.w[i], rank - (PAIR ? 8 * (g & 1) : 32 * (i >> 2) + 8 * g));
     }
-    float4_t acc[4];
+    float4_t acc[4], low[4];  // sums of hi and of lo
 #pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) acc[t] = low[t] = float4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int p = 1; p >= 0; --p) {  // lo, then hi
+    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
+      for (int p = 0; p < 2; ++p) {
+        float4_t* to = p ? low : acc;
         const f16x8_t h =
             *reinterpret_cast<const f16x8_t*>(smem + (p * S + r) * kRow + 64 * c + 16 * (PAIR ? g & 1 : g));
         if constexpr (PAIR) {
@@ -698,17 +710,14 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
             const f16x8_t part = lora_keep(h, (g >> 1) == o ? 8 : 0);
 #pragma unroll
             for (int v = 0; v < 2; ++v)
-              acc[2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[v], part, acc[2 * v + o], 0, 0, 0);
+              to[2 * v + o] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[v], part, to[2 * v + o], 0, 0, 0);
           }
         } else {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[4 * c + t], h, acc[t], 0, 0, 0);
+          for (int t = 0; t < 4; ++t) to[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.w[4 * c + t], h, to[t], 0, 0, 0);
         }
       }
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (p) acc[t] *= kLoraLow;
-    }
+    lora_join(acc, low);
     const float f0 = factor[r], f1 = factor[S + r];
     float odd = 0.f;  // NaN if a sum is not finite
 #pragma unroll
@@ -857,7 +866,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kCopies + 2 * kIo) : "memory");
     fetch(tile + 2, (place + 2) % kLoraRing);
     load_base(tile + 1, next);
-    float4_t acc[4], low[4];  // hi's sums and lo's; of one chunk lo's go first, which takes fewer registers
+    float4_t acc[4], low[4];  // sums of hi and of lo
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = low[t] = float4_t{0.f, 0.f, 0.f, 0.f};
     const uint32_t at = ring + (uint32_t)place * kTile;
@@ -874,20 +883,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
         for (int t = 0; t < 4; ++t) w[t] = lora_keep(w[t], rank - 32 * c - 8 * g);
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) low[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][1], low[t], 0, 0, 0);
-      if constexpr (CH == 1) {
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = low[t] * kLoraLow;
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][0], acc[t], 0, 0, 0);
+        for (int t = 0; t < 4; ++t) {
+          float4_t* to = p ? low : acc;
+          to[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t], h[c][p], to[t], 0, 0, 0);
+        }
     }
-    if constexpr (CH > 1) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = __builtin_fmaf(low[t][j], kLoraLow, acc[t][j]);
-    }
+    lora_join(acc, low);
     place = place == kLoraRing - 1 ? 0 : place + 1;
     if (i0 >= count) return;
     float odd = 0.f;  // NaN if a sum is not finite

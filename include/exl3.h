@@ -618,7 +618,8 @@ typedef struct exl3_router_weight {
 size_t exl3_router_linear_workspace_size(const exl3_router_weight* w, int64_t t);
 
 /* exl3_router_linear - the logits of t tokens: fp16 rows and weights, products exact
- * in fp32, sums fp32, not rounded.
+ * in fp32, sums fp32, not rounded (products of subnormal elements are summed as if those
+ * were 2^-14: alone, they keep fewer bits).
  *   x       fp16 [t][ldx], ldx >= hidden, multiple of 8, 16-byte aligned
  *   logits  fp32 [t][ldl], ldl >= experts, 4-byte aligned; it may not overlap x
  *   ws      device workspace of at least the queried size (may be NULL when that is
@@ -681,7 +682,9 @@ size_t exl3_lora_workspace_size(const exl3_lora_stack* l, int64_t m);
  * each row's request adds to a projection's output (exl3_linear, exl3_mx4_linear, ...).
  * Products of A are exact in fp32, sums fp32; between the products A x is kept to 23 bits
  * at least (each element within 2^-23 of itself; below 2^-29 of the row's largest, within
- * 2^-51 of that); one rounding to an fp16 output.
+ * 2^-51 of that); one rounding to an fp16 output.  The matrix cores sum the product of a
+ * subnormal fp16 as if it were one of 2^-14: sums of subnormal elements alone keep fewer
+ * bits.
  *   x     fp16 [m][ldx], ldx >= k, multiple of 8, 16-byte aligned
  *   rows  int32 [m] device pointer, 4-byte aligned: each row's adapter; a value outside
  *         0 .. adapters-1 (-1, say) stands for none, and y_i is base_i

@@ -181,3 +181,30 @@ def test_lora_keeps_small_inner_sums_beside_large_ones(rank, m, adapters):
     bad = np.abs(y - h) > limit
     assert not bad.any(), (f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {h[bad][0]!r}, "
                            f"row's largest {np.broadcast_to(top, h.shape)[bad][0]!r}")
+
+
+@pytest.mark.parametrize("m,adapters", SEGMENTS)
+@pytest.mark.parametrize("rank", [8, 16, 32, 40, 128, 256])
+@pytest.mark.parametrize("weight", [2.0 ** -24, 2.0 ** -22, 2.0 ** -16, 1.0])
+def test_lora_inner_sums_times_subnormal_weights(weight, rank, m, adapters):
+    """y_c is one inner sum of 22 bits times one weight, a power of two: the inner sum
+    kept to 2^-23, and the sum of its pieces' products.  Those are exact for the high
+    piece (its last place times the weight's is at least 2^-21, and a matrix instruction
+    cuts about 2^-24 of an fp16 of exponent 14 times a subnormal); the low piece's are cut
+    there too, which its factor makes 2^-36 beside a result of 2^-11 at least.  One
+    rounding, 2^-24."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(rank + m)
+    k, n = 72, rank + 3
+    x, a = np.zeros((m, k)), np.zeros((adapters, rank, k))
+    x[:, 5], a[:, :, 5] = rng.integers(1024, 2048, m), rng.integers(1024, 2048, (adapters, rank))
+    b = np.zeros((adapters, n, rank))
+    b[:, :rank] = np.eye(rank) * weight
+    rows = (np.arange(m) % adapters).astype(np.int32)
+    want = np.zeros((m, n))
+    want[:, :rank] = x[:, 5:6] * a[rows][:, :, 5] * weight
+    lora = X.Exl3Lora(*(G.to_dev(v.astype(np.float16)) for v in (a, b)))
+    y = X.exl3_lora(G.to_dev(x.astype(np.float16)), lora, G.to_dev(rows), out_dtype=torch.float32).cpu().numpy()
+    bad = np.abs(y - want) > 4 * 2.0 ** -24 * want
+    assert not bad.any(), f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {want[bad][0]!r}"
