@@ -481,10 +481,13 @@ __host__ __device__ constexpr int lora_piece_row(int chunks) { return 64 * chunk
 
 constexpr float kLoraLow = 1.f / 4096;  // of lo
 
-// The task's h as pieces in LDS, and each row's factors of the sums.
+// The task's h as pieces in LDS, and each row's factor of the sums, 2^-e.  (h is a sum of
+// at most 2^20 products of fp16 and a multiple of 2^-48, so e lies between -37 and 62 and
+// the sums, freed of it, well inside fp32: the adapter's scale, which may be any, is a
+// factor of its own.)
 template <int S, int CHUNKS>
-__device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& task, int rank, float scale,
-                                            uint8_t* lds, float* factor) {
+__device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& task, int rank, uint8_t* lds,
+                                            float* factor) {
   constexpr int kEach = kLoraThreads / S;  // threads of a row
   constexpr int kMost = (8 * CHUNKS + kEach - 1) / kEach;
   constexpr int kAtOnce = kMost == 1 ? 8 : 4;  // shares whose loads go out together
@@ -518,10 +521,7 @@ __device__ __forceinline__ void lora_pieces(const LoraArgs& q, const LoraTask& t
 #pragma unroll
   for (int d = 1; d < kEach; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
   const int e = top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
-  if (part == 0) {  // scale 2^-e in two factors, neither of which leaves fp32 by itself
-    factor[row] = __builtin_ldexpf(1.f, -e / 2);
-    factor[S + row] = __builtin_ldexpf(scale, -e - -e / 2);
-  }
+  if (part == 0) factor[row] = __builtin_ldexpf(1.f, -e);
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int at = 4 * (part + i * kEach);
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
   constexpr int kRow = lora_piece_row(kChunks);
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ LoraTask task;
-  __shared__ float factor[2 * S];
+  __shared__ float factor[S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int sub = lane / Io::kLanes;  // a lane's row of an instruction's
@@ -685,7 +685,7 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
     load_base(tile, to.from);
   };
   load(first_tile, even);
-  lora_pieces<S, kChunks>(q, task, rank, scale, smem, factor);
+  lora_pieces<S, kChunks>(q, task, rank, smem, factor);
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem + 2 * S * kRow) + wave * (16 * kLoraOutStride);
   const auto take = [&](int tile, Tile& now) {
@@ -718,13 +718,13 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
         }
       }
     lora_join(acc, low);
-    const float f0 = factor[r], f1 = factor[S + r];
+    const float f = factor[r];
     float odd = 0.f;  // NaN if a sum is not finite
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
-      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f * scale;
     }
     wave_lds_sync();
     if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, 0, 64 * tile, rank, scale, b, out);
@@ -787,7 +787,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
   constexpr int kCopies = kTile / 1024 / 4;                   // a wave's
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   __shared__ LoraTask task;
-  __shared__ float factor[2 * S];
+  __shared__ float factor[S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
   const int sub = lane / Io::kLanes;  // a lane's row of an instruction's
@@ -817,7 +817,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
   const int rank = lora_rank(q, adapter);
   const float scale = q.d.scales ? q.d.scales[adapter] : 1.f;
   const uint16_t* b = q.d.b + (int64_t)adapter * N * R;
-  lora_pieces<S, CH>(q, task, rank, scale, smem, factor);
+  lora_pieces<S, CH>(q, task, rank, smem, factor);
   __syncthreads();
   f16x8_t h[CH][2];
 #pragma unroll
@@ -826,7 +826,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
     for (int p = 0; p < 2; ++p)
       h[c][p] = *reinterpret_cast<const f16x8_t*>(smem + (p * S + i0 + r) * kRow + 64 * c + 16 * g);
   __syncthreads();
-  const float f0 = factor[i0 + r], f1 = factor[S + i0 + r];
+  const float f = factor[i0 + r];
   float* out = reinterpret_cast<float*>(smem + kLoraRing * kTile) + wave * (16 * kLoraOutStride);
   const uint32_t ring = (uint32_t)(uintptr_t)(lds_u8*)smem;
   const u32x4_t rsrc = buffer_words(reinterpret_cast<const uint8_t*>(b), (uint64_t)N * R * 2);
@@ -898,7 +898,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) odd = __builtin_fmaf(acc[t][j], 0.f, odd);
-      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f0 * f1;
+      *reinterpret_cast<float4_t*>(out + r * kLoraOutStride + 16 * t + 4 * g) = acc[t] * f * scale;
     }
     wave_lds_sync();
     if (__builtin_expect(__any(odd != 0.f), 0)) lora_mend(q, task, i0, 64 * tile, rank, scale, b, out);

@@ -208,3 +208,39 @@ def test_lora_inner_sums_times_subnormal_weights(weight, rank, m, adapters):
     y = X.exl3_lora(G.to_dev(x.astype(np.float16)), lora, G.to_dev(rows), out_dtype=torch.float32).cpu().numpy()
     bad = np.abs(y - want) > 4 * 2.0 ** -24 * want
     assert not bad.any(), f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {want[bad][0]!r}"
+
+
+@pytest.mark.parametrize("m,adapters", [(1, 4)] + SEGMENTS)
+@pytest.mark.parametrize("rank", [8, 40, 256])
+def test_lora_scales_at_the_ends_of_fp32(rank, m, adapters):
+    """Adapter i has a large scale and small weights, or a small one and large weights,
+    or columns of B that are 0 beside inner sums and a scale of any size: results inside
+    fp32 are right, and 0 stays 0.  y_c is one inner sum, kept to 2^-23 of itself, times
+    one weight, one scale: three roundings of 2^-24 more."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(rank + m)
+    k, n = 72, rank + 3
+    x, a = np.zeros((m, k)), np.zeros((adapters, rank, k))
+    b, scales = np.zeros((adapters, n, rank)), np.zeros(adapters, dtype=np.float32)
+    x[:, 5] = rng.integers(1024, 2048, m)                        # [2^10, 2^11)
+    kinds = np.arange(adapters) % 4
+    a[:, :, 5] = rng.integers(1024, 2048, (adapters, rank))
+    for i, kind in enumerate(kinds):
+        h = (2.0 ** 4, 2.0 ** -22, 2.0 ** 4, 2.0 ** -20)[kind]   # inner sums about 2^25, 2^-1, 2^25, 2
+        a[i] *= h
+        w = (2.0 ** -22, 2.0 ** 15, 0.0, 2.0 ** 14)[kind]
+        b[i, :rank] = np.eye(rank) * w
+        scales[i] = np.float32((1.1 * 2.0 ** 120, 1.1 * 2.0 ** -125, 3e38, 1.1 * 2.0 ** 110)[kind])
+    a16, b16, x16 = a.astype(np.float16), b.astype(np.float16), x.astype(np.float16)
+    assert (a16 == a).all() and (b16 == b).all() and (x16 == x).all()
+    rows = (np.arange(m) % adapters).astype(np.int32)
+    want = np.zeros((m, n))
+    want[:, :rank] = (x[:, 5:6] * a[rows][:, :, 5]) * b[rows][:, np.arange(rank), np.arange(rank)]
+    want *= scales[rows].astype(np.float64)[:, None]
+    assert (np.abs(want[want != 0]) < 2.0 ** 127).all() and (np.abs(want[want != 0]) > 2.0 ** -126).all()
+    lora = X.Exl3Lora(G.to_dev(a16), G.to_dev(b16), scales=G.to_dev(scales))
+    y = X.exl3_lora(G.to_dev(x16), lora, G.to_dev(rows), out_dtype=torch.float32).cpu().numpy().astype(np.float64)
+    assert (y[want == 0] == 0).all()
+    bad = ~(np.abs(y - want) <= 5 * 2.0 ** -24 * np.abs(want))
+    assert not bad.any(), f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {want[bad][0]!r}"
