@@ -913,6 +913,14 @@ def exl3_mx4_moe(x, layer: Exl3Mx4Moe, topk: int, out_dtype=None, out=None, topk
 # ---------------------------------------------------------------------------
 # Routing to experts
 # ---------------------------------------------------------------------------
+def _int32(v, what: str) -> int:
+    """v as a C int, which a record's field would else take modulo 2^32."""
+    i = operator.index(v)
+    if not -(1 << 31) <= i < 1 << 31:
+        _refuse(f"{what} is {i}, past 32 bits")
+    return i
+
+
 class _Record:
     """A record of tensors: subclasses give `_tensors()` (the checked tensors, None
     left out) and `_make(...)`, the C record of them."""
@@ -954,7 +962,8 @@ class Exl3Router(_Record):
         return parts
 
     def _make(self):
-        return _RouterWeight(_ptr(self.weight), _ptr(self.bias), self.experts, self.hidden)
+        return _RouterWeight(_ptr(self.weight), _ptr(self.bias), _int32(self.experts, "experts"),
+                             _int32(self.hidden, "hidden"))
 
     @property
     def experts(self) -> int:
@@ -993,10 +1002,11 @@ class Exl3RouteRule(_Record):
             _refuse(f"scoring {self.scoring!r} is not softmax or sigmoid")
         if self.group_score not in ("max", "top2"):
             _refuse(f"group_score {self.group_score!r} is not max or top2")
-        return _RouteRule(_ptr(self.balance), self.experts, self.topk,
-                          ROUTE_SOFTMAX if self.scoring == "softmax" else ROUTE_SIGMOID, self.groups,
-                          self.groups if self.topk_groups is None else self.topk_groups,
-                          GROUP_MAX if self.group_score == "max" else GROUP_TOP2, int(self.renormalize),
+        topk_groups = self.groups if self.topk_groups is None else self.topk_groups
+        return _RouteRule(_ptr(self.balance), _int32(self.experts, "experts"), _int32(self.topk, "topk"),
+                          ROUTE_SOFTMAX if self.scoring == "softmax" else ROUTE_SIGMOID,
+                          _int32(self.groups, "groups"), _int32(topk_groups, "topk_groups"),
+                          GROUP_MAX if self.group_score == "max" else GROUP_TOP2, int(bool(self.renormalize)),
                           float(self.scale))
 
 
@@ -1117,8 +1127,8 @@ class Exl3Lora(_Record):
         return parts
 
     def _make(self):
-        return _LoraStack(_ptr(self.a), _ptr(self.b), _ptr(self.scales), _ptr(self.ranks), self.adapters, self.rank,
-                          self.k, self.n)
+        return _LoraStack(_ptr(self.a), _ptr(self.b), _ptr(self.scales), _ptr(self.ranks),
+                          _int32(self.adapters, "adapters"), _int32(self.rank, "rank"), self.k, self.n)
 
     @property
     def adapters(self) -> int:
