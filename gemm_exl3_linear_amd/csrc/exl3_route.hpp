@@ -433,9 +433,10 @@ __device__ __forceinline__ void route_token(const RouteRule& q, float (&l)[VPL],
     const bool fours = VPL >= 4 && q.group_size % 4 == 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      // four neighbours are of the first one's group
+      // four neighbours are of the first one's group; places past the experts, which hold
+      // none, may lie past 64 groups
       const uint32_t e = route_expert<LANES, VPL>(fours ? i & ~3 : i, lane);
-      v[i] = (kept >> ((e * q.group_inverse) >> 20) & 1) ? v[i] : kKeyNone;
+      v[i] = (kept >> (((e * q.group_inverse) >> 20) & 63) & 1) ? v[i] : kKeyNone;
     }
   }
   double top[K];

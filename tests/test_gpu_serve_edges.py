@@ -37,6 +37,22 @@ def test_route_logits_that_end_with_their_memory(t, experts, topk, groups, topk_
     R.check(ids[-400:], w[-400:], l, rule)
 
 
+@pytest.mark.parametrize("t", [5, 2100])
+@pytest.mark.parametrize("balanced", [False, True])
+@pytest.mark.parametrize("experts,topk,groups,topk_groups", [(576, 16, 64, 5), (64, 8, 64, 9), (128, 4, 64, 3),
+                                                             (66, 5, 33, 4), (576, 8, 64, 63), (192, 8, 64, 7)])
+def test_route_many_small_groups(experts, topk, groups, topk_groups, balanced, t):
+    """Places past the experts, up to the next size that lanes hold, are of no group: their
+    number may be past 64."""
+    import gemm_exl3_linear_amd as X
+    rng = np.random.default_rng(experts + t)
+    l = (rng.standard_normal((t, experts)) * 1.5).astype(np.float32)
+    rule = R.rule_of(experts, topk, rng.standard_normal(experts) * 0.1 if balanced else None, scoring="sigmoid",
+                     groups=groups, topk_groups=topk_groups)
+    ids, w = X.exl3_route_topk(G.to_dev(l), rule)
+    R.check(ids, w, l, rule)
+
+
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("scoring,balanced,group_score", [("softmax", False, "max"), ("softmax", True, "max"),
                                                           ("softmax", True, "top2"), ("softmax", False, "top2"),
