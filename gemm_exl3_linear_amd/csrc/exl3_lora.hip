@@ -290,7 +290,9 @@ __device__ __forceinline__ bool lora_search(const LoraArgs& q, int z, int* lds, 
 template <int S, int W>
 __device__ __forceinline__ bool lora_task(const LoraArgs& q, int z, int* lds, LoraTask& task) {
   if (q.planned) return lora_read<S>(q, z, task);
-  const bool there = q.m <= 64 ? lora_ballots<S>(q, z, task) : lora_search<S, W>(q, z, lds, task);
+  bool there;
+  if (S < kLoraMaxSeg && q.m <= 64) there = lora_ballots<S>(q, z, task);  // long segments have 512 rows at least
+  else there = lora_search<S, W>(q, z, lds, task);
   if (blockIdx.y == 0 && blockIdx.z == 0) {
     if (there && threadIdx.x < S) q.order[(int64_t)z * S + threadIdx.x] = task.row[threadIdx.x];
     if (threadIdx.x == 0) q.segs[z] = there ? LoraSeg{task.adapter, task.count} : LoraSeg{0, 0};
@@ -312,10 +314,9 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& q, int adapter) {
 // of 5120 and 64 adapters of rank 16, 11 MB, in 5.6 us: start, loads' latency and end.
 template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
-  constexpr int MT = 1;
   constexpr int U = 4 / RT;  // lines whose loads go out together
   extern __shared__ int lds[];
-  __shared__ float4_t part[4][MT * RT][64];
+  __shared__ float4_t part[4][RT][64];
   __shared__ LoraTask task;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int g = lane >> 4, r = lane & 15;
@@ -324,24 +325,20 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
   if (!lora_task<16, 4>(q, blockIdx.x, lds, task)) return;
   const int rank = task.adapter < 0 ? 0 : lora_rank(q, task.adapter);
   if (rank > r0) {
-    const uint16_t* x[MT];
+    const uint16_t* x = q.x + (int64_t)task.row[r] * q.ldx;
     const uint16_t* a[RT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = q.x + (int64_t)task.row[16 * i + r] * q.ldx;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {  // past the rank: the last rank's, whose sums are not used
       const int of = r0 + 16 * j + r;
       a[j] = q.d.a + ((int64_t)task.adapter * q.d.rank + (of < rank ? of : rank - 1)) * k;
     }
-    float4_t acc[MT][RT];
+    float4_t acc[RT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < RT; ++j) acc[j] = float4_t{0.f, 0.f, 0.f, 0.f};
     const int lines = (int)((k + 63) / 64);
     const int first = (int)((int64_t)lines * split / q.splits), end = (int)((int64_t)lines * (split + 1) / q.splits);
     for (int u0 = first + wave; u0 < end; u0 += 4 * U) {
-      u32x4_t xv[U][2][MT], av[U][2][RT];
+      u32x4_t xv[U][2], av[U][2][RT];
 #pragma unroll
       for (int v = 0; v < U; ++v)
 #pragma unroll
@@ -349,8 +346,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
           const int u = u0 + 4 * v;
           const int64_t at = 64 * (int64_t)u + 16 * g + 8 * s;
           const int64_t from = u < end && at < k ? at : 0;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) xv[v][s][i] = load16(x[i] + from);
+          xv[v][s] = load16(x + from);
 #pragma unroll
           for (int j = 0; j < RT; ++j) av[v][s][j] = load16(a[j] + from);
         }
@@ -362,8 +358,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
             const int u = u0 + 4 * v;
             const bool there = u < end && 64 * (int64_t)u + 16 * g + 8 * s < k;
             const u32x4_t zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int i = 0; i < MT; ++i) xv[v][s][i] = there ? xv[v][s][i] : zero;
+            xv[v][s] = there ? xv[v][s] : zero;
 #pragma unroll
             for (int j = 0; j < RT; ++j) av[v][s][j] = there ? av[v][s][j] : zero;
           }
@@ -373,28 +368,23 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < RT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xv[v][s][i]),
-                                                                 __builtin_bit_cast(f16x8_t, av[v][s][j]), acc[i][j],
-                                                                 0, 0, 0);
+          for (int j = 0; j < RT; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, xv[v][s]),
+                                                            __builtin_bit_cast(f16x8_t, av[v][s][j]), acc[j], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) part[wave][i * RT + j][lane] = acc[i][j];
+    for (int j = 0; j < RT; ++j) part[wave][j][lane] = acc[j];
   }
   __syncthreads();
   if (rank > r0) {
-    for (int t = wave; t < MT * RT; t += 4) {
-      const int col = r0 + 16 * (t % RT) + r;
+    for (int t = wave; t < RT; t += 4) {
+      const int col = r0 + 16 * t + r;
       float4_t sum = part[0][t][lane];
 #pragma unroll
       for (int w = 1; w < 4; ++w) sum += part[w][t][lane];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = 16 * (t / RT) + 4 * g + j;
+        const int i = 4 * g + j;
         if (i < task.count && col < q.rpad) q.h[((int64_t)split * q.m + task.row[i]) * q.rpad + col] = sum[j];
       }
     }
