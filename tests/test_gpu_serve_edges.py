@@ -97,6 +97,56 @@ def test_a_tokens_route_beside_bad_tokens():
                     assert torch.equal(a[::4], b[:t:4])
 
 
+def near_bound(w, l, scoring):
+    """As tests/test_gpu_route.py's, with the span of one token's logits that can have a
+    say: a softmax's terms 110 below its largest are below 2^-158, and a sigmoid, which
+    takes no difference of logits, has none."""
+    finite = l[np.isfinite(l)]
+    span = 0.0
+    if scoring == "softmax" and finite.size:
+        span = float(finite.max() - finite[finite >= finite.max() - 110].min())
+    return (2 * span + 44) * 2.0 ** -24 * np.abs(w) + 2.0 ** -120
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts", [8, 60, 256, 1024])
+def test_route_weights_beside_masks_of_the_lowest_value(experts, renormalize, scoring):
+    """Weights of tokens with masked, far and infinite logits, each within the bound of its
+    own token, and masks of the type's lowest value give the bits of infinite ones."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    for f32 in (True, False):
+        l = R.special_logits(experts)
+        l = np.delete(l, [7, 15] if renormalize else [], axis=0)  # weights divided by a sum of subnormals, or of 0
+        if not f32:
+            l = np.clip(l, np.finfo(np.float16).min, np.finfo(np.float16).max,
+                        where=np.isfinite(l), out=l.copy()).astype(np.float16)
+        rule = R.rule_of(experts, 4, None, scoring=scoring, renormalize=renormalize, scale=2.5)
+        ids, w = X.exl3_route_topk(G.to_dev(l), rule)
+        ref_ids, ref = S.route(l, 4, scoring, renormalize=renormalize, scale=2.5)
+        np.testing.assert_array_equal(ids.cpu().numpy(), ref_ids)
+        got = w.cpu().numpy().astype(np.float64)
+        for i, row in enumerate(l.astype(np.float64)):
+            np.testing.assert_array_equal(np.isnan(got[i]), np.isnan(ref[i]))
+            ok = ~np.isnan(ref[i])
+            assert (np.abs(got[i] - ref[i])[ok] <= near_bound(ref[i], row, scoring)[ok]).all(), (i, got[i], ref[i])
+        # masks
+        rng = np.random.default_rng(experts)
+        dt = np.float32 if f32 else np.float16
+        l = (rng.standard_normal((40, experts)) * 1.5).astype(dt)
+        masked = rng.random(l.shape) < 0.5
+        masked[::5] = True
+        masked[::5, experts // 2] = False
+        b = rng.standard_normal(experts) * 0.1
+        for balance in (None, b):
+            rule = R.rule_of(experts, 4, balance, scoring=scoring, renormalize=renormalize)
+            low = X.exl3_route_topk(G.to_dev(np.where(masked, np.finfo(dt).min, l)), rule)
+            inf = X.exl3_route_topk(G.to_dev(np.where(masked, dt(-np.inf), l)), rule)
+            assert torch.equal(low[0], inf[0])  # 0 / 0 is NaN on either side
+            assert torch.equal(low[1].view(torch.int32), inf[1].view(torch.int32))
+
+
 # both in a call: tokens in one launch, in rows, in tiles, in shares of either, past 2048
 @pytest.mark.parametrize("scoring,balanced,group_score", [("softmax", False, "max"), ("softmax", True, "top2"),
                                                           ("sigmoid", True, "max")])
