@@ -311,7 +311,7 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& q, int adapter) {
 // ---------------------------------------------------------------------------
 // 16 rows against 16 RT ranks (from 64 blockIdx.z on); a wave takes whole lines of 64
 // k one after the other, lane (row or rank r, g) their places 16 g .. 16 g + 15.  64 rows
-// of 5120 and 64 adapters of rank 16, 11 MB, in 5.6 us: start, loads' latency and end.
+// of 5120 and 64 adapters of rank 16, 11 MB, in 6.6 us: start, loads' latency and end.
 template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
   constexpr int U = 4 / RT;  // lines whose loads go out together
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink(LoraArgs q) {
 }
 
 // 64 rows against 64 ranks (from 64 blockIdx.z on), for rows that 32-bit offsets reach.
-// 4096 x 5120 of rank 64 in 18 us: 84 MB to LDS, 42 of them from memory, behind 4 us of
+// 4096 x 5120 of rank 64 in 19 us: 84 MB to LDS, 42 of them from memory, behind 4 us of
 // start and end.
 __global__ __launch_bounds__(kTile64Waves * 64) void lora_shrink_tiled(LoraArgs q) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
@@ -603,7 +603,7 @@ struct LoraIo {
 // CH: chunks of 32 ranks; 0: up to 16 ranks, where an operand's upper half of k holds
 // another 16 columns, met by pieces that are zero in the other half.
 // What bounds it is base, y and B: 64 rows 5120 -> 17408 of 64 adapters of rank 16, 40 MB
-// in 12.7 us (3.2 TB/s) where a workgroup's start, 4 us, counts.
+// in 12.5 to 13.6 us (3 TB/s) where a workgroup's start, 4 us, counts.
 //
 // Workgroups a CU:
 __host__ __device__ constexpr int lora_expand_groups(int ch) { return ch == 0 ? 5 : ch == 1 ? 4 : ch == 2 ? 3 : 2; }
@@ -754,10 +754,13 @@ __global__ __launch_bounds__(kLoraThreads, lora_expand_groups(CH)) void lora_exp
 }
 
 // Up to 64 rows, 16 a wave, whose pieces stay in registers while tiles of 64 columns pass:
-// a tile's B goes from memory straight to LDS, two tiles ahead, and serves the four waves.
-// (Loaded by the lanes that multiply it, 16 rows an instruction, it comes at 16 bytes a
-// clock and CU, which for 64 ranks is as long as base and y take.)  Bound by base and y:
-// 4096 rows, n 17408, rank 64, four adapters, 294 MB in 66 us (4.4 TB/s).
+// a tile's B goes from memory straight to LDS, sent two tiles ahead, and serves the four
+// waves.  (Loaded by the lanes that multiply it, 16 rows an instruction, it comes at 16
+// bytes a clock and CU, which for 64 ranks is as long as base and y take.)  4096 rows, n
+// 17408, rank 64, four adapters, 294 MB in 69 to 71 us (4.1 to 4.3 TB/s).  Bound by base
+// and y and by waits: the compiler, which does not count the copies, waits for all vector
+// memory at the top of every second tile, and before the stores for all but the newest
+// two or three accesses, so that B and y are waited for once in two tiles at least.
 //
 // LDS: a tile holds a row of 4 CH 16-byte pieces for each column; piece c of row n lies at
 // place c ^ turn(n), so that sixteen rows' pieces c cover all 64 banks.
@@ -920,7 +923,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_long(LoraArgs q) {
 // A workgroup takes a row (blockIdx.y) and 8192 / RJ columns: it makes the row's whole h
 // itself (A from L2, which costs less than a launch) and then its columns, RJ / 8 threads
 // a column.  RJ: a power of two >= rank.  A wave takes 8 ranks of every 512 k from its
-// place on.  One row 5120 -> 17408 of rank 16, 0.8 MB, in 6.2 us: latency, first of A and
+// place on.  One row 5120 -> 17408 of rank 16, 0.8 MB, in 6.6 us: latency, first of A and
 // x, then of the sums' way through LDS.
 constexpr int kLoraFewThreads = 1024;
 
@@ -1001,9 +1004,9 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int lora_few_rank(int rank) { return rank <= 8 ? 8 : rank <= 16 ? 16 : rank <= 32 ? 32 : 64; }
 
 // One launch while a round of workgroups holds it and the A that each reads is short (us,
-// one launch / two, 16 adapters): 5120 -> 17408 of rank 16, 1 row 6.2 / 8.9, 4 6.4 / 9.5, 8
-// (272 workgroups) 11.2 / 9.9; of rank 32, 1 row 7.0 / 8.5; of rank 64 (655 KB) 9.9 / 9.9;
-// 17408 -> 5120 of rank 16 (557 KB), 8 rows 12.0 / 10.6; 2048 -> 512, 64 rows 5.2 / 8.9.
+// one launch / two, 16 adapters): 5120 -> 17408 of rank 16, 1 row 6.1 / 8.5, 4 6.4 / 8.6, 8
+// (272 workgroups) 11.4 / 9.2; of rank 32, 1 row 6.9 / 8.5; of rank 64 (655 KB) 9.7 / 9.9;
+// 17408 -> 5120 of rank 16 (557 KB), 8 rows 11.9 / 9.4; 2048 -> 512, 64 rows 5.2 / 9.4.
 bool lora_is_few(const LoraDesc& d, int64_t m) {
   if (d.rank > kLoraFewRank || m > 256) return false;
   const int64_t cols = kLoraFewThreads * 8 / lora_few_rank(d.rank);
@@ -1013,9 +1016,9 @@ bool lora_is_few(const LoraDesc& d, int64_t m) {
 
 // 64 rows a segment where adapters have more than 16 each on average, enough of them for
 // the chip and 32-bit offsets for the copies to LDS.  Segments of 64 / of 16 rows, us,
-// 5120 -> 17408 of rank 64: 256 rows of one adapter 23.6 / 20.4, 512 27.2 / 28.6, 1024 rows
-// of 16 adapters 44 / 57, of 63 83 / 87, of 128 133 / 131, 4096 rows of 64 128 / 211, of 200
-// 269 / 252; 5120 -> 5120 of rank 16: 512 rows of 8 19.4 / 18.4, 4096 of 64 47 / 58.
+// 5120 -> 17408 of rank 64: 256 rows of one adapter 23.4 / 20.4, 512 27.1 / 29.8, 1024 rows
+// of 16 adapters 45 / 59, of 63 83 / 87, of 128 134 / 118, 4096 rows of 64 129 / 193, of 200
+// 271 / 246; 5120 -> 5120 of rank 16: 512 rows of 8 19.1 / 17.4, 4096 of 64 47 / 53.
 bool lora_long(const LoraDesc& d, int64_t m, int64_t ldx) {
   return m >= 512 && d.n >= 8 && m > 16 * (int64_t)d.adapters && m * ldx < (int64_t)1 << 31;
 }
@@ -1030,11 +1033,11 @@ int64_t lora_most_segs(const LoraDesc& d, int64_t m, bool longer) {
 int64_t lora_long_segs(const LoraDesc& d, int64_t m) { return (m + 63) / 64 + d.adapters / 2; }
 
 // Shares of k: workgroups for the chip against what each share costs lora_expand, which
-// adds them, the more the longer h is.  Fitted to 744 shapes of 8 to 2048 rows, rank 8 to
-// 256, k 2048 to 17408 and 1 to 64 adapters, at most 18 % from their best (us, shares in
-// brackets, 5120 -> 5120: 333 rows of 8 adapters of rank 16 15.4 (4), 13.7 (8), 16.6 (16); 64
-// rows of rank 256 27 (2), 22 (4), 28 (16); 17408 -> 5120, 600 rows of rank 8 26 (4), 21 (8),
-// 600 of rank 256 45 (4), 56 (8)).
+// adds them, the more the longer h is.  Over 432 shapes of 8 to 2048 rows, rank 8 to 256,
+// k 2048 to 17408 and 1 to 64 adapters, 2.9 % from each shape's best on average and 19 % at
+// most (us, shares in brackets, 5120 -> 5120: 333 rows of 8 adapters of rank 16 15.3 (4),
+// 13.9 (8), 16.6 (16); 64 rows of 8 adapters of rank 256 27 (2), 22 (4), 28 (16); 17408 ->
+// 5120 of one adapter, 600 rows of rank 8 26 (4), 21 (8), of rank 256 45 (4), 56 (8)).
 int lora_splits(const LoraDesc& d, int64_t m, bool longer) {
   const int64_t ranks = (d.rank + 63) / 64;
   int64_t s, most, cap;
@@ -1088,7 +1091,7 @@ template <int CH, bool TINY = false>
 void launch_expand(LoraArgs q, bool f32, hipStream_t s) {
   const size_t lds = 2 * 16 * lora_piece_row(CH ? CH : 1) + 4 * 16 * kLoraOutStride * 4;
   const int64_t segs = lora_most_segs(q.d, q.m, false), tiles = (q.d.n + 63) / 64;
-  // one round of workgroups: each begins with the segment's search and its h, 4 us
+  // one round of workgroups: each begins with its segment and its h, 4 us
   const int64_t slots = 256 * lora_expand_groups(CH);
   q.tiles = 1;
   while (segs * ((tiles + 4 * q.tiles - 1) / (4 * q.tiles)) > slots && 4 * q.tiles < tiles && q.tiles < 16) ++q.tiles;

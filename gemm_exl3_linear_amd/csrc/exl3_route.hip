@@ -4,10 +4,10 @@
 // they cost (a merge of two lists of eight is 56 of them), and four tokens share them.
 // Few tokens wait for one wave's instructions, and for their way from memory: they take
 // a wave each, whose lanes hold a quarter of the values.
-// Measured (us of the kernel, a wave / 16 lanes a token, 8 of 256 experts): softmax, 1
-// token 3.2 / 4.3, 2048 4.5 / 4.7, 4096 6.5 / 4.8, 16384 19.0 / 10.0; balanced sigmoids
-// in 8 groups 4.9 / 7.2, 6.1 / 7.7, 8.8 / 7.9, 25.6 / 16.5; 4 of 60 experts, 2048 tokens
-// 3.2 / 2.9, 16384 10.3 / 4.0.
+// Measured (us of a call in a graph of 20, a wave / 16 lanes a token, 8 of 256 experts):
+// softmax, 1 token 2.8 / 3.3, 2048 4.2 / 3.8, 4096 6.2 / 3.8, 16384 18.5 / 7.5; balanced
+// sigmoids in 8 groups 4.5 / 6.6, 6.0 / 7.1, 8.8 / 7.2, 24.8 / 14.6; 4 of 60 experts, 2048
+// tokens 3.1 / 2.7, 16384 9.8 / 3.9.
 #include "exl3_mx4.hpp"
 #include "exl3_route.hpp"
 

@@ -35,7 +35,7 @@ enum class RouterEnd { kStore, kAdd, kRoute };
 // Sums of 16 experts (blockIdx.x / splits) for 16 tokens (from blockIdx.y on) over a
 // share of hidden.  END == kRoute: at most 64 VPL experts, topk <= K.  kAdd and kRoute: one
 // tile of tokens (gridDim.y is 1).  Small calls, bound by a chain of latencies: 333 x 1440
-// x 60 in 4.4 us; one token's 2048 x 256 with its routing in 7.2, of which the way of the
+// x 60 in 4.9 us; one token's 2048 x 256 with its routing in 7.6, of which the way of the
 // sums to the last workgroup takes 2 and the routing 1.5.
 template <RouterEnd END, int VPL, int K>
 __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterArgs q) {
@@ -129,9 +129,10 @@ __global__ __launch_bounds__(kRouterWaves * 64) void router_rows_kernel(RouterAr
 // many tokens
 // ---------------------------------------------------------------------------
 // 64 tokens x 64 experts over a share of k (blockIdx.y): exl3_tile64.hpp.  4096 x 5120 x
-// 256 in 21 us (0.51 PFLOP/s), of which the 335 MB that 256 CUs copy to LDS take 17 by
-// themselves, and as long to registers.  Larger tiles halve them, but leave CUs idle or
-// shares to be added: 128 x 128 in four shares took as long.
+// 256 in 20 to 22 us (0.5 PFLOP/s), of which the 335 MB that 256 CUs copy to LDS take 17
+// by themselves, and as long to registers.  (Larger tiles halve them; 128 x 128 makes 64
+// workgroups of that product, so that three CUs of four are idle or shares of k are to be
+// added.)
 __global__ __launch_bounds__(kTile64Waves * 64) void router_gemm_kernel(RouterArgs q) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile64Lds];
   // a row tile's workgroups run on one XCD (workgroup i on XCD i % 8), one behind the
@@ -199,18 +200,21 @@ struct RouterCut {
 };
 
 // Routed by the launch that makes the logits: the last workgroup's waves route a token
-// after the other (us, fused / in two launches, of which the host bounds the latter at
-// 10.5: 256 experts, 4 tokens 8.5 / 10.4, 8 9.7 / 10.6, 16 14.1 / 10.5; 64 experts, 16
-// tokens 8.6 / 10.6; 1024 experts, 1 token 22 / 10.9).  One tile of tokens: the arrivals
-// that make a workgroup the last are counted over the experts and shares of one.
+// after the other (us of 2048 hidden, calls one behind the other, fused / in two launches,
+// which the host bounds: 256 experts, 1 token 7.1 / 9.5, 4 7.5 / 9.1, 8 9.2 / 9.5, 16 12.9 /
+// 9.4; 64 experts, 16 tokens 9.2 / 9.5.  In a graph, where the host has no part, 7.2 / 6.1,
+// 7.6 / 6.7, 9.4 / 6.8, 13.1 / 6.9 and 9.3 / 6.5).  One tile of tokens: the arrivals that
+// make a workgroup the last are counted over the experts and shares of one.
 bool router_fused(const RouterDesc& d, int64_t t) {
   return t <= kRouterRows && d.experts <= 256 && t * d.experts <= 1024;
 }
 
 // The cut by estimates in us, fitted to kernels alone, and measured where they meet
-// (tokens x hidden x experts, by rows / tiled, shares in brackets): 64 x 5120 x 256 8.0
-// (8) / 8.8 (8), 256 13.1 (1) / 9.6 (8), 1000 38 (1) / 13.9 (4); 17 x 5120 x 1000 9.4 (4) /
-// 8.4 (8), 512 74 (1) / 21 (2); 1000 x 2048 x 60 7.2 (1) / 9.0 (8), 2000 10.6 (1) / 9.2 (1).
+// (tokens x hidden x experts, by rows / tiled, shares in brackets): 64 x 5120 x 256 8.1
+// (8) / 8.8 (8), 256 13.0 (1) / 9.6 (8), 1000 38 (1) / 14.0 (4); 17 x 5120 x 1000 9.3 (4) /
+// 8.5 (8), 512 75 (1) / 21 (2); 1000 x 2048 x 60 7.2 (1) / 9.0 (8), 2000 10.6 (1) / 9.3 (1).
+// Over 203 shapes of 17 to 8000 tokens 1.1 % from each shape's best on average, 15 % at
+// most; routed, 293 shapes from one token on, 0.6 and 18 %.
 RouterCut router_cut(const RouterDesc& d, int64_t t, int64_t ldx, RouterJoin join) {
   const int64_t groups = (d.experts + 15) / 16, rows = (t + kRouterRows - 1) / kRouterRows;
   const auto joined = [&](int splits) {
