@@ -310,3 +310,76 @@ def test_lora_scales_at_the_ends_of_fp32(rank, m, adapters):
     assert (y[want == 0] == 0).all()
     bad = ~(np.abs(y - want) <= 5 * 2.0 ** -24 * np.abs(want))
     assert not bad.any(), f"{bad.sum()} of {bad.size}: {y[bad][0]!r} for {want[bad][0]!r}"
+
+
+# ---------------------------------------------------------------------------
+# the largest sizes
+# ---------------------------------------------------------------------------
+def test_route_of_the_most_tokens():
+    """2^24 tokens: the bits of a sixteenth at a time, and the oracle at the last."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    t, experts = 1 << 24, 5
+    g = torch.Generator(device=G.dev()).manual_seed(3)
+    l = torch.randn(t, experts, generator=g, device=G.dev()).half()
+    rule = R.rule_of(experts, 2, np.random.default_rng(3).standard_normal(experts) * 0.1, scoring="softmax")
+    ids, w = X.exl3_route_topk(l, rule)
+    for i in range(0, t, t // 16):
+        part = X.exl3_route_topk(l[i:i + t // 16], rule)
+        assert torch.equal(part[0], ids[i:i + t // 16]) and torch.equal(part[1], w[i:i + t // 16])
+    # fp16 logits that are equal give s + b of two experts that may be, to rounding: none here
+    R.check(ids[-500:], w[-500:], l[-500:].cpu().numpy().astype(np.float64), rule)
+
+
+@pytest.mark.parametrize("t,hidden,experts", [(1 << 24, 8, 3), ((1 << 20) + 5, 64, 70), (3, 65536, 1024),
+                                              (40, 65536, 1024)])
+def test_router_of_the_largest_sizes(t, hidden, experts):
+    """Whole numbers, whose sums are exact; choices by the logits' order."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    g = torch.Generator(device=G.dev()).manual_seed(experts)
+    x = torch.randint(-2, 3, (t, hidden), generator=g, device=G.dev(), dtype=torch.int8).half()
+    w = torch.randint(-2, 3, (experts, hidden), generator=g, device=G.dev(), dtype=torch.int8).half()
+    r, rule = X.Exl3Router(w), X.Exl3RouteRule(experts, min(2, experts))
+    logits = torch.empty((t, experts), device=G.dev())
+    ids, wt = X.exl3_router(x, r, rule, logits=logits)
+    apart = X.exl3_router_linear(x, r)
+    step = min(t, 1 << 20)
+    for i in range(0, t, step):
+        ref = x[i:i + step].double() @ w.double().t()
+        assert torch.equal(logits[i:i + step].double(), ref) and torch.equal(apart[i:i + step].double(), ref)
+        order = torch.sort(ref, dim=-1, descending=True, stable=True).indices[:, :rule.topk]
+        assert torch.equal(ids[i:i + step].long(), order)
+    again = X.exl3_route_topk(logits, rule)
+    assert torch.equal(again[0], ids) and torch.equal(again[1], wt)
+
+
+@pytest.mark.parametrize("m,k,n,rank,adapters", [(1 << 24, 8, 9, 8, 3), (1 << 24, 8, 1, 8, 2), (1 << 21, 8, 5, 8, 4096),
+                                                 (5, 1 << 20, 64, 8, 2), (70, 64, 1 << 20, 16, 2),
+                                                 (600, 64, 1 << 20, 256, 1)])
+def test_lora_of_the_largest_sizes(m, k, n, rank, adapters):
+    """Whole numbers below 2^24 at every step (k 4 times rank at most), in place."""
+    import torch
+    import gemm_exl3_linear_amd as X
+    g = torch.Generator(device=G.dev()).manual_seed(adapters)
+    whole = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=G.dev(), dtype=torch.int8)
+    x, a, b = whole(-1, 2, m, k).half(), whole(-1, 2, adapters, rank, k).half(), whole(-1, 2, adapters, n, rank).half()
+    rows = torch.randint(-1, adapters, (m,), generator=g, device=G.dev()).int()
+    base = whole(-9, 10, m, n)
+    y = base.float()
+    X.exl3_lora(x, X.Exl3Lora(a, b), rows, y, out=y)
+    step = max(1, min(m, (1 << 24) // max(n, k)))
+    if adapters > 100:  # one product a row
+        ref = lambda i, r: torch.bmm(b[r].float(), torch.bmm(a[r].float(), x[i].float().unsqueeze(-1))).squeeze(-1)
+    for i0 in range(0, m, step):
+        want = base[i0:i0 + step].double()
+        if adapters > 100:
+            for j in range(i0, min(m, i0 + step), 1 << 16):
+                i = torch.arange(j, min(m, i0 + step, j + (1 << 16)), device=G.dev())
+                i = i[rows[i] >= 0]
+                want[i - i0] += ref(i, rows[i].long()).double()
+        else:
+            for e in range(adapters):
+                mine = rows[i0:i0 + step] == e
+                want[mine] += ((x[i0:i0 + step][mine].float() @ a[e].float().t()).double() @ b[e].double().t())
+        assert torch.equal(y[i0:i0 + step].double(), want), i0
